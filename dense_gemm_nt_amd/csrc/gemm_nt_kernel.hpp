@@ -41,12 +41,13 @@
 #include <type_traits>
 
 #include "gemm_nt_common.hpp"
+#include "gemm_nt_ext.hpp"
 
 namespace gnt {
 
 // ROT: the tiles walk their k-slabs in the rotated order (SlabOrder).
 template <int BM, int BN, int BK, int WM, int WN, int STAGES, int IN, int OUT, bool KMASK, bool ROT>
-__global__ __launch_bounds__(WM *WN * 64, 1) void gemm_nt_kernel(KernelArgs p)
+__global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)(GNT_EXT_ARGS p)
 {
     constexpr int NWAVES = WM * WN;
     constexpr int NT = NWAVES * 64;
@@ -72,10 +73,16 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_nt_kernel(KernelArgs p)
     const int wave_m = wave / WN, wave_n = wave % WN;
 
     int tm, tn, split;
+#ifdef GNT_EXT_LOOKUP
+    split = 0;
+    if (!GNT_EXT_LOOKUP(p, tm, tn))
+        return;
+#else
     if (p.inreduce)       // the K splits of a tile adjacent in launch order (splitk_arrive)
         map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
     else
         map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+#endif
     const int tile = tm * p.tiles_n + tn;
     const int m0 = tm * BM, n0 = tn * BN;
     const int kt_begin = split * p.kt_per_split;
@@ -262,6 +269,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void gemm_nt_kernel(KernelArgs p)
         else
             main_loop(std::false_type{});
     }
+
+    GNT_EXT_ACC(p, acc, m0 + wave_m * WTM, n0 + wave_n * WTN, split, lane)
 
     // K splits reduced here: the last split of the tile to finish adds the
     // others' partials and stores the tile as an unsplit one (the flag word is

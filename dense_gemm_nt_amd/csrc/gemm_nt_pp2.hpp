@@ -60,6 +60,7 @@
 #include <type_traits>
 
 #include "gemm_nt_common.hpp"
+#include "gemm_nt_ext.hpp"
 
 #ifdef GNT_PP2_TRACE
 #include "gemm_nt_trace.hpp"
@@ -78,7 +79,7 @@ namespace gnt {
 // 2 stream-K segments, each stored as an FP32 partial slot (no epilogue).
 template <int IN, int OUT, bool AM = false, bool BNM = false, int SC = 0, bool GR = false,
           int PS = 0>
-__global__ __launch_bounds__(512, 1) void gemm_nt_pp2(KernelArgs p0)
+__global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_ARGS p0)
 {
     constexpr bool F8 = IN >= IN_F8;
     constexpr int ESZ = F8 ? 1 : 2;          // bytes per element
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_pp2(KernelArgs p0)
     const int wm0 = group * 128 + (q >> 1) * 64;   // wave's first row within the tile
     const int wn0 = (q & 1) * 128;                 // and first column
 
-    KernelArgs p = p0;
+    GNT_EXT_ARGS p = p0;
 
     constexpr bool streamk = PS == 2;
     // Grouped launches re-read row 0 for A loads wholly past M (see the loader):
@@ -509,6 +510,7 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_pp2(KernelArgs p0)
         }
 
         GNT_PP2_DUMP
+        GNT_EXT_ACC(p, acc, m0 + wm0, n0 + wn0, split, lane)
         // Epilogue (the ring is free: the last fragment read and the last load
         // completed before the loop's last barrier).  Each wave stages its own
         // 64 x 128 block in its own 16 KB of LDS.
@@ -587,6 +589,12 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_pp2(KernelArgs p0)
 
     int tm, tn, split;
     if constexpr (GR) {
+#ifdef GNT_EXT_LOOKUP
+        split = 0;
+        if (!GNT_EXT_LOOKUP(p, tm, tn))
+            return;
+        tile(tm, tn, split);
+#else
         // Grouped launch: this block's launch position names its problem and
         // the tile within it; the problem's fields replace the launch's.
         const int v = xcd_order(blockIdx.x, gridDim.x);
@@ -623,6 +631,7 @@ __global__ __launch_bounds__(512, 1) void gemm_nt_pp2(KernelArgs p0)
         split = 0;
         tile_order(v - u32(d->tile_start), p.tiles_m, p.tiles_n, p.group_m, tm, tn);
         tile(tm, tn, split);
+#endif
     } else if constexpr (PS == 2) {
         // Stream-K: block b takes the contiguous units [b T / G, (b + 1) T / G)
         // of the T = tiles * k_tiles (tile, k-slab) units in tile-major order,

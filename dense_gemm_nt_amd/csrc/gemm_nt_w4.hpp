@@ -46,6 +46,7 @@
 #include <type_traits>
 
 #include "gemm_nt_common.hpp"
+#include "gemm_nt_ext.hpp"
 
 namespace gnt {
 
@@ -174,7 +175,7 @@ __device__ __forceinline__ void store_wave_block_any(const KernelArgs &p, const 
 }
 
 template <int IN, int OUT, int BN>
-__global__ __launch_bounds__(256, 1) void gemm_nt_w4(KernelArgs p)
+__global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARGS p)
 {
     constexpr int BM = 256, BK = 64;
     constexpr int PITCH = 128;                // bytes per LDS row (64 16-bit values)
@@ -380,6 +381,8 @@ __global__ __launch_bounds__(256, 1) void gemm_nt_w4(KernelArgs p)
         else
             main_loop(std::false_type{});
     }
+
+    GNT_EXT_ACC(p, acc, m0 + wm * 128, n0 + wn * (BN / 2), split, lane)
 
     if (p.inreduce) {
         // two K splits: the second to arrive holds the sum and stores it as an
