@@ -20,10 +20,23 @@ SOURCES = [os.path.join(CSRC, f) for f in (
     "launch_pp2_f8_e5e5.hip", "launch_pp2_grouped.hip", "launch_pp2_persistent.hip", "launch_w4.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("gemm_nt_common.hpp", "gemm_nt_kernel.hpp",
                                            "gemm_nt_pp2.hpp", "gemm_nt_w4.hpp", "gemm_nt_trace.hpp",
-                                           "gemm_nt_launch.hpp", "launch_pp2.hip",
+                                           "gemm_nt_launch.hpp", "gemm_nt_ext.hpp", "gemm_nt_plan.hpp",
+                                           "launch_pp2.hip",
                                            "launch_pp2_f8.hip", "launch_tiles_a.hip")] + \
     [os.path.join(ROOT, "include", "gemm_nt.h")]
 LIB = os.path.join(PKG, "libgemm_nt.so")
+# the row-indexed products (include/gemm_rows.h): a library of its own, whose
+# tiles are the headers above with an addition
+ROWS = os.path.join(CSRC, "rows")
+ROWS_SOURCES = [os.path.join(ROWS, f) for f in (
+    "rows_lora.hip", "rows_route.hip", "rows_routed.hip", "launch_lora_tiles.hip",
+    "launch_lora_tiles_b.hip", "launch_lora_w4.hip", "launch_lora_pp2.hip",
+    "launch_lora_pp2_km.hip", "launch_routed_tiles.hip", "launch_routed_pp2.hip",
+    "launch_routed_pp2_km.hip", "launch_routed_pp2_mm.hip")]
+ROWS_HEADERS = [os.path.join(ROWS, f) for f in ("rows_common.hpp", "rows_group.hpp",
+                                                "rows_host.hpp", "rows_launch.hpp")] + \
+    [os.path.join(ROOT, "include", "gemm_rows.h")]
+ROWS_LIB = os.path.join(PKG, "libgemm_rows.so")
 ARCH = "gfx950"
 
 
@@ -56,13 +69,14 @@ def _run(cmd):
     return out
 
 
-def build(verbose: bool = False, jobs: int = 0, out: str = LIB, defines=()) -> str:
+def build(verbose: bool = False, jobs: int = 0, out: str = LIB, defines=(), sources=None) -> str:
     """Compile every source and link them into `out` (the library by default;
     `defines` are extra -D flags, e.g. for an instrumented copy)."""
+    sources = SOURCES if sources is None else sources
     tmpdir = tempfile.mkdtemp(prefix="gemm_nt_build_")
     try:
-        objs = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in SOURCES]
-        cmds = [[hipcc(), *flags(), *defines, "-c", src, "-o", obj] for src, obj in zip(SOURCES, objs)]
+        objs = [os.path.join(tmpdir, os.path.basename(src) + ".o") for src in sources]
+        cmds = [[hipcc(), *flags(), *defines, "-c", src, "-o", obj] for src, obj in zip(sources, objs)]
         jobs = jobs or max(1, min(len(cmds), os.cpu_count() or 1, 8))
         if verbose:
             for c in cmds:
@@ -80,6 +94,18 @@ def build(verbose: bool = False, jobs: int = 0, out: str = LIB, defines=()) -> s
     return out
 
 
+def build_rows(verbose: bool = False, jobs: int = 0) -> str:
+    """The library of the row-indexed products."""
+    return build(verbose, jobs, ROWS_LIB, sources=ROWS_SOURCES)
+
+
+def stale_rows() -> bool:
+    if not os.path.exists(ROWS_LIB):
+        return True
+    t = os.path.getmtime(ROWS_LIB)
+    return any(os.path.getmtime(f) > t for f in ROWS_SOURCES + ROWS_HEADERS + HEADERS)
+
+
 def stale() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -89,3 +115,4 @@ def stale() -> bool:
 
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
+    print(build_rows(verbose="-v" in sys.argv))

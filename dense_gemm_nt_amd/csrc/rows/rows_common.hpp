@@ -1,0 +1,400 @@
+// rows_common.hpp -- pieces shared by the kernels whose weight depends on the
+// row: argument blocks, conversions, the walk over a row block's adapters.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../gemm_nt_common.hpp"
+
+namespace gnt {
+
+// A projection with low-rank adapters: the tile's arguments plus the adapters.
+// low[s][m][rank_pad] holds K split s's part of row m's unscaled low-rank
+// product; up is [adapter][N][rank] (adapter a at a * up_stride elements, rows
+// of up_ld elements).
+struct LoraArgs : KernelArgs {
+    const float *low;
+    const uint16_t *up;
+    const float *scale;
+    const int32_t *ids;
+    int64_t up_stride;
+    int up_ld;
+    int adapters;          // 0: no adapters, nothing is added
+    int rank, rank_pad;    // rank_pad: rank rounded up to 16
+    int low_splits;
+};
+
+// Products over rows sorted by expert.  A, B, C (and lda, ldb, ldc) are the whole
+// arrays; every block finds its expert, hence its tile, from the offsets.
+struct RoutedArgs : KernelArgs {
+    const int32_t *offsets;   // [experts + 1]
+    int experts;
+    int rows;                 // of the sorted arrays
+    int tile_m;               // rows (weight gradient: rows of dW_e) of a tile
+    int tail;                 // rows behind the last expert's are set to zero
+    int wgrad;                // dW_e [N][K] = dY_e^T X_e, else C_e = X_e op(W_e)
+    int64_t b_stride;         // elements between experts' W
+    int64_t c_stride;         // wgrad: elements between experts' dW
+    int c_size;               // bytes of an element of C
+};
+
+// v combined with the lanes below it, inclusively.
+template <typename F>
+__device__ __forceinline__ int wave_scan(int v, int lane, F op)
+{
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(v, o);
+        v = lane >= o ? op(v, y) : v;
+    }
+    return v;
+}
+
+// Block id -> its tile's expert, and the expert's problem and tile within it;
+// false for a block past the last tile.  The grid is the host's bound on the
+// tiles (which it does not know).  Every wave scans the offsets by itself, 64
+// experts at a time, stopping at its own: about a microsecond for up to 64
+// experts, where a launch of its own to write a problem list costs several.
+// Offsets are read clamped to [0, rows] and to their running maximum, so that
+// whatever they hold no row outside the arrays is touched.
+//
+// Launch order: block ids go round-robin over the 8 XCDs, and the ids of one
+// XCD take runs of 32 consecutive tiles (its compute units) within every 256,
+// so that tiles sharing panels meet in one L2; the order does not depend on the
+// number of tiles, so the blocks without one are spread over the XCDs.
+__device__ __forceinline__ bool routed_lookup(RoutedArgs &p, int &tm, int &tn)
+{
+    const int lane = threadIdx.x & 63;
+    const int bid = blockIdx.x;
+    const int v = (bid & ~255) + (bid & 7) * 32 + ((bid >> 3) & 31);
+    const int E = p.experts, rows = p.rows;
+    auto at = [&](int e) { return min(max(p.offsets[e], 0), rows); };
+    int top = 0, before = 0;                 // carried over the experts scanned
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+        const int e = e0 + lane;
+        const int lo = e <= E ? at(e) : 0, hi = e < E ? at(e + 1) : 0;
+        const int start = max(top, wave_scan(lo, lane, [](int a, int b) { return max(a, b); }));
+        // entry E is the tail's
+        const int count = e < E ? max(start, hi) - start : (e == E && p.tail ? rows - start : 0);
+        const int tall = p.wgrad ? (e < E ? p.M : 0) : count;
+        const int tiles = ((tall + p.tile_m - 1) / p.tile_m) * p.tiles_n;
+        const int past = before + wave_scan(tiles, lane, [](int a, int b) { return a + b; });
+        const uint64_t holds = __builtin_amdgcn_ballot_w64(v < past);
+        if (holds) {
+            const int l = __builtin_ctzll(holds);
+            const int g = e0 + l;
+            const int s = __builtin_amdgcn_readlane(start, l), n = __builtin_amdgcn_readlane(count, l);
+            const int t = v - (__builtin_amdgcn_readlane(past, l) - __builtin_amdgcn_readlane(tiles, l));
+            p.A += (int64_t)s * p.lda;
+            if (p.wgrad) {
+                p.B += (int64_t)s * p.ldb;
+                p.C = static_cast<uint8_t *>(p.C) + (int64_t)g * p.c_stride * p.c_size;
+                p.K = n;
+            } else {
+                p.B += (int64_t)(g < E ? g : 0) * p.b_stride;
+                p.C = static_cast<uint8_t *>(p.C) + (int64_t)s * p.ldc * p.c_size;
+                p.M = n;
+                p.K = g < E ? p.K : 0;       // the tail: a sum over nothing
+            }
+            p.tiles_m = (p.M + p.tile_m - 1) / p.tile_m;
+            p.k_tiles = (p.K + 63) / 64;
+            p.splits = 1;
+            p.kt_per_split = p.k_tiles;
+            p.nt_b = p.tiles_m <= 2;
+            tile_order(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+            return true;
+        }
+        top = __builtin_amdgcn_readlane(start, 63);
+        before = __builtin_amdgcn_readlane(past, 63);
+    }
+    return false;
+}
+
+template <int IN>
+__device__ __forceinline__ uint16_t to16(float x)
+{
+    if constexpr (IN == IN_BF16)
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+    else
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+
+template <int IN>
+__device__ __forceinline__ float from16(uint16_t h)
+{
+    if constexpr (IN == IN_BF16)
+        return static_cast<float>(__builtin_bit_cast(__bf16, h));
+    else
+        return static_cast<float>(__builtin_bit_cast(_Float16, h));
+}
+
+// An FP32 value as the sum of two 16-bit ones, for the matrix cores: hi the
+// nearest, lo the nearest to what is left, so hi + lo is within 2^-16 (bf16) or
+// 2^-22 (fp16; 2^-25 absolute below its normal range) of x relative to it, where
+// one 16-bit value would be within 2^-8 or 2^-11.  The low-rank products are intermediates that the caller never
+// sees: rounding them to 16 bits would put an error into an FP32 output that
+// nothing else in it has.  It costs a second MFMA per rank-16 step, of which an
+// output tile has rank / 16 beside its K / 16.  An infinite hi (an infinity, or
+// past fp16's range) stands alone.
+template <int IN>
+__device__ __forceinline__ void split16(float x, uint16_t &hi, uint16_t &lo)
+{
+    hi = to16<IN>(x);
+    const float h = from16<IN>(hi);
+    lo = __builtin_isfinite(h) ? to16<IN>(x - h) : (uint16_t)0;
+}
+
+template <int IN>
+__device__ __forceinline__ f32x4 mfma16x16x32(u32x4 a, u32x4 b, f32x4 c)
+{
+    if constexpr (IN == IN_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Wait states between a loop of MFMAs and what reads their results by other
+// units.  The compiler places these itself, but was seen to leave them out where
+// the loop's end and a path around the loop meet before an LDS store (the stored
+// values were then those of some cycles before); after such loops they are
+// placed here.  24 states cover the longest MFMA used (19).
+__device__ __forceinline__ void mfma_settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Nonzero where one of eight 16-bit values is an infinity or NaN: an exponent of
+// all ones carries into the sign's place when one is added to it.
+template <int IN>
+__device__ __forceinline__ uint32_t has_special(u32x4 x)
+{
+    constexpr uint32_t one = IN == IN_BF16 ? 0x00800080u : 0x04000400u;
+    uint32_t c = 0;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        c |= (x[d] & 0x7fff7fffu) + one;
+    return c & 0x80008000u;
+}
+
+// Each 16-bit value v of a fragment replaced by f(v).
+template <typename F>
+__device__ __forceinline__ u32x4 each16(u32x4 x, F f)
+{
+    u32x4 y;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+        y[d] = f(x[d] & 0xffffu) | f(x[d] >> 16) << 16;
+    return y;
+}
+
+// acc += up . (hi + lo) for the rows that are `own`, where up holds infinities or
+// NaNs (hi, lo are zero in the other rows): without any operand that could make
+// another row's zero into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the
+// infinity that is due in an own row and is 0 in the others', and a NaN (also
+// that of infinity times 0) is made as the sum of both infinities.  Rarely run,
+// and written for few registers: one operand pair at a time.
+template <int IN>
+__device__ __forceinline__ void add_special(f32x16 &acc, u32x4 up, u32x4 hi, u32x4 lo, bool own)
+{
+    constexpr uint32_t exp = IN == IN_BF16 ? 0x7f80u : 0x7c00u, big = 0x7f00u;
+    auto step = [&](auto f, auto g, uint32_t flip) {
+        const u32x4 x = each16(up, f), y = each16(hi, g) ^ flip;
+        acc = mfma32x32x16<IN_BF16>(x, y, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto is_nan = [](uint32_t v) { return (v & 0x7fffu) > exp ? big : 0u; };
+    auto is_inf = [](uint32_t v) { return (v & 0x7fffu) == exp ? big : 0u; };
+    auto inf = [](uint32_t v) { return (v & 0x7fffu) == exp ? (v & 0x8000u) | big : 0u; };
+    auto sign = [](uint32_t v) { return v & 0x7fffu ? (v & 0x8000u) | big : 0u; };
+    const uint32_t mine = own ? big : 0u;
+    auto row = [&](uint32_t) { return mine; };
+    auto zero = [&](uint32_t v) { return v & 0x7fffu ? 0u : mine; };
+    {
+        const u32x4 x = each16(up, [](uint32_t v) { return (v & exp) == exp ? 0u : v; });
+        acc = mfma32x32x16<IN>(x, hi, acc);
+        acc = mfma32x32x16<IN>(x, lo, acc);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    step(inf, sign, 0u);
+    step(is_nan, row, 0u);
+    step(is_nan, row, 0x80008000u);
+    step(is_inf, zero, 0u);
+    step(is_inf, zero, 0x80008000u);
+}
+
+// Adds every row's low-rank part to a wave's accumulators:
+//   acc[m][n] += s_a sum_r low[m][r] up_a[n][r],  a = ids[m]
+// for the 32 FM rows from r0 and 32 FN columns from c0, in the accumulators'
+// own layout (the up rows are the MFMA's first operand), so the shared
+// projection's sum is rounded once, together with the adapters'.  The wave walks the
+// adapters of its rows (a scalar walk over ballots: any order of rows, no
+// sorting), and for each the rows of other adapters enter as zeros: an adapter's
+// up rows are read once by every wave that has a row of it.  (Zero times an
+// infinity or NaN among those up rows would reach the other rows: adapters
+// whose fragments hold one are taken apart, add_special.)  A tile's K splits
+// share its adapters, split s taking the adapters s, s + splits, ... of each
+// wave's walk, so that all of a decode grid's blocks stream them; NB adapters'
+// fragments are in flight together.  Rows without an adapter, and ids that name
+// none, add nothing.  Nothing here waits on the tile's own loads.
+template <int IN, int FN, int FM>
+__device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM], int r0, int c0, int split,
+                                         int lane)
+{
+    constexpr int NB = FM * FN == 1 || FM == 4 ? 8 : FN == 4 ? 2 : 4;   // (fewer where registers are short)
+    if (p.adapters == 0 || r0 >= p.M || c0 >= p.N)
+        return;
+    int id[FM];
+    uint32_t rows[FM];
+    uint32_t any = 0;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+        const int m = r0 + fm * 32 + (lane & 31);
+        const int a = m < p.M ? p.ids[m] : -1;
+        id[fm] = (uint32_t)a < (uint32_t)p.adapters ? a : -1;
+        rows[fm] = (uint32_t)__builtin_amdgcn_ballot_w64(id[fm] >= 0);
+        any |= rows[fm];
+    }
+    if (any == 0)
+        return;
+    const int h = lane >> 5;
+    for (int rs = 0; rs < p.rank; rs += 16) {
+        // the wave's scaled low-rank values of ranks rs + 8 h .. +8, split in two
+        u32x4 hi[FM], lo[FM];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+            f32x4 v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
+            if (id[fm] >= 0 && rs + 8 * h < p.rank) {
+                const int m = r0 + fm * 32 + (lane & 31);
+                const float *src = p.low + (int64_t)m * p.rank_pad + rs + 8 * h;
+                for (int s = 0; s < p.low_splits; ++s) {
+                    v0 += *reinterpret_cast<const f32x4 *>(src);
+                    v1 += *reinterpret_cast<const f32x4 *>(src + 4);
+                    src += (int64_t)p.M * p.rank_pad;
+                }
+                const float sc = p.scale[id[fm]];
+                v0 *= sc;
+                v1 *= sc;
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                uint16_t h0, l0, h1, l1;
+                split16<IN>(d < 2 ? v0[2 * d] : v1[2 * d - 4], h0, l0);
+                split16<IN>(d < 2 ? v0[2 * d + 1] : v1[2 * d - 3], h1, l1);
+                hi[fm][d] = (uint32_t)h0 | ((uint32_t)h1 << 16);
+                lo[fm][d] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+            }
+        }
+        // the walk: the adapter of the first row left, until none is
+        uint32_t left[FM];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+            left[fm] = rows[fm];
+        int nth = 0;
+        auto next = [&]() -> int {
+            for (;;) {
+                int a = -1;
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm)
+                    if (a < 0 && left[fm])
+                        a = __builtin_amdgcn_readlane(id[fm], __builtin_ctz(left[fm]));
+                if (a < 0)
+                    return -1;
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm)
+                    left[fm] &= ~(uint32_t)__builtin_amdgcn_ballot_w64(id[fm] == a);
+                const bool mine = nth % p.splits == split;
+                ++nth;
+                if (mine)
+                    return a;
+            }
+        };
+        const bool rank_in = rs + 8 * h < p.rank;
+        const uint32_t voff = (uint32_t)(c0 + (lane & 31)) * (uint32_t)p.up_ld * 2u + (uint32_t)(rs + 8 * h) * 2u;
+        const uint32_t bytes = (uint32_t)p.N * (uint32_t)p.up_ld * 2u;   // below 2^31 (host)
+        auto load_up = [&](int a, int fn) {
+            return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 make_rsrc(p.up + (int64_t)a * p.up_stride, bytes),
+                                                 rank_in && c0 + fn * 32 + (lane & 31) < p.N
+                                                     ? voff + (uint32_t)(fn * 32) * (uint32_t)p.up_ld * 2u
+                                                     : kOutOfRange,
+                                                 0, 0));
+        };
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        bool apart = false;
+        for (;;) {
+            int a[NB];
+            u32x4 up[NB][FN];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                a[b] = b == 0 || a[b - 1] >= 0 ? next() : -1;
+                if (a[b] >= 0)
+#pragma unroll
+                    for (int fn = 0; fn < FN; ++fn)
+                        up[b][fn] = load_up(a[b], fn);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                if (a[b] < 0)
+                    continue;
+                uint32_t special = 0;
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn)
+                    special |= has_special<IN>(up[b][fn]);
+                if (__builtin_amdgcn_ballot_w64(special != 0)) {
+                    apart = true;
+                    continue;
+                }
+#pragma unroll
+                for (int fm = 0; fm < FM; ++fm) {
+                    const bool own = id[fm] == a[b];
+                    if (__builtin_amdgcn_ballot_w64(own) == 0)
+                        continue;
+                    const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
+#pragma unroll
+                    for (int fn = 0; fn < FN; ++fn) {
+                        acc[fn][fm] = mfma32x32x16<IN>(up[b][fn], th, acc[fn][fm]);
+                        acc[fn][fm] = mfma32x32x16<IN>(up[b][fn], tl, acc[fn][fm]);
+                    }
+                }
+            }
+            if (a[NB - 1] < 0)
+                break;
+        }
+        if (!apart)
+            continue;
+        // the adapters left out above, one at a time
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+            left[fm] = rows[fm];
+        nth = 0;
+        for (int a = next(); a >= 0; a = next()) {
+            uint32_t special = 0;
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+                special |= has_special<IN>(load_up(a, fn));
+            if (__builtin_amdgcn_ballot_w64(special != 0) == 0)
+                continue;
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm) {
+                const bool own = id[fm] == a;
+                if (__builtin_amdgcn_ballot_w64(own) == 0)
+                    continue;
+                const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn) {
+                    int again = a;                    // (a load of its own: registers)
+                    asm volatile("" : "+s"(again));
+                    add_special<IN>(acc[fn][fm], load_up(again, fn), th, tl, own);
+                }
+            }
+        }
+    }
+    mfma_settle();
+}
+
+}  // namespace gnt

@@ -1,0 +1,900 @@
+// rows_lora.hip -- a shared projection with low-rank adapters picked per row:
+// the low-rank products, the adapters' gradients, and the host side.  (The
+// product with the up matrices is part of the projection's own kernel:
+// lora_add in rows_common.hpp.)
+#include "rows_group.hpp"
+#include "rows_host.hpp"
+#include "rows_launch.hpp"
+
+namespace gnt {
+namespace {
+
+constexpr int kShrinkWaves = 8;
+constexpr int kMaxLowSplits = 16;
+
+struct ShrinkArgs {
+    const uint16_t *x;        // [M][K]
+    const uint16_t *down;     // adapter a: rank rows of down_ld at a * down_stride
+    const int32_t *ids;
+    float *low;               // [splits][M][rank_pad]
+    int64_t down_stride;
+    int M, K, ldx, down_ld, adapters, rank, rank_pad;
+    int k_per_split;          // a multiple of 128
+    int lanes_j;              // blocks sharing a row tile's adapters (gridDim.y)
+    unsigned *counters;       // zeroed here for the projection's split reduction
+    int num_counters;
+};
+
+// low[s][m][r] = sum over split s of K of x[m][k] down_a[r][k], a = ids[m].
+//
+// One block takes RM x 16 rows and one K split; its eight waves take K in steps
+// of 128 in turn (a wave reads 256 contiguous bytes of each row and of each
+// rank's row per step) and add up through LDS in wave order.  For each adapter
+// among the tile's rows all the rows are multiplied and the adapter's own kept:
+// MFMA work is free here (the bytes of x and of the adapters bound the kernel),
+// and no sorting of rows is needed.  A decode batch puts the adapters of a row
+// tile on different blocks (lanes_j), and K splits over more of them.
+template <int IN, int RM, int RT>
+__global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p)
+{
+    constexpr int W = kShrinkWaves, ROWS = 16 * RM, COLS = 16 * RT;
+    __shared__ float part[W][ROWS][COLS + 1];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    const int linear = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int i = linear * (W * 64) + tid; i < p.num_counters; i += gridDim.x * gridDim.y * gridDim.z * W * 64)
+        p.counters[i] = 0;
+
+    const int r0 = blockIdx.x * ROWS;
+    const int m = r0 + (lane & (ROWS - 1));
+    const int a_in = m < p.M ? p.ids[m] : -1;
+    const int id = (uint32_t)a_in < (uint32_t)p.adapters ? a_in : -1;
+    uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0) & ((1ull << ROWS) - 1);
+    const int kb = blockIdx.z * p.k_per_split;
+    const int ke = min(p.K, kb + p.k_per_split);
+    const int rows = min(ROWS, p.M - r0);
+    const __amdgpu_buffer_rsrc_t rs_x =
+        make_rsrc(p.x + (int64_t)r0 * p.ldx, (uint32_t)rows * (uint32_t)p.ldx * 2u);
+    const int li = lane & 15, kq = 8 * (lane >> 4);
+    float *out = p.low + (int64_t)blockIdx.z * p.M * p.rank_pad;
+
+    for (int nth = 0; left; ++nth) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        left &= ~__builtin_amdgcn_ballot_w64(id == a);
+        if (nth % p.lanes_j != (int)blockIdx.y)
+            continue;
+        for (int c0 = 0; c0 < p.rank_pad; c0 += COLS) {
+            const uint32_t d_bytes = __builtin_amdgcn_readfirstlane(
+                (uint32_t)max(0, min(COLS, p.rank - c0)) * (uint32_t)p.down_ld * 2u);
+            const __amdgpu_buffer_rsrc_t rs_d =
+                make_rsrc(p.down + a * p.down_stride + (int64_t)c0 * p.down_ld, d_bytes);
+            f32x4 acc[RM][RT];
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+                    acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k0 = kb + wave * 128; k0 < ke; k0 += W * 128) {
+                u32x4 xf[4][RM], df[4][RT];
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int k = k0 + 32 * s + kq;
+                    const bool in = k < ke;         // K is a multiple of 8
+#pragma unroll
+                    for (int i = 0; i < RM; ++i)
+                        xf[s][i] = __builtin_bit_cast(
+                            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       rs_x,
+                                       in && 16 * i + li < rows ? ((uint32_t)(16 * i + li) * (uint32_t)p.ldx + (uint32_t)k) * 2u
+                                                                : kOutOfRange,
+                                       0, 0));
+#pragma unroll
+                    for (int j = 0; j < RT; ++j)
+                        df[s][j] = __builtin_bit_cast(
+                            u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                       rs_d,
+                                       in && c0 + 16 * j + li < p.rank
+                                           ? ((uint32_t)(16 * j + li) * (uint32_t)p.down_ld + (uint32_t)k) * 2u
+                                           : kOutOfRange,
+                                       0, 0));
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int i = 0; i < RM; ++i)
+#pragma unroll
+                        for (int j = 0; j < RT; ++j)
+                            acc[i][j] = mfma16x16x32<IN>(xf[s][i], df[s][j], acc[i][j]);
+            }
+            mfma_settle();
+            __syncthreads();          // the last adapter's sums have been read
+#pragma unroll
+            for (int i = 0; i < RM; ++i)
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        part[wave][16 * i + 4 * (lane >> 4) + e][16 * j + li] = acc[i][j][e];
+            __syncthreads();
+            for (int t = tid; t < ROWS * COLS; t += W * 64) {
+                const int row = t / COLS, col = t % COLS;
+                if (r0 + row < p.M && c0 + col < p.rank_pad && p.ids[r0 + row] == a) {
+                    float v = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        v += part[w][row][col];
+                    out[(int64_t)(r0 + row) * p.rank_pad + c0 + col] = v;
+                }
+            }
+        }
+    }
+}
+
+// Zeros (a kernel, so that a captured call replays it like any other).
+__global__ void clear_words(uint32_t *p, int64_t words)
+{
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += step)
+        p[i] = 0;
+}
+
+// ---- gradients ----
+
+struct Stretch {
+    int adapter, first, end;    // places [first, end) of the sorted rows
+};
+
+struct GradArgs {
+    const int32_t *ids;
+    int M, adapters, rank, rank_pad, N, K;
+    // grouping of the rows by adapter
+    int *hist;
+    int64_t per_block;
+    int blocks;
+    int32_t *counts, *offsets, *order;
+    int chunk;                  // rows of a stretch, at most
+    int max_stretches;
+    Stretch *stretches;         // [max_stretches]; adapter -1 past the last
+    int *first_stretch;         // [adapters + 1]
+    // dA: z = x [M][K] with v = the gradient of the low-rank values; dB: z = dy
+    // [M][N] with v = the low-rank values.  v is [v_splits][M][rank_pad], scaled here.
+    const uint16_t *z[2];
+    const float *v[2];
+    int ldz[2], cols[2], v_splits[2];
+    float *part[2];             // [stretch][rank_pad][cols]
+    const float *scale;
+    void *out[2];               // dA [adapter][rank][K], dB [adapter][N][rank]
+    int out_dtype;
+};
+
+__global__ __launch_bounds__(kGroupThreads) void lora_count(GradArgs a)
+{
+    __shared__ int hist[kMaxGroups + 1];
+    for (int e = threadIdx.x; e <= a.adapters; e += kGroupThreads)
+        hist[e] = 0;
+    __syncthreads();
+    const int64_t t0 = blockIdx.x * a.per_block;
+    const int64_t t1 = t0 + a.per_block < a.M ? t0 + a.per_block : a.M;
+    for (int64_t i = t0 + threadIdx.x; i < t1; i += kGroupThreads) {
+        const int g = a.ids[i];
+        atomicAdd(&hist[(uint32_t)g < (uint32_t)a.adapters ? g : a.adapters], 1);
+    }
+    __syncthreads();
+    store_hist(hist, a.hist, a.adapters);
+}
+
+// The rows' order by adapter, and (a block of its own) the stretches: each
+// adapter's rows in runs of at most `chunk`, so that a stretch is one unit of
+// work with one adapter.
+__global__ __launch_bounds__(kGroupThreads) void lora_place(GradArgs a)
+{
+    __shared__ PlaceLds l;
+    if ((int)blockIdx.x < a.blocks) {
+        place_block(l, a.ids, a.M, a.adapters, a.per_block, a.hist, blockIdx.x, a.blocks, a.counts, a.offsets,
+                    a.order);
+        return;
+    }
+    const int tid = threadIdx.x, L = a.adapters;
+    for (int e = tid; e < L; e += kGroupThreads) {
+        int c = 0;
+#pragma unroll 8
+        for (int i = 0; i < a.blocks; ++i)
+            c += a.hist[(int64_t)i * (L + 1) + e];
+        l.wave[0][e] = l.wave[1][e] = c;
+        l.start[e] = (c + a.chunk - 1) / a.chunk;
+    }
+    if (tid == 0)
+        l.start[L] = l.wave[0][L] = 0;
+    __syncthreads();
+    scan_lds(l.start, L + 1, l.part);       // stretches before adapter e
+    scan_lds(l.wave[0], L + 1, l.part);     // rows before it
+    for (int e = tid; e <= L; e += kGroupThreads) {
+        a.first_stretch[e] = l.start[e];
+        if (e < L) {
+            const int rows = l.wave[0][e], end = rows + l.wave[1][e];
+            for (int s = l.start[e], at = rows; at < end; ++s, at += a.chunk)
+                a.stretches[s] = Stretch{e, at, min(end, at + a.chunk)};
+        }
+    }
+    for (int s = l.start[L] + tid; s < a.max_stretches; s += kGroupThreads)
+        a.stretches[s] = Stretch{-1, 0, 0};
+}
+
+// [adapter][rows][cols] (rows of ld) to [adapter][cols][rows], so that the
+// gradients' products read the adapters as the forward kernels do.
+struct FlipArgs {
+    const uint16_t *src[2];
+    uint16_t *dst[2];
+    int64_t stride[2];
+    int ld[2], rows[2], cols[2];
+    int tiles[2];               // 64 x 64 tiles of one adapter's matrix
+};
+
+__global__ __launch_bounds__(256) void lora_flip(FlipArgs p)
+{
+    __shared__ uint16_t t[64][65];
+    const int w = (int)blockIdx.x >= p.tiles[0];
+    const int tile = blockIdx.x - (w ? p.tiles[0] : 0);
+    const int tc = (p.cols[w] + 63) / 64;
+    const int r0 = tile / tc * 64, c0 = tile % tc * 64;
+    const uint16_t *src = p.src[w] + blockIdx.y * p.stride[w];
+    uint16_t *dst = p.dst[w] + (int64_t)blockIdx.y * p.rows[w] * p.cols[w];
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    for (int r = y; r < 64; r += 4)
+        if (r0 + r < p.rows[w] && c0 + x < p.cols[w])
+            t[r][x] = src[(int64_t)(r0 + r) * p.ld[w] + c0 + x];
+    __syncthreads();
+    for (int c = y; c < 64; c += 4)
+        if (c0 + c < p.cols[w] && r0 + x < p.rows[w])
+            dst[(int64_t)(c0 + c) * p.rows[w] + r0 + x] = t[x][c];
+}
+
+// part[stretch][r][c] = sum over the stretch's rows m of s_a v[m][r] z[m][c]:
+// the contraction runs over rows, so z's tile (64 rows of 128 columns, gathered
+// by the rows' order) is staged in LDS as it lies and read back transposed
+// (ds_read_b64_tr_b16), and v's is split into two 16-bit values on its way to LDS.
+// Bytes bound it: z is read once, in whole 256-byte row pieces, the next tile's
+// loads in flight while a tile is multiplied.  Sorted into stretches of one
+// adapter, partial sums need no atomics.
+template <int IN, int RT>
+__global__ __launch_bounds__(256) void lora_grad(GradArgs p)
+{
+    constexpr int ROWS = 64, COLS = 128, VP = ROWS + 8;   // (+ 8: 16-byte aligned rows, banks apart)
+    __shared__ __attribute__((aligned(16))) uint8_t zs[ROWS * COLS * 2];
+    __shared__ __attribute__((aligned(16))) uint16_t vs[2][16 * RT][VP];
+    const int w = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c0 = blockIdx.x * COLS;
+    if (c0 >= p.cols[w])
+        return;
+    const Stretch st = p.stretches[blockIdx.y];
+    if (st.adapter < 0)
+        return;
+    const float sc = p.scale[st.adapter];
+    const int64_t v_split = (int64_t)p.M * p.rank_pad;
+
+    for (int rg = 0; rg < p.rank_pad; rg += 16 * RT) {
+        f32x4 acc[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            acc[r][0] = acc[r][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        // this thread's four pieces of a z tile: row tid / 16 + 16 i, chunk tid % 16
+        u32x4 zr[4];
+        auto load = [&](int at) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int place = at + (tid >> 4) + 16 * i;
+                const int col = c0 + 8 * (tid & 15);
+                zr[i] = (u32x4){0u, 0u, 0u, 0u};
+                if (place < st.end && col < p.cols[w])     // cols is a multiple of 8
+                    zr[i] = *reinterpret_cast<const u32x4 *>(p.z[w] + (int64_t)p.order[place] * p.ldz[w] + col);
+            }
+        };
+        load(st.first);
+        for (int at = st.first; at < st.end; at += ROWS) {
+            __syncthreads();                // the last tile has been read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 4) + 16 * i, c = tid & 15;
+                // 32-byte pieces of a row permuted by the row, so that the 16
+                // rows of a transposing read fall into different banks
+                const int key = (row & 3) | ((row >> 3) & 1) << 2;
+                *reinterpret_cast<u32x4 *>(zs + row * 256 + ((((c >> 1) ^ key) << 1) | (c & 1)) * 16) = zr[i];
+            }
+            for (int t = tid; t < ROWS * 16 * RT; t += 256) {
+                const int row = t / (16 * RT), r = t % (16 * RT);
+                float v = 0.0f;
+                if (at + row < st.end && rg + r < p.rank_pad) {
+                    const float *src = p.v[w] + (int64_t)p.order[at + row] * p.rank_pad + rg + r;
+                    for (int s = 0; s < p.v_splits[w]; ++s)
+                        v += src[s * v_split];
+                    v *= sc;
+                }
+                split16<IN>(v, vs[0][r][row], vs[1][r][row]);
+            }
+            __syncthreads();
+            if (at + ROWS < st.end)
+                load(at + ROWS);
+            typedef short v4s __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) v4s lds_v4s;
+#pragma unroll
+            for (int ks = 0; ks < ROWS / 32; ++ks) {
+                // columns 32 wave + 16 j + lane % 16, rows 32 ks + 8 (lane / 16) .. +8
+                u32x4 zf[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v4s got[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int row = 32 * ks + 8 * (lane >> 4) + 4 * half + ((lane & 15) >> 2);
+                        const int key = (row & 3) | ((row >> 3) & 1) << 2;
+                        const int piece = 2 * wave + j;
+                        const uint8_t *a = zs + row * 256 + (piece ^ key) * 32 + (lane & 3) * 8;
+                        got[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)a);
+                    }
+                    const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
+                    zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+                }
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const u32x4 vf = *reinterpret_cast<const u32x4 *>(
+                            &vs[h][16 * r + (lane & 15)][32 * ks + 8 * (lane >> 4)]);
+                        acc[r][0] = mfma16x16x32<IN>(vf, zf[0], acc[r][0]);
+                        acc[r][1] = mfma16x16x32<IN>(vf, zf[1], acc[r][1]);
+                    }
+            }
+        }
+        mfma_settle();
+        float *out = p.part[w] + (int64_t)blockIdx.y * p.rank_pad * p.cols[w];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int rank = rg + 16 * r + 4 * (lane >> 4) + e;
+                    const int col = c0 + 32 * wave + 16 * j + (lane & 15);
+                    if (rank < p.rank && col < p.cols[w])
+                        out[(int64_t)rank * p.cols[w] + col] = acc[r][j][e];
+                }
+    }
+}
+
+// The stretches' sums, in order: dA as it lies, dB transposed.
+__global__ __launch_bounds__(256) void lora_grad_sum(GradArgs p)
+{
+    const int w = blockIdx.z, a = blockIdx.y;
+    const int col = blockIdx.x * 64 + (threadIdx.x & 63);
+    if (blockIdx.x * 64 >= (unsigned)p.cols[w])
+        return;
+    const int s0 = p.first_stretch[a], s1 = p.first_stretch[a + 1];
+    __shared__ float t[64][65];
+    for (int rb = 0; rb < p.rank; rb += 64) {
+        __syncthreads();
+        for (int r = threadIdx.x >> 6; r < 64 && rb + r < p.rank; r += 4) {
+            float v = 0.0f;
+            if (col < p.cols[w])
+                for (int s = s0; s < s1; ++s)
+                    v += p.part[w][((int64_t)s * p.rank_pad + rb + r) * p.cols[w] + col];
+            if (w == 0) {
+                if (col < p.cols[w]) {
+                    const int64_t at = ((int64_t)a * p.rank + rb + r) * p.cols[w] + col;
+                    if (p.out_dtype == GEMM_FP32)
+                        static_cast<float *>(p.out[w])[at] = v;
+                    else
+                        static_cast<uint16_t *>(p.out[w])[at] =
+                            p.out_dtype == GEMM_BF16 ? to16<IN_BF16>(v) : to16<IN_FP16>(v);
+                }
+            } else {
+                t[threadIdx.x & 63][r] = v;
+            }
+        }
+        if (w == 0)
+            continue;
+        __syncthreads();
+        const int r = threadIdx.x & 63;
+        for (int c = threadIdx.x >> 6; c < 64; c += 4) {
+            const int n = blockIdx.x * 64 + c;
+            if (n < p.cols[w] && rb + r < p.rank) {
+                const int64_t at = ((int64_t)a * p.cols[w] + n) * p.rank + rb + r;
+                const float v = t[c][r];
+                if (p.out_dtype == GEMM_FP32)
+                    static_cast<float *>(p.out[w])[at] = v;
+                else
+                    static_cast<uint16_t *>(p.out[w])[at] =
+                        p.out_dtype == GEMM_BF16 ? to16<IN_BF16>(v) : to16<IN_FP16>(v);
+            }
+        }
+    }
+}
+
+// ---- host ----
+
+constexpr int64_t kPartialBytes = (int64_t)64 << 20;   // bound on a plan's K-split partials
+
+// How a low-rank product is spread over the machine.
+struct ShrinkPlan {
+    int rm, rt, lanes_j, splits, k_per_split, tiles;
+};
+
+ShrinkPlan plan_shrink(int64_t M, int64_t K, int64_t adapters, int64_t rank)
+{
+    ShrinkPlan s{};
+    const int64_t pad = cdiv(rank, 16);
+    s.rt = pad >= 4 ? 4 : pad >= 2 ? 2 : 1;
+    // 32 rows a block where that leaves a block for every compute unit
+    s.rm = cdiv(M, 32) >= kNumCUs ? 2 : 1;
+    s.tiles = (int)std::max<int64_t>(1, cdiv(M, 16 * s.rm));
+    // a row tile's adapters on blocks of their own while there are few row tiles
+    s.lanes_j = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(adapters, std::min<int64_t>(M, 16)),
+                                                            2 * kNumCUs / s.tiles));
+    const int64_t blocks = (int64_t)s.tiles * s.lanes_j;
+    const int64_t steps = cdiv(K, 128);
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kNumCUs / blocks, cdiv(steps, kShrinkWaves)));
+    splits = std::min<int64_t>(splits, kMaxLowSplits);
+    s.k_per_split = (int)std::max<int64_t>(128, cdiv(steps, splits) * 128);
+    s.splits = (int)std::max<int64_t>(1, cdiv(K, s.k_per_split));
+    return s;
+}
+
+template <typename F>
+void shrink_variant(const ShrinkPlan &s, F launch)
+{
+    auto by_rt = [&](auto rm) {
+        if (s.rt == 1)
+            launch(rm, std::integral_constant<int, 1>{});
+        else if (s.rt == 2)
+            launch(rm, std::integral_constant<int, 2>{});
+        else
+            launch(rm, std::integral_constant<int, 4>{});
+    };
+    if (s.rm == 2)
+        by_rt(std::integral_constant<int, 2>{});
+    else
+        by_rt(std::integral_constant<int, 1>{});
+}
+
+hipError_t run_shrink(const ShrinkPlan &s, ShrinkArgs p, int in_dtype, hipStream_t stream)
+{
+    p.k_per_split = s.k_per_split;
+    p.lanes_j = s.lanes_j;
+    const dim3 grid(s.tiles, s.lanes_j, s.splits), block(kShrinkWaves * 64);
+    shrink_variant(s, [&](auto rm, auto rt) {
+        if (in_dtype == GEMM_BF16)
+            hipLaunchKernelGGL((lora_shrink<IN_BF16, rm.value, rt.value>), grid, block, 0, stream, p);
+        else
+            hipLaunchKernelGGL((lora_shrink<IN_FP16, rm.value, rt.value>), grid, block, 0, stream, p);
+    });
+    return hipGetLastError();
+}
+
+// The projection's plan: the library's own, without stream-K (whose partials
+// leave in segments that are not whole tiles).
+Plan plan_projection(int64_t M, int64_t N, int64_t K)
+{
+    return make_plan(M, N, K, kPartialBytes, -1, -1, 0);
+}
+Plan plan_mn_major(int64_t M, int64_t N, int64_t K)
+{
+    return make_plan(M, N, K, kPartialBytes, CFG_PP2_256x256, -1, 0);
+}
+
+lora_fn projection_fn(const Plan &p, int64_t M, int in_dtype, int out_dtype)
+{
+    const bool rot = rotate_slabs(1, M);
+    switch (p.cfg) {
+    case CFG_T128x128: return (rot ? kLora_128_s4_rot : kLora_128_s4)[in_dtype][out_dtype];
+    case CFG_T128x128_S2: return kLora_128_s2[in_dtype][out_dtype];
+    case CFG_T32x128: return kLora_32_rot[in_dtype][out_dtype];
+    case CFG_W4_256x128: return kLora_w4[in_dtype][out_dtype];
+    default: return kLora_pp2[in_dtype][out_dtype];
+    }
+}
+
+struct ProjectionWs {
+    float *partials;
+    unsigned *counters;
+    int num_counters;
+};
+
+ProjectionWs carve_projection(Carver &c, const Plan &p)
+{
+    ProjectionWs w;
+    w.num_counters = p.inreduce ? p.tiles_m * p.tiles_n : 0;
+    w.partials = c.take<float>(p.splits > 1 ? p.ws_bytes / 4 : 0);
+    w.counters = c.take<unsigned>(w.num_counters);
+    return w;
+}
+
+// The arguments of the projection's tile from its plan (operands set by the caller).
+void fill_projection(LoraArgs &a, const Plan &p, const ProjectionWs &w, void *C, int64_t M, int64_t N, int64_t K,
+                     int64_t ldc, int out_dtype, const gemm_epilogue_t *epi)
+{
+    a.C = C;
+    a.M = (int)M, a.N = (int)N, a.K = (int)K;
+    a.ldc = (int)ldc;
+    a.tiles_m = p.tiles_m, a.tiles_n = p.tiles_n;
+    a.k_tiles = p.k_tiles;
+    a.splits = p.splits;
+    a.kt_per_split = p.kt_per_split;
+    a.group_m = p.group_m;
+    const int64_t size = size_of(out_dtype);
+    a.vec_store = ldc % 4 == 0 && (uintptr_t)C % (4 * size) == 0;
+    a.rows16 = (ldc * size) % 16 == 0 && (uintptr_t)C % 16 == 0;
+    a.nt_b = p.tiles_m <= 2;
+    a.partials = w.partials;
+    a.counters = w.counters;
+    a.inreduce = p.inreduce;
+    a.alpha = 1.0f;
+    if (epi) {
+        a.alpha = epi->alpha;
+        a.beta = epi->beta;
+        a.bias = epi->bias_along != GEMM_BIAS_NONE ? epi->bias : nullptr;
+        a.bias_along = epi->bias_along;
+        a.act = epi->activation;
+        a.bias_vec = (uintptr_t)a.bias % 16 == 0;
+        a.epi = !(a.alpha == 1.0f && a.beta == 0.0f && a.bias_along == GEMM_BIAS_NONE && a.act == GEMM_ACT_NONE);
+    }
+}
+
+hipError_t run_projection(lora_fn fn, const Plan &p, const LoraArgs &a, int out_dtype, hipStream_t stream)
+{
+    hipError_t e = fn(a, (unsigned)p.grid, stream);
+    if (e != hipSuccess || p.splits <= 1 || p.inreduce)
+        return e;
+    const KernelArgs &k = a;
+    const unsigned grid = (unsigned)cdiv((int64_t)a.M * ((a.N + 3) / 4), 256);
+    if (out_dtype == GEMM_BF16)
+        hipLaunchKernelGGL(splitk_sum<OUT_BF16>, dim3(grid), dim3(256), 0, stream, k);
+    else if (out_dtype == GEMM_FP16)
+        hipLaunchKernelGGL(splitk_sum<OUT_FP16>, dim3(grid), dim3(256), 0, stream, k);
+    else
+        hipLaunchKernelGGL(splitk_sum<OUT_FP32>, dim3(grid), dim3(256), 0, stream, k);
+    return hipGetLastError();
+}
+
+// `count` zeros of `size` bytes (rank is a multiple of 8, so a count of them fills
+// whole words)
+hipError_t zero_fill(void *p, int64_t count, int64_t size, hipStream_t stream)
+{
+    const int64_t words = count * size / 4;
+    if (words == 0)
+        return hipSuccess;
+    hipLaunchKernelGGL(clear_words, dim3((unsigned)std::min<int64_t>(cdiv(words, 256), 4096)), dim3(256), 0, stream,
+                       static_cast<uint32_t *>(p), words);
+    return hipGetLastError();
+}
+
+gemm_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank)
+{
+    if (M < 0 || N < 0 || K < 0 || adapters < 0 || rank < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (M >= kMaxSize || N >= kMaxSize || K >= kMaxSize || adapters >= kMaxSize || rank > 128 || rank % 8 || K % 8)
+        return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+gemm_status_t check_adapters(const gemm_adapters_t *ad, int64_t N, int64_t K)
+{
+    if (ad->num_adapters == 0 || ad->rank == 0)
+        return GEMM_OK;
+    if (!ad->scale || !ad->ids || ad->a_stride < 0 || ad->b_stride < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if ((uintptr_t)ad->scale % 4 || (uintptr_t)ad->ids % 4)
+        return GEMM_ERR_MISALIGNED;
+    gemm_status_t st;
+    if ((st = check_operand(ad->A, K, ad->a_ld)) != GEMM_OK ||
+        (st = check_operand(ad->B, ad->rank, ad->b_ld)) != GEMM_OK)
+        return st;
+    if (ad->a_stride % 8 || ad->b_stride % 8)
+        return GEMM_ERR_MISALIGNED;
+    const int64_t most = (int64_t)1 << 30;
+    return ad->rank * ad->a_ld >= most || N * ad->b_ld >= most ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+}
+
+bool has_adapters(int64_t adapters, int64_t rank) { return adapters > 0 && rank > 0; }
+
+struct ForwardWs {
+    float *low;
+    ProjectionWs proj;
+};
+
+ForwardWs carve_forward(Carver &c, const Plan &p, const ShrinkPlan &s, int64_t M, int64_t adapters, int64_t rank)
+{
+    ForwardWs w;
+    w.low = c.take<float>(has_adapters(adapters, rank) ? (int64_t)s.splits * M * cdiv(rank, 16) * 16 : 0);
+    w.proj = carve_projection(c, p);
+    return w;
+}
+
+void set_adapters(LoraArgs &a, const gemm_adapters_t *ad, const float *low, int low_splits, const uint16_t *up,
+                  int64_t up_stride, int64_t up_ld)
+{
+    a.low = low;
+    a.low_splits = low_splits;
+    a.up = up;
+    a.up_stride = up_stride;
+    a.up_ld = (int)up_ld;
+    a.scale = ad->scale;
+    a.ids = ad->ids;
+    a.adapters = (int)ad->num_adapters;
+    a.rank = (int)ad->rank;
+    a.rank_pad = (int)cdiv(ad->rank, 16) * 16;
+}
+
+ShrinkArgs shrink_args(const gemm_adapters_t *ad, const void *x, int64_t M, int64_t K, int64_t ldx,
+                       const void *down, int64_t down_stride, int64_t down_ld, float *low)
+{
+    ShrinkArgs p{};
+    p.x = static_cast<const uint16_t *>(x);
+    p.down = static_cast<const uint16_t *>(down);
+    p.ids = ad->ids;
+    p.low = low;
+    p.down_stride = down_stride;
+    p.M = (int)M, p.K = (int)K, p.ldx = (int)ldx;
+    p.down_ld = (int)down_ld;
+    p.adapters = (int)ad->num_adapters;
+    p.rank = (int)ad->rank;
+    p.rank_pad = (int)cdiv(ad->rank, 16) * 16;
+    return p;
+}
+
+// Everything a backward call keeps in its workspace.
+struct BackwardWs {
+    ShrinkPlan t, u;
+    Plan dx;
+    float *low_t, *low_u;
+    uint16_t *flip_a, *flip_b;
+    GradArgs g;
+    ProjectionWs proj;
+};
+
+BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank)
+{
+    BackwardWs w{};
+    const int64_t pad = cdiv(rank, 16) * 16;
+    w.t = plan_shrink(M, K, adapters, rank);
+    w.u = plan_shrink(M, N, adapters, rank);
+    if (M > 0 && K > 0)
+        w.dx = plan_mn_major(M, K, N);
+    w.proj = carve_projection(c, w.dx);
+    if (!has_adapters(adapters, rank) || M == 0 || N == 0 || K == 0)
+        return w;      // nothing but a product, or less
+    w.low_t = c.take<float>(w.t.splits * M * pad);
+    w.low_u = c.take<float>(w.u.splits * M * pad);
+    w.flip_a = c.take<uint16_t>(adapters * rank * K);
+    w.flip_b = c.take<uint16_t>(adapters * rank * N);
+    GradArgs &g = w.g;
+    g.M = (int)M, g.N = (int)N, g.K = (int)K;
+    g.adapters = (int)adapters, g.rank = (int)rank, g.rank_pad = (int)pad;
+    g.per_block = std::max<int64_t>(cdiv(cdiv(M, 64), 512) * 512, 512);
+    g.blocks = (int)cdiv(M, g.per_block);
+    g.hist = c.take<int>((int64_t)g.blocks * (adapters + 1));
+    g.counts = c.take<int32_t>(adapters);
+    g.offsets = c.take<int32_t>(adapters + 1);
+    g.order = c.take<int32_t>(M);
+    // stretches so long that column tiles x stretches give about four blocks a
+    // compute unit, and no longer: each stretch writes a partial sum
+    const int64_t tiles = cdiv(K, 128) + cdiv(N, 128);
+    const int64_t want = std::max<int64_t>(1, 4 * kNumCUs / tiles);
+    g.chunk = (int)std::max<int64_t>(64, cdiv(cdiv(M, want), 64) * 64);
+    g.max_stretches = (int)(M / g.chunk + std::min<int64_t>(adapters, M));
+    g.stretches = c.take<Stretch>(g.max_stretches);
+    g.first_stretch = c.take<int>(adapters + 1);
+    g.cols[0] = (int)K, g.cols[1] = (int)N;
+    for (int i = 0; i < 2; ++i)
+        g.part[i] = c.take<float>((int64_t)g.max_stretches * pad * g.cols[i]);
+    return w;
+}
+
+}  // namespace
+}  // namespace gnt
+
+using namespace gnt;
+
+extern "C" {
+
+gemm_status_t gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t num_adapters,
+                                  int64_t rank, int64_t *bytes)
+{
+    if (!bytes)
+        return GEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    const gemm_status_t st = check_sizes(M, N, K, num_adapters, rank);
+    if (st != GEMM_OK || M == 0 || N == 0)
+        return st;
+    Carver c{nullptr};
+    carve_forward(c, plan_projection(M, N, K), plan_shrink(M, K, num_adapters, rank), M, num_adapters, rank);
+    *bytes = c.used;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, int64_t N, int64_t K,
+                            int64_t ldx, int64_t ldw, int64_t ldy, int in_dtype, int out_dtype,
+                            const gemm_adapters_t *adapters, const gemm_epilogue_t *epi,
+                            void *workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    if (!adapters)
+        return GEMM_ERR_INVALID_ARG;
+    if (!is_16bit(in_dtype) || !is_out(out_dtype))
+        return GEMM_ERR_UNSUPPORTED;
+    gemm_status_t st = check_sizes(M, N, K, adapters->num_adapters, adapters->rank);
+    if (st != GEMM_OK || (st = check_epilogue(epi)) != GEMM_OK)
+        return st;
+    if (M == 0 || N == 0)
+        return GEMM_OK;
+    if ((st = check_output(Y, N, ldy, out_dtype)) != GEMM_OK)
+        return st;
+    if (K > 0 && ((st = check_operand(X, K, ldx)) != GEMM_OK || (st = check_operand(W, K, ldw)) != GEMM_OK ||
+                  (st = check_adapters(adapters, N, K)) != GEMM_OK))
+        return st;
+    const Plan p = plan_projection(M, N, K);
+    const ShrinkPlan s = plan_shrink(M, K, adapters->num_adapters, adapters->rank);
+    if (p.grid <= 0 || p.grid >= kMaxSize)
+        return GEMM_ERR_UNSUPPORTED;
+    Carver c{static_cast<uint8_t *>(workspace)};
+    const ForwardWs w = carve_forward(c, p, s, M, adapters->num_adapters, adapters->rank);
+    if ((st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
+        return st;
+    LoraArgs a{};
+    a.A = static_cast<const uint16_t *>(X);
+    a.B = static_cast<const uint16_t *>(W);
+    a.lda = (int)ldx;
+    a.ldb = (int)ldw;
+    fill_projection(a, p, w.proj, Y, M, N, K, ldy, out_dtype, epi);
+    hipError_t e;
+    if (K > 0 && has_adapters(adapters->num_adapters, adapters->rank)) {
+        set_adapters(a, adapters, w.low, s.splits, static_cast<const uint16_t *>(adapters->B), adapters->b_stride,
+                     adapters->b_ld);
+        ShrinkArgs q = shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld, w.low);
+        q.counters = w.proj.counters;
+        q.num_counters = w.proj.num_counters;
+        e = run_shrink(s, q, in_dtype, stream);
+    } else {
+        e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
+    }
+    if (e == hipSuccess)
+        e = run_projection(projection_fn(p, M, in_dtype, out_dtype), p, a, out_dtype, stream);
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+static gemm_status_t check_backward(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t rank)
+{
+    const gemm_status_t st = check_sizes(M, N, K, adapters, rank);
+    if (st != GEMM_OK)
+        return st;
+    return N % 8 || adapters > kMaxGroups ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
+}
+
+gemm_status_t gemm_lora_backward_workspace(int64_t M, int64_t N, int64_t K, int64_t num_adapters,
+                                           int64_t rank, int64_t *bytes)
+{
+    if (!bytes)
+        return GEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    const gemm_status_t st = check_backward(M, N, K, num_adapters, rank);
+    if (st != GEMM_OK || M == 0 || K == 0)
+        return st;
+    Carver c{nullptr};
+    carve_backward(c, M, N, K, num_adapters, rank);
+    *bytes = c.used;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *W, void *dX,
+                                     void *dA, void *dB, int64_t M, int64_t N, int64_t K,
+                                     int64_t lddy, int64_t ldx, int64_t ldw, int64_t lddx,
+                                     int in_dtype, int dx_dtype, int grad_dtype,
+                                     const gemm_adapters_t *adapters, void *workspace,
+                                     int64_t workspace_bytes, hipStream_t stream)
+{
+    if (!adapters)
+        return GEMM_ERR_INVALID_ARG;
+    if (!is_16bit(in_dtype) || !is_out(dx_dtype) || !is_out(grad_dtype))
+        return GEMM_ERR_UNSUPPORTED;
+    const int64_t L = adapters->num_adapters, R = adapters->rank;
+    gemm_status_t st = check_backward(M, N, K, L, R);
+    if (st != GEMM_OK)
+        return st;
+    // both or neither (an array without elements may be null)
+    const bool grads = dA || dB;
+    if (grads && ((!dA && L * R * K > 0) || (!dB && L * R * N > 0)))
+        return GEMM_ERR_INVALID_ARG;
+    const bool some = M > 0 && N > 0 && K > 0;
+    if (some && ((st = check_operand(dY, N, lddy)) != GEMM_OK || (st = check_operand(X, K, ldx)) != GEMM_OK ||
+                 (st = check_operand(W, K, ldw)) != GEMM_OK || (st = check_adapters(adapters, N, K)) != GEMM_OK))
+        return st;
+    const bool want_dx = dX && M > 0 && K > 0;
+    if (want_dx && (st = check_output(dX, K, lddx, dx_dtype)) != GEMM_OK)
+        return st;
+    // (zero_fill writes words)
+    if ((uintptr_t)dA % 4 || (uintptr_t)dB % 4)
+        return GEMM_ERR_MISALIGNED;
+    Carver c{static_cast<uint8_t *>(workspace)};
+    BackwardWs w = carve_backward(c, M, N, K, L, R);
+    if ((want_dx || (some && grads)) && (st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
+        return st;
+    if (want_dx && (w.dx.grid <= 0 || w.dx.grid >= kMaxSize))
+        return GEMM_ERR_UNSUPPORTED;
+
+    hipError_t e = hipSuccess;
+    const bool adapt = some && has_adapters(L, R) && (want_dx || grads);
+    if (!adapt && grads) {
+        e = zero_fill(dA, L * R * K, size_of(grad_dtype), stream);
+        if (e == hipSuccess)
+            e = zero_fill(dB, L * R * N, size_of(grad_dtype), stream);
+    }
+    LoraArgs a{};
+    if (adapt) {
+        // B_a transposed: the low-rank gradients are then products like the forward's
+        FlipArgs f{};
+        f.src[0] = static_cast<const uint16_t *>(adapters->A);
+        f.src[1] = static_cast<const uint16_t *>(adapters->B);
+        f.dst[0] = w.flip_a, f.dst[1] = w.flip_b;
+        f.stride[0] = adapters->a_stride, f.stride[1] = adapters->b_stride;
+        f.ld[0] = (int)adapters->a_ld, f.ld[1] = (int)adapters->b_ld;
+        f.rows[0] = (int)R, f.cols[0] = (int)K;
+        f.rows[1] = (int)N, f.cols[1] = (int)R;
+        for (int i = 0; i < 2; ++i)
+            f.tiles[i] = (int)(cdiv(f.rows[i], 64) * cdiv(f.cols[i], 64));
+        hipLaunchKernelGGL(lora_flip, dim3(f.tiles[0] + f.tiles[1], (unsigned)L), dim3(256), 0, stream, f);
+        e = hipGetLastError();
+        ShrinkArgs u = shrink_args(adapters, dY, M, N, lddy, w.flip_b, R * N, N, w.low_u);
+        u.counters = w.proj.counters;
+        u.num_counters = w.proj.num_counters;
+        if (e == hipSuccess)
+            e = run_shrink(w.u, u, in_dtype, stream);
+        set_adapters(a, adapters, w.low_u, w.u.splits, w.flip_a, R * K, R);
+    } else if (want_dx && e == hipSuccess) {
+        e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
+    }
+    if (want_dx && e == hipSuccess) {
+        a.A = static_cast<const uint16_t *>(dY);
+        a.B = static_cast<const uint16_t *>(W);
+        a.lda = (int)lddy;
+        a.ldb = (int)ldw;
+        fill_projection(a, w.dx, w.proj, dX, M, K, N, lddx, dx_dtype, nullptr);
+        e = run_projection(kLora_pp2_km[in_dtype][dx_dtype], w.dx, a, dx_dtype, stream);
+    }
+    if (adapt && grads && e == hipSuccess) {
+        e = run_shrink(w.t, shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld,
+                                        w.low_t),
+                       in_dtype, stream);
+        GradArgs &g = w.g;
+        g.ids = adapters->ids;
+        g.scale = adapters->scale;
+        g.z[0] = static_cast<const uint16_t *>(X), g.z[1] = static_cast<const uint16_t *>(dY);
+        g.ldz[0] = (int)ldx, g.ldz[1] = (int)lddy;
+        g.v[0] = w.low_u, g.v[1] = w.low_t;
+        g.v_splits[0] = w.u.splits, g.v_splits[1] = w.t.splits;
+        g.out[0] = dA, g.out[1] = dB;
+        g.out_dtype = grad_dtype;
+        if (e == hipSuccess) {
+            hipLaunchKernelGGL(lora_count, dim3(g.blocks), dim3(kGroupThreads), 0, stream, g);
+            hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
+            const unsigned widest = (unsigned)std::max(g.cols[0], g.cols[1]);
+            const dim3 grid((widest + 127) / 128, g.max_stretches, 2);
+            const int pad = g.rank_pad / 16;
+            auto grad = [&](auto in) {
+                if (pad == 1)
+                    hipLaunchKernelGGL((lora_grad<in.value, 1>), grid, dim3(256), 0, stream, g);
+                else if (pad <= 3)
+                    hipLaunchKernelGGL((lora_grad<in.value, 2>), grid, dim3(256), 0, stream, g);
+                else
+                    hipLaunchKernelGGL((lora_grad<in.value, 4>), grid, dim3(256), 0, stream, g);
+            };
+            if (in_dtype == GEMM_BF16)
+                grad(std::integral_constant<int, IN_BF16>{});
+            else
+                grad(std::integral_constant<int, IN_FP16>{});
+            hipLaunchKernelGGL(lora_grad_sum, dim3((widest + 63) / 64, (unsigned)L, 2), dim3(256), 0, stream, g);
+            e = hipGetLastError();
+        }
+    }
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+}  // extern "C"

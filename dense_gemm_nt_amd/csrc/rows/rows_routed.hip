@@ -1,0 +1,144 @@
+// rows_routed.hip -- host side of the experts' products over rows sorted by
+// expert: argument checks, the tile by the rows per expert, one launch.
+#include "rows_host.hpp"
+#include "rows_launch.hpp"
+
+namespace gnt {
+namespace {
+
+gemm_status_t check_sizes(int64_t rows, int64_t N, int64_t K, int64_t E, int in_dtype, int out_dtype)
+{
+    if (rows < 0 || N < 0 || K < 0 || E < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (!is_16bit(in_dtype) || !is_out(out_dtype))
+        return GEMM_ERR_UNSUPPORTED;
+    if (rows >= kMaxSize || N >= kMaxSize || K >= kMaxSize || E > 1024 || K % 8)
+        return GEMM_ERR_UNSUPPORTED;
+    return GEMM_OK;
+}
+
+void fill_output(RoutedArgs &a, void *C, int64_t ldc, int out_dtype)
+{
+    const int64_t size = size_of(out_dtype);
+    a.C = C;
+    a.ldc = (int)ldc;
+    a.c_size = (int)size;
+    a.vec_store = ldc % 4 == 0 && (uintptr_t)C % (4 * size) == 0;
+    a.rows16 = (ldc * size) % 16 == 0 && (uintptr_t)C % 16 == 0;
+    a.group_m = 4;
+    a.alpha = 1.0f;
+}
+
+gemm_status_t launch(routed_fn fn, const RoutedArgs &a, int64_t tiles, hipStream_t stream)
+{
+    // whole runs of 256 blocks: the launch order permutes ids within them
+    const int64_t grid = cdiv(tiles, 256) * 256;
+    if (grid >= kMaxSize)
+        return GEMM_ERR_UNSUPPORTED;
+    return fn(a, (unsigned)grid, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+}  // namespace
+}  // namespace gnt
+
+using namespace gnt;
+
+extern "C" {
+
+gemm_status_t gemm_run_routed(const void *X, const void *W, void *C, const int32_t *offsets,
+                              int64_t rows, int64_t N, int64_t K, int64_t num_experts, int64_t ldx,
+                              int64_t ldw, int64_t w_stride, int64_t ldc, int layout_w,
+                              int in_dtype, int out_dtype, int tail, hipStream_t stream)
+{
+    gemm_status_t st = check_sizes(rows, N, K, num_experts, in_dtype, out_dtype);
+    if (st != GEMM_OK)
+        return st;
+    if ((layout_w != GEMM_K_MAJOR && layout_w != GEMM_MN_MAJOR) ||
+        (tail != GEMM_TAIL_KEEP && tail != GEMM_TAIL_ZERO) || w_stride < 0)
+        return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || N == 0)
+        return GEMM_OK;
+    const bool mn = layout_w == GEMM_MN_MAJOR;
+    if (!offsets || (st = check_output(C, N, ldc, out_dtype)) != GEMM_OK)
+        return offsets ? st : GEMM_ERR_INVALID_ARG;
+    if ((uintptr_t)offsets % 4)
+        return GEMM_ERR_MISALIGNED;
+    if (K > 0 && num_experts > 0) {
+        if ((st = check_operand(X, K, ldx)) != GEMM_OK || (st = check_operand(W, mn ? N : K, ldw)) != GEMM_OK)
+            return st;
+        if (w_stride % 8)
+            return GEMM_ERR_MISALIGNED;
+    }
+    RoutedArgs a{};
+    a.A = static_cast<const uint16_t *>(X);
+    a.B = static_cast<const uint16_t *>(W);
+    a.lda = (int)ldx;
+    a.ldb = (int)ldw;
+    a.offsets = offsets;
+    a.experts = (int)num_experts;
+    a.rows = (int)rows;
+    a.tail = tail == GEMM_TAIL_ZERO;
+    a.b_stride = w_stride;
+    a.N = (int)N;
+    a.K = (int)K;
+    fill_output(a, C, ldc, out_dtype);
+    // The tile by the rows an expert has on average, which the host knows.
+    const int64_t each = rows / std::max<int64_t>(1, num_experts);
+    routed_fn fn;
+    int bn = 256;
+    if (mn) {
+        a.tile_m = 256;
+        fn = kRouted_pp2_km[in_dtype][out_dtype];
+    } else if (each > 128) {
+        a.tile_m = 256;
+        fn = kRouted_pp2[in_dtype][out_dtype];
+    } else {
+        a.tile_m = each > 32 ? 128 : 32;
+        bn = 128;
+        fn = (each > 32 ? kRouted_128 : kRouted_32)[in_dtype][out_dtype];
+    }
+    a.tiles_n = (int)cdiv(N, bn);
+    // sum of ceil(rows_e / tile_m) over the experts and the tail
+    const int64_t tall = std::min<int64_t>(num_experts + 1, rows) + rows / a.tile_m;
+    return launch(fn, a, tall * a.tiles_n, stream);
+}
+
+gemm_status_t gemm_run_routed_wgrad(const void *dY, const void *X, void *dW,
+                                    const int32_t *offsets, int64_t rows, int64_t N, int64_t K,
+                                    int64_t num_experts, int64_t lddy, int64_t ldx, int in_dtype,
+                                    int out_dtype, hipStream_t stream)
+{
+    gemm_status_t st = check_sizes(rows, N, K, num_experts, in_dtype, out_dtype);
+    if (st != GEMM_OK)
+        return st;
+    if (N % 8)
+        return GEMM_ERR_UNSUPPORTED;
+    if (N == 0 || K == 0 || num_experts == 0)
+        return GEMM_OK;
+    if (!offsets || (st = check_output(dW, K, K, out_dtype)) != GEMM_OK)
+        return offsets ? st : GEMM_ERR_INVALID_ARG;
+    if ((uintptr_t)offsets % 4)
+        return GEMM_ERR_MISALIGNED;
+    if (rows > 0 &&
+        ((st = check_operand(dY, N, lddy)) != GEMM_OK || (st = check_operand(X, K, ldx)) != GEMM_OK))
+        return st;
+    RoutedArgs a{};
+    a.A = static_cast<const uint16_t *>(dY);
+    a.B = static_cast<const uint16_t *>(X);
+    a.lda = (int)lddy;
+    a.ldb = (int)ldx;
+    a.offsets = offsets;
+    a.experts = (int)num_experts;
+    a.rows = (int)rows;
+    a.wgrad = 1;
+    a.tile_m = 256;
+    a.c_stride = N * K;
+    a.M = (int)N;
+    a.N = (int)K;
+    fill_output(a, dW, K, out_dtype);
+    // (each expert's array starts N K elements after the last one's: of 8 values)
+    a.tiles_n = (int)cdiv(K, 256);
+    return launch(kRouted_pp2_mm[in_dtype][out_dtype], a, num_experts * cdiv(N, 256) * a.tiles_n, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,317 @@
+"""Products whose weight depends on the row (include/gemm_rows.h) on CUDA tensors:
+
+- a shared projection with low-rank adapters picked per row: ``gemm_lora``,
+  ``gemm_lora_backward``;
+- the top-k router with its balance loss and per-expert counts: ``route_topk``,
+  ``route_topk_backward``;
+- the experts' products over rows sorted by expert: ``gemm_routed``,
+  ``gemm_routed_wgrad``.
+
+What picks the weight stays on the device: no call reads it on the host.  Every
+call runs on the tensors' device, on its current stream, with workspaces and
+results from torch's allocator, so calls on several streams do not share any
+memory, and a captured call (``torch.cuda.graph``) replays with what its input
+tensors then hold.
+"""
+from __future__ import annotations
+
+import collections
+import ctypes
+
+from . import _lib, _rows
+from .api import _code
+
+Routing = collections.namedtuple("Routing", "ids weights counts offsets order tokens loss "
+                                            "renormalize")
+Routing.__doc__ = """What route_topk gives for T tokens, E experts, k choices (int32 but for
+weights and loss): ids [T, k] (-1: none), weights [T, k] float32, counts [E],
+offsets [E + 1], order [T * k] (the pairs t * k + j by expert, stable; those
+without an expert last), tokens [1] (how many were routed), loss (float32
+scalar), and the call's `renormalize`."""
+
+
+def _on(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+
+
+def _matrix(name, X, rows, cols):
+    """Leading dimension of a [rows, cols] tensor with unit stride along its columns."""
+    if X.dim() != 2 or tuple(X.shape) != (rows, cols):
+        raise ValueError("%s must be [%d, %d], got %s" % (name, rows, cols, tuple(X.shape)))
+    if cols > 1 and rows > 0 and X.stride(1) != 1:
+        raise ValueError("%s needs unit stride along its columns" % name)
+    return X.stride(0) if rows > 1 else max(cols, X.stride(0))
+
+
+def _vector(name, v, n, dtype):
+    if v.dtype != dtype or tuple(v.shape) != (n,) or not v.is_contiguous():
+        raise ValueError("%s must be a contiguous %s vector of %d values" % (name, dtype, n))
+
+
+def _out(name, out, shape, dtype, dev):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(out.shape) != tuple(shape) or out.device != dev:
+        raise ValueError("%s must be %s on %s" % (name, list(shape), dev))
+    return out
+
+
+def _workspace(fn, sizes, dev, what):
+    """The call's device workspace (or None) and its size."""
+    import torch
+    st, n = _rows.workspace_bytes(fn, *sizes)
+    _lib.check(st, what)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    return ws, n
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(dev):
+    import torch
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _adapters(A, B, ids, scale, M, N, K, dtype, dev):
+    """A checked GemmAdapters of A [L, R, K], B [L, N, R], ids [M], scale [L]."""
+    import torch
+    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[2] != K or \
+            tuple(B.shape[1:]) != (N, A.shape[1]):
+        raise ValueError("adapters must be A [L, R, %d] and B [L, %d, R], got %s and %s"
+                         % (K, N, tuple(A.shape), tuple(B.shape)))
+    L, R, _ = A.shape
+    if A.dtype != dtype or B.dtype != dtype:
+        raise TypeError("the adapters must have the operands' dtype %s" % dtype)
+    _on(dev, A=A, B=B, ids=ids, scale=scale)
+    _vector("ids", ids, M, torch.int32)
+    _vector("scale", scale, L, torch.float32)
+    for name, X in (("A", A), ("B", B)):
+        if X.numel() and X.shape[2] > 1 and X.stride(2) != 1:
+            raise ValueError("%s needs unit stride along its last axis" % name)
+
+    def ld(X):
+        return X.stride(1) if X.shape[1] > 1 else max(X.shape[2], X.stride(1))
+
+    def step(X):                       # a single adapter's stride is never used
+        return X.stride(0) if L > 1 else 0
+    return _rows.GemmAdapters(A.data_ptr(), B.data_ptr(), scale.data_ptr(), ids.data_ptr(), L, R,
+                              step(A), ld(A), step(B), ld(B))
+
+
+def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=0.0, bias=None,
+              bias_along="n", activation="none"):
+    """y[m] = act(alpha (x[m] W^T + scale[a] (x[m] A[a]^T) B[a]^T) + beta y_old[m] + bias),
+    a = ids[m], for x [M, K] and W [N, K] (bfloat16 or float16), A [L, R, K] and
+    B [L, N, R] of their dtype, ids int32 [M] (outside 0 .. L - 1: no adapter)
+    and scale float32 [L].  R a multiple of 8 up to 128, K a multiple of 8.  beta != 0
+    needs `out` holding y_old; the epilogue as gemm_nt's."""
+    import torch
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x and W must be 2-D")
+    M, K = x.shape
+    N = W.shape[0]
+    dev = x.device
+    if x.dtype != W.dtype:
+        raise TypeError("x and W must share a dtype")
+    _on(dev, W=W, bias=bias)
+    ldx, ldw = _matrix("x", x, M, K), _matrix("W", W, N, K)
+    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, dev)
+    if beta != 0.0 and out is None:
+        raise ValueError("beta != 0 reads the prior y: pass it as `out`")
+    out = _out("out", out, (M, N), out_dtype or x.dtype, dev)
+    ldy = _matrix("out", out, M, N)
+    epi = None
+    if not (alpha == 1.0 and beta == 0.0 and bias is None and activation == "none"):
+        if bias is not None:
+            _vector("bias", bias, N if bias_along == "n" else M, torch.float32)
+        epi = _lib.epilogue(alpha, beta, bias.data_ptr() if bias is not None else 0,
+                            bias_along if bias is not None else "none", activation)
+    with torch.cuda.device(dev):
+        ws, n = _workspace("gemm_lora_workspace", (M, N, K, ad.num_adapters, ad.rank), dev, "gemm_lora")
+        st = _rows.lib().gemm_run_lora(
+            x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy, _code(x.dtype),
+            _code(out.dtype), ctypes.byref(ad), ctypes.byref(epi) if epi is not None else None,
+            _ptr(ws), n, _stream(dev))
+    _lib.check(st, "gemm_lora(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, ad.num_adapters, ad.rank))
+    return out
+
+
+def gemm_lora_backward(dy, x, W, A, B, ids, scale, grad_dtype=None, dx_dtype=None, need_dx=True,
+                       need_adapters=True):
+    """(dx, dA, dB) of gemm_lora without an epilogue, W frozen, for dy [M, N]: dx [M, K]
+    of dx_dtype (default: x's), dA [L, R, K] and dB [L, N, R] of grad_dtype
+    (default float32; zeros for adapters without a row).  need_dx or
+    need_adapters False: that part is not computed, and None.  N and K
+    multiples of 8, at most 1024 adapters."""
+    import torch
+    if dy.dim() != 2 or x.dim() != 2 or W.dim() != 2:
+        raise ValueError("dy, x and W must be 2-D")
+    M, K = x.shape
+    N = W.shape[0]
+    dev = x.device
+    if x.dtype != W.dtype or dy.dtype != x.dtype:
+        raise TypeError("dy, x and W must share a dtype")
+    _on(dev, dy=dy, W=W)
+    lddy, ldx, ldw = _matrix("dy", dy, M, N), _matrix("x", x, M, K), _matrix("W", W, N, K)
+    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, dev)
+    L, R = ad.num_adapters, ad.rank
+    gdt = grad_dtype or torch.float32
+    dx = torch.empty((M, K), dtype=dx_dtype or x.dtype, device=dev) if need_dx else None
+    dA = torch.empty((L, R, K), dtype=gdt, device=dev) if need_adapters else None
+    dB = torch.empty((L, N, R), dtype=gdt, device=dev) if need_adapters else None
+    with torch.cuda.device(dev):
+        ws, n = _workspace("gemm_lora_backward_workspace", (M, N, K, L, R), dev, "gemm_lora_backward")
+        st = _rows.lib().gemm_run_lora_backward(
+            dy.data_ptr(), x.data_ptr(), W.data_ptr(), _ptr(dx), _ptr(dA) or None, _ptr(dB) or None,
+            M, N, K, lddy, ldx, ldw, K, _code(x.dtype), _code(dx_dtype or x.dtype), _code(gdt),
+            ctypes.byref(ad), _ptr(ws), n, _stream(dev))
+    _lib.check(st, "gemm_lora_backward(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, L, R))
+    return dx, dA, dB
+
+
+def _mask(mask, T):
+    import torch
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,) or \
+            not mask.is_contiguous():
+        raise ValueError("mask must be a contiguous bool or uint8 vector of %d values" % T)
+    return mask
+
+
+def _c_routing(r):
+    return _rows.GemmRouting(*(_ptr(getattr(r, n)) for n, _ in _rows.GemmRouting._fields_))
+
+
+def route_topk(logits, top_k, mask=None, renormalize=True):
+    """The top_k experts of each token of logits [T, E] (bfloat16, float16 or float32):
+    a Routing.  Weights are softmax probabilities, divided by their sum over
+    the choices where `renormalize`; equal logits go to the lower expert; a
+    logit of -inf closes an expert to its token.  Tokens whose mask (bool or
+    uint8 [T]) is 0 are left out.  loss = E sum_e f_e P_e with f_e the share of
+    choices that fell on e and P_e the mean probability of e, over the routed
+    tokens."""
+    import torch
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    k = int(top_k)
+    dev = logits.device
+    ld = _matrix("logits", logits, T, E)
+    mask = _mask(mask, T)
+    _on(dev, mask=mask)
+    i32 = dict(dtype=torch.int32, device=dev)
+    with torch.cuda.device(dev):
+        ws, n = _workspace("gemm_route_workspace", (T, E, k), dev, "route_topk")
+        f32 = dict(dtype=torch.float32, device=dev)
+        r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), **f32), torch.empty(E, **i32),
+                    torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty(1, **i32),
+                    torch.empty((), **f32), bool(renormalize))
+        st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k,
+                                        int(r.renormalize), _code(logits.dtype),
+                                        ctypes.byref(_c_routing(r)), _ptr(ws), n, _stream(dev))
+    _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
+    return r
+
+
+def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=None):
+    """The gradient in the logits of `routing` = route_topk(logits, ...): of its
+    weights (grad_weights float32 [T, k]) and its loss (grad_loss, a float32
+    scalar tensor), either None for zero; counts are constants.  Of the logits'
+    dtype; zeros for tokens that were not routed and closed experts."""
+    import torch
+    if logits.dim() != 2 or routing.ids.dim() != 2 or routing.ids.shape[0] != logits.shape[0] or \
+            routing.counts.shape[0] != logits.shape[1]:
+        raise ValueError("routing does not belong to these logits")
+    T, E = logits.shape
+    k = routing.ids.shape[1]
+    dev = logits.device
+    ld = _matrix("logits", logits, T, E)
+    _on(dev, ids=routing.ids, grad_weights=grad_weights, grad_loss=grad_loss)
+    if grad_weights is not None and (grad_weights.dtype != torch.float32 or
+                                     tuple(grad_weights.shape) != (T, k) or
+                                     not grad_weights.is_contiguous()):
+        raise ValueError("grad_weights must be contiguous float32 [%d, %d]" % (T, k))
+    if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
+        raise ValueError("grad_loss must be one float32 value")
+    out = _out("out", out, (T, E), logits.dtype, dev)
+    if out.dtype != logits.dtype:
+        raise TypeError("out must have the logits' dtype")
+    with torch.cuda.device(dev):
+        st = _rows.lib().gemm_run_route_backward(
+            logits.data_ptr(), ctypes.byref(_c_routing(routing)), _ptr(grad_weights), _ptr(grad_loss),
+            out.data_ptr(), T, E, ld, _matrix("out", out, T, E), k, int(routing.renormalize),
+            _code(logits.dtype), _stream(dev))
+    _lib.check(st, "route_topk_backward(T=%d, E=%d, k=%d)" % (T, E, k))
+    return out
+
+
+def gemm_routed(x, W, offsets, out=None, out_dtype=None):
+    """C[i] = x[i] W[e]^T for offsets[e] <= i < offsets[e + 1]: x [S, K] rows sorted by
+    expert, W [E, N, K], offsets int32 [E + 1] on the device (route_topk's).  W[e]
+    is K-major (unit stride along K) or a transposed view of [E, K, N] (unit
+    stride along N): gemm_routed(dy, W.transpose(1, 2), offsets) is the gradient
+    in x of gemm_routed(x, W, offsets).  Rows behind offsets[E] are zero in a new
+    result, and left as they are in `out`."""
+    import torch
+    if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
+        raise ValueError("x must be [S, K] and W [E, N, K], got %s and %s"
+                         % (tuple(x.shape), tuple(W.shape)))
+    S, K = x.shape
+    E, N, _ = W.shape
+    dev = x.device
+    if x.dtype != W.dtype:
+        raise TypeError("x and W must share a dtype")
+    _on(dev, W=W, offsets=offsets)
+    _vector("offsets", offsets, E + 1, torch.int32)
+    ldx = _matrix("x", x, S, K)
+    if W.numel() == 0:
+        layout, ldw = _lib.GEMM_K_MAJOR, max(K, 1)
+    elif W.stride(2) == 1 and (N == 1 or W.stride(1) >= K):
+        layout, ldw = _lib.GEMM_K_MAJOR, W.stride(1) if N > 1 else max(K, W.stride(1))
+    elif W.stride(1) == 1 and (K == 1 or W.stride(2) >= N):
+        layout, ldw = _lib.GEMM_MN_MAJOR, W.stride(2) if K > 1 else max(N, W.stride(2))
+    else:
+        raise ValueError("W's strides %s are neither K-major nor MN-major" % (tuple(W.stride()),))
+    tail = _rows.GEMM_TAIL_ZERO if out is None else _rows.GEMM_TAIL_KEEP
+    out = _out("out", out, (S, N), out_dtype or x.dtype, dev)
+    with torch.cuda.device(dev):
+        st = _rows.lib().gemm_run_routed(
+            x.data_ptr(), W.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, ldx, ldw,
+            W.stride(0) if E > 1 else 0, _matrix("out", out, S, N), layout, _code(x.dtype),
+            _code(out.dtype), tail, _stream(dev))
+    _lib.check(st, "gemm_routed(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
+    return out
+
+
+def gemm_routed_wgrad(dy, x, offsets, out_dtype=None):
+    """dW [E, N, K]: dW[e] = sum over e's rows i of dy[i]^T x[i], for dy [S, N] and
+    x [S, K] sorted by expert and offsets int32 [E + 1] on the device; zeros for an
+    expert without rows.  N and K multiples of 8; out_dtype defaults to x's."""
+    import torch
+    if x.dim() != 2 or dy.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [S, N] and x [S, K], got %s and %s"
+                         % (tuple(dy.shape), tuple(x.shape)))
+    S, K = x.shape
+    N = dy.shape[1]
+    dev = x.device
+    if x.dtype != dy.dtype:
+        raise TypeError("dy and x must share a dtype")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [E + 1]")
+    E = offsets.shape[0] - 1
+    _on(dev, dy=dy, offsets=offsets)
+    _vector("offsets", offsets, E + 1, torch.int32)
+    lddy, ldx = _matrix("dy", dy, S, N), _matrix("x", x, S, K)
+    out = torch.empty((E, N, K), dtype=out_dtype or x.dtype, device=dev)
+    with torch.cuda.device(dev):
+        st = _rows.lib().gemm_run_routed_wgrad(
+            dy.data_ptr(), x.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, lddy, ldx,
+            _code(x.dtype), _code(out.dtype), _stream(dev))
+    _lib.check(st, "gemm_routed_wgrad(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
+    return out
