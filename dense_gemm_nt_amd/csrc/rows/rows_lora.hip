@@ -191,8 +191,8 @@ __global__ __launch_bounds__(kGroupThreads) void lora_place(GradArgs a)
 {
     __shared__ PlaceLds l;
     if ((int)blockIdx.x < a.blocks) {
-        place_block(l, a.ids, a.M, a.adapters, a.per_block, a.hist, blockIdx.x, a.blocks, a.counts, a.offsets,
-                    a.order);
+        place_block<false>(l, a.ids, a.M, a.adapters, a.per_block, a.hist, nullptr, blockIdx.x, a.blocks, a.counts,
+                           a.offsets, a.order);
         return;
     }
     const int tid = threadIdx.x, L = a.adapters;
@@ -670,7 +670,7 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     GradArgs &g = w.g;
     g.M = (int)M, g.N = (int)N, g.K = (int)K;
     g.adapters = (int)adapters, g.rank = (int)rank, g.rank_pad = (int)pad;
-    g.per_block = std::max<int64_t>(cdiv(cdiv(M, 64), 512) * 512, 512);
+    g.per_block = std::max<int64_t>(cdiv(cdiv(M, 32), kGroupThreads) * kGroupThreads, kGroupThreads);
     g.blocks = (int)cdiv(M, g.per_block);
     g.hist = c.take<int>((int64_t)g.blocks * (adapters + 1));
     g.counts = c.take<int32_t>(adapters);

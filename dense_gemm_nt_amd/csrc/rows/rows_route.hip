@@ -1,11 +1,15 @@
 // rows_route.hip -- the top-k router: softmax, choices, per-expert counts and
 // order, balance loss; and its gradient.
 //
-// A token's logits are spread over LPR lanes of 4 Q columns each (columns
-// 4 LPR q + 4 li + i for lane li), so a row is read once, coalesced, and held
-// in registers: maximum, sum and the k choices come from reductions over the
+// A token's logits are spread over LPR lanes of 4 Q columns each (from column
+// 4 Q li for lane li), so a row is read once and held in registers: maximum, sum and the k choices come from reductions over the
 // LPR lanes.  A choice is one maximum over the lanes and a ballot for its
-// first holder, so ties fall to the lowest column.
+// first holder, so ties fall to the lowest column.  Up to 64 experts several
+// rows share a wave and a choice is worked out in vector registers (route_rows_narrow);
+// with more a wave has one row, each lane its columns sorted, so that a choice
+// compares one value a lane: the maximum is a scalar, its holder a scalar search
+// in one ballot (route_rows_wide), about 17 vector operations a choice, where
+// maxima over all of a lane's columns and ballots for each took about 45.
 #include <type_traits>
 
 #include "rows_group.hpp"
@@ -30,6 +34,8 @@ struct RouteArgs {
     int *hist;                // [blocks][E + 1]
     float *psum;              // [blocks][E]
     int *live;                // [blocks]
+    int *totals;              // [E + 1]
+    float *loss_part;         // [(E + 64) / 64]
     // backward
     const float *grad_w, *grad_loss;
     void *dlogits;
@@ -40,8 +46,8 @@ struct RouteArgs {
 template <int CTRL>
 __device__ __forceinline__ float dpp(float x)
 {
-    const int v = __builtin_bit_cast(int, x);
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+    // (every lane has a source under these patterns; said so, the move folds into its use)
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
 
 // x combined over the LPR lanes of a row, in every one of them.
@@ -168,13 +174,21 @@ __device__ __forceinline__ bool softmax_row(f32x4 (&x)[Q], f32x4 (&key)[Q])
             sum += x[q][i];
         }
     sum = row_sum<LPR>(sum);
-    const float inv = open ? 1.0f / sum : 0.0f;
+    const float inv = open ? __builtin_amdgcn_rcpf(sum) : 0.0f;      // within an ulp
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[q][i] *= inv;
     return open;
+}
+
+// The balance loss of n routed tokens from s = sum_e counts_e psum_e.
+__device__ __forceinline__ void write_loss(const RouteArgs &a, int n, float s)
+{
+    const float nf = (float)n;
+    *a.loss = n > 0 ? (float)a.E * (s / nf) / (nf * (float)a.k) : 0.0f;
+    *a.tokens = n;
 }
 
 // The balance loss from counts (a function of e) and the routed tokens' sums of p.
@@ -192,10 +206,206 @@ __device__ __forceinline__ void balance_loss(const RouteArgs &a, int n, P psum, 
         float s = 0.0f;
         for (int w = 0; w < (int)(blockDim.x >> 6); ++w)
             s += red[w];
-        const float nf = (float)n;
-        *a.loss = n > 0 ? (float)a.E * (s / nf) / (nf * (float)a.k) : 0.0f;
-        *a.tokens = n;
+        write_loss(a, n, s);
     }
+}
+
+// Integers in the order of the floats (-0 is made +0); NaN as the lowest finite
+// value.
+__device__ __forceinline__ int rank_key(float x)
+{
+    const int b = __builtin_bit_cast(int, x != x ? -3.402823466e38f : x + 0.0f);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+constexpr int kClosedKey = (int)0x807fffffu;     // rank_key(-inf); a taken column is below it
+
+__device__ __forceinline__ float rank_value(int k)
+{
+    return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7fffffff));
+}
+
+// The largest of a wave's values, as a scalar.
+__device__ __forceinline__ int wave_max(int x)
+{
+    x = max(x, __builtin_amdgcn_mov_dpp(x, 0xB1, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_mov_dpp(x, 0x4E, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true));
+    x = max(x, __builtin_amdgcn_mov_dpp(x, 0x140, 0xf, 0xf, true));
+    int a = max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16));
+    int b = max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48));
+    asm("" : "+s"(a), "+s"(b));        // (kept apart, or they become a vector maximum of three)
+    return max(a, b);
+}
+
+// One wave's walk over its rows, one at a time.  `sum` collects p, hist (in LDS)
+// the choices; returns how many of the wave's rows were routed.
+template <int DT, int Q, int NW>
+__device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, int64_t t1, int wave, int lane,
+                                               f32x4 (&sum)[Q], int *hist)
+{
+    constexpr int V = 4 * Q, BITS = Q == 1 ? 2 : Q == 2 ? 3 : 4;
+    typedef std::conditional_t<Q == 4, uint64_t, uint32_t> order_t;
+    const int64_t mine = t0 + wave;
+    // (the mask is not waited for: a masked row is loaded like any other)
+    f32x4 next[Q];
+    uint8_t next_on = 1;
+    auto load = [&](int64_t t) {
+        if (t >= t1)
+            return;
+        if (a.mask)
+            next_on = a.mask[t];
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            next[q] = load_logits<DT>(a.logits, t * a.ld, lane * V + 4 * q, a.E, a.vec);
+    };
+    int routed = 0;
+    load(mine);
+    for (int64_t t = mine; t < t1; t += NW) {
+        f32x4 x[Q];
+        int key[V], at[V];
+        const bool on = __builtin_amdgcn_readfirstlane(next_on) != 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float value = next[v / 4][v % 4];
+            x[v / 4][v % 4] = value;
+            key[v] = rank_key(value);
+            at[v] = v;
+        }
+        load(t + NW);                   // the next row's loads run under this row
+        int found = 0, my_e = -1, my_key = 0;
+        float inv = 0.0f, top = 0.0f;
+        int best = key[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v)
+            best = max(best, key[v]);
+        best = on ? wave_max(best) : kClosedKey;
+        if (best > kClosedKey) {
+            ++routed;
+            top = rank_value(best);
+            float total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[v / 4][v % 4] = __expf(x[v / 4][v % 4] - top);
+                total += x[v / 4][v % 4];
+            }
+            inv = __builtin_amdgcn_rcpf(row_sum<64>(total));
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                sum[q] += x[q] * inv;
+            // the lane's columns by falling key, by odd-even transposition: neighbours
+            // only change places where they must, so equal ones stay in order
+#pragma unroll
+            for (int r = 0; r < V; ++r)
+#pragma unroll
+                for (int v = r & 1; v + 1 < V; v += 2) {
+                    const bool swap = key[v + 1] > key[v];
+                    const int hi = max(key[v], key[v + 1]), lo = min(key[v], key[v + 1]);
+                    const int i = swap ? at[v + 1] : at[v], j = swap ? at[v] : at[v + 1];
+                    key[v] = hi, key[v + 1] = lo, at[v] = i, at[v + 1] = j;
+                }
+            // ... and the columns in that order, BITS bits each
+            order_t order = 0;
+#pragma unroll
+            for (int v = V - 1; v >= 0; --v)
+                order = order << BITS | (order_t)at[v];
+            // (best: the largest value left)
+            for (;;) {
+                // its first holder, and that lane's next column
+                const uint64_t has = __builtin_amdgcn_ballot_w64(key[0] == best);
+                const int l = __builtin_ctzll(has);
+                const int e = l * V + (__builtin_amdgcn_readlane((int)order, l) & (V - 1));
+                my_e = lane == found ? e : my_e;
+                my_key = lane == found ? best : my_key;
+                if (++found == a.k)
+                    break;
+                // (masks, not selections: those of array elements became searches)
+                const int holder = lane == l ? -1 : 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    key[v] = ((v + 1 < V ? key[v + 1] : INT32_MIN) & holder) | (key[v] & ~holder);
+                order >>= holder & BITS;
+                best = wave_max(key[0]);
+                if (best <= kClosedKey)
+                    break;
+            }
+        }
+        // lane j holds choice j: its weight from its logit, as p was made
+        const bool chose = lane < found;
+        float w = chose ? __expf(rank_value(my_key) - top) * inv : 0.0f;
+        if (a.renorm && found)
+            w *= __builtin_amdgcn_rcpf(row_sum<64>(w));
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = my_e;
+            a.weights[t * a.k + lane] = w;
+            atomicAdd(&hist[chose ? my_e : a.E], 1);
+        }
+    }
+    return routed;
+}
+
+// GPW rows at a time, LPR lanes each; counts a row in its first lane.
+template <int DT, int LPR, int NW>
+__device__ __forceinline__ int route_rows_narrow(const RouteArgs &a, int64_t t0, int64_t t1, int wave, int lane,
+                                                 f32x4 (&sum)[1], int *hist)
+{
+    constexpr int GPW = 64 / LPR;
+    const int li = lane % LPR, grp = lane / LPR;
+    int routed = 0;
+    for (int64_t base = t0 + wave * GPW; base < t1; base += NW * GPW) {
+        const int64_t t = base + grp;
+        const bool in = t < t1;
+        const f32x4 closed = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        f32x4 x[1], key[1];
+        x[0] = in ? load_logits<DT>(a.logits, t * a.ld, li * 4, a.E, a.vec) : closed;
+        if (a.mask && in)               // (after the row's own load, which does not wait for it)
+            x[0] = a.mask[t] ? x[0] : closed;
+        const bool open = softmax_row<LPR, 1>(x, key);
+        routed += open && li == 0;
+        sum[0] += x[0];
+        uint8_t place_of[4] = {0xff, 0xff, 0xff, 0xff};
+        float chosen = 0.0f;
+        int found = 0;
+        for (int j = 0; j < a.k; ++j) {
+            float best = fmaxf(fmaxf(key[0][0], key[0][1]), fmaxf(key[0][2], key[0][3]));
+            best = row_max<LPR>(best);
+            const bool more = best > -INFINITY;
+            if (__builtin_amdgcn_ballot_w64(more) == 0)
+                break;
+            found += more;
+            const bool mine = more && (key[0][0] == best || key[0][1] == best || key[0][2] == best ||
+                                       key[0][3] == best);
+            const uint64_t row = (__builtin_amdgcn_ballot_w64(mine) >> (grp * LPR)) & ((1ull << LPR) - 1);
+            if (mine && __builtin_ctzll(row) == li) {
+                bool taken = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!taken && key[0][i] == best) {
+                        taken = true;
+                        key[0][i] = -INFINITY;
+                        place_of[i] = (uint8_t)j;
+                        chosen += x[0][i];
+                    }
+            }
+        }
+        chosen = row_sum<LPR>(chosen);
+        const float scale = a.renorm && found ? 1.0f / chosen : 1.0f;
+        if (in) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (place_of[i] != 0xff) {
+                    const int e = li * 4 + i;
+                    a.ids[t * a.k + place_of[i]] = e;
+                    a.weights[t * a.k + place_of[i]] = x[0][i] * scale;
+                    atomicAdd(&hist[e], 1);
+                }
+            for (int j = found + li; j < a.k; j += LPR) {
+                a.ids[t * a.k + j] = -1;
+                a.weights[t * a.k + j] = 0.0f;
+                atomicAdd(&hist[a.E], 1);
+            }
+        }
+    }
+    return routed;
 }
 
 // One block of tokens: choices, weights, the block's counts and sums of p.
@@ -203,12 +413,13 @@ __device__ __forceinline__ void balance_loss(const RouteArgs &a, int n, P psum, 
 template <int DT, int LPR, int Q, bool ONE>
 __global__ __launch_bounds__(kGroupThreads) void route_forward(RouteArgs a)
 {
-    constexpr int NW = kGroupThreads / 64, GPW = 64 / LPR, COLS = LPR * 4 * Q;
+    constexpr int NW = kGroupThreads / 64, COLS = LPR * 4 * Q;
     __shared__ int hist[kMaxGroups + 1];
     __shared__ float ps[NW][COLS];
     __shared__ int live[NW];
     __shared__ std::conditional_t<ONE, PlaceLds, int> place;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane % LPR, grp = lane / LPR;
     for (int e = tid; e <= a.E; e += kGroupThreads)
         hist[e] = 0;
@@ -220,77 +431,13 @@ __global__ __launch_bounds__(kGroupThreads) void route_forward(RouteArgs a)
 #pragma unroll
     for (int q = 0; q < Q; ++q)
         sum[q] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    int routed = 0;
-    for (int64_t base = t0 + wave * GPW; base < t1; base += NW * GPW) {
-        const int64_t t = base + grp;
-        const bool in = t < t1;
-        const bool on = in && (!a.mask || a.mask[t]);
-        f32x4 x[Q], key[Q];
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            x[q] = on ? load_logits<DT>(a.logits, t * a.ld, q * LPR * 4 + li * 4, a.E, a.vec)
-                      : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const bool open = softmax_row<LPR, Q>(x, key);
-        routed += open && li == 0;
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-            sum[q] += x[q];
-        // the k largest, one at a time: the maximum over the row, its first holder
-        uint8_t place_of[4 * Q];
-#pragma unroll
-        for (int i = 0; i < 4 * Q; ++i)
-            place_of[i] = 0xff;
-        float chosen = 0.0f;
-        int found = 0;
-        for (int j = 0; j < a.k; ++j) {
-            float best = -INFINITY;
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-                best = fmaxf(best, fmaxf(fmaxf(key[q][0], key[q][1]), fmaxf(key[q][2], key[q][3])));
-            best = row_max<LPR>(best);
-            if (__builtin_amdgcn_ballot_w64(best > -INFINITY) == 0)
-                break;
-            bool open_yet = best > -INFINITY;
-            found += open_yet;
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                const bool mine = open_yet && (key[q][0] == best || key[q][1] == best || key[q][2] == best ||
-                                               key[q][3] == best);
-                const uint64_t all = __builtin_amdgcn_ballot_w64(mine);
-                const uint64_t row = LPR == 64 ? all : (all >> (grp * LPR)) & ((1ull << (LPR & 63)) - 1);
-                if (row && mine && __builtin_ctzll(row) == li) {
-                    bool taken = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!taken && key[q][i] == best) {
-                            taken = true;
-                            key[q][i] = -INFINITY;
-                            place_of[4 * q + i] = (uint8_t)j;
-                            chosen += x[q][i];
-                        }
-                }
-                open_yet = open_yet && row == 0;
-            }
-        }
-        chosen = row_sum<LPR>(chosen);
-        const float scale = a.renorm && found ? 1.0f / chosen : 1.0f;
-        if (in) {
-#pragma unroll
-            for (int q = 0; q < Q; ++q)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (place_of[4 * q + i] != 0xff) {
-                        const int e = q * LPR * 4 + li * 4 + i;
-                        a.ids[t * a.k + place_of[4 * q + i]] = e;
-                        a.weights[t * a.k + place_of[4 * q + i]] = x[q][i] * scale;
-                        atomicAdd(&hist[e], 1);
-                    }
-            for (int j = found + li; j < a.k; j += LPR) {
-                a.ids[t * a.k + j] = -1;
-                a.weights[t * a.k + j] = 0.0f;
-                atomicAdd(&hist[a.E], 1);
-            }
-        }
+    int routed;
+    if constexpr (LPR == 64) {
+        routed = route_rows_wide<DT, Q, NW>(a, t0, t1, wave, lane, sum, hist);
+    } else {
+        routed = route_rows_narrow<DT, LPR, NW>(a, t0, t1, wave, lane, sum, hist);
+        for (int o = 32; o; o >>= 1)
+            routed += __shfl_xor(routed, o);
     }
     // the block's sums of p: over the rows of a wave, then over the waves
 #pragma unroll
@@ -301,10 +448,8 @@ __global__ __launch_bounds__(kGroupThreads) void route_forward(RouteArgs a)
             for (int o = LPR; o < 64; o <<= 1)
                 v += __shfl_xor(v, o);
             if (grp == 0)
-                ps[wave][q * LPR * 4 + li * 4 + i] = v;
+                ps[wave][li * 4 * Q + 4 * q + i] = v;
         }
-    for (int o = 32; o; o >>= 1)
-        routed += __shfl_xor(routed, o);
     if (lane == 0)
         live[wave] = routed;
     __syncthreads();
@@ -319,14 +464,13 @@ __global__ __launch_bounds__(kGroupThreads) void route_forward(RouteArgs a)
 #pragma unroll
     for (int w = 0; w < NW; ++w)
         n += live[w];
+    store_hist(hist, a.hist, a.E);
     if constexpr (ONE) {
-        store_hist(hist, a.hist, a.E);
         balance_loss(a, n, psum, [&](int e) { return hist[e]; }, reinterpret_cast<float *>(place.part));
         __syncthreads();
-        place_block(place, a.ids, a.T * a.k, a.E, a.per_block * a.k, a.hist, 0, 1, a.counts, a.offsets,
-                    a.order);
+        place_block<false>(place, a.ids, a.T * a.k, a.E, a.per_block * a.k, a.hist, nullptr, 0, 1, a.counts,
+                           a.offsets, a.order);
     } else {
-        store_hist(hist, a.hist, a.E);
         for (int e = tid; e < a.E; e += kGroupThreads)
             a.psum[(int64_t)blockIdx.x * a.E + e] = psum(e);
         if (tid == 0)
@@ -334,44 +478,76 @@ __global__ __launch_bounds__(kGroupThreads) void route_forward(RouteArgs a)
     }
 }
 
-// The second launch of a larger batch: counts, offsets, order; the loss.
-__global__ __launch_bounds__(kGroupThreads) void route_finish(RouteArgs a)
+// The second launch of a larger batch: 64 experts a block, what each forward
+// block places and the experts' part of the loss sum_e counts_e psum_e, the
+// blocks' sums of p added in order.
+__global__ __launch_bounds__(kGroupThreads) void route_scan(RouteArgs a)
+{
+    __shared__ int part[kGroupWaves][64];
+    __shared__ float sums[kGroupWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int e = blockIdx.x * 64 + lane;
+    const int b0 = (int)((int64_t)wave * a.blocks / kGroupWaves), b1 = (int)((int64_t)(wave + 1) * a.blocks / kGroupWaves);
+    float v = 0.0f;
+    if (e < a.E)
+#pragma unroll 8
+        for (int b = b0; b < b1; ++b)
+            v += a.psum[(int64_t)b * a.E + e];
+    sums[wave][lane] = v;
+    scan_column(a.hist, a.totals, a.E, a.blocks, part);     // (a barrier between)
+    if (wave == 0) {
+        float p = 0.0f;
+        int c = 0;
+        for (int w = 0; w < kGroupWaves; ++w) {
+            p += sums[w][lane];
+            c += part[w][lane];
+        }
+        const float s = row_sum<64>(e < a.E ? (float)c * p : 0.0f);
+        if (lane == 0)
+            a.loss_part[blockIdx.x] = s;
+    }
+}
+
+// The third: counts, offsets, order; the loss (a block more than the entries').
+__global__ __launch_bounds__(kGroupThreads) void route_place(RouteArgs a)
 {
     __shared__ PlaceLds place;
-    if ((int)blockIdx.x == a.blocks) {
-        // one block more than the entries': the loss, from the blocks' sums in order
-        int n = 0;
-        for (int i = 0; i < a.blocks; ++i)
-            n += a.live[i];
-        auto psum = [&](int e) {
-            float v = 0.0f;
-#pragma unroll 8
-            for (int i = 0; i < a.blocks; ++i)
-                v += a.psum[(int64_t)i * a.E + e];
-            return v;
-        };
-        auto count = [&](int e) {
-            int c = 0;
-#pragma unroll 8
-            for (int i = 0; i < a.blocks; ++i)
-                c += a.hist[(int64_t)i * (a.E + 1) + e];
-            return c;
-        };
-        balance_loss(a, n, psum, count, reinterpret_cast<float *>(place.part));
+    if ((int)blockIdx.x < a.blocks) {
+        place_block<true>(place, a.ids, a.T * a.k, a.E, a.per_block * a.k, a.hist, a.totals, blockIdx.x, a.blocks,
+                          a.counts, a.offsets, a.order);
         return;
     }
-    place_block(place, a.ids, a.T * a.k, a.E, a.per_block * a.k, a.hist, blockIdx.x, a.blocks, a.counts,
-                a.offsets, a.order);
+    int n = 0;
+    for (int i = threadIdx.x; i < a.blocks; i += kGroupThreads)
+        n += a.live[i];
+    for (int o = 32; o; o >>= 1)
+        n += __shfl_xor(n, o);
+    if ((threadIdx.x & 63) == 0)
+        place.part[threadIdx.x >> 6] = n;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        n = 0;
+        for (int w = 0; w < kGroupWaves; ++w)
+            n += place.part[w];
+        float s = 0.0f;
+        for (int i = 0; i < (a.E + 64) / 64; ++i)
+            s += a.loss_part[i];
+        write_loss(a, n, s);
+    }
 }
 
 // dlogit = p (dp - sum p dp), dp_e = g_loss E f_e / n + (the gradient of e's
-// weight, if chosen): p is recomputed from the logits, which are read once.
+// weight, if chosen): p is recomputed from the logits, which are read once.  Lane j
+// of a row takes choice j's gradient, and LDS carries it to the lane that holds
+// the expert's column (a wave's own 256 Q values: no barrier).
 template <int DT, int LPR, int Q>
 __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
 {
-    constexpr int GPW = 64 / LPR;
+    constexpr int GPW = 64 / LPR, COLS = LPR * 4 * Q;
+    __shared__ __attribute__((aligned(16))) float chosen[4][GPW][COLS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane % LPR, grp = lane / LPR;
+    float *mine = chosen[wave][grp];
     const float n = (float)*a.tokens;
     const float gl = a.grad_loss && n > 0.0f ? *a.grad_loss * (float)a.E / (n * n * (float)a.k) : 0.0f;
     f32x4 from_loss[Q];
@@ -379,51 +555,72 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = q * LPR * 4 + li * 4 + i;
+            const int e = li * 4 * Q + 4 * q + i;
             from_loss[q][i] = e < a.E ? gl * (float)a.counts[e] : 0.0f;
         }
     const int64_t step = (int64_t)gridDim.x * 4 * GPW;
-    for (int64_t base = ((int64_t)blockIdx.x * 4 + wave) * GPW; base < a.T; base += step) {
-        const int64_t t = base + grp;
+    const bool vec = a.vec;
+    auto load = [&](int64_t t, f32x4 (&x)[Q]) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            x[q] = t < a.T ? load_logits<DT>(a.logits, t * a.ld, li * 4 * Q + 4 * q, a.E, vec)
+                           : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    };
+    f32x4 next[Q];
+    const int64_t first = ((int64_t)blockIdx.x * 4 + wave) * GPW + grp;
+    load(first, next);
+    for (int64_t t = first; t - grp < a.T; t += step) {
         const bool in = t < a.T;
         const bool on = in && a.ids[t * a.k] >= 0;     // a routed token has a first choice
         f32x4 x[Q], key[Q], dp[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            x[q] = on ? load_logits<DT>(a.logits, t * a.ld, q * LPR * 4 + li * 4, a.E, a.vec)
-                      : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            x[q] = on ? next[q] : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        load(t + step, next);
         softmax_row<LPR, Q>(x, key);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
             dp[q] = from_loss[q];
         if (a.grad_w) {
-            // sums over the choices: of g w, and (renormalized) of p
-            float gw = 0.0f, total = 1.0f;
+            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            auto wave_sync = [] {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+            };
+            float mean = 0.0f, inv = 1.0f;
             if (a.renorm) {
-                float s = 0.0f;
-                for (int j = 0; j < a.k; ++j) {
-                    const int e = on ? a.ids[t * a.k + j] : -1;
-                    if (e >= 0)
-                        gw += a.grad_w[t * a.k + j] * a.weights[t * a.k + j];
-#pragma unroll
-                    for (int q = 0; q < Q; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (e == q * LPR * 4 + li * 4 + i)
-                                s += x[q][i];
-                }
-                s = row_sum<LPR>(s);
-                total = s != 0.0f ? s : 1.0f;
-            }
-            for (int j = 0; j < a.k; ++j) {
-                const int e = on ? a.ids[t * a.k + j] : -1;
-                const float h = e >= 0 ? (a.grad_w[t * a.k + j] - gw) / total : 0.0f;
+                // p where the choices are: their sum, and sum of g w
 #pragma unroll
                 for (int q = 0; q < Q; ++q)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dp[q][i] += e == q * LPR * 4 + li * 4 + i ? h : 0.0f;
+                    *reinterpret_cast<f32x4 *>(mine + li * 4 * Q + 4 * q) = x[q];
+                wave_sync();
+                float total = 0.0f;
+                for (int j = li; j < a.k; j += LPR) {
+                    const int e = on ? a.ids[t * a.k + j] : -1;
+                    if ((uint32_t)e < (uint32_t)a.E) {
+                        total += mine[e];
+                        mean += a.grad_w[t * a.k + j] * a.weights[t * a.k + j];
+                    }
+                }
+                total = row_sum<LPR>(total);
+                mean = row_sum<LPR>(mean);
+                inv = total != 0.0f ? 1.0f / total : 1.0f;
+                wave_sync();
             }
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                *reinterpret_cast<f32x4 *>(mine + li * 4 * Q + 4 * q) = zero;
+            wave_sync();
+            for (int j = li; j < a.k; j += LPR) {
+                const int e = on ? a.ids[t * a.k + j] : -1;
+                if ((uint32_t)e < (uint32_t)a.E)
+                    mine[e] = (a.grad_w[t * a.k + j] - mean) * inv;
+            }
+            wave_sync();
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                dp[q] += *reinterpret_cast<const f32x4 *>(mine + li * 4 * Q + 4 * q);
+            wave_sync();
         }
         float dot = 0.0f;
 #pragma unroll
@@ -435,15 +632,14 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
         if (in)
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-                store_logits<DT>(a.dlogits, t * a.ldd, q * LPR * 4 + li * 4, a.E, a.vec_d, x[q] * (dp[q] - dot));
+                store_logits<DT>(a.dlogits, t * a.ldd, li * 4 * Q + 4 * q, a.E, a.vec_d, x[q] * (dp[q] - dot));
     }
 }
 
-// The number of blocks of the forward launch, at most 128: each later block
-// reads every block's counts.
+// At most two blocks for every compute unit: all of them at once.
 int64_t tokens_per_block(int64_t T)
 {
-    return std::max<int64_t>(cdiv(cdiv(T, 128), 64) * 64, 64);
+    return std::max<int64_t>(cdiv(cdiv(T, 2 * kNumCUs), 16) * 16, 64);
 }
 
 template <typename F>
@@ -492,6 +688,8 @@ void carve_route(Carver &c, RouteArgs &a)
     a.hist = c.take<int>((int64_t)a.blocks * (a.E + 1));
     a.psum = c.take<float>((int64_t)a.blocks * a.E);
     a.live = c.take<int>(a.blocks);
+    a.totals = c.take<int>(a.E + 1);
+    a.loss_part = c.take<float>((a.E + 64) / 64);
 }
 
 }  // namespace
@@ -571,7 +769,8 @@ gemm_status_t gemm_run_route(const void *logits, const uint8_t *mask, int64_t T,
     });
     if (st != GEMM_OK || one)
         return st;
-    hipLaunchKernelGGL(route_finish, dim3(a.blocks + 1), dim3(kGroupThreads), 0, stream, a);
+    hipLaunchKernelGGL(route_scan, dim3((unsigned)((E + 64) / 64)), dim3(kGroupThreads), 0, stream, a);
+    hipLaunchKernelGGL(route_place, dim3(a.blocks + 1), dim3(kGroupThreads), 0, stream, a);
     return hipGetLastError() == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 

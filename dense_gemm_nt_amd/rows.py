@@ -16,10 +16,12 @@ tensors then hold.
 from __future__ import annotations
 
 import collections
+import contextlib
 import ctypes
+import functools
 
 from . import _lib, _rows
-from .api import _code
+from .api import _code as _code_of_name
 
 Routing = collections.namedtuple("Routing", "ids weights counts offsets order tokens loss "
                                             "renormalize")
@@ -30,10 +32,23 @@ without an expert last), tokens [1] (how many were routed), loss (float32
 scalar), and the call's `renormalize`."""
 
 
+@functools.lru_cache(maxsize=None)
+def _code(dtype):
+    return _code_of_name(dtype)
+
+
 def _on(dev, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != dev:
             raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+
+
+def _current(dev):
+    """A context in which `dev` is the current device (none needed where it is)."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors, got %s" % dev)
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
 def _matrix(name, X, rows, cols):
@@ -59,10 +74,14 @@ def _out(name, out, shape, dtype, dev):
     return out
 
 
+# (a function of the sizes only; calls repeat them)
+_workspace_bytes = functools.lru_cache(maxsize=256)(_rows.workspace_bytes)
+
+
 def _workspace(fn, sizes, dev, what):
     """The call's device workspace (or None) and its size."""
     import torch
-    st, n = _rows.workspace_bytes(fn, *sizes)
+    st, n = _workspace_bytes(fn, *sizes)
     _lib.check(st, what)
     ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
     return ws, n
@@ -74,7 +93,7 @@ def _ptr(t):
 
 def _stream(dev):
     import torch
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.current_stream(dev.index).cuda_stream
 
 
 def _adapters(A, B, ids, scale, M, N, K, dtype, dev):
@@ -131,7 +150,7 @@ def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=
             _vector("bias", bias, N if bias_along == "n" else M, torch.float32)
         epi = _lib.epilogue(alpha, beta, bias.data_ptr() if bias is not None else 0,
                             bias_along if bias is not None else "none", activation)
-    with torch.cuda.device(dev):
+    with _current(dev):
         ws, n = _workspace("gemm_lora_workspace", (M, N, K, ad.num_adapters, ad.rank), dev, "gemm_lora")
         st = _rows.lib().gemm_run_lora(
             x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy, _code(x.dtype),
@@ -164,7 +183,7 @@ def gemm_lora_backward(dy, x, W, A, B, ids, scale, grad_dtype=None, dx_dtype=Non
     dx = torch.empty((M, K), dtype=dx_dtype or x.dtype, device=dev) if need_dx else None
     dA = torch.empty((L, R, K), dtype=gdt, device=dev) if need_adapters else None
     dB = torch.empty((L, N, R), dtype=gdt, device=dev) if need_adapters else None
-    with torch.cuda.device(dev):
+    with _current(dev):
         ws, n = _workspace("gemm_lora_backward_workspace", (M, N, K, L, R), dev, "gemm_lora_backward")
         st = _rows.lib().gemm_run_lora_backward(
             dy.data_ptr(), x.data_ptr(), W.data_ptr(), _ptr(dx), _ptr(dA) or None, _ptr(dB) or None,
@@ -205,16 +224,24 @@ def route_topk(logits, top_k, mask=None, renormalize=True):
     ld = _matrix("logits", logits, T, E)
     mask = _mask(mask, T)
     _on(dev, mask=mask)
-    i32 = dict(dtype=torch.int32, device=dev)
-    with torch.cuda.device(dev):
+    # one allocation for the integers and one for the rest: allocations are most of a
+    # small call's time on the host
+    n_pairs = T * max(k, 0)
+    with _current(dev):
         ws, n = _workspace("gemm_route_workspace", (T, E, k), dev, "route_topk")
-        f32 = dict(dtype=torch.float32, device=dev)
-        r = Routing(torch.empty((T, k), **i32), torch.empty((T, k), **f32), torch.empty(E, **i32),
-                    torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty(1, **i32),
-                    torch.empty((), **f32), bool(renormalize))
+        ints = torch.empty(2 * n_pairs + 2 * E + 2, dtype=torch.int32, device=dev)
+        reals = torch.empty(n_pairs + 1, dtype=torch.float32, device=dev)
+        ids, order, counts, offsets, tokens = ints.split((n_pairs, n_pairs, E, E + 1, 1))
+        weights, loss = reals.split((n_pairs, 1))
+        p, q = ints.data_ptr(), reals.data_ptr()
+        at = p + 8 * n_pairs
+        c_out = _rows.GemmRouting(p, q, at, at + 4 * E, p + 4 * n_pairs, at + 8 * E + 4,
+                                  q + 4 * n_pairs)
+        r = Routing(ids.view(T, k), weights.view(T, k), counts, offsets, order, tokens,
+                    loss.view(()), bool(renormalize))
         st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k,
                                         int(r.renormalize), _code(logits.dtype),
-                                        ctypes.byref(_c_routing(r)), _ptr(ws), n, _stream(dev))
+                                        ctypes.byref(c_out), _ptr(ws), n, _stream(dev))
     _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
     return r
 
@@ -242,7 +269,7 @@ def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=
     out = _out("out", out, (T, E), logits.dtype, dev)
     if out.dtype != logits.dtype:
         raise TypeError("out must have the logits' dtype")
-    with torch.cuda.device(dev):
+    with _current(dev):
         st = _rows.lib().gemm_run_route_backward(
             logits.data_ptr(), ctypes.byref(_c_routing(routing)), _ptr(grad_weights), _ptr(grad_loss),
             out.data_ptr(), T, E, ld, _matrix("out", out, T, E), k, int(routing.renormalize),
@@ -280,7 +307,7 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
         raise ValueError("W's strides %s are neither K-major nor MN-major" % (tuple(W.stride()),))
     tail = _rows.GEMM_TAIL_ZERO if out is None else _rows.GEMM_TAIL_KEEP
     out = _out("out", out, (S, N), out_dtype or x.dtype, dev)
-    with torch.cuda.device(dev):
+    with _current(dev):
         st = _rows.lib().gemm_run_routed(
             x.data_ptr(), W.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, ldx, ldw,
             W.stride(0) if E > 1 else 0, _matrix("out", out, S, N), layout, _code(x.dtype),
@@ -309,7 +336,7 @@ def gemm_routed_wgrad(dy, x, offsets, out_dtype=None):
     _vector("offsets", offsets, E + 1, torch.int32)
     lddy, ldx = _matrix("dy", dy, S, N), _matrix("x", x, S, K)
     out = torch.empty((E, N, K), dtype=out_dtype or x.dtype, device=dev)
-    with torch.cuda.device(dev):
+    with _current(dev):
         st = _rows.lib().gemm_run_routed_wgrad(
             dy.data_ptr(), x.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, lddy, ldx,
             _code(x.dtype), _code(out.dtype), _stream(dev))
