@@ -239,13 +239,13 @@ __device__ __forceinline__ void add_special(f32x16 &acc, u32x4 up, u32x4 hi, u32
 // whose fragments hold one are taken apart, add_special.)  A tile's K splits
 // share its adapters, split s taking the adapters s, s + splits, ... of each
 // wave's walk, so that all of a decode grid's blocks stream them; NB adapters'
-// fragments are in flight together.  Rows without an adapter, and ids that name
+// fragments are in flight together, and AHEAD the next ranks' low-rank values (as
+// the tile leaves registers for).  Rows without an adapter, and ids that name
 // none, add nothing.  Nothing here waits on the tile's own loads.
-template <int IN, int FN, int FM>
+template <int IN, int NB, bool AHEAD, int FN, int FM>
 __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM], int r0, int c0, int split,
                                          int lane)
 {
-    constexpr int NB = FM * FN == 1 || FM == 4 ? 8 : FN == 4 ? 2 : 4;   // (fewer where registers are short)
     if (p.adapters == 0 || r0 >= p.M || c0 >= p.N)
         return;
     int id[FM];
@@ -262,24 +262,97 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
     if (any == 0)
         return;
     const int h = lane >> 5;
-    for (int rs = 0; rs < p.rank; rs += 16) {
-        // the wave's scaled low-rank values of ranks rs + 8 h .. +8, split in two
-        u32x4 hi[FM], lo[FM];
+    const uint32_t bytes = (uint32_t)p.N * (uint32_t)p.up_ld * 2u;   // below 2^31 (host)
+    const uint32_t voff = (uint32_t)(c0 + (lane & 31)) * (uint32_t)p.up_ld * 2u + (uint32_t)(8 * h) * 2u;
+    auto load_up = [&](int a, int fn, int rs) {
+        return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             make_rsrc(p.up + (int64_t)a * p.up_stride, bytes),
+                                             rs + 8 * h < p.rank && c0 + fn * 32 + (lane & 31) < p.N
+                                                 ? voff + (uint32_t)(fn * 32) * (uint32_t)p.up_ld * 2u
+                                                 : kOutOfRange,
+                                             (uint32_t)rs * 2u, 0));
+    };
+    // the walk: the adapter of the first row left, until none is; this split's share
+    uint32_t left[FM];
+    int nth = 0;
+    auto start = [&] {
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+            left[fm] = rows[fm];
+        nth = 0;
+    };
+    auto next = [&]() -> int {
+        for (;;) {
+            int a = -1;
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+                if (a < 0 && left[fm])
+                    a = __builtin_amdgcn_readlane(id[fm], __builtin_ctz(left[fm]));
+            if (a < 0)
+                return -1;
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+                left[fm] &= ~(uint32_t)__builtin_amdgcn_ballot_w64(id[fm] == a);
+            const bool mine = nth % p.splits == split;
+            ++nth;
+            if (mine)
+                return a;
+        }
+    };
+    // the next NB adapters and their fragments of ranks rs .. +16
+    int a[NB];
+    u32x4 up[NB][FN];
+    auto fetch = [&](int rs) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            a[b] = b == 0 || a[b - 1] >= 0 ? next() : -1;
+            if (a[b] >= 0)
+#pragma unroll
+                for (int fn = 0; fn < FN; ++fn)
+                    up[b][fn] = load_up(a[b], fn, rs);
+        }
+    };
+    // the wave's low-rank values of ranks rs + 8 h .. +8 (the first split's, to begin with)
+    f32x4 low[FM][2];
+    auto fetch_low = [&](int rs) {
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
-            f32x4 v0 = {0.0f, 0.0f, 0.0f, 0.0f}, v1 = v0;
+            low[fm][0] = low[fm][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
             if (id[fm] >= 0 && rs + 8 * h < p.rank) {
                 const int m = r0 + fm * 32 + (lane & 31);
                 const float *src = p.low + (int64_t)m * p.rank_pad + rs + 8 * h;
-                for (int s = 0; s < p.low_splits; ++s) {
+                low[fm][0] = *reinterpret_cast<const f32x4 *>(src);
+                low[fm][1] = *reinterpret_cast<const f32x4 *>(src + 4);
+            }
+        }
+    };
+    float scale[FM];
+    start();
+    fetch(0);
+    if constexpr (AHEAD)
+        fetch_low(0);
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+        scale[fm] = id[fm] >= 0 ? p.scale[id[fm]] : 0.0f;
+    for (int rs = 0; rs < p.rank; rs += 16) {
+        if constexpr (!AHEAD)
+            fetch_low(rs);
+        // scaled, and split in two
+        u32x4 hi[FM], lo[FM];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+            f32x4 v0 = low[fm][0], v1 = low[fm][1];
+            if (p.low_splits > 1 && id[fm] >= 0 && rs + 8 * h < p.rank) {
+                const int m = r0 + fm * 32 + (lane & 31);
+                const float *src = p.low + (int64_t)m * p.rank_pad + rs + 8 * h;
+                for (int s = 1; s < p.low_splits; ++s) {
+                    src += (int64_t)p.M * p.rank_pad;
                     v0 += *reinterpret_cast<const f32x4 *>(src);
                     v1 += *reinterpret_cast<const f32x4 *>(src + 4);
-                    src += (int64_t)p.M * p.rank_pad;
                 }
-                const float sc = p.scale[id[fm]];
-                v0 *= sc;
-                v1 *= sc;
             }
+            v0 *= scale[fm];
+            v1 *= scale[fm];
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 uint16_t h0, l0, h1, l1;
@@ -289,54 +362,12 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                 lo[fm][d] = (uint32_t)l0 | ((uint32_t)l1 << 16);
             }
         }
-        // the walk: the adapter of the first row left, until none is
-        uint32_t left[FM];
-#pragma unroll
-        for (int fm = 0; fm < FM; ++fm)
-            left[fm] = rows[fm];
-        int nth = 0;
-        auto next = [&]() -> int {
-            for (;;) {
-                int a = -1;
-#pragma unroll
-                for (int fm = 0; fm < FM; ++fm)
-                    if (a < 0 && left[fm])
-                        a = __builtin_amdgcn_readlane(id[fm], __builtin_ctz(left[fm]));
-                if (a < 0)
-                    return -1;
-#pragma unroll
-                for (int fm = 0; fm < FM; ++fm)
-                    left[fm] &= ~(uint32_t)__builtin_amdgcn_ballot_w64(id[fm] == a);
-                const bool mine = nth % p.splits == split;
-                ++nth;
-                if (mine)
-                    return a;
-            }
-        };
-        const bool rank_in = rs + 8 * h < p.rank;
-        const uint32_t voff = (uint32_t)(c0 + (lane & 31)) * (uint32_t)p.up_ld * 2u + (uint32_t)(rs + 8 * h) * 2u;
-        const uint32_t bytes = (uint32_t)p.N * (uint32_t)p.up_ld * 2u;   // below 2^31 (host)
-        auto load_up = [&](int a, int fn) {
-            return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 make_rsrc(p.up + (int64_t)a * p.up_stride, bytes),
-                                                 rank_in && c0 + fn * 32 + (lane & 31) < p.N
-                                                     ? voff + (uint32_t)(fn * 32) * (uint32_t)p.up_ld * 2u
-                                                     : kOutOfRange,
-                                                 0, 0));
-        };
+        // (the next ranks' values are on their way while these are multiplied)
+        if (AHEAD && rs + 16 < p.rank)
+            fetch_low(rs + 16);
         const u32x4 zero = {0u, 0u, 0u, 0u};
         bool apart = false;
         for (;;) {
-            int a[NB];
-            u32x4 up[NB][FN];
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                a[b] = b == 0 || a[b - 1] >= 0 ? next() : -1;
-                if (a[b] >= 0)
-#pragma unroll
-                    for (int fn = 0; fn < FN; ++fn)
-                        up[b][fn] = load_up(a[b], fn);
-            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 if (a[b] < 0)
@@ -364,34 +395,36 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
             }
             if (a[NB - 1] < 0)
                 break;
+            fetch(rs);
         }
-        if (!apart)
-            continue;
-        // the adapters left out above, one at a time
+        if (apart) {
+            // the adapters left out above, one at a time
+            start();
+            for (int s = next(); s >= 0; s = next()) {
+                uint32_t special = 0;
 #pragma unroll
-        for (int fm = 0; fm < FM; ++fm)
-            left[fm] = rows[fm];
-        nth = 0;
-        for (int a = next(); a >= 0; a = next()) {
-            uint32_t special = 0;
-#pragma unroll
-            for (int fn = 0; fn < FN; ++fn)
-                special |= has_special<IN>(load_up(a, fn));
-            if (__builtin_amdgcn_ballot_w64(special != 0) == 0)
-                continue;
-#pragma unroll
-            for (int fm = 0; fm < FM; ++fm) {
-                const bool own = id[fm] == a;
-                if (__builtin_amdgcn_ballot_w64(own) == 0)
+                for (int fn = 0; fn < FN; ++fn)
+                    special |= has_special<IN>(load_up(s, fn, rs));
+                if (__builtin_amdgcn_ballot_w64(special != 0) == 0)
                     continue;
-                const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
 #pragma unroll
-                for (int fn = 0; fn < FN; ++fn) {
-                    int again = a;                    // (a load of its own: registers)
-                    asm volatile("" : "+s"(again));
-                    add_special<IN>(acc[fn][fm], load_up(again, fn), th, tl, own);
+                for (int fm = 0; fm < FM; ++fm) {
+                    const bool own = id[fm] == s;
+                    if (__builtin_amdgcn_ballot_w64(own) == 0)
+                        continue;
+                    const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
+#pragma unroll
+                    for (int fn = 0; fn < FN; ++fn) {
+                        int again = s;                    // (a load of its own: registers)
+                        asm volatile("" : "+s"(again));
+                        add_special<IN>(acc[fn][fm], load_up(again, fn, rs), th, tl, own);
+                    }
                 }
             }
+        }
+        if (rs + 16 < p.rank) {
+            start();
+            fetch(rs + 16);
         }
     }
     mfma_settle();

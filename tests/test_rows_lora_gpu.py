@@ -59,6 +59,7 @@ SHAPES = [
     (256, 2048, 8192, 16, 200, "mixed"), (250, 1032, 8192, 128, 3, "wild"), (2048, 4096, 64, 16, 4, "runs"),
     (2050, 4100, 72, 64, 9, "mixed"), (1024, 4096, 2560, 8, 2, "runs"), (130, 300, 264, 120, 2, "mixed"),
     (300, 77, 40, 16, 5, "none"), (256, 8192, 8192, 16, 30, "mixed"),
+    (2100, 264, 1000, 128, 3, "mixed"), (2100, 136, 328, 16, 70, "wild"), (2049, 77, 4096, 24, 5, "runs"),
 ]
 
 
@@ -168,7 +169,7 @@ def _check_backward(c, dy, got, dt, dx_dt, g_dt, what):
     (1, 8, 8, 8, 1, "one"), (3, 136, 64, 16, 2, "mixed"), (65, 264, 520, 24, 7, "wild"),
     (129, 1000, 72, 8, 3, "runs"), (300, 256, 512, 40, 70, "mixed"), (700, 512, 1032, 128, 2, "mixed"),
     (1000, 4096, 64, 64, 3, "runs"), (2500, 136, 4096, 16, 1, "one"), (777, 4096, 2048, 8, 3, "mixed"),
-    (64, 64, 64, 16, 4, "none"),
+    (64, 64, 64, 16, 4, "none"), (2100, 264, 1000, 128, 3, "mixed"), (2100, 136, 328, 16, 70, "wild"),
 ])
 @pytest.mark.parametrize("dt", [BF16, FP16])
 def test_backward(M, N, K, R, L, kind, dt):
