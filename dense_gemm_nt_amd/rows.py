@@ -37,31 +37,41 @@ def _code(dtype):
     return _code_of_name(dtype)
 
 
-def _on(dev, **tensors):
+def _on(index, **tensors):
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+        if t is not None and t.get_device() != index:
+            raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
 
 
-def _current(dev):
-    """A context in which `dev` is the current device (none needed where it is)."""
+def _device(t):
+    """(device, index) of a CUDA tensor."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors, got one on %s" % t.device)
+    return t.device, index
+
+
+def _current(index):
+    """A context in which device `index` is current (none needed where it is)."""
     import torch
-    if dev.type != "cuda":
-        raise ValueError("expected CUDA tensors, got %s" % dev)
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _matrix(name, X, rows, cols):
     """Leading dimension of a [rows, cols] tensor with unit stride along its columns."""
-    if X.dim() != 2 or tuple(X.shape) != (rows, cols):
+    if X.shape != (rows, cols):
         raise ValueError("%s must be [%d, %d], got %s" % (name, rows, cols, tuple(X.shape)))
-    if cols > 1 and rows > 0 and X.stride(1) != 1:
+    ld, step = X.stride()
+    if step != 1 and cols > 1 and rows > 0:
         raise ValueError("%s needs unit stride along its columns" % name)
-    return X.stride(0) if rows > 1 else max(cols, X.stride(0))
+    return ld if rows > 1 else max(cols, ld)
 
 
 def _vector(name, v, n, dtype):
-    if v.dtype != dtype or tuple(v.shape) != (n,) or not v.is_contiguous():
+    if v.dtype != dtype or v.shape != (n,) or not v.is_contiguous():
         raise ValueError("%s must be a contiguous %s vector of %d values" % (name, dtype, n))
 
 
@@ -69,7 +79,7 @@ def _out(name, out, shape, dtype, dev):
     import torch
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(out.shape) != tuple(shape) or out.device != dev:
+    if out.shape != shape or out.device != dev:
         raise ValueError("%s must be %s on %s" % (name, list(shape), dev))
     return out
 
@@ -91,35 +101,35 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _stream(dev):
+def _stream(index):
     import torch
-    return torch.cuda.current_stream(dev.index).cuda_stream
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-def _adapters(A, B, ids, scale, M, N, K, dtype, dev):
+def _adapters(A, B, ids, scale, M, N, K, dtype, index):
     """A checked GemmAdapters of A [L, R, K], B [L, N, R], ids [M], scale [L]."""
     import torch
-    if A.dim() != 3 or B.dim() != 3 or A.shape[0] != B.shape[0] or A.shape[2] != K or \
-            tuple(B.shape[1:]) != (N, A.shape[1]):
+    if A.dim() != 3 or B.shape != (A.shape[0], N, A.shape[1]) or A.shape[2] != K:
         raise ValueError("adapters must be A [L, R, %d] and B [L, %d, R], got %s and %s"
                          % (K, N, tuple(A.shape), tuple(B.shape)))
     L, R, _ = A.shape
     if A.dtype != dtype or B.dtype != dtype:
         raise TypeError("the adapters must have the operands' dtype %s" % dtype)
-    _on(dev, A=A, B=B, ids=ids, scale=scale)
+    _on(index, A=A, B=B, ids=ids, scale=scale)
     _vector("ids", ids, M, torch.int32)
     _vector("scale", scale, L, torch.float32)
-    for name, X in (("A", A), ("B", B)):
-        if X.numel() and X.shape[2] > 1 and X.stride(2) != 1:
-            raise ValueError("%s needs unit stride along its last axis" % name)
-
-    def ld(X):
-        return X.stride(1) if X.shape[1] > 1 else max(X.shape[2], X.stride(1))
-
-    def step(X):                       # a single adapter's stride is never used
-        return X.stride(0) if L > 1 else 0
+    a_step, a_ld, a_unit = A.stride()
+    b_step, b_ld, b_unit = B.stride()
+    if (a_unit != 1 and K > 1 and A.numel()) or (b_unit != 1 and R > 1 and B.numel()):
+        raise ValueError("A and B need unit stride along their last axis")
+    if R <= 1:
+        a_ld = max(K, a_ld)
+    if N <= 1:
+        b_ld = max(R, b_ld)
+    if L <= 1:                         # a single adapter's stride is never used
+        a_step = b_step = 0
     return _rows.GemmAdapters(A.data_ptr(), B.data_ptr(), scale.data_ptr(), ids.data_ptr(), L, R,
-                              step(A), ld(A), step(B), ld(B))
+                              a_step, a_ld, b_step, b_ld)
 
 
 def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=0.0, bias=None,
@@ -134,12 +144,12 @@ def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=
         raise ValueError("x and W must be 2-D")
     M, K = x.shape
     N = W.shape[0]
-    dev = x.device
+    dev, index = _device(x)
     if x.dtype != W.dtype:
         raise TypeError("x and W must share a dtype")
-    _on(dev, W=W, bias=bias)
+    _on(index, W=W, bias=bias)
     ldx, ldw = _matrix("x", x, M, K), _matrix("W", W, N, K)
-    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, dev)
+    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, index)
     if beta != 0.0 and out is None:
         raise ValueError("beta != 0 reads the prior y: pass it as `out`")
     out = _out("out", out, (M, N), out_dtype or x.dtype, dev)
@@ -150,12 +160,12 @@ def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=
             _vector("bias", bias, N if bias_along == "n" else M, torch.float32)
         epi = _lib.epilogue(alpha, beta, bias.data_ptr() if bias is not None else 0,
                             bias_along if bias is not None else "none", activation)
-    with _current(dev):
+    with _current(index):
         ws, n = _workspace("gemm_lora_workspace", (M, N, K, ad.num_adapters, ad.rank), dev, "gemm_lora")
         st = _rows.lib().gemm_run_lora(
             x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy, _code(x.dtype),
             _code(out.dtype), ctypes.byref(ad), ctypes.byref(epi) if epi is not None else None,
-            _ptr(ws), n, _stream(dev))
+            _ptr(ws), n, _stream(index))
     _lib.check(st, "gemm_lora(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, ad.num_adapters, ad.rank))
     return out
 
@@ -172,23 +182,23 @@ def gemm_lora_backward(dy, x, W, A, B, ids, scale, grad_dtype=None, dx_dtype=Non
         raise ValueError("dy, x and W must be 2-D")
     M, K = x.shape
     N = W.shape[0]
-    dev = x.device
+    dev, index = _device(x)
     if x.dtype != W.dtype or dy.dtype != x.dtype:
         raise TypeError("dy, x and W must share a dtype")
-    _on(dev, dy=dy, W=W)
+    _on(index, dy=dy, W=W)
     lddy, ldx, ldw = _matrix("dy", dy, M, N), _matrix("x", x, M, K), _matrix("W", W, N, K)
-    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, dev)
+    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, index)
     L, R = ad.num_adapters, ad.rank
     gdt = grad_dtype or torch.float32
     dx = torch.empty((M, K), dtype=dx_dtype or x.dtype, device=dev) if need_dx else None
     dA = torch.empty((L, R, K), dtype=gdt, device=dev) if need_adapters else None
     dB = torch.empty((L, N, R), dtype=gdt, device=dev) if need_adapters else None
-    with _current(dev):
+    with _current(index):
         ws, n = _workspace("gemm_lora_backward_workspace", (M, N, K, L, R), dev, "gemm_lora_backward")
         st = _rows.lib().gemm_run_lora_backward(
             dy.data_ptr(), x.data_ptr(), W.data_ptr(), _ptr(dx), _ptr(dA) or None, _ptr(dB) or None,
             M, N, K, lddy, ldx, ldw, K, _code(x.dtype), _code(dx_dtype or x.dtype), _code(gdt),
-            ctypes.byref(ad), _ptr(ws), n, _stream(dev))
+            ctypes.byref(ad), _ptr(ws), n, _stream(index))
     _lib.check(st, "gemm_lora_backward(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, L, R))
     return dx, dA, dB
 
@@ -220,19 +230,19 @@ def route_topk(logits, top_k, mask=None, renormalize=True):
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
     k = int(top_k)
-    dev = logits.device
+    dev, index = _device(logits)
     ld = _matrix("logits", logits, T, E)
     mask = _mask(mask, T)
-    _on(dev, mask=mask)
+    _on(index, mask=mask)
     # one allocation for the integers and one for the rest: allocations are most of a
     # small call's time on the host
     n_pairs = T * max(k, 0)
-    with _current(dev):
+    with _current(index):
         ws, n = _workspace("gemm_route_workspace", (T, E, k), dev, "route_topk")
         ints = torch.empty(2 * n_pairs + 2 * E + 2, dtype=torch.int32, device=dev)
         reals = torch.empty(n_pairs + 1, dtype=torch.float32, device=dev)
-        ids, order, counts, offsets, tokens = ints.split((n_pairs, n_pairs, E, E + 1, 1))
-        weights, loss = reals.split((n_pairs, 1))
+        ids, order, counts, offsets, tokens = ints.split_with_sizes((n_pairs, n_pairs, E, E + 1, 1))
+        weights, loss = reals.split_with_sizes((n_pairs, 1))
         p, q = ints.data_ptr(), reals.data_ptr()
         at = p + 8 * n_pairs
         c_out = _rows.GemmRouting(p, q, at, at + 4 * E, p + 4 * n_pairs, at + 8 * E + 4,
@@ -241,7 +251,7 @@ def route_topk(logits, top_k, mask=None, renormalize=True):
                     loss.view(()), bool(renormalize))
         st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k,
                                         int(r.renormalize), _code(logits.dtype),
-                                        ctypes.byref(c_out), _ptr(ws), n, _stream(dev))
+                                        ctypes.byref(c_out), _ptr(ws), n, _stream(index))
     _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
     return r
 
@@ -257,9 +267,9 @@ def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=
         raise ValueError("routing does not belong to these logits")
     T, E = logits.shape
     k = routing.ids.shape[1]
-    dev = logits.device
+    dev, index = _device(logits)
     ld = _matrix("logits", logits, T, E)
-    _on(dev, ids=routing.ids, grad_weights=grad_weights, grad_loss=grad_loss)
+    _on(index, ids=routing.ids, grad_weights=grad_weights, grad_loss=grad_loss)
     if grad_weights is not None and (grad_weights.dtype != torch.float32 or
                                      tuple(grad_weights.shape) != (T, k) or
                                      not grad_weights.is_contiguous()):
@@ -269,11 +279,11 @@ def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=
     out = _out("out", out, (T, E), logits.dtype, dev)
     if out.dtype != logits.dtype:
         raise TypeError("out must have the logits' dtype")
-    with _current(dev):
+    with _current(index):
         st = _rows.lib().gemm_run_route_backward(
             logits.data_ptr(), ctypes.byref(_c_routing(routing)), _ptr(grad_weights), _ptr(grad_loss),
             out.data_ptr(), T, E, ld, _matrix("out", out, T, E), k, int(routing.renormalize),
-            _code(logits.dtype), _stream(dev))
+            _code(logits.dtype), _stream(index))
     _lib.check(st, "route_topk_backward(T=%d, E=%d, k=%d)" % (T, E, k))
     return out
 
@@ -291,10 +301,10 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
                          % (tuple(x.shape), tuple(W.shape)))
     S, K = x.shape
     E, N, _ = W.shape
-    dev = x.device
+    dev, index = _device(x)
     if x.dtype != W.dtype:
         raise TypeError("x and W must share a dtype")
-    _on(dev, W=W, offsets=offsets)
+    _on(index, W=W, offsets=offsets)
     _vector("offsets", offsets, E + 1, torch.int32)
     ldx = _matrix("x", x, S, K)
     if W.numel() == 0:
@@ -307,11 +317,11 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
         raise ValueError("W's strides %s are neither K-major nor MN-major" % (tuple(W.stride()),))
     tail = _rows.GEMM_TAIL_ZERO if out is None else _rows.GEMM_TAIL_KEEP
     out = _out("out", out, (S, N), out_dtype or x.dtype, dev)
-    with _current(dev):
+    with _current(index):
         st = _rows.lib().gemm_run_routed(
             x.data_ptr(), W.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, ldx, ldw,
             W.stride(0) if E > 1 else 0, _matrix("out", out, S, N), layout, _code(x.dtype),
-            _code(out.dtype), tail, _stream(dev))
+            _code(out.dtype), tail, _stream(index))
     _lib.check(st, "gemm_routed(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
     return out
 
@@ -326,19 +336,19 @@ def gemm_routed_wgrad(dy, x, offsets, out_dtype=None):
                          % (tuple(dy.shape), tuple(x.shape)))
     S, K = x.shape
     N = dy.shape[1]
-    dev = x.device
+    dev, index = _device(x)
     if x.dtype != dy.dtype:
         raise TypeError("dy and x must share a dtype")
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be [E + 1]")
     E = offsets.shape[0] - 1
-    _on(dev, dy=dy, offsets=offsets)
+    _on(index, dy=dy, offsets=offsets)
     _vector("offsets", offsets, E + 1, torch.int32)
     lddy, ldx = _matrix("dy", dy, S, N), _matrix("x", x, S, K)
     out = torch.empty((E, N, K), dtype=out_dtype or x.dtype, device=dev)
-    with _current(dev):
+    with _current(index):
         st = _rows.lib().gemm_run_routed_wgrad(
             dy.data_ptr(), x.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, lddy, ldx,
-            _code(x.dtype), _code(out.dtype), _stream(dev))
+            _code(x.dtype), _code(out.dtype), _stream(index))
     _lib.check(st, "gemm_routed_wgrad(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
     return out
