@@ -19,7 +19,15 @@ struct ShrinkArgs {
     float *low;               // [splits][M][rank_pad]
     int64_t down_stride;
     int M, K, ldx, down_ld, adapters, rank, rank_pad;
-    int k_per_split;          // a multiple of 128
+    int k_per_split;          // a multiple of the kernel's K step
+};
+
+// One or two low-rank products of the same rows and adapters in one launch (a
+// training step's two: x with A, dy with B transposed): K splits z < first of the
+// one, the rest of the other.
+struct ShrinkPair {
+    ShrinkArgs a[2];
+    int first;
     int lanes_j;              // blocks sharing a row tile's adapters (gridDim.y)
     unsigned *counters;       // zeroed here for the projection's split reduction
     int num_counters;
@@ -35,34 +43,37 @@ struct ShrinkArgs {
 // and no sorting of rows is needed.  A decode batch puts the adapters of a row
 // tile on different blocks (lanes_j), and K splits over more of them.
 template <int IN, int RT>
-__global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p)
+__global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkPair pair)
 {
+    const bool second = (int)blockIdx.z >= pair.first;
+    const ShrinkArgs &p = pair.a[second];
+    const int z = blockIdx.z - (second ? pair.first : 0);
     constexpr int W = kShrinkWaves, ROWS = 16, COLS = 16 * RT;
     __shared__ float part[W][ROWS][COLS + 1];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const int linear = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-    for (int i = linear * (W * 64) + tid; i < p.num_counters; i += gridDim.x * gridDim.y * gridDim.z * W * 64)
-        p.counters[i] = 0;
+    for (int i = linear * (W * 64) + tid; i < pair.num_counters; i += gridDim.x * gridDim.y * gridDim.z * W * 64)
+        pair.counters[i] = 0;
 
     const int r0 = blockIdx.x * ROWS;
     const int m = r0 + (lane & (ROWS - 1));
     const int a_in = m < p.M ? p.ids[m] : -1;
     const int id = (uint32_t)a_in < (uint32_t)p.adapters ? a_in : -1;
     uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0) & ((1ull << ROWS) - 1);
-    const int kb = blockIdx.z * p.k_per_split;
+    const int kb = z * p.k_per_split;
     const int ke = min(p.K, kb + p.k_per_split);
     const int rows = min(ROWS, p.M - r0);
     const __amdgpu_buffer_rsrc_t rs_x =
         make_rsrc(p.x + (int64_t)r0 * p.ldx, (uint32_t)rows * (uint32_t)p.ldx * 2u);
     const int li = lane & 15, kq = 8 * (lane >> 4);
-    float *out = p.low + (int64_t)blockIdx.z * p.M * p.rank_pad;
+    float *out = p.low + (int64_t)z * p.M * p.rank_pad;
 
     for (int nth = 0; left; ++nth) {
         const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
         left &= ~__builtin_amdgcn_ballot_w64(id == a);
-        if (nth % p.lanes_j != (int)blockIdx.y)
+        if (nth % pair.lanes_j != (int)blockIdx.y)
             continue;
         for (int c0 = 0; c0 < p.rank_pad; c0 += COLS) {
             const uint32_t d_bytes = __builtin_amdgcn_readfirstlane(
@@ -131,21 +142,24 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkArgs p)
 // passes.  Wave w multiplies rows 16 w .. +16 with all 64 ranks, and keeps each row's
 // own adapter's.  Bytes bound it: 8 slabs, 64 KB of x, are in flight a compute unit.
 template <int IN>
-__global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkArgs p)
+__global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkPair pair)
 {
+    const bool second = (int)blockIdx.z >= pair.first;
+    const ShrinkArgs &p = pair.a[second];
+    const int z = blockIdx.z - (second ? pair.first : 0);
     constexpr int STAGES = 8, X_BYTES = 64 * 128, STAGE = 2 * X_BYTES, NL = 4;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int linear = blockIdx.z * gridDim.x + blockIdx.x;
-    for (int i = linear * 256 + tid; i < p.num_counters; i += gridDim.x * gridDim.z * 256)
-        p.counters[i] = 0;
+    for (int i = linear * 256 + tid; i < pair.num_counters; i += gridDim.x * gridDim.z * 256)
+        pair.counters[i] = 0;
 
     const int r0 = blockIdx.x * 64, rows = min(64, p.M - r0);
     const int a_in = lane < rows ? p.ids[r0 + lane] : -1;
     const int id = (uint32_t)a_in < (uint32_t)p.adapters ? a_in : -1;
     uint64_t left = __builtin_amdgcn_ballot_w64(id >= 0);
-    const int kb = blockIdx.z * p.k_per_split;
+    const int kb = z * p.k_per_split;
     const int ke = min(p.K, kb + p.k_per_split);
     const int slabs = (ke - kb + 63) / 64;
     // (blocks start at different slabs: rows a power of two apart, read in step,
@@ -157,7 +171,7 @@ __global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkArgs p)
     // load row of this lane within 8 rows, and the chunk that the swizzle puts here
     const int lr = lane >> 3;
     const int per = p.rank <= 16 ? 16 : p.rank <= 32 ? 32 : 64;     // rank rows of an adapter
-    float *out = p.low + (int64_t)blockIdx.z * p.M * p.rank_pad;
+    float *out = p.low + (int64_t)z * p.M * p.rank_pad;
 
     while (left) {
         // up to 64 / per adapters for this pass; slot s holds ranks from per s on
@@ -291,22 +305,6 @@ struct GradArgs {
     int out_dtype;
 };
 
-__global__ __launch_bounds__(kGroupThreads) void lora_count(GradArgs a)
-{
-    __shared__ int hist[kMaxGroups + 1];
-    for (int e = threadIdx.x; e <= a.adapters; e += kGroupThreads)
-        hist[e] = 0;
-    __syncthreads();
-    const int64_t t0 = blockIdx.x * a.per_block;
-    const int64_t t1 = t0 + a.per_block < a.M ? t0 + a.per_block : a.M;
-    for (int64_t i = t0 + threadIdx.x; i < t1; i += kGroupThreads) {
-        const int g = a.ids[i];
-        atomicAdd(&hist[(uint32_t)g < (uint32_t)a.adapters ? g : a.adapters], 1);
-    }
-    __syncthreads();
-    store_hist(hist, a.hist, a.adapters);
-}
-
 // The rows' order by adapter, and (a block of its own) the stretches: each
 // adapter's rows in runs of at most `chunk`, so that a stretch is one unit of
 // work with one adapter.
@@ -358,9 +356,30 @@ struct FlipArgs {
     int tiles[2];               // 64 x 64 tiles of one adapter's matrix
 };
 
-__global__ __launch_bounds__(256) void lora_flip(FlipArgs p)
+// The first launch of a training step: the adapters transposed, and (the first
+// a.blocks blocks of row y = 0 past the tiles') the rows of each adapter counted.
+__global__ __launch_bounds__(256) void lora_prepare(FlipArgs p, GradArgs a)
 {
     __shared__ uint16_t t[64][66];
+    const int block = (int)blockIdx.x - p.tiles[0] - p.tiles[1];
+    if (block >= 0) {
+        __shared__ int hist[kMaxGroups + 1];
+        if (blockIdx.y != 0)
+            return;
+        for (int e = threadIdx.x; e <= a.adapters; e += 256)
+            hist[e] = 0;
+        __syncthreads();
+        const int64_t t0 = block * a.per_block;
+        const int64_t t1 = t0 + a.per_block < a.M ? t0 + a.per_block : a.M;
+        for (int64_t i = t0 + threadIdx.x; i < t1; i += 256) {
+            const int g = a.ids[i];
+            atomicAdd(&hist[(uint32_t)g < (uint32_t)a.adapters ? g : a.adapters], 1);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e <= a.adapters; e += 256)
+            a.hist[(int64_t)block * (a.adapters + 1) + e] = hist[e];
+        return;
+    }
     const int w = (int)blockIdx.x >= p.tiles[0];
     const int tile = blockIdx.x - (w ? p.tiles[0] : 0);
     const int tc = (p.cols[w] + 63) / 64;
@@ -646,11 +665,20 @@ ShrinkPlan plan_shrink(int64_t M, int64_t K, int64_t adapters, int64_t rank)
     return s;
 }
 
-hipError_t run_shrink(const ShrinkPlan &s, ShrinkArgs p, int in_dtype, hipStream_t stream)
+// Adds a product to a launch (at most two, of the same rows and adapters: their
+// plans then differ in K alone).
+void add_shrink(ShrinkPair &pair, const ShrinkPlan &s, ShrinkArgs p)
 {
     p.k_per_split = s.k_per_split;
-    p.lanes_j = s.lanes_j;
-    const dim3 grid(s.tiles, s.lanes_j, s.splits);
+    pair.lanes_j = s.lanes_j;
+    pair.a[pair.first > 0] = p;
+    if (pair.first == 0)
+        pair.first = s.splits;
+}
+
+hipError_t run_shrink(const ShrinkPlan &s, const ShrinkPair &p, int splits, int in_dtype, hipStream_t stream)
+{
+    const dim3 grid(s.tiles, s.lanes_j, splits);
     auto launch = [&](auto in) {
         if (s.rows)
             hipLaunchKernelGGL(lora_shrink_rows<in.value>, grid, dim3(256), 0, stream, p);
@@ -684,9 +712,41 @@ Plan plan_projection(int64_t M, int64_t N, int64_t K)
     }
     return make_plan(M, N, K, kPartialBytes, -1, -1, 0);
 }
-Plan plan_mn_major(int64_t M, int64_t N, int64_t K)
+// The input gradient's: the ping-pong tile, or (`tile`) the 128 x 128 one of
+// rows_tile.hpp.
+struct GradPlan {
+    Plan plan;
+    bool tile;
+};
+GradPlan plan_mn_major(int64_t M, int64_t N, int64_t K)
 {
-    return make_plan(M, N, K, kPartialBytes, CFG_PP2_256x256, -1, 0);
+    GradPlan g{make_plan(M, N, K, kPartialBytes, CFG_PP2_256x256, -1, 0), false};
+    // The ping-pong tiles from a quarter of the machine on (product and gradient
+    // parts, 4096 deep: 777 x 2048, 32 tiles, 51 us against 42 on the smaller tile;
+    // 1024 x 4096, 64 tiles, 62 against 58; 2048 x 4096, 128 tiles, 84 against 91).
+    if (cdiv(M, 256) * cdiv(N, 256) >= kNumCUs / 4)
+        return g;
+    Plan &p = g.plan;
+    g.tile = true;
+    p = Plan{};
+    p.tiles_m = (int)cdiv(M, 128);
+    p.tiles_n = (int)cdiv(N, 128);
+    p.k_tiles = (int)cdiv(K, 64);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    // K splits while all blocks, two to a compute unit, run at once; at least 8
+    // slabs each
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kNumCUs / tiles, p.k_tiles / 8));
+    while (splits > 1 && (tiles * splits * 128 * 128 * 4 > kPartialBytes || tiles * 4 > GEMM_COUNTER_BYTES))
+        --splits;
+    p.kt_per_split = (int)cdiv(p.k_tiles, splits);
+    p.splits = p.k_tiles ? (int)cdiv(p.k_tiles, p.kt_per_split) : 1;
+    p.group_m = std::min(4, p.tiles_m);
+    p.grid = tiles * p.splits;
+    if (p.splits > 1) {
+        p.inreduce = 1;
+        p.ws_bytes = p.grid * 128 * 128 * 4;
+    }
+    return g;
 }
 
 lora_fn projection_fn(const Plan &p, int64_t M, int in_dtype, int out_dtype)
@@ -852,7 +912,7 @@ ShrinkArgs shrink_args(const gemm_adapters_t *ad, const void *x, int64_t M, int6
 // Everything a backward call keeps in its workspace.
 struct BackwardWs {
     ShrinkPlan t, u;
-    Plan dx;
+    GradPlan dx;
     float *low_t, *low_u;
     uint16_t *flip_a, *flip_b;
     GradArgs g;
@@ -867,7 +927,7 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     w.u = plan_shrink(M, N, adapters, rank);
     if (M > 0 && K > 0)
         w.dx = plan_mn_major(M, K, N);
-    w.proj = carve_projection(c, w.dx);
+    w.proj = carve_projection(c, w.dx.plan);
     if (!has_adapters(adapters, rank) || M == 0 || N == 0 || K == 0)
         return w;      // nothing but a product, or less
     w.low_t = c.take<float>(w.t.splits * M * pad);
@@ -960,10 +1020,11 @@ gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, in
     if (K > 0 && has_adapters(adapters->num_adapters, adapters->rank)) {
         set_adapters(a, adapters, w.low, s.splits, static_cast<const uint16_t *>(adapters->B), adapters->b_stride,
                      adapters->b_ld);
-        ShrinkArgs q = shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld, w.low);
+        ShrinkPair q{};
         q.counters = w.proj.counters;
         q.num_counters = w.proj.num_counters;
-        e = run_shrink(s, q, in_dtype, stream);
+        add_shrink(q, s, shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld, w.low));
+        e = run_shrink(s, q, s.splits, in_dtype, stream);
     } else {
         e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
     }
@@ -1028,7 +1089,7 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
     BackwardWs w = carve_backward(c, M, N, K, L, R);
     if ((want_dx || (some && grads)) && (st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
         return st;
-    if (want_dx && (w.dx.grid <= 0 || w.dx.grid >= kMaxSize))
+    if (want_dx && (w.dx.plan.grid <= 0 || w.dx.plan.grid >= kMaxSize))
         return GEMM_ERR_UNSUPPORTED;
 
     hipError_t e = hipSuccess;
@@ -1051,13 +1112,21 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
         f.rows[1] = (int)N, f.cols[1] = (int)R;
         for (int i = 0; i < 2; ++i)
             f.tiles[i] = (int)(cdiv(f.rows[i], 64) * cdiv(f.cols[i], 64));
-        hipLaunchKernelGGL(lora_flip, dim3(f.tiles[0] + f.tiles[1], (unsigned)L), dim3(256), 0, stream, f);
+        w.g.ids = adapters->ids;
+        w.g.scale = adapters->scale;
+        hipLaunchKernelGGL(lora_prepare, dim3(f.tiles[0] + f.tiles[1] + (grads ? w.g.blocks : 0), (unsigned)L), dim3(256),
+                           0, stream, f, w.g);
         e = hipGetLastError();
-        ShrinkArgs u = shrink_args(adapters, dY, M, N, lddy, w.flip_b, R * N, N, w.low_u);
+        // dy with B transposed, and for the adapters' gradients x with A
+        ShrinkPair u{};
         u.counters = w.proj.counters;
         u.num_counters = w.proj.num_counters;
+        add_shrink(u, w.u, shrink_args(adapters, dY, M, N, lddy, w.flip_b, R * N, N, w.low_u));
+        if (grads)
+            add_shrink(u, w.t, shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld,
+                                           w.low_t));
         if (e == hipSuccess)
-            e = run_shrink(w.u, u, in_dtype, stream);
+            e = run_shrink(w.u, u, w.u.splits + (grads ? w.t.splits : 0), in_dtype, stream);
         set_adapters(a, adapters, w.low_u, w.u.splits, w.flip_a, R * K, R);
     } else if (want_dx && e == hipSuccess) {
         e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
@@ -1067,44 +1136,37 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
         a.B = static_cast<const uint16_t *>(W);
         a.lda = (int)lddy;
         a.ldb = (int)ldw;
-        fill_projection(a, w.dx, w.proj, dX, M, K, N, lddx, dx_dtype, nullptr);
-        e = run_projection(kLora_pp2_km[in_dtype][dx_dtype], w.dx, a, dx_dtype, stream);
+        fill_projection(a, w.dx.plan, w.proj, dX, M, K, N, lddx, dx_dtype, nullptr);
+        e = run_projection((w.dx.tile ? kLora_tile_km : kLora_pp2_km)[in_dtype][dx_dtype], w.dx.plan, a, dx_dtype,
+                           stream);
     }
     if (adapt && grads && e == hipSuccess) {
-        e = run_shrink(w.t, shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld,
-                                        w.low_t),
-                       in_dtype, stream);
         GradArgs &g = w.g;
-        g.ids = adapters->ids;
-        g.scale = adapters->scale;
         g.z[0] = static_cast<const uint16_t *>(X), g.z[1] = static_cast<const uint16_t *>(dY);
         g.ldz[0] = (int)ldx, g.ldz[1] = (int)lddy;
         g.v[0] = w.low_u, g.v[1] = w.low_t;
         g.v_splits[0] = w.u.splits, g.v_splits[1] = w.t.splits;
         g.out[0] = dA, g.out[1] = dB;
         g.out_dtype = grad_dtype;
-        if (e == hipSuccess) {
-            hipLaunchKernelGGL(lora_count, dim3(g.blocks), dim3(kGroupThreads), 0, stream, g);
-            hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
-            const unsigned widest = (unsigned)std::max(g.cols[0], g.cols[1]);
-            const dim3 grid((widest + 127) / 128, g.max_stretches, 2);
-            const int pad = g.rank_pad / 16;
-            auto grad = [&](auto in) {
-                hipLaunchKernelGGL(lora_pack<in.value>, dim3(g.chunk / 64, g.max_stretches, 2), dim3(256), 0, stream, g);
-                if (pad == 1)
-                    hipLaunchKernelGGL((lora_grad<in.value, 1>), grid, dim3(256), 0, stream, g);
-                else if (pad <= 3)
-                    hipLaunchKernelGGL((lora_grad<in.value, 2>), grid, dim3(256), 0, stream, g);
-                else
-                    hipLaunchKernelGGL((lora_grad<in.value, 4>), grid, dim3(256), 0, stream, g);
-            };
-            if (in_dtype == GEMM_BF16)
-                grad(std::integral_constant<int, IN_BF16>{});
+        hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
+        const unsigned widest = (unsigned)std::max(g.cols[0], g.cols[1]);
+        const dim3 grid((widest + 127) / 128, g.max_stretches, 2);
+        const int pad = g.rank_pad / 16;
+        auto grad = [&](auto in) {
+            hipLaunchKernelGGL(lora_pack<in.value>, dim3(g.chunk / 64, g.max_stretches, 2), dim3(256), 0, stream, g);
+            if (pad == 1)
+                hipLaunchKernelGGL((lora_grad<in.value, 1>), grid, dim3(256), 0, stream, g);
+            else if (pad <= 3)
+                hipLaunchKernelGGL((lora_grad<in.value, 2>), grid, dim3(256), 0, stream, g);
             else
-                grad(std::integral_constant<int, IN_FP16>{});
-            hipLaunchKernelGGL(lora_grad_sum, dim3((widest + 31) / 32, (unsigned)L, 2 * pad), dim3(256), 0, stream, g);
-            e = hipGetLastError();
-        }
+                hipLaunchKernelGGL((lora_grad<in.value, 4>), grid, dim3(256), 0, stream, g);
+        };
+        if (in_dtype == GEMM_BF16)
+            grad(std::integral_constant<int, IN_BF16>{});
+        else
+            grad(std::integral_constant<int, IN_FP16>{});
+        hipLaunchKernelGGL(lora_grad_sum, dim3((widest + 31) / 32, (unsigned)L, 2 * pad), dim3(256), 0, stream, g);
+        e = hipGetLastError();
     }
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }

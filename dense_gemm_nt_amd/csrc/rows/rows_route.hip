@@ -258,9 +258,13 @@ __device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, i
         for (int q = 0; q < Q; ++q)
             next[q] = load_logits<DT>(a.logits, t * a.ld, lane * V + 4 * q, a.E, a.vec);
     };
+    constexpr bool AHEAD = Q < 4;        // (16 columns a lane leave no registers for it)
     int routed = 0;
-    load(mine);
+    if constexpr (AHEAD)
+        load(mine);
     for (int64_t t = mine; t < t1; t += NW) {
+        if constexpr (!AHEAD)
+            load(t);
         f32x4 x[Q];
         int key[V], at[V];
         const bool on = __builtin_amdgcn_readfirstlane(next_on) != 0;
@@ -271,7 +275,8 @@ __device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, i
             key[v] = rank_key(value);
             at[v] = v;
         }
-        load(t + NW);                   // the next row's loads run under this row
+        if constexpr (AHEAD)
+            load(t + NW);               // the next row's loads run under this row
         int found = 0, my_e = -1, my_key = 0;
         float inv = 0.0f, top = 0.0f;
         int best = key[0];

@@ -35,6 +35,8 @@ def test_every_family_is_built(kernels):
     assert _count(kernels, "gemm_nt_kernel_lora") == 4 * 6 and _count(kernels, "gemm_nt_w4_lora") == 6
     assert _count(kernels, "gemm_nt_pp2_lora") == 2 * 6
     assert _count(kernels, "gemm_nt_kernel_routed") == 2 * 6 and _count(kernels, "gemm_nt_pp2_routed") == 3 * 6
+    # the 128 x 128 tile for MN-major weights, with adapters and routed
+    assert _count(kernels, "rows_tile") == 2 * 6
     assert not [n for n in kernels if re.search(r"gemm_nt_(kernel|pp2|w4)I", n)]    # the plain tiles are not
 
 
@@ -50,10 +52,13 @@ def test_lds_and_register_budget(kernels):
         assert m[".group_segment_fixed_size"] <= k.LDS_BYTES, n
         waves = -(-m[".max_flat_workgroup_size"] // 64)
         assert -(-waves // 4) * m[".vgpr_count"] <= k.REGS_PER_SIMD_LANE, n
-    two = [n for n in kernels if "gemm_nt_kernel_lora" in n and "Li4ELi2E" in n]    # the two-stage ring
-    assert len(two) == 6
+    # the two-stage ring and the tile for MN-major weights run two blocks a compute unit
+    two = [n for n in kernels if "gemm_nt_kernel_lora" in n and "Li4ELi2E" in n or "rows_tile" in n]
+    assert len(two) == 6 + 12
     for n in two:
-        assert 2 * 2 * kernels[n][".vgpr_count"] <= k.REGS_PER_SIMD_LANE, (n, kernels[n][".vgpr_count"])
+        waves = kernels[n][".max_flat_workgroup_size"] // 64
+        assert 2 * kernels[n][".group_segment_fixed_size"] <= k.LDS_BYTES, n
+        assert 2 * (waves // 4) * kernels[n][".vgpr_count"] <= k.REGS_PER_SIMD_LANE, (n, kernels[n][".vgpr_count"])
 
 
 def _registers(text):
@@ -83,7 +88,7 @@ def test_waits_before_results_are_stored(lib):
             if m:
                 name, recent = m.group(1), []
                 continue
-            if name is None or not ("lora_shrink" in name or "lora_grad" in name):
+            if name is None or not any(f in name for f in ("lora_shrink", "lora_grad", "rows_tile")):
                 continue
             s = line.split("//")[0].strip()
             if not s:
@@ -92,7 +97,8 @@ def test_waits_before_results_are_stored(lib):
             args = s[len(op):]
             recent = [(left - 1, r) for left, r in recent if left > 1]
             if op.startswith("v_mfma"):
-                recent.append((12, _registers(args.split(",")[0])))       # 8 passes and 3, at most
+                # 8 or 16 passes and 3, at most
+                recent.append((20 if "32x32" in op else 12, _registers(args.split(",")[0])))
                 checked += 1
             elif op == "s_nop":
                 n = int(args)
