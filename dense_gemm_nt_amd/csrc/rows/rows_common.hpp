@@ -10,8 +10,8 @@
 namespace gnt {
 
 // A projection with low-rank adapters: the tile's arguments plus the adapters.
-// low[s][m][rank_pad] holds K split s's part of row m's unscaled low-rank
-// product; up is [adapter][N][rank] (adapter a at a * up_stride elements, rows
+// low holds, in K split s's plane of low_stride values, row m's unscaled low-rank
+// product (its part) at m * rank_pad; up is [adapter][N][rank] (adapter a at a * up_stride elements, rows
 // of up_ld elements).
 struct LoraArgs : KernelArgs {
     const float *low;
@@ -19,6 +19,7 @@ struct LoraArgs : KernelArgs {
     const float *scale;
     const int32_t *ids;
     int64_t up_stride;
+    int64_t low_stride;
     int up_ld;
     int adapters;          // 0: no adapters, nothing is added
     int rank, rank_pad;    // rank_pad: rank rounded up to 16
@@ -346,7 +347,7 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                 const int m = r0 + fm * 32 + (lane & 31);
                 const float *src = p.low + (int64_t)m * p.rank_pad + rs + 8 * h;
                 for (int s = 1; s < p.low_splits; ++s) {
-                    src += (int64_t)p.M * p.rank_pad;
+                    src += p.low_stride;
                     v0 += *reinterpret_cast<const f32x4 *>(src);
                     v1 += *reinterpret_cast<const f32x4 *>(src + 4);
                 }

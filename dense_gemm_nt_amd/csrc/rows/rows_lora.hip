@@ -749,6 +749,39 @@ GradPlan plan_mn_major(int64_t M, int64_t N, int64_t K)
     return g;
 }
 
+// A product's rows in one launch, or in two: where the ping-pong tiles' last pass
+// over the machine is at most half full, the rows of the full passes, and then the
+// rest, with K splits that give the idle units a share.  5001 x 8192 x 8192 (640
+// tiles: two passes and a half) 642 us in one launch, 458 + 144 in two.
+struct Pieces {
+    Plan plan[2];
+    int64_t rows[2];
+    int count;
+};
+
+Pieces plan_pieces(int64_t M, int64_t N, int64_t K)
+{
+    Pieces s{};
+    s.plan[0] = plan_projection(M, N, K);
+    s.rows[0] = M;
+    s.count = 1;
+    const Plan &p = s.plan[0];
+    if (p.cfg != CFG_PP2_256x256 || p.splits != 1 || p.grid <= kNumCUs)
+        return s;
+    // passes of the machine, in k-slabs; a tile's start and end cost about 8
+    auto cost = [](const Plan &x) { return cdiv(x.grid, kNumCUs) * (x.kt_per_split + 8); };
+    const int64_t full = p.grid / kNumCUs * kNumCUs / p.tiles_n * 256;      // rows
+    if (full == 0 || full >= M)
+        return s;
+    Pieces t{};
+    t.plan[0] = make_plan(full, N, K, kPartialBytes, CFG_PP2_256x256, 1, 0);
+    t.plan[1] = plan_projection(M - full, N, K);
+    t.rows[0] = full;
+    t.rows[1] = M - full;
+    t.count = 2;
+    return t.plan[1].cfg == CFG_PP2_256x256 && cost(t.plan[0]) + cost(t.plan[1]) + 8 < cost(p) ? t : s;
+}
+
 lora_fn projection_fn(const Plan &p, int64_t M, int in_dtype, int out_dtype)
 {
     const bool rot = rotate_slabs(1, M);
@@ -866,22 +899,26 @@ bool has_adapters(int64_t adapters, int64_t rank) { return adapters > 0 && rank 
 
 struct ForwardWs {
     float *low;
-    ProjectionWs proj;
+    ProjectionWs proj[2];
 };
 
-ForwardWs carve_forward(Carver &c, const Plan &p, const ShrinkPlan &s, int64_t M, int64_t adapters, int64_t rank)
+ForwardWs carve_forward(Carver &c, const Pieces &p, const ShrinkPlan &s, int64_t M, int64_t adapters, int64_t rank)
 {
     ForwardWs w;
     w.low = c.take<float>(has_adapters(adapters, rank) ? (int64_t)s.splits * M * cdiv(rank, 16) * 16 : 0);
-    w.proj = carve_projection(c, p);
+    w.proj[0] = carve_projection(c, p.plan[0]);
+    w.proj[1] = w.proj[0];
+    if (p.count > 1)
+        w.proj[1] = carve_projection(c, p.plan[1]);
     return w;
 }
 
-void set_adapters(LoraArgs &a, const gemm_adapters_t *ad, const float *low, int low_splits, const uint16_t *up,
-                  int64_t up_stride, int64_t up_ld)
+void set_adapters(LoraArgs &a, const gemm_adapters_t *ad, const float *low, int low_splits, int64_t M,
+                  const uint16_t *up, int64_t up_stride, int64_t up_ld)
 {
     a.low = low;
     a.low_splits = low_splits;
+    a.low_stride = M * cdiv(ad->rank, 16) * 16;
     a.up = up;
     a.up_stride = up_stride;
     a.up_ld = (int)up_ld;
@@ -978,7 +1015,7 @@ gemm_status_t gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t num_a
     if (st != GEMM_OK || M == 0 || N == 0)
         return st;
     Carver c{nullptr};
-    carve_forward(c, plan_projection(M, N, K), plan_shrink(M, K, num_adapters, rank), M, num_adapters, rank);
+    carve_forward(c, plan_pieces(M, N, K), plan_shrink(M, K, num_adapters, rank), M, num_adapters, rank);
     *bytes = c.used;
     return GEMM_OK;
 }
@@ -1002,34 +1039,48 @@ gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, in
     if (K > 0 && ((st = check_operand(X, K, ldx)) != GEMM_OK || (st = check_operand(W, K, ldw)) != GEMM_OK ||
                   (st = check_adapters(adapters, N, K)) != GEMM_OK))
         return st;
-    const Plan p = plan_projection(M, N, K);
+    const Pieces p = plan_pieces(M, N, K);
     const ShrinkPlan s = plan_shrink(M, K, adapters->num_adapters, adapters->rank);
-    if (p.grid <= 0 || p.grid >= kMaxSize)
-        return GEMM_ERR_UNSUPPORTED;
+    for (int i = 0; i < p.count; ++i)
+        if (p.plan[i].grid <= 0 || p.plan[i].grid >= kMaxSize)
+            return GEMM_ERR_UNSUPPORTED;
     Carver c{static_cast<uint8_t *>(workspace)};
     const ForwardWs w = carve_forward(c, p, s, M, adapters->num_adapters, adapters->rank);
     if ((st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
         return st;
+    // (of two pieces only the second splits K)
+    const ProjectionWs &counted = w.proj[p.count - 1];
     LoraArgs a{};
-    a.A = static_cast<const uint16_t *>(X);
-    a.B = static_cast<const uint16_t *>(W);
-    a.lda = (int)ldx;
-    a.ldb = (int)ldw;
-    fill_projection(a, p, w.proj, Y, M, N, K, ldy, out_dtype, epi);
     hipError_t e;
     if (K > 0 && has_adapters(adapters->num_adapters, adapters->rank)) {
-        set_adapters(a, adapters, w.low, s.splits, static_cast<const uint16_t *>(adapters->B), adapters->b_stride,
+        set_adapters(a, adapters, w.low, s.splits, M, static_cast<const uint16_t *>(adapters->B), adapters->b_stride,
                      adapters->b_ld);
         ShrinkPair q{};
-        q.counters = w.proj.counters;
-        q.num_counters = w.proj.num_counters;
+        q.counters = counted.counters;
+        q.num_counters = counted.num_counters;
         add_shrink(q, s, shrink_args(adapters, X, M, K, ldx, adapters->A, adapters->a_stride, adapters->a_ld, w.low));
         e = run_shrink(s, q, s.splits, in_dtype, stream);
     } else {
-        e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
+        e = zero_fill(counted.counters, counted.num_counters, 4, stream);
     }
-    if (e == hipSuccess)
-        e = run_projection(projection_fn(p, M, in_dtype, out_dtype), p, a, out_dtype, stream);
+    int64_t row = 0;
+    for (int i = 0; i < p.count && e == hipSuccess; ++i) {
+        LoraArgs b = a;
+        b.A = static_cast<const uint16_t *>(X) + row * ldx;
+        b.B = static_cast<const uint16_t *>(W);
+        b.lda = (int)ldx;
+        b.ldb = (int)ldw;
+        if (b.adapters) {
+            b.ids += row;
+            b.low += row * b.rank_pad;
+        }
+        fill_projection(b, p.plan[i], w.proj[i], static_cast<uint8_t *>(Y) + row * ldy * size_of(out_dtype), p.rows[i], N,
+                        K, ldy, out_dtype, epi);
+        if (b.bias_along == GEMM_BIAS_M)
+            b.bias += row;
+        e = run_projection(projection_fn(p.plan[i], p.rows[i], in_dtype, out_dtype), p.plan[i], b, out_dtype, stream);
+        row += p.rows[i];
+    }
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
@@ -1127,7 +1178,7 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
                                            w.low_t));
         if (e == hipSuccess)
             e = run_shrink(w.u, u, w.u.splits + (grads ? w.t.splits : 0), in_dtype, stream);
-        set_adapters(a, adapters, w.low_u, w.u.splits, w.flip_a, R * K, R);
+        set_adapters(a, adapters, w.low_u, w.u.splits, M, w.flip_a, R * K, R);
     } else if (want_dx && e == hipSuccess) {
         e = zero_fill(w.proj.counters, w.proj.num_counters, 4, stream);
     }

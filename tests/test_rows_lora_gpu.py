@@ -60,6 +60,7 @@ SHAPES = [
     (2050, 4100, 72, 64, 9, "mixed"), (1024, 4096, 2560, 8, 2, "runs"), (130, 300, 264, 120, 2, "mixed"),
     (300, 77, 40, 16, 5, "none"), (256, 8192, 8192, 16, 30, "mixed"),
     (2100, 264, 1000, 128, 3, "mixed"), (2100, 136, 328, 16, 70, "wild"), (2049, 77, 4096, 24, 5, "runs"),
+    (2400, 8192, 2560, 16, 3, "wild"),       # full passes of the machine, and the rest with K splits
 ]
 
 
@@ -91,6 +92,17 @@ def test_forward_epilogue(M, beta, act):
     err = lora_bound(torch.zeros_like(y), sb, sl, K, K, R, dt, FP32) * 1.13
     err = err + 2.0 ** -20 * (sb + sl + old.double().abs() + bias.double().abs())
     check(got, ref, err, "epilogue %s" % act)
+
+
+def test_epilogue_along_rows_in_two_pieces():
+    import dense_gemm_nt_amd as g
+    M, N, K, R, L, dt = 2400, 8192, 2560, 8, 2, BF16
+    c = _case(M, N, K, R, L, "mixed", dt)
+    bias = randn(M, seed=7)
+    got = g.gemm_lora(**_dev(c), bias=bias.to(DEV), bias_along="m", out_dtype=FP32)
+    y, sb, sl = o.lora(**c)
+    err = lora_bound(torch.zeros_like(y), sb, sl, K, K, R, dt, FP32) + 2.0 ** -20 * (sb + sl + bias.double().abs()[:, None])
+    check(got, y + bias.double()[:, None], err, "row bias")
 
 
 def test_forward_strides_and_untouched_columns():
