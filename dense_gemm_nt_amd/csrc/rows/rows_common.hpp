@@ -5,14 +5,16 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../gemm_nt_common.hpp"
 
 namespace gnt {
 
 // A projection with low-rank adapters: the tile's arguments plus the adapters.
 // low holds, in K split s's plane of low_stride values, row m's unscaled low-rank
-// product (its part) at m * rank_pad; up is [adapter][N][rank] (adapter a at a * up_stride elements, rows
-// of up_ld elements).
+// product (its part) at m * rank_pad; up is [adapter][N][rank] (adapter a at
+// a * up_stride elements, rows of up_ld elements).
 struct LoraArgs : KernelArgs {
     const float *low;
     const uint16_t *up;
@@ -193,19 +195,21 @@ __device__ __forceinline__ u32x4 each16(u32x4 x, F f)
     return y;
 }
 
-// acc += up . (hi + lo) for the rows that are `own`, where up holds infinities or
-// NaNs (hi, lo are zero in the other rows): without any operand that could make
-// another row's zero into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the
-// infinity that is due in an own row and is 0 in the others', and a NaN (also
-// that of infinity times 0) is made as the sum of both infinities.  Rarely run,
-// and written for few registers: one operand pair at a time.
-template <int IN>
-__device__ __forceinline__ void add_special(f32x16 &acc, u32x4 up, u32x4 hi, u32x4 lo, bool own)
+// acc += x . (hi + lo) where x holds infinities or NaNs: as the sum of x's finite
+// values (its others as +-1 to 2, by their exponents' highest bit: an infinite
+// hi then stays one, and a NaN a NaN)
+// and of what its others make, without any operand that could make a zero of
+// another row, or lo's, into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the infinity
+// that is due and is 0 where hi is masked to 0; a NaN (also that of infinity times 0) is
+// made as the sum of both infinities.  Where not `own`, hi and lo are zeros that
+// are to add nothing.  mul(type, x, y) multiplies and adds to acc.  Rarely run, and
+// written for few registers: one operand pair at a time.
+template <int IN, typename F>
+__device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, u32x4 lo, bool own, F mul)
 {
     constexpr uint32_t exp = IN == IN_BF16 ? 0x7f80u : 0x7c00u, big = 0x7f00u;
     auto step = [&](auto f, auto g, uint32_t flip) {
-        const u32x4 x = each16(up, f), y = each16(hi, g) ^ flip;
-        acc = mfma32x32x16<IN_BF16>(x, y, acc);
+        mul(std::integral_constant<int, IN_BF16>{}, each16(x, f), each16(hi, g) ^ flip);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto is_nan = [](uint32_t v) { return (v & 0x7fffu) > exp ? big : 0u; };
@@ -213,17 +217,21 @@ __device__ __forceinline__ void add_special(f32x16 &acc, u32x4 up, u32x4 hi, u32
     auto inf = [](uint32_t v) { return (v & 0x7fffu) == exp ? (v & 0x8000u) | big : 0u; };
     auto sign = [](uint32_t v) { return v & 0x7fffu ? (v & 0x8000u) | big : 0u; };
     const uint32_t mine = own ? big : 0u;
-    auto row = [&](uint32_t) { return mine; };
+    auto all = [&](uint32_t) { return mine; };
     auto zero = [&](uint32_t v) { return v & 0x7fffu ? 0u : mine; };
     {
-        const u32x4 x = each16(up, [](uint32_t v) { return (v & exp) == exp ? 0u : v; });
-        acc = mfma32x32x16<IN>(x, hi, acc);
-        acc = mfma32x32x16<IN>(x, lo, acc);
+        constexpr uint32_t exps = exp << 16 | exp, lowest = exps & ~(exps << 1);
+        u32x4 y;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            y[d] = x[d] & ~((((x[d] & exps) + lowest) & 0x80008000u) >> 1);
+        mul(std::integral_constant<int, IN>{}, y, hi);
+        mul(std::integral_constant<int, IN>{}, y, lo);
         __builtin_amdgcn_sched_barrier(0);
     }
     step(inf, sign, 0u);
-    step(is_nan, row, 0u);
-    step(is_nan, row, 0x80008000u);
+    step(is_nan, all, 0u);
+    step(is_nan, all, 0x80008000u);
     step(is_inf, zero, 0u);
     step(is_inf, zero, 0x80008000u);
 }
@@ -418,7 +426,9 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                     for (int fn = 0; fn < FN; ++fn) {
                         int again = s;                    // (a load of its own: registers)
                         asm volatile("" : "+s"(again));
-                        add_special<IN>(acc[fn][fm], load_up(again, fn, rs), th, tl, own);
+                        add_special<IN>(load_up(again, fn, rs), th, tl, own, [&](auto type, u32x4 x, u32x4 y) {
+                            acc[fn][fm] = mfma32x32x16<type.value>(x, y, acc[fn][fm]);
+                        });
                     }
                 }
             }

@@ -12,6 +12,10 @@
 namespace gnt {
 
 constexpr int64_t kMaxSize = (int64_t)INT32_MAX;
+// A launch has fewer than 2^32 threads: blocks of at most 512, and 64 rows to
+// 256 threads of the low-rank products.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
 
 inline bool is_16bit(int dt) { return dt == GEMM_BF16 || dt == GEMM_FP16; }
 inline bool is_out(int dt) { return is_16bit(dt) || dt == GEMM_FP32; }

@@ -552,6 +552,18 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
                     const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
                     zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
                 }
+                // (an infinity in z times a value's second part, 0 or of the other
+                // sign, would be a NaN: such pieces are taken apart)
+                if (__builtin_amdgcn_ballot_w64((has_special<IN>(zf[0]) | has_special<IN>(zf[1])) != 0)) {
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            add_special<IN>(zf[j], vf[ks][r][0], vf[ks][r][1], true, [&](auto type, u32x4 x, u32x4 y) {
+                                acc[r][j] = mfma16x16x32<type.value>(y, x, acc[r][j]);
+                            });
+                    continue;
+                }
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -872,7 +884,7 @@ gemm_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t adapters, int
 {
     if (M < 0 || N < 0 || K < 0 || adapters < 0 || rank < 0)
         return GEMM_ERR_INVALID_ARG;
-    if (M >= kMaxSize || N >= kMaxSize || K >= kMaxSize || adapters >= kMaxSize || rank > 128 || rank % 8 || K % 8)
+    if (M >= kMaxRows || N >= kMaxSize || K >= kMaxSize || adapters >= kMaxSize || rank > 128 || rank % 8 || K % 8)
         return GEMM_ERR_UNSUPPORTED;
     return GEMM_OK;
 }
@@ -1042,7 +1054,7 @@ gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, in
     const Pieces p = plan_pieces(M, N, K);
     const ShrinkPlan s = plan_shrink(M, K, adapters->num_adapters, adapters->rank);
     for (int i = 0; i < p.count; ++i)
-        if (p.plan[i].grid <= 0 || p.plan[i].grid >= kMaxSize)
+        if (p.plan[i].grid <= 0 || p.plan[i].grid >= kMaxBlocks)
             return GEMM_ERR_UNSUPPORTED;
     Carver c{static_cast<uint8_t *>(workspace)};
     const ForwardWs w = carve_forward(c, p, s, M, adapters->num_adapters, adapters->rank);
@@ -1140,7 +1152,7 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
     BackwardWs w = carve_backward(c, M, N, K, L, R);
     if ((want_dx || (some && grads)) && (st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
         return st;
-    if (want_dx && (w.dx.plan.grid <= 0 || w.dx.plan.grid >= kMaxSize))
+    if (want_dx && (w.dx.plan.grid <= 0 || w.dx.plan.grid >= kMaxBlocks))
         return GEMM_ERR_UNSUPPORTED;
 
     hipError_t e = hipSuccess;

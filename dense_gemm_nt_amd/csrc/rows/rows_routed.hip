@@ -33,7 +33,7 @@ gemm_status_t launch(routed_fn fn, const RoutedArgs &a, int64_t tiles, hipStream
 {
     // whole runs of 256 blocks: the launch order permutes ids within them
     const int64_t grid = cdiv(tiles, 256) * 256;
-    if (grid >= kMaxSize)
+    if (grid >= kMaxBlocks)
         return GEMM_ERR_UNSUPPORTED;
     return fn(a, (unsigned)grid, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }

@@ -269,7 +269,13 @@ def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=
     k = routing.ids.shape[1]
     dev, index = _device(logits)
     ld = _matrix("logits", logits, T, E)
-    _on(index, ids=routing.ids, grad_weights=grad_weights, grad_loss=grad_loss)
+    for name, n in (("ids", T * k), ("weights", T * k), ("counts", E), ("tokens", 1)):
+        t = getattr(routing, name)
+        if t.dtype != (torch.float32 if name == "weights" else torch.int32) or t.numel() != n or \
+                not t.is_contiguous():
+            raise ValueError("routing.%s is not what route_topk gave" % name)
+    _on(index, ids=routing.ids, weights=routing.weights, counts=routing.counts, tokens=routing.tokens,
+        grad_weights=grad_weights, grad_loss=grad_loss)
     if grad_weights is not None and (grad_weights.dtype != torch.float32 or
                                      tuple(grad_weights.shape) != (T, k) or
                                      not grad_weights.is_contiguous()):

@@ -14,8 +14,9 @@
  * Storage, types, rounding: row-major with element strides, BF16 or FP16
  * operands (all of one call's 16-bit operands share the type), FP32 sums,
  * results rounded once to nearest even.  Limits as gemm_run's: sizes below
- * 2^31, leading dimensions of operands below 2^22 and multiples of 8, operand
- * bases 16-byte aligned.  For given arguments every call on the same device
+ * 2^31 (rows of gemm_run_lora and its backward below 2^30), fewer than 2^23
+ * output tiles, leading dimensions of operands below 2^22 and multiples of 8,
+ * operand bases 16-byte aligned.  For given arguments every call on the same device
  * returns the same bits.
  *
  * Workspaces: no handle; a call that needs one takes a device workspace of the
@@ -80,6 +81,7 @@ gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, in
  *   dX[m,:] = dY[m,:] W + s_a (dY[m,:] B_a) A_a          [M][K], dx_dtype
  *   dA_a    = s_a sum_{m: ids[m] = a} (dY[m,:] B_a)^T X[m,:]   [adapter][rank][K]
  *   dB_a    = s_a sum_{m: ids[m] = a} dY[m,:]^T (X[m,:] A_a^T) [adapter][N][rank]
+ * dY B_a and X A_a^T are FP32 sums and enter the second products as above.
  * dA and dB are contiguous, of grad_dtype, and written whole: adapters without
  * a row get zeros.  dX may be NULL (not computed), and so may dA and dB, both
  * or neither.  K % 8 == 0, N % 8 == 0 and num_adapters <= 1024 (else

@@ -53,6 +53,7 @@ def _lora(L, ad=None, epi=None, **kw):
     (dict(ldx=56), INVALID), (dict(ldw=56), INVALID), (dict(ldy=31), INVALID),
     (dict(ldx=68), MISALIGNED), (dict(x=P + 8), MISALIGNED), (dict(W=P + 2), MISALIGNED),
     (dict(y=P + 1), MISALIGNED), (dict(ldw=1 << 22), UNSUPPORTED), (dict(M=1 << 31), UNSUPPORTED),
+    (dict(M=1 << 30), UNSUPPORTED), (dict(M=1 << 29, N=1 << 17, ldy=1 << 17), UNSUPPORTED),    # launches too large
     (dict(), INVALID),                       # the workspace is missing
     (dict(ws=P, n=64), INVALID),             # or too small
     (dict(ws=P + 16, n=1 << 30), MISALIGNED),

@@ -245,6 +245,47 @@ def test_backward_keeps_broken_rows_apart():
     assert bool(torch.isfinite(ref["dA"][0][0]).all()) and bool(torch.isfinite(ref["dB"][0][0]).all())
 
 
+@pytest.mark.parametrize("M,R", [(150, 16), (150, 8), (700, 64)])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_backward_infinities_are_the_formulas(M, R, dt):
+    """An infinity gives infinities of the formula's signs, not NaNs."""
+    import dense_gemm_nt_amd as g
+    N, K, L = 264, 328, 4
+    c = _case(M, N, K, R, L, "mixed", dt)
+    dy = randn(M, N, seed=9, dtype=dt)
+    c["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    inf = float("inf")
+    c["x"][1, 5], dy[2, 7] = -inf, inf
+    c["x"][0, 9], dy[0, 11] = inf, float("nan")
+    got = g.gemm_lora_backward(dy.to(DEV), **_dev(c), dx_dtype=FP32)
+    ref = o.lora_backward(dy, **c)
+    for name, x in zip(("dx", "dA", "dB"), got):
+        r, x = ref[name][0], x.cpu()
+        assert torch.equal(x.isnan(), r.isnan()), name
+        assert torch.equal(x == inf, r == inf) and torch.equal(x == -inf, r == -inf), name
+    assert bool(ref["dB"][0][2].isinf().any()) and not bool(ref["dB"][0][2].isnan().any())
+    assert bool(ref["dA"][0][1].isinf().any()) and not bool(ref["dA"][0][1].isnan().any())
+
+
+def test_forward_infinity_times_infinity():
+    """An infinite row meets an infinite adapter: the formula's infinities."""
+    import dense_gemm_nt_amd as g
+    M, N, K, R, L = 40, 136, 64, 8, 2
+    c = _case(M, N, K, R, L, "mixed", BF16)
+    c["ids"][:2] = torch.tensor([1, 1], dtype=torch.int32)
+    c["x"][0, 3] = float("inf")
+    c["A"][1, 1:] = 0.0
+    c["A"][1, 1:, 3] = 1.0                 # all low-rank values of row 0 infinite
+    c["A"][1, 0, 3] = 1.0
+    c["B"][1].abs_().add_(0.01)
+    c["W"].abs_().add_(0.01)
+    c["B"][1, 5, 0] = float("inf")
+    c["scale"].abs_().add_(0.1)
+    y = o.lora(**c)[0]
+    got = g.gemm_lora(**_dev(c), out_dtype=FP32).cpu()
+    assert torch.equal(got.isnan(), y.isnan()) and torch.equal(got.isinf(), y.isinf())
+
+
 def test_same_bits_and_other_streams():
     import dense_gemm_nt_amd as g
     c = _dev(_case(300, 520, 1032, 16, 5, "mixed", BF16))

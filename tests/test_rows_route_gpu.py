@@ -214,3 +214,18 @@ def test_python_refusals():
                 lambda: g.route_topk_backward(x, g.route_topk(x, 2), grad_loss=torch.ones(2, device=DEV))):
         with pytest.raises((ValueError, TypeError, g.GemmError)):
             bad()
+
+
+def test_backward_refuses_a_routing_of_other_making():
+    import dense_gemm_nt_amd as g
+    x = torch.randn(6, 9, device=DEV)
+    r = g.route_topk(x, 2)
+    for name in ("ids", "counts", "tokens"):
+        with pytest.raises(ValueError):
+            g.route_topk_backward(x, r._replace(**{name: getattr(r, name).long()}))
+    with pytest.raises(ValueError):
+        g.route_topk_backward(x, r._replace(weights=r.weights.t().contiguous().t()))
+    with pytest.raises(ValueError):
+        g.route_topk_backward(x, r._replace(weights=r.weights[:5]))
+    with pytest.raises(ValueError):
+        g.route_topk_backward(x, r._replace(counts=r.counts.cpu()))
