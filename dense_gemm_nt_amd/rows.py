@@ -16,7 +16,6 @@ tensors then hold.
 from __future__ import annotations
 
 import collections
-import contextlib
 import ctypes
 import functools
 
@@ -43,21 +42,17 @@ def _on(index, **tensors):
             raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
 
 
-def _device(t):
-    """(device, index) of a CUDA tensor."""
+# A small call's time is the host's, so the calls below ask torch for the current
+# device and stream as plain integers (a third of a microsecond for both, where
+# the stream object alone takes more than one), read what they check from the tensors
+# directly, and make error messages only for errors.
+
+def _index(t):
+    """The device index of a CUDA tensor."""
     index = t.get_device()
     if index < 0:
         raise ValueError("expected CUDA tensors, got one on %s" % t.device)
-    return t.device, index
-
-
-def _current(index):
-    """A context in which device `index` is current (none needed where it is)."""
-    import torch
-    return _NOTHING if torch.cuda.current_device() == index else torch.cuda.device(index)
-
-
-_NOTHING = contextlib.nullcontext()
+    return index
 
 
 def _matrix(name, X, rows, cols):
@@ -75,47 +70,35 @@ def _vector(name, v, n, dtype):
         raise ValueError("%s must be a contiguous %s vector of %d values" % (name, dtype, n))
 
 
-def _out(name, out, shape, dtype, dev):
-    import torch
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _out(name, out, shape, dev):
     if out.shape != shape or out.device != dev:
         raise ValueError("%s must be %s on %s" % (name, list(shape), dev))
     return out
 
 
 # (a function of the sizes only; calls repeat them)
-_workspace_bytes = functools.lru_cache(maxsize=256)(_rows.workspace_bytes)
-
-
-def _workspace(fn, sizes, dev, what):
-    """The call's device workspace (or None) and its size."""
-    import torch
-    st, n = _workspace_bytes(fn, *sizes)
-    _lib.check(st, what)
-    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    return ws, n
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(fn, *sizes):
+    st, n = _rows.workspace_bytes(fn, *sizes)
+    if st:
+        _lib.check(st, "%s%s" % (fn, sizes))
+    return n
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
-def _stream(index):
-    import torch
-    return torch.cuda.current_stream(index).cuda_stream
-
-
-def _adapters(A, B, ids, scale, M, N, K, dtype, index):
+def _adapters(A, B, ids, scale, M, N, K, dtype, index, torch):
     """A checked GemmAdapters of A [L, R, K], B [L, N, R], ids [M], scale [L]."""
-    import torch
     if A.dim() != 3 or B.shape != (A.shape[0], N, A.shape[1]) or A.shape[2] != K:
         raise ValueError("adapters must be A [L, R, %d] and B [L, %d, R], got %s and %s"
                          % (K, N, tuple(A.shape), tuple(B.shape)))
     L, R, _ = A.shape
     if A.dtype != dtype or B.dtype != dtype:
         raise TypeError("the adapters must have the operands' dtype %s" % dtype)
-    _on(index, A=A, B=B, ids=ids, scale=scale)
+    if not A.get_device() == B.get_device() == ids.get_device() == scale.get_device() == index:
+        _on(index, A=A, B=B, ids=ids, scale=scale)
     _vector("ids", ids, M, torch.int32)
     _vector("scale", scale, L, torch.float32)
     a_step, a_ld, a_unit = A.stride()
@@ -144,29 +127,40 @@ def gemm_lora(x, W, A, B, ids, scale, out=None, out_dtype=None, alpha=1.0, beta=
         raise ValueError("x and W must be 2-D")
     M, K = x.shape
     N = W.shape[0]
-    dev, index = _device(x)
-    if x.dtype != W.dtype:
+    index = _index(x)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return gemm_lora(x, W, A, B, ids, scale, out, out_dtype, alpha, beta, bias, bias_along,
+                             activation)
+    dt = x.dtype
+    if W.dtype != dt:
         raise TypeError("x and W must share a dtype")
-    _on(index, W=W, bias=bias)
+    if W.get_device() != index or bias is not None:
+        _on(index, W=W, bias=bias)
     ldx, ldw = _matrix("x", x, M, K), _matrix("W", W, N, K)
-    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, index)
-    if beta != 0.0 and out is None:
-        raise ValueError("beta != 0 reads the prior y: pass it as `out`")
-    out = _out("out", out, (M, N), out_dtype or x.dtype, dev)
-    ldy = _matrix("out", out, M, N)
+    ad = _adapters(A, B, ids, scale, M, N, K, dt, index, torch)
+    if out is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 reads the prior y: pass it as `out`")
+        out = torch.empty((M, N), dtype=out_dtype or dt, device=x.device)
+        ldy = N
+    else:
+        ldy = _matrix("out", _out("out", out, (M, N), x.device), M, N)
     epi = None
     if not (alpha == 1.0 and beta == 0.0 and bias is None and activation == "none"):
         if bias is not None:
             _vector("bias", bias, N if bias_along == "n" else M, torch.float32)
         epi = _lib.epilogue(alpha, beta, bias.data_ptr() if bias is not None else 0,
                             bias_along if bias is not None else "none", activation)
-    with _current(index):
-        ws, n = _workspace("gemm_lora_workspace", (M, N, K, ad.num_adapters, ad.rank), dev, "gemm_lora")
-        st = _rows.lib().gemm_run_lora(
-            x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy, _code(x.dtype),
-            _code(out.dtype), ctypes.byref(ad), ctypes.byref(epi) if epi is not None else None,
-            _ptr(ws), n, _stream(index))
-    _lib.check(st, "gemm_lora(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, ad.num_adapters, ad.rank))
+    L, R = A.shape[:2]
+    n = _workspace_bytes("gemm_lora_workspace", M, N, K, L, R)
+    ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+    st = _rows.lib().gemm_run_lora(
+        x.data_ptr(), W.data_ptr(), out.data_ptr(), M, N, K, ldx, ldw, ldy, _code(dt), _code(out.dtype),
+        ctypes.byref(ad), ctypes.byref(epi) if epi is not None else None, _ptr(ws), n,
+        torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "gemm_lora(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, L, R))
     return out
 
 
@@ -182,24 +176,31 @@ def gemm_lora_backward(dy, x, W, A, B, ids, scale, grad_dtype=None, dx_dtype=Non
         raise ValueError("dy, x and W must be 2-D")
     M, K = x.shape
     N = W.shape[0]
-    dev, index = _device(x)
-    if x.dtype != W.dtype or dy.dtype != x.dtype:
+    index, dev = _index(x), x.device
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return gemm_lora_backward(dy, x, W, A, B, ids, scale, grad_dtype, dx_dtype, need_dx,
+                                      need_adapters)
+    dt = x.dtype
+    if W.dtype != dt or dy.dtype != dt:
         raise TypeError("dy, x and W must share a dtype")
-    _on(index, dy=dy, W=W)
+    if not dy.get_device() == W.get_device() == index:
+        _on(index, dy=dy, W=W)
     lddy, ldx, ldw = _matrix("dy", dy, M, N), _matrix("x", x, M, K), _matrix("W", W, N, K)
-    ad = _adapters(A, B, ids, scale, M, N, K, x.dtype, index)
-    L, R = ad.num_adapters, ad.rank
-    gdt = grad_dtype or torch.float32
-    dx = torch.empty((M, K), dtype=dx_dtype or x.dtype, device=dev) if need_dx else None
+    ad = _adapters(A, B, ids, scale, M, N, K, dt, index, torch)
+    L, R = A.shape[:2]
+    gdt, xdt = grad_dtype or torch.float32, dx_dtype or dt
+    dx = torch.empty((M, K), dtype=xdt, device=dev) if need_dx else None
     dA = torch.empty((L, R, K), dtype=gdt, device=dev) if need_adapters else None
     dB = torch.empty((L, N, R), dtype=gdt, device=dev) if need_adapters else None
-    with _current(index):
-        ws, n = _workspace("gemm_lora_backward_workspace", (M, N, K, L, R), dev, "gemm_lora_backward")
-        st = _rows.lib().gemm_run_lora_backward(
-            dy.data_ptr(), x.data_ptr(), W.data_ptr(), _ptr(dx), _ptr(dA) or None, _ptr(dB) or None,
-            M, N, K, lddy, ldx, ldw, K, _code(x.dtype), _code(dx_dtype or x.dtype), _code(gdt),
-            ctypes.byref(ad), _ptr(ws), n, _stream(index))
-    _lib.check(st, "gemm_lora_backward(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, L, R))
+    n = _workspace_bytes("gemm_lora_backward_workspace", M, N, K, L, R)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    st = _rows.lib().gemm_run_lora_backward(
+        dy.data_ptr(), x.data_ptr(), W.data_ptr(), _ptr(dx), _ptr(dA) or None, _ptr(dB) or None, M, N,
+        K, lddy, ldx, ldw, K, _code(dt), _code(xdt), _code(gdt), ctypes.byref(ad), _ptr(ws), n,
+        torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "gemm_lora_backward(M=%d, N=%d, K=%d, L=%d, R=%d)" % (M, N, K, L, R))
     return dx, dA, dB
 
 
@@ -211,10 +212,6 @@ def _mask(mask, T):
             not mask.is_contiguous():
         raise ValueError("mask must be a contiguous bool or uint8 vector of %d values" % T)
     return mask
-
-
-def _c_routing(r):
-    return _rows.GemmRouting(*(_ptr(getattr(r, n)) for n, _ in _rows.GemmRouting._fields_))
 
 
 def route_topk(logits, top_k, mask=None, renormalize=True):
@@ -230,30 +227,32 @@ def route_topk(logits, top_k, mask=None, renormalize=True):
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
     k = int(top_k)
-    dev, index = _device(logits)
+    index = _index(logits)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return route_topk(logits, k, mask, renormalize)
     ld = _matrix("logits", logits, T, E)
-    mask = _mask(mask, T)
-    _on(index, mask=mask)
-    # one allocation for the integers and one for the rest: allocations are most of a
-    # small call's time on the host
-    n_pairs = T * max(k, 0)
-    with _current(index):
-        ws, n = _workspace("gemm_route_workspace", (T, E, k), dev, "route_topk")
-        ints = torch.empty(2 * n_pairs + 2 * E + 2, dtype=torch.int32, device=dev)
-        reals = torch.empty(n_pairs + 1, dtype=torch.float32, device=dev)
-        ids, order, counts, offsets, tokens = ints.split_with_sizes((n_pairs, n_pairs, E, E + 1, 1))
-        weights, loss = reals.split_with_sizes((n_pairs, 1))
-        p, q = ints.data_ptr(), reals.data_ptr()
-        at = p + 8 * n_pairs
-        c_out = _rows.GemmRouting(p, q, at, at + 4 * E, p + 4 * n_pairs, at + 8 * E + 4,
-                                  q + 4 * n_pairs)
-        r = Routing(ids.view(T, k), weights.view(T, k), counts, offsets, order, tokens,
-                    loss.view(()), bool(renormalize))
-        st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k,
-                                        int(r.renormalize), _code(logits.dtype),
-                                        ctypes.byref(c_out), _ptr(ws), n, _stream(index))
-    _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
-    return r
+    if mask is not None:
+        _on(index, mask=_mask(mask, T))
+    n = _workspace_bytes("gemm_route_workspace", T, E, k)
+    # One allocation, the workspace first (of the order of the results in size: it
+    # stays with them): each would be a tenth of a small call's time.
+    nk, words = T * k, n // 4
+    buf = torch.empty(words + 3 * nk + 2 * E + 3, dtype=torch.int32, device=logits.device)
+    _, ids, order, weights, counts, offsets, tokens, loss = buf.split_with_sizes(
+        (words, nk, nk, nk, E, E + 1, 1, 1))
+    ws = buf.data_ptr()
+    p = ws + n
+    at = p + 12 * nk
+    c_out = _rows.GemmRouting(p, p + 8 * nk, at, at + 4 * E, p + 4 * nk, at + 8 * E + 4, at + 8 * E + 8)
+    st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k, 1 if renormalize else 0,
+                                    _code(logits.dtype), ctypes.byref(c_out), ws, n,
+                                    torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
+    f32 = torch.float32
+    return Routing(ids.view(T, k), weights.view(f32).view(T, k), counts, offsets, order, tokens,
+                   loss.view(f32).view(()), bool(renormalize))
 
 
 def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=None):
@@ -267,30 +266,39 @@ def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=
         raise ValueError("routing does not belong to these logits")
     T, E = logits.shape
     k = routing.ids.shape[1]
-    dev, index = _device(logits)
+    index = _index(logits)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return route_topk_backward(logits, routing, grad_weights, grad_loss, out)
     ld = _matrix("logits", logits, T, E)
-    for name, n in (("ids", T * k), ("weights", T * k), ("counts", E), ("tokens", 1)):
-        t = getattr(routing, name)
-        if t.dtype != (torch.float32 if name == "weights" else torch.int32) or t.numel() != n or \
-                not t.is_contiguous():
-            raise ValueError("routing.%s is not what route_topk gave" % name)
-    _on(index, ids=routing.ids, weights=routing.weights, counts=routing.counts, tokens=routing.tokens,
-        grad_weights=grad_weights, grad_loss=grad_loss)
+    ids, weights, counts, _, _, tokens, _, renormalize = routing
+    for t, n, dt in ((ids, T * k, torch.int32), (weights, T * k, torch.float32), (counts, E, torch.int32),
+                     (tokens, 1, torch.int32)):
+        if t.dtype != dt or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+            raise ValueError("the routing is not what route_topk gave for these logits")
+    if grad_weights is not None or grad_loss is not None:
+        _on(index, grad_weights=grad_weights, grad_loss=grad_loss)
     if grad_weights is not None and (grad_weights.dtype != torch.float32 or
                                      tuple(grad_weights.shape) != (T, k) or
                                      not grad_weights.is_contiguous()):
         raise ValueError("grad_weights must be contiguous float32 [%d, %d]" % (T, k))
     if grad_loss is not None and (grad_loss.dtype != torch.float32 or grad_loss.numel() != 1):
         raise ValueError("grad_loss must be one float32 value")
-    out = _out("out", out, (T, E), logits.dtype, dev)
-    if out.dtype != logits.dtype:
-        raise TypeError("out must have the logits' dtype")
-    with _current(index):
-        st = _rows.lib().gemm_run_route_backward(
-            logits.data_ptr(), ctypes.byref(_c_routing(routing)), _ptr(grad_weights), _ptr(grad_loss),
-            out.data_ptr(), T, E, ld, _matrix("out", out, T, E), k, int(routing.renormalize),
-            _code(logits.dtype), _stream(index))
-    _lib.check(st, "route_topk_backward(T=%d, E=%d, k=%d)" % (T, E, k))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+        ldd = E
+    else:
+        ldd = _matrix("out", _out("out", out, (T, E), logits.device), T, E)
+        if out.dtype != logits.dtype:
+            raise TypeError("out must have the logits' dtype")
+    c_in = _rows.GemmRouting(ids.data_ptr(), weights.data_ptr(), counts.data_ptr(), None, None,
+                             tokens.data_ptr(), None)
+    st = _rows.lib().gemm_run_route_backward(
+        logits.data_ptr(), ctypes.byref(c_in), _ptr(grad_weights), _ptr(grad_loss), out.data_ptr(), T, E,
+        ld, ldd, k, 1 if renormalize else 0, _code(logits.dtype),
+        torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "route_topk_backward(T=%d, E=%d, k=%d)" % (T, E, k))
     return out
 
 
@@ -307,28 +315,39 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
                          % (tuple(x.shape), tuple(W.shape)))
     S, K = x.shape
     E, N, _ = W.shape
-    dev, index = _device(x)
-    if x.dtype != W.dtype:
+    index = _index(x)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return gemm_routed(x, W, offsets, out, out_dtype)
+    dt = x.dtype
+    if W.dtype != dt:
         raise TypeError("x and W must share a dtype")
-    _on(index, W=W, offsets=offsets)
+    if not W.get_device() == offsets.get_device() == index:
+        _on(index, W=W, offsets=offsets)
     _vector("offsets", offsets, E + 1, torch.int32)
     ldx = _matrix("x", x, S, K)
+    w_stride, w_row, w_col = W.stride()
     if W.numel() == 0:
         layout, ldw = _lib.GEMM_K_MAJOR, max(K, 1)
-    elif W.stride(2) == 1 and (N == 1 or W.stride(1) >= K):
-        layout, ldw = _lib.GEMM_K_MAJOR, W.stride(1) if N > 1 else max(K, W.stride(1))
-    elif W.stride(1) == 1 and (K == 1 or W.stride(2) >= N):
-        layout, ldw = _lib.GEMM_MN_MAJOR, W.stride(2) if K > 1 else max(N, W.stride(2))
+    elif w_col == 1 and (N == 1 or w_row >= K):
+        layout, ldw = _lib.GEMM_K_MAJOR, w_row if N > 1 else max(K, w_row)
+    elif w_row == 1 and (K == 1 or w_col >= N):
+        layout, ldw = _lib.GEMM_MN_MAJOR, w_col if K > 1 else max(N, w_col)
     else:
-        raise ValueError("W's strides %s are neither K-major nor MN-major" % (tuple(W.stride()),))
-    tail = _rows.GEMM_TAIL_ZERO if out is None else _rows.GEMM_TAIL_KEEP
-    out = _out("out", out, (S, N), out_dtype or x.dtype, dev)
-    with _current(index):
-        st = _rows.lib().gemm_run_routed(
-            x.data_ptr(), W.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, ldx, ldw,
-            W.stride(0) if E > 1 else 0, _matrix("out", out, S, N), layout, _code(x.dtype),
-            _code(out.dtype), tail, _stream(index))
-    _lib.check(st, "gemm_routed(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
+        raise ValueError("W's strides %s are neither K-major nor MN-major" % (W.stride(),))
+    if out is None:
+        tail = _rows.GEMM_TAIL_ZERO
+        out = torch.empty((S, N), dtype=out_dtype or dt, device=x.device)
+        ldc = N
+    else:
+        tail = _rows.GEMM_TAIL_KEEP
+        ldc = _matrix("out", _out("out", out, (S, N), x.device), S, N)
+    st = _rows.lib().gemm_run_routed(
+        x.data_ptr(), W.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, ldx, ldw,
+        w_stride if E > 1 else 0, ldc, layout, _code(dt), _code(out.dtype), tail,
+        torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "gemm_routed(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
     return out
 
 
@@ -342,19 +361,23 @@ def gemm_routed_wgrad(dy, x, offsets, out_dtype=None):
                          % (tuple(dy.shape), tuple(x.shape)))
     S, K = x.shape
     N = dy.shape[1]
-    dev, index = _device(x)
+    index = _index(x)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return gemm_routed_wgrad(dy, x, offsets, out_dtype)
     if x.dtype != dy.dtype:
         raise TypeError("dy and x must share a dtype")
     if offsets.dim() != 1 or offsets.shape[0] < 1:
         raise ValueError("offsets must be [E + 1]")
     E = offsets.shape[0] - 1
-    _on(index, dy=dy, offsets=offsets)
+    if not dy.get_device() == offsets.get_device() == index:
+        _on(index, dy=dy, offsets=offsets)
     _vector("offsets", offsets, E + 1, torch.int32)
     lddy, ldx = _matrix("dy", dy, S, N), _matrix("x", x, S, K)
-    out = torch.empty((E, N, K), dtype=out_dtype or x.dtype, device=dev)
-    with _current(index):
-        st = _rows.lib().gemm_run_routed_wgrad(
-            dy.data_ptr(), x.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, lddy, ldx,
-            _code(x.dtype), _code(out.dtype), _stream(index))
-    _lib.check(st, "gemm_routed_wgrad(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
+    out = torch.empty((E, N, K), dtype=out_dtype or x.dtype, device=x.device)
+    st = _rows.lib().gemm_run_routed_wgrad(
+        dy.data_ptr(), x.data_ptr(), out.data_ptr(), offsets.data_ptr(), S, N, K, E, lddy, ldx,
+        _code(x.dtype), _code(out.dtype), torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "gemm_routed_wgrad(S=%d, N=%d, K=%d, E=%d)" % (S, N, K, E))
     return out
