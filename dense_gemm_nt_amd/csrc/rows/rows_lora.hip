@@ -992,10 +992,13 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.counts = c.take<int32_t>(adapters);
     g.offsets = c.take<int32_t>(adapters + 1);
     g.order = c.take<int32_t>(M);
-    // stretches so long that column tiles x stretches give about four blocks a
-    // compute unit, and no longer: each stretch writes a partial sum
+    // stretches so long that column tiles x stretches give about two blocks a
+    // compute unit, and no longer: each stretch writes a partial sum (gradients and
+    // their sums with two against four: 8192 rows, 12288 columns, rank 32 76 us
+    // against 83; 5918, 2256, 64 46 against 66; 2048, 4096, 16 17 against 23; but
+    // 7164, 10328, 24 66 against 61)
     const int64_t tiles = cdiv(K, 128) + cdiv(N, 128);
-    const int64_t want = std::max<int64_t>(1, 4 * kNumCUs / tiles);
+    const int64_t want = std::max<int64_t>(1, 2 * kNumCUs / tiles);
     g.chunk = (int)std::max<int64_t>(64, cdiv(cdiv(M, want), 64) * 64);
     g.max_stretches = (int)(M / g.chunk + std::min<int64_t>(adapters, M));
     g.stretches = c.take<Stretch>(g.max_stretches);

@@ -30,6 +30,7 @@ CASES = [
     (1, 1, 1, 8, "one"), (1, 5, 130, 72, "one"), (40, 8, 300, 136, "skew"), (512, 64, 264, 200, "skew"),
     (600, 9, 1000, 64, "skew"), (700, 7, 129, 328, "wild"), (3000, 16, 520, 264, "skew"), (2000, 4, 700, 1032, "late"),
     (1500, 3, 256, 512, "one"), (900, 130, 136, 64, "skew"), (64, 1024, 40, 16, "skew"), (333, 2, 77, 40, "wild"),
+    (1500, 3, 8200, 264, "one"), (2500, 3, 8300, 72, "skew"), (2500, 3, 8204, 136, "late"), (2500, 4, 8200, 40, "wild"),
 ]
 
 
