@@ -454,21 +454,80 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
     }
 }
 
+// A z tile of the gradients' products in LDS: 64 rows of 128 columns, 256 bytes a
+// row; 32-byte pieces of a row are permuted by the row, so that the 16 rows of
+// a transposing read fall into different banks.
+constexpr int kGradRows = 64, kGradCols = 128;
+
+__device__ __forceinline__ int z_key(int row) { return (row & 3) | ((row >> 3) & 1) << 2; }
+
+// This thread's four pieces of a tile: row tid / 16 + 16 i, chunk tid % 16 of 16 bytes.
+__device__ __forceinline__ void store_z(uint8_t *zs, const u32x4 (&zr)[4], int tid)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (tid >> 4) + 16 * i, c = tid & 15;
+        *reinterpret_cast<u32x4 *>(zs + row * 256 + ((((c >> 1) ^ z_key(row)) << 1) | (c & 1)) * 16) = zr[i];
+    }
+}
+
+// acc += v z over a tile's rows 32 ks .. +32, read transposed (ds_read_b64_tr_b16):
+// acc[r][j] holds ranks 16 r .. +16 of columns 32 wave + 16 j .. +16.  vf: rank
+// 16 r + lane % 16, rows 32 ks + 8 (lane / 16) .. +8, of both parts.
+template <int IN, int RT>
+__device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x4 (&vf)[RT][2], f32x4 (&acc)[RT][2],
+                                           int wave, int lane)
+{
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4s lds_v4s;
+    u32x4 zf[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        v4s got[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = 32 * ks + 8 * (lane >> 4) + 4 * half + ((lane & 15) >> 2);
+            const uint8_t *a = zs + row * 256 + ((2 * wave + j) ^ z_key(row)) * 32 + (lane & 3) * 8;
+            got[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)a);
+        }
+        const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
+        zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
+    }
+    // (an infinity in z times a value's second part, 0 or of the other sign, would
+    // be a NaN: such pieces are taken apart)
+    if (__builtin_amdgcn_ballot_w64((has_special<IN>(zf[0]) | has_special<IN>(zf[1])) != 0)) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                add_special<IN>(zf[j], vf[r][0], vf[r][1], true, [&](auto type, u32x4 x, u32x4 y) {
+                    acc[r][j] = mfma16x16x32<type.value>(y, x, acc[r][j]);
+                });
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            acc[r][0] = mfma16x16x32<IN>(vf[r][h], zf[0], acc[r][0]);
+            acc[r][1] = mfma16x16x32<IN>(vf[r][h], zf[1], acc[r][1]);
+        }
+}
+
 // part[stretch][r][c] = sum over the stretch's rows m of s_a v[m][r] z[m][c]:
 // the contraction runs over rows, so z's tile (64 rows of 128 columns, gathered
-// by the rows' order) is staged in LDS as it lies and read back transposed
-// (ds_read_b64_tr_b16); v comes packed (lora_pack).  Bytes bound it: z is read
+// by the rows' order) is staged in LDS as it lies and read back transposed;
+// v comes packed (lora_pack).  Bytes bound it: z is read
 // once, in whole 256-byte row pieces, the next tile's loads in flight while a
 // tile is multiplied, the order of the one after that already there.  Sorted into
 // stretches of one adapter, partial sums need no atomics.
 template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {
-    constexpr int ROWS = 64, COLS = 128;
-    __shared__ __attribute__((aligned(16))) uint8_t zs[2][ROWS * COLS * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t zs[2][kGradRows * 256];
     const int w = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int c0 = blockIdx.x * COLS;
+    const int c0 = blockIdx.x * kGradCols;
     if (c0 >= p.cols[w])
         return;
     const Stretch st = p.stretches[blockIdx.y];
@@ -482,7 +541,6 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 #pragma unroll
         for (int r = 0; r < RT; ++r)
             acc[r][0] = acc[r][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        // this thread's four pieces of a z tile: row tid / 16 + 16 i, chunk tid % 16
         int row_at[4];
         u32x4 zr[4];
         auto load_order = [&](int at) {
@@ -502,21 +560,12 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
         };
         load_order(st.first);
         load();
-        load_order(st.first + ROWS);
+        load_order(st.first + kGradRows);
         int turn = 0;
-        for (int at = st.first; at < st.end; at += ROWS, turn ^= 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (tid >> 4) + 16 * i, c = tid & 15;
-                // 32-byte pieces of a row permuted by the row, so that the 16
-                // rows of a transposing read fall into different banks
-                const int key = (row & 3) | ((row >> 3) & 1) << 2;
-                *reinterpret_cast<u32x4 *>(zs[turn] + row * 256 + ((((c >> 1) ^ key) << 1) | (c & 1)) * 16) = zr[i];
-            }
+        for (int at = st.first; at < st.end; at += kGradRows, turn ^= 1) {
+            store_z(zs[turn], zr, tid);
             load();
-            load_order(at + 2 * ROWS);
-            // the packed values of this tile's rows: rank 16 r + lane % 16, rows
-            // 32 ks + 8 (lane / 16) .. +8
+            load_order(at + 2 * kGradRows);
             const uint16_t *v = p.pack[w] + (int64_t)(rg + (lane & 15)) * p.max_packed + st.packed + (at - st.first) +
                                 8 * (lane >> 4);
             u32x4 vf[2][RT][2];
@@ -532,46 +581,9 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
             // (a tile's buffer is written again two turns later, after the barrier
             // of the turn between, which follows this turn's reads)
             __syncthreads();
-            typedef short v4s __attribute__((ext_vector_type(4)));
-            typedef __attribute__((address_space(3))) v4s lds_v4s;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                // columns 32 wave + 16 j + lane % 16, rows 32 ks + 8 (lane / 16) .. +8
-                u32x4 zf[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    v4s got[2];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int row = 32 * ks + 8 * (lane >> 4) + 4 * half + ((lane & 15) >> 2);
-                        const int key = (row & 3) | ((row >> 3) & 1) << 2;
-                        const int piece = 2 * wave + j;
-                        const uint8_t *a = zs[turn] + row * 256 + (piece ^ key) * 32 + (lane & 3) * 8;
-                        got[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)a);
-                    }
-                    const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
-                    zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
-                }
-                // (an infinity in z times a value's second part, 0 or of the other
-                // sign, would be a NaN: such pieces are taken apart)
-                if (__builtin_amdgcn_ballot_w64((has_special<IN>(zf[0]) | has_special<IN>(zf[1])) != 0)) {
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            add_special<IN>(zf[j], vf[ks][r][0], vf[ks][r][1], true, [&](auto type, u32x4 x, u32x4 y) {
-                                acc[r][j] = mfma16x16x32<type.value>(y, x, acc[r][j]);
-                            });
-                    continue;
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        acc[r][0] = mfma16x16x32<IN>(vf[ks][r][h], zf[0], acc[r][0]);
-                        acc[r][1] = mfma16x16x32<IN>(vf[ks][r][h], zf[1], acc[r][1]);
-                    }
-            }
+            for (int ks = 0; ks < 2; ++ks)
+                multiply_z<IN, RT>(zs[turn], ks, vf[ks], acc, wave, lane);
         }
         mfma_settle();
         float *out = p.part[w] + (int64_t)blockIdx.y * p.rank_pad * p.cols[w];
@@ -596,6 +608,147 @@ __device__ __forceinline__ void store_grad(void *out, int64_t at, float v, int d
         static_cast<float *>(out)[at] = v;
     else
         static_cast<uint16_t *>(out)[at] = dtype == GEMM_BF16 ? to16<IN_BF16>(v) : to16<IN_FP16>(v);
+}
+
+// The gradients for few rows (few_rows), in one launch where grouping the rows,
+// packing v, the products and their sums are four: a block finds the rows of its
+// adapter itself and takes them all.  v is staged for as many rows as kFewStage
+// values hold, scaled, in FP32; a lane splits what it multiplies.
+constexpr int kFewRows = 1024, kFewStage = 8192;
+
+// Measured for three adapters, in us: 777 rows, 6144 columns, rank 8 13 against 20
+// in four launches; 731, 4448, 24 26 against 24; with few rows three launches' time
+// less (18 rows, all of a backward call: 31 against 42).
+__host__ __device__ constexpr bool few_rows(int64_t M, int64_t rank_pad)
+{
+    return M <= kFewRows && M * rank_pad <= 16 * kFewRows;
+}
+
+template <int IN, int RT>
+__global__ __launch_bounds__(256) void lora_grad_few(GradArgs p)
+{
+    constexpr int RANKS = 16 * RT, GROUP = kFewStage / RANKS, PITCH = RANKS + 1;
+    __shared__ __attribute__((aligned(16))) uint8_t zs[2][kGradRows * 256];
+    __shared__ float vs[GROUP * PITCH];
+    __shared__ int rows[kFewRows];
+    __shared__ int found[4];
+    const int w = blockIdx.z, a = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c0 = blockIdx.x * kGradCols;
+    if (c0 >= p.cols[w])
+        return;
+    // the adapter's rows, in order: each wave's stretch of the ids, then put together
+    constexpr int STEPS = kFewRows / 256;
+    const int per = (p.M + 255) / 256 * 64;
+    int mine[STEPS];
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int m = wave * per + 64 * i + lane;
+        mine[i] = 64 * i < per && m < p.M ? p.ids[m] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        n += __builtin_popcountll(__builtin_amdgcn_ballot_w64(mine[i] == a));
+    if (lane == 0)
+        found[wave] = n;
+    __syncthreads();
+    int at = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        at += i < wave ? found[i] : 0;
+        total += found[i];
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const uint64_t has = __builtin_amdgcn_ballot_w64(mine[i] == a);
+        if (mine[i] == a)
+            rows[at + __builtin_popcountll(has & ((1ull << lane) - 1))] = wave * per + 64 * i + lane;
+        at += __builtin_popcountll(has);
+    }
+    __syncthreads();
+
+    const int col = c0 + 8 * (tid & 15);               // cols is a multiple of 8
+    const bool col_in = col < p.cols[w];
+    const float sc = p.scale[a];
+    const int64_t v_split = (int64_t)p.M * p.rank_pad;
+    for (int rg = 0; rg < p.rank_pad; rg += RANKS) {
+        f32x4 acc[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            acc[r][0] = acc[r][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        u32x4 zr[4];
+        auto load = [&](int t) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int place = t + (tid >> 4) + 16 * i;
+                zr[i] = (u32x4){0u, 0u, 0u, 0u};
+                if (col_in && place < total)
+                    zr[i] = *reinterpret_cast<const u32x4 *>(p.z[w] + (int64_t)rows[place] * p.ldz[w] + col);
+            }
+        };
+        load(0);
+        int turn = 0;
+        for (int g0 = 0; g0 < total; g0 += GROUP) {
+            __syncthreads();                           // the last group's values have been read
+            for (int i = tid; i < GROUP * (RANKS / 4); i += 256) {
+                const int row = i / (RANKS / 4), r = i % (RANKS / 4) * 4;
+                if (row >= (total - g0 + 63) / 64 * 64)
+                    break;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (g0 + row < total && rg + r < p.rank_pad) {
+                    const float *src = p.v[w] + (int64_t)rows[g0 + row] * p.rank_pad + rg + r;
+#pragma unroll 4
+                    for (int s = 0; s < p.v_splits[w]; ++s)
+                        v += *reinterpret_cast<const f32x4 *>(src + s * v_split);
+                    v *= sc;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    vs[row * PITCH + r + e] = v[e];
+            }
+            const int end = min(total, g0 + GROUP);
+            for (int t = g0; t < end; t += kGradRows, turn ^= 1) {
+                store_z(zs[turn], zr, tid);
+                load(t + kGradRows);
+                // (a tile's buffer is written again two turns later, after the barrier
+                // of the turn between, which follows this turn's reads)
+                __syncthreads();
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    u32x4 vf[RT][2];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            const float *src = vs + (t - g0 + 32 * ks + 8 * (lane >> 4) + 2 * d) * PITCH + 16 * r + (lane & 15);
+                            uint16_t h0, l0, h1, l1;
+                            split16<IN>(src[0], h0, l0);
+                            split16<IN>(src[PITCH], h1, l1);
+                            vf[r][0][d] = (uint32_t)h0 | (uint32_t)h1 << 16;
+                            vf[r][1][d] = (uint32_t)l0 | (uint32_t)l1 << 16;
+                        }
+                    multiply_z<IN, RT>(zs[turn], ks, vf, acc, wave, lane);
+                }
+            }
+        }
+        mfma_settle();
+        // dA [adapter][rank][K], dB [adapter][N][rank]
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int rank = rg + 16 * r + 4 * (lane >> 4) + e;
+                    const int c = c0 + 32 * wave + 16 * j + (lane & 15);
+                    if (rank < p.rank && c < p.cols[w])
+                        store_grad(p.out[w], w == 0 ? ((int64_t)a * p.rank + rank) * p.cols[w] + c
+                                                    : ((int64_t)a * p.cols[w] + c) * p.rank + rank,
+                                   acc[r][j][e], p.out_dtype);
+                }
+        __syncthreads();
+    }
 }
 
 // The stretches' sums, in order: dA as it lies, dB transposed.  A block takes 32
@@ -986,6 +1139,9 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     GradArgs &g = w.g;
     g.M = (int)M, g.N = (int)N, g.K = (int)K;
     g.adapters = (int)adapters, g.rank = (int)rank, g.rank_pad = (int)pad;
+    g.cols[0] = (int)K, g.cols[1] = (int)N;
+    if (few_rows(M, pad))
+        return w;
     g.per_block = std::max<int64_t>(cdiv(cdiv(M, 32), kGroupThreads) * kGroupThreads, kGroupThreads);
     g.blocks = (int)cdiv(M, g.per_block);
     g.hist = c.take<int>((int64_t)g.blocks * (adapters + 1));
@@ -1003,7 +1159,6 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.max_stretches = (int)(M / g.chunk + std::min<int64_t>(adapters, M));
     g.stretches = c.take<Stretch>(g.max_stretches);
     g.first_stretch = c.take<int>(adapters + 1);
-    g.cols[0] = (int)K, g.cols[1] = (int)N;
     // pieces of 64 places: each adapter's rows end inside one
     g.max_packed = (int)(cdiv(M, 64) + adapters) * 64;
     for (int i = 0; i < 2; ++i) {
@@ -1214,11 +1369,21 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
         g.v_splits[0] = w.u.splits, g.v_splits[1] = w.t.splits;
         g.out[0] = dA, g.out[1] = dB;
         g.out_dtype = grad_dtype;
-        hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
         const unsigned widest = (unsigned)std::max(g.cols[0], g.cols[1]);
         const dim3 grid((widest + 127) / 128, g.max_stretches, 2);
         const int pad = g.rank_pad / 16;
         auto grad = [&](auto in) {
+            if (few_rows(M, g.rank_pad)) {
+                const dim3 few((widest + 127) / 128, (unsigned)L, 2);
+                if (pad == 1)
+                    hipLaunchKernelGGL((lora_grad_few<in.value, 1>), few, dim3(256), 0, stream, g);
+                else if (pad <= 3)
+                    hipLaunchKernelGGL((lora_grad_few<in.value, 2>), few, dim3(256), 0, stream, g);
+                else
+                    hipLaunchKernelGGL((lora_grad_few<in.value, 4>), few, dim3(256), 0, stream, g);
+                return;
+            }
+            hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
             hipLaunchKernelGGL(lora_pack<in.value>, dim3(g.chunk / 64, g.max_stretches, 2), dim3(256), 0, stream, g);
             if (pad == 1)
                 hipLaunchKernelGGL((lora_grad<in.value, 1>), grid, dim3(256), 0, stream, g);
@@ -1226,12 +1391,12 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
                 hipLaunchKernelGGL((lora_grad<in.value, 2>), grid, dim3(256), 0, stream, g);
             else
                 hipLaunchKernelGGL((lora_grad<in.value, 4>), grid, dim3(256), 0, stream, g);
+            hipLaunchKernelGGL(lora_grad_sum, dim3((widest + 31) / 32, (unsigned)L, 2 * pad), dim3(256), 0, stream, g);
         };
         if (in_dtype == GEMM_BF16)
             grad(std::integral_constant<int, IN_BF16>{});
         else
             grad(std::integral_constant<int, IN_FP16>{});
-        hipLaunchKernelGGL(lora_grad_sum, dim3((widest + 31) / 32, (unsigned)L, 2 * pad), dim3(256), 0, stream, g);
         e = hipGetLastError();
     }
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;

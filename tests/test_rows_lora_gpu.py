@@ -182,6 +182,8 @@ def _check_backward(c, dy, got, dt, dx_dt, g_dt, what):
     (129, 1000, 72, 8, 3, "runs"), (300, 256, 512, 40, 70, "mixed"), (700, 512, 1032, 128, 2, "mixed"),
     (1000, 4096, 64, 64, 3, "runs"), (2500, 136, 4096, 16, 1, "one"), (777, 4096, 2048, 8, 3, "mixed"),
     (64, 64, 64, 16, 4, "none"), (2100, 264, 1000, 128, 3, "mixed"), (2100, 136, 328, 16, 70, "wild"),
+    (1024, 136, 72, 48, 1, "one"), (1025, 136, 72, 48, 2, "runs"), (1024, 264, 136, 72, 2, "one"), (1023, 8, 264, 32, 1000, "wild"),
+    (1024, 136, 72, 16, 1, "one"), (512, 136, 328, 24, 1, "one"), (128, 136, 264, 128, 1, "one"), (256, 264, 136, 64, 2, "mixed"),
 ])
 @pytest.mark.parametrize("dt", [BF16, FP16])
 def test_backward(M, N, K, R, L, kind, dt):
@@ -192,9 +194,10 @@ def test_backward(M, N, K, R, L, kind, dt):
     _check_backward(c, dy, got, dt, dt, FP32, "lora grad %s" % ((M, N, K, R, L, kind),))
 
 
-def test_backward_types_parts_and_strides():
+@pytest.mark.parametrize("M", [200, 1100])          # few rows and many have kernels of their own
+def test_backward_types_parts_and_strides(M):
     import dense_gemm_nt_amd as g
-    M, N, K, R, L, dt = 200, 264, 328, 16, 3, BF16
+    N, K, R, L, dt = 264, 328, 16, 3, BF16
     c = _case(M, N, K, R, L, "mixed", dt)
     dy = randn(M, N, seed=9, dtype=dt)
     d = _dev(c)
@@ -229,9 +232,10 @@ def test_backward_of_nothing(M, N, K, R, L):
     check(dx, ref["dx"][0], ref["dx"][0].abs() * 0.05 + 0.1, "dx of little")
 
 
-def test_backward_keeps_broken_rows_apart():
+@pytest.mark.parametrize("M", [150, 1100])
+def test_backward_keeps_broken_rows_apart(M):
     import dense_gemm_nt_amd as g
-    M, N, K, R, L, dt = 150, 264, 328, 16, 4, BF16
+    N, K, R, L, dt = 264, 328, 16, 4, BF16
     c = _case(M, N, K, R, L, "mixed", dt)
     dy = randn(M, N, seed=9, dtype=dt)
     c["ids"][:4] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
@@ -245,7 +249,7 @@ def test_backward_keeps_broken_rows_apart():
     assert bool(torch.isfinite(ref["dA"][0][0]).all()) and bool(torch.isfinite(ref["dB"][0][0]).all())
 
 
-@pytest.mark.parametrize("M,R", [(150, 16), (150, 8), (700, 64)])
+@pytest.mark.parametrize("M,R", [(150, 16), (150, 8), (700, 64), (1100, 24), (1500, 64)])
 @pytest.mark.parametrize("dt", [BF16, FP16])
 def test_backward_infinities_are_the_formulas(M, R, dt):
     """An infinity gives infinities of the formula's signs, not NaNs."""
@@ -303,7 +307,7 @@ def test_same_bits_and_other_streams():
         assert all(torch.equal(a, b) for a, b in zip(r, first))
 
 
-@pytest.mark.parametrize("M", [8, 520])
+@pytest.mark.parametrize("M", [8, 520, 1100])
 def test_captured_and_replayed(M):
     """Two graphs with memory of their own, replayed after each other with other
     inputs (ids included) in the same tensors; eager work in between."""
