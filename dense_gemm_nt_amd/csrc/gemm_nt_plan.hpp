@@ -136,8 +136,7 @@ inline Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t ws_bytes, int for
         // few N tiles the 256-row tiles' splits (at least 20 slabs each) leave
         // most compute units idle.  Interleaved medians: 192 x 4096 x 4096
         // 22.4 us on the 128x128 tile against 42.8 on the ping-pong tile,
-        // 200 x 6144 x 3072 24.3 against 55.1, 256 x 8192 x 2048 21.7 against
-        // 41.6, 256 x 2048 x 8192 26.5 against 33.9 on the four-wave tile; and
+        // 256 x 8192 x 2048 21.7 against 41.6, 256 x 2048 x 8192 26.5 against 33.9 on the four-wave tile; and
         // the four-wave tile over the ping-pong one when it fills more
         // (256 x 16384 x 4096: 45.3 against 53.0 us), or as much while the
         // ping-pong tile's splits would hold fewer than 64 slabs each
