@@ -42,6 +42,9 @@ struct ShrinkPair {
 // MFMA work is free here (the bytes of x and of the adapters bound the kernel),
 // and no sorting of rows is needed.  A decode batch puts the adapters of a row
 // tile on different blocks (lanes_j), and K splits over more of them.
+// 1 x 4096, rank 16: 3.6 us; 64 x 8192, rank 16, 48 adapters 7.5 us (16 MB: the
+// round trips bound it, not the bytes); 836 x 5952, rank 16, 61 adapters 48 us (every row tile
+// reads about 14 adapters: 280 MB out of the caches).
 template <int IN, int RT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkPair pair)
 {
@@ -141,6 +144,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkPair pair
 // that a tile's adapters take few passes over its rows; a higher rank takes two
 // passes.  Wave w multiplies rows 16 w .. +16 with all 64 ranks, and keeps each row's
 // own adapter's.  Bytes bound it: 8 slabs, 64 KB of x, are in flight a compute unit.
+// 5001 x 8192, rank 64, 4 adapters 45 us (140 MB); 8192 x 4096 and 8192 x 8192 in one
+// launch, rank 32 51 us (208 MB, 4.1 TB/s; a device copy moves 4.85).
 template <int IN>
 __global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkPair pair)
 {
@@ -412,7 +417,7 @@ __global__ __launch_bounds__(256) void lora_prepare(FlipArgs p, GradArgs a)
     }
 }
 
-// v's 64 rows from a stretch's place 64 piece, scaled, split in two 16-bit values and
+// v's 64 rows from a stretch's piece of 64 places, scaled, split in two 16-bit values and
 // transposed to [2][rank][place] (zeros behind the stretch), so that the gradient's
 // kernel reads them as they go into the MFMA, not once but for every column tile.
 template <int IN>
@@ -520,7 +525,9 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
 // v comes packed (lora_pack).  Bytes bound it: z is read
 // once, in whole 256-byte row pieces, the next tile's loads in flight while a
 // tile is multiplied, the order of the one after that already there.  Sorted into
-// stretches of one adapter, partial sums need no atomics.
+// stretches of one adapter, partial sums need no atomics.  8192 rows, 12288
+// columns, rank 32 70 us (220 MB, 3.3 TB/s: two tiles a block in flight, through registers, do
+// not cover the gathered rows' latency), their sums 7 us.
 template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {

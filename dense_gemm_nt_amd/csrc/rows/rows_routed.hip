@@ -169,6 +169,11 @@ gemm_status_t gemm_run_routed_wgrad(const void *dY, const void *X, void *dW,
     a.N = (int)K;
     fill_output(a, dW, K, out_dtype);
     // (each expert's array starts N K elements after the last one's: of 8 values)
+    // One expert's tiles after the other's, so that their panels meet in the L2s.  16384
+    // rows of 32 uneven experts, 2048 x 4096, FP32 results 456 us, of which the
+    // stores alone (no rows) take 179.  Experts' tiles taking turns, so that one's
+    // stores would run under another's products, was slower: 2, 4 and 8 at a time
+    // 395, 429 and 450 us against 380 in one session.
     a.tiles_n = (int)cdiv(K, 256);
     return launch(kRouted_pp2_mm[in_dtype][out_dtype], a, num_experts * cdiv(N, 256) * a.tiles_n, stream);
 }
