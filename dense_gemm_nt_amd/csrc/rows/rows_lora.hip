@@ -302,8 +302,7 @@ struct GradArgs {
     const uint16_t *z[2];
     const float *v[2];
     int ldz[2], cols[2], v_splits[2];
-    uint16_t *pack[2];          // v scaled, split and transposed: [2][rank_pad][max_packed]
-    int max_packed;
+    u32x4 *pack[2];             // v scaled, split and transposed, as fragments (lora_pack)
     float *part[2];             // [stretch][rank_pad][cols]
     const float *scale;
     void *out[2];               // dA [adapter][rank][K], dB [adapter][N][rank]
@@ -417,9 +416,10 @@ __global__ __launch_bounds__(256) void lora_prepare(FlipArgs p, GradArgs a)
     }
 }
 
-// v's 64 rows from a stretch's piece of 64 places, scaled, split in two 16-bit values and
-// transposed to [2][rank][place] (zeros behind the stretch), so that the gradient's
-// kernel reads them as they go into the MFMA, not once but for every column tile.
+// v's rows of a piece of 64 places of a stretch, scaled, split in two 16-bit values and
+// transposed (zeros behind the stretch) to fragments as they go into the MFMA,
+// [piece][16 ranks][32 rows][part][lane] of 16 bytes: done once, where each column
+// tile of the gradient's kernel would do it again.
 template <int IN>
 __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
 {
@@ -434,8 +434,7 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
     const int64_t v_split = (int64_t)p.M * p.rank_pad;
     if (tid < 64)
         row_of[tid] = at + tid < st.end ? p.order[at + tid] : -1;
-    uint16_t *hi = p.pack[w] + st.packed + blockIdx.x * 64;
-    uint16_t *lo = hi + (int64_t)p.rank_pad * p.max_packed;
+    const int64_t piece = st.packed / 64 + blockIdx.x;
     for (int r0 = 0; r0 < p.rank_pad; r0 += 64) {
         const int ranks = min(64, p.rank_pad - r0), quads = ranks / 4;
         __syncthreads();
@@ -453,9 +452,23 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
                 t[row][r + e] = v[e];
         }
         __syncthreads();
-        for (int r = tid >> 6; r < ranks; r += 4)
-            split16<IN>(t[tid & 63][r], hi[(int64_t)(r0 + r) * p.max_packed + (tid & 63)],
-                        lo[(int64_t)(r0 + r) * p.max_packed + (tid & 63)]);
+        u32x4 *out = p.pack[w] + (piece * (p.rank_pad / 16) + r0 / 16) * 256;
+        // lane l of a fragment: rank l % 16, rows 8 (l / 16) .. +8 of its 32
+        for (int i = tid; i < ranks * 8; i += 256) {
+            const int lane = i % 64, ks = i / 64 % 2, g = i / 128;
+            u32x4 hi, lo;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const float *src = &t[32 * ks + 8 * (lane >> 4) + 2 * d][16 * g + (lane & 15)];
+                uint16_t h0, l0, h1, l1;
+                split16<IN>(src[0], h0, l0);
+                split16<IN>(src[65], h1, l1);
+                hi[d] = (uint32_t)h0 | (uint32_t)h1 << 16;
+                lo[d] = (uint32_t)l0 | (uint32_t)l1 << 16;
+            }
+            out[(g * 4 + ks * 2) * 64 + lane] = hi;
+            out[(g * 4 + ks * 2 + 1) * 64 + lane] = lo;
+        }
     }
 }
 
@@ -521,17 +534,18 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
 
 // part[stretch][r][c] = sum over the stretch's rows m of s_a v[m][r] z[m][c]:
 // the contraction runs over rows, so z's tile (64 rows of 128 columns, gathered
-// by the rows' order) is staged in LDS as it lies and read back transposed;
-// v comes packed (lora_pack).  Bytes bound it: z is read
+// by the rows' order) is staged in LDS as it lies and read back transposed, v's
+// fragments (lora_pack) beside it for all four waves.  Bytes bound it: z is read
 // once, in whole 256-byte row pieces, the next tile's loads in flight while a
 // tile is multiplied, the order of the one after that already there.  Sorted into
 // stretches of one adapter, partial sums need no atomics.  8192 rows, 12288
-// columns, rank 32 70 us (220 MB, 3.3 TB/s: two tiles a block in flight, through registers, do
-// not cover the gathered rows' latency), their sums 7 us.
+// columns, rank 32 42 us (220 MB, 5.2 TB/s); 70 while each wave read v's parts for
+// itself, in 64-byte pieces.
 template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {
     __shared__ __attribute__((aligned(16))) uint8_t zs[2][kGradRows * 256];
+    __shared__ u32x4 vs[2][RT * 256];
     const int w = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c0 = blockIdx.x * kGradCols;
@@ -540,57 +554,81 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
     const Stretch st = p.stretches[blockIdx.y];
     if (st.adapter < 0)
         return;
-    const int col = c0 + 8 * (tid & 15);               // cols is a multiple of 8
-    const bool col_in = col < p.cols[w];
+    const bool col_in = c0 + 8 * (tid & 15) < p.cols[w];            // cols is a multiple of 8
+    const int col = col_in ? c0 + 8 * (tid & 15) : c0;
+    const int last = st.first + (st.end - 1 - st.first) / kGradRows * kGradRows;   // the last tile
+    const int groups = p.rank_pad / 16;
 
     for (int rg = 0; rg < p.rank_pad; rg += 16 * RT) {
         f32x4 acc[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
             acc[r][0] = acc[r][1] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        int row_at[4];
-        u32x4 zr[4];
-        auto load_order = [&](int at) {
+        // In flight while tile t is multiplied: the rows and fragments of t + 1 and t + 2,
+        // the order of t + 3.  A turn's loads are issued in the order in which they are
+        // waited for, and none is under a condition (what lies behind the stretch
+        // re-reads its last row or tile; rows are zeroed on their way to LDS): the waits
+        // are then for some of the loads, not all.
+        int row_at[2][4];
+        u32x4 zr[2][4], vr[2][RT];
+        auto load_order = [&](int (&rows)[4], int at) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int place = at + (tid >> 4) + 16 * i;
-                row_at[i] = place < st.end ? p.order[place] : -1;
-            }
+            for (int i = 0; i < 4; ++i)
+                rows[i] = p.order[min(at + (tid >> 4) + 16 * i, st.end - 1)];
         };
-        auto load = [&]() {
+        auto load = [&](u32x4 (&z)[4], const int (&rows)[4]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                zr[i] = (u32x4){0u, 0u, 0u, 0u};
-                if (col_in && row_at[i] >= 0)
-                    zr[i] = *reinterpret_cast<const u32x4 *>(p.z[w] + (int64_t)row_at[i] * p.ldz[w] + col);
-            }
+            for (int i = 0; i < 4; ++i)
+                z[i] = *reinterpret_cast<const u32x4 *>(p.z[w] + (int64_t)rows[i] * p.ldz[w] + col);
         };
-        load_order(st.first);
-        load();
-        load_order(st.first + kGradRows);
-        int turn = 0;
-        for (int at = st.first; at < st.end; at += kGradRows, turn ^= 1) {
-            store_z(zs[turn], zr, tid);
-            load();
-            load_order(at + 2 * kGradRows);
-            const uint16_t *v = p.pack[w] + (int64_t)(rg + (lane & 15)) * p.max_packed + st.packed + (at - st.first) +
-                                8 * (lane >> 4);
-            u32x4 vf[2][RT][2];
+        auto load_v = [&](u32x4 (&v)[RT], int at) {
+            const int64_t piece = (st.packed + min(at, last) - st.first) / 64;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
+            for (int r = 0; r < RT; ++r)          // (past rank_pad: not kept)
+                v[r] = p.pack[w][(piece * groups + min(rg / 16 + r, groups - 1)) * 256 + tid];
+        };
+        auto turn = [&](auto parity, int at) {
+            constexpr int P = decltype(parity)::value;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!col_in || at + (tid >> 4) + 16 * i >= st.end)
+                    zr[P][i] = (u32x4){0u, 0u, 0u, 0u};
+            store_z(zs[P], zr[P], tid);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+                vs[P][r * 256 + tid] = vr[P][r];
+            load_order(row_at[1 - P], at + 3 * kGradRows);
+            load(zr[P], row_at[P]);
+            load_v(vr[P], at + 2 * kGradRows);
+            // (a tile's buffers are written again two turns later, after the barrier
+            // of the turn between, which follows this turn's reads)
+            wait_lgkmcnt0();
+            wg_barrier();
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                u32x4 vf[RT][2];
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        vf[ks][r][h] = rg + 16 * r < p.rank_pad
-                            ? *reinterpret_cast<const u32x4 *>(v + ((int64_t)h * p.rank_pad + 16 * r) * p.max_packed + 32 * ks)
-                            : (u32x4){0u, 0u, 0u, 0u};
-            // (a tile's buffer is written again two turns later, after the barrier
-            // of the turn between, which follows this turn's reads)
-            __syncthreads();
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                multiply_z<IN, RT>(zs[turn], ks, vf[ks], acc, wave, lane);
+                        vf[r][h] = vs[P][(r * 4 + ks * 2 + h) * 64 + lane];
+                multiply_z<IN, RT>(zs[P], ks, vf, acc, wave, lane);
+            }
+        };
+        load_order(row_at[0], st.first);
+        load_order(row_at[1], st.first + kGradRows);
+        load(zr[0], row_at[0]);
+        load_v(vr[0], st.first);
+        load_order(row_at[0], st.first + 2 * kGradRows);
+        load(zr[1], row_at[1]);
+        load_v(vr[1], st.first + kGradRows);
+        for (int at = st.first;; at += 2 * kGradRows) {
+            turn(std::integral_constant<int, 0>{}, at);
+            if (at >= last)
+                break;
+            turn(std::integral_constant<int, 1>{}, at + kGradRows);
+            if (at + kGradRows >= last)
+                break;
         }
         mfma_settle();
         float *out = p.part[w] + (int64_t)blockIdx.y * p.rank_pad * p.cols[w];
@@ -759,34 +797,39 @@ __global__ __launch_bounds__(256) void lora_grad_few(GradArgs p)
 }
 
 // The stretches' sums, in order: dA as it lies, dB transposed.  A block takes 32
-// columns of 16 ranks.
+// columns of 16 ranks; a thread four columns of one rank and one half of the
+// stretches, so that a few loads of a thread cover them (24 stretches of 64 ranks,
+// 2256 columns: 6.2 us against 16.6 with a column of two ranks a thread).
 __global__ __launch_bounds__(256) void lora_grad_sum(GradArgs p)
 {
     __shared__ float t[16][33];
+    __shared__ f32x4 second[128];
     const int w = blockIdx.z & 1, a = blockIdx.y, r0 = (blockIdx.z >> 1) * 16;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + x;
     if (blockIdx.x * 32 >= (unsigned)p.cols[w])
         return;
-    const int s0 = p.first_stretch[a], s1 = p.first_stretch[a + 1];
-    float v[2] = {0.0f, 0.0f};
-    if (col < p.cols[w])
+    const int x = (threadIdx.x & 7) * 4, y = (threadIdx.x >> 3) & 15, half = threadIdx.x >> 7;
+    const int col = blockIdx.x * 32 + x;
+    const bool in = col < p.cols[w] && r0 + y < p.rank;          // cols is a multiple of 8
+    const int s0 = p.first_stretch[a], s1 = p.first_stretch[a + 1], mid = (s0 + s1) / 2;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (in)
 #pragma unroll 8
-        for (int s = s0; s < s1; ++s)
+        for (int s = half ? mid : s0; s < (half ? s1 : mid); ++s)
+            v += *reinterpret_cast<const f32x4 *>(p.part[w] + ((int64_t)s * p.rank_pad + r0 + y) * p.cols[w] + col);
+    if (half)
+        second[threadIdx.x & 127] = v;
+    __syncthreads();
+    if (!half) {
+        v += second[threadIdx.x];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (r0 + y * 2 + i < p.rank)
-                    v[i] += p.part[w][((int64_t)s * p.rank_pad + r0 + y * 2 + i) * p.cols[w] + col];
-    if (w == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (col < p.cols[w] && r0 + y * 2 + i < p.rank)
-                store_grad(p.out[w], ((int64_t)a * p.rank + r0 + y * 2 + i) * p.cols[w] + col, v[i], p.out_dtype);
-        return;
+        for (int i = 0; i < 4; ++i) {
+            if (w == 0 && in)
+                store_grad(p.out[w], ((int64_t)a * p.rank + r0 + y) * p.cols[w] + col + i, v[i], p.out_dtype);
+            t[y][x + i] = v[i];
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        t[y * 2 + i][x] = v[i];
+    if (w == 0)
+        return;
     __syncthreads();
     const int r = threadIdx.x & 15;
 #pragma unroll
@@ -1166,10 +1209,9 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.max_stretches = (int)(M / g.chunk + std::min<int64_t>(adapters, M));
     g.stretches = c.take<Stretch>(g.max_stretches);
     g.first_stretch = c.take<int>(adapters + 1);
-    // pieces of 64 places: each adapter's rows end inside one
-    g.max_packed = (int)(cdiv(M, 64) + adapters) * 64;
+    const int64_t pieces = cdiv(M, 64) + adapters;     // each adapter's rows end inside one
     for (int i = 0; i < 2; ++i) {
-        g.pack[i] = c.take<uint16_t>((int64_t)2 * pad * g.max_packed);
+        g.pack[i] = c.take<u32x4>(pieces * (pad / 16) * 256);
         g.part[i] = c.take<float>((int64_t)g.max_stretches * pad * g.cols[i]);
     }
     return w;
