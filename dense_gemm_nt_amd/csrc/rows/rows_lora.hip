@@ -661,8 +661,8 @@ __device__ __forceinline__ void store_grad(void *out, int64_t at, float v, int d
 // values hold, scaled, in FP32; a lane splits what it multiplies.
 constexpr int kFewRows = 1024, kFewStage = 8192;
 
-// Measured for three adapters, in us: 777 rows, 6144 columns, rank 8 13 against 20
-// in four launches; 731, 4448, 24 26 against 24; with few rows three launches' time
+// Measured for three adapters, in us: 777 rows, 6144 columns, rank 8 13 against 19
+// in four launches; 731, 4448, 24 26 against 22; with few rows three launches' time
 // less (18 rows, all of a backward call: 31 against 42).
 __host__ __device__ constexpr bool few_rows(int64_t M, int64_t rank_pad)
 {
@@ -1200,9 +1200,9 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.order = c.take<int32_t>(M);
     // stretches so long that column tiles x stretches give about two blocks a
     // compute unit, and no longer: each stretch writes a partial sum (gradients and
-    // their sums with two against four: 8192 rows, 12288 columns, rank 32 76 us
-    // against 83; 5918, 2256, 64 46 against 66; 2048, 4096, 16 17 against 23; but
-    // 7164, 10328, 24 66 against 61)
+    // their sums with two against four: 8192 rows, 12288 columns, rank 32 48 us
+    // against 52; 5918, 2256, 64 26 against 36; 2048, 4096, 16 12 against 13; but 7164,
+    // 10328, 24 48 against 45)
     const int64_t tiles = cdiv(K, 128) + cdiv(N, 128);
     const int64_t want = std::max<int64_t>(1, 2 * kNumCUs / tiles);
     g.chunk = (int)std::max<int64_t>(64, cdiv(cdiv(M, want), 64) * 64);

@@ -107,3 +107,44 @@ def test_waits_before_results_are_stored(lib):
                 hit = [left for left, r in recent if r & _registers(args)]
                 assert not hit, (name, s, hit)
     assert checked > 0
+
+
+def _scalars(text):
+    out = {"vcc"} if "vcc" in text else set()
+    for m in re.finditer(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b", text):
+        out |= set(range(int(m.group(1)), int(m.group(2)) + 1)) if m.group(1) else {int(m.group(3))}
+    return out
+
+
+@pytest.mark.skipif(not os.path.exists(k.OBJDUMP), reason="llvm-objdump not installed")
+def test_scalars_are_settled_before_loads(lib):
+    """A scalar that a vector instruction wrote is read by a memory instruction five wait
+    states later at the earliest (text order).  The compiler sees to that for its
+    own loads, but not for those written in asm, whose scalars it may have put
+    away in vector registers."""
+    checked = 0
+    for co in k._code_objects(lib):
+        with tempfile.TemporaryDirectory() as d:
+            path = os.path.join(d, "co.o")
+            open(path, "wb").write(co)
+            text = subprocess.run([k.OBJDUMP, "-d", "--no-show-raw-insn", path], check=True, capture_output=True,
+                                  text=True).stdout
+        recent = []
+        for line in text.splitlines():
+            if re.match(r"^[0-9a-f]+ <(\S+)>:$", line):
+                recent = []
+                continue
+            s = line.split("//")[0].strip()
+            if not s:
+                continue
+            op = s.split()[0]
+            args = s[len(op):]
+            if re.match(r"(buffer|global)_", op):
+                checked += 1
+                hit = [left for left, r in recent if r & _scalars(args)]
+                assert not hit, (s, hit)
+            states = int(args, 0) + 1 if op == "s_nop" else 1
+            recent = [(left - states, r) for left, r in recent if left > states]
+            if re.match(r"v_(readlane|readfirstlane|cmp)", op):
+                recent.append((5, _scalars(args.split(",")[0])))
+    assert checked > 0
