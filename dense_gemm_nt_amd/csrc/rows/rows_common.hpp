@@ -148,6 +148,24 @@ __device__ __forceinline__ void split16(float x, uint16_t &hi, uint16_t &lo)
     lo = __builtin_isfinite(h) ? to16<IN>(x - h) : (uint16_t)0;
 }
 
+// The same for the gradients' contraction over rows, whose FP32 results keep what
+// their operands hold: three bf16 parts (24 bits) or two fp16 ones (22).  With two
+// bf16 parts the adapters' gradients were 2.5e-6 off, with three as near as FP32
+// sums are; its MFMAs are few beside the bytes.
+template <int IN>
+constexpr int kParts = IN == IN_BF16 ? 3 : 2;
+
+template <int IN>
+__device__ __forceinline__ void split_parts(float x, uint16_t (&part)[kParts<IN>])
+{
+#pragma unroll
+    for (int i = 0; i < kParts<IN>; ++i) {
+        part[i] = to16<IN>(x);
+        const float h = from16<IN>(part[i]);
+        x = __builtin_isfinite(h) ? x - h : 0.0f;
+    }
+}
+
 template <int IN>
 __device__ __forceinline__ f32x4 mfma16x16x32(u32x4 a, u32x4 b, f32x4 c)
 {
@@ -195,18 +213,19 @@ __device__ __forceinline__ u32x4 each16(u32x4 x, F f)
     return y;
 }
 
-// acc += x . (hi + lo) where x holds infinities or NaNs: as the sum of x's finite
+// acc += x . (v[0] + v[1] + ...) where x holds infinities or NaNs: as the sum of x's finite
 // values (its others as +-1 to 2, by their exponents' highest bit: an infinite
 // hi then stays one, and a NaN a NaN)
 // and of what its others make, without any operand that could make a zero of
-// another row, or lo's, into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the infinity
+// another row, or of a later part, into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the infinity
 // that is due and is 0 where hi is masked to 0; a NaN (also that of infinity times 0) is
-// made as the sum of both infinities.  Where not `own`, hi and lo are zeros that
+// made as the sum of both infinities.  Where not `own`, v's parts are zeros that
 // are to add nothing.  mul(type, x, y) multiplies and adds to acc.  Rarely run, and
 // written for few registers: one operand pair at a time.
-template <int IN, typename F>
-__device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, u32x4 lo, bool own, F mul)
+template <int IN, int NP, typename F>
+__device__ __forceinline__ void add_special(u32x4 x, const u32x4 (&v)[NP], bool own, F mul)
 {
+    const u32x4 hi = v[0];
     constexpr uint32_t exp = IN == IN_BF16 ? 0x7f80u : 0x7c00u, big = 0x7f00u;
     auto step = [&](auto f, auto g, uint32_t flip) {
         mul(std::integral_constant<int, IN_BF16>{}, each16(x, f), each16(hi, g) ^ flip);
@@ -225,8 +244,9 @@ __device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, u32x4 lo, bool ow
 #pragma unroll
         for (int d = 0; d < 4; ++d)
             y[d] = x[d] & ~((((x[d] & exps) + lowest) & 0x80008000u) >> 1);
-        mul(std::integral_constant<int, IN>{}, y, hi);
-        mul(std::integral_constant<int, IN>{}, y, lo);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            mul(std::integral_constant<int, IN>{}, y, v[i]);
         __builtin_amdgcn_sched_barrier(0);
     }
     step(inf, sign, 0u);
@@ -425,12 +445,12 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                     const bool own = id[fm] == s;
                     if (__builtin_amdgcn_ballot_w64(own) == 0)
                         continue;
-                    const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
+                    const u32x4 t[2] = {own ? hi[fm] : zero, own ? lo[fm] : zero};
 #pragma unroll
                     for (int fn = 0; fn < FN; ++fn) {
                         int again = s;                    // (a load of its own: registers)
                         asm volatile("" : "+s"(again));
-                        add_special<IN>(load_up(again, fn, rs), th, tl, own, [&](auto type, u32x4 x, u32x4 y) {
+                        add_special<IN>(load_up(again, fn, rs), t, own, [&](auto type, u32x4 x, u32x4 y) {
                             acc[fn][fm] = mfma32x32x16<type.value>(x, y, acc[fn][fm]);
                         });
                     }

@@ -452,22 +452,25 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
                 t[row][r + e] = v[e];
         }
         __syncthreads();
-        u32x4 *out = p.pack[w] + (piece * (p.rank_pad / 16) + r0 / 16) * 256;
+        constexpr int NP = kParts<IN>;
+        u32x4 *out = p.pack[w] + (piece * (p.rank_pad / 16) + r0 / 16) * (NP * 128);
         // lane l of a fragment: rank l % 16, rows 8 (l / 16) .. +8 of its 32
         for (int i = tid; i < ranks * 8; i += 256) {
             const int lane = i % 64, ks = i / 64 % 2, g = i / 128;
-            u32x4 hi, lo;
+            u32x4 f[NP];
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const float *src = &t[32 * ks + 8 * (lane >> 4) + 2 * d][16 * g + (lane & 15)];
-                uint16_t h0, l0, h1, l1;
-                split16<IN>(src[0], h0, l0);
-                split16<IN>(src[65], h1, l1);
-                hi[d] = (uint32_t)h0 | (uint32_t)h1 << 16;
-                lo[d] = (uint32_t)l0 | (uint32_t)l1 << 16;
+                uint16_t a[NP], b[NP];
+                split_parts<IN>(src[0], a);
+                split_parts<IN>(src[65], b);
+#pragma unroll
+                for (int h = 0; h < NP; ++h)
+                    f[h][d] = (uint32_t)a[h] | (uint32_t)b[h] << 16;
             }
-            out[(g * 4 + ks * 2) * 64 + lane] = hi;
-            out[(g * 4 + ks * 2 + 1) * 64 + lane] = lo;
+#pragma unroll
+            for (int h = 0; h < NP; ++h)
+                out[((g * 2 + ks) * NP + h) * 64 + lane] = f[h];
         }
     }
 }
@@ -491,10 +494,10 @@ __device__ __forceinline__ void store_z(uint8_t *zs, const u32x4 (&zr)[4], int t
 
 // acc += v z over a tile's rows 32 ks .. +32, read transposed (ds_read_b64_tr_b16):
 // acc[r][j] holds ranks 16 r .. +16 of columns 32 wave + 16 j .. +16.  vf: rank
-// 16 r + lane % 16, rows 32 ks + 8 (lane / 16) .. +8, of both parts.
+// 16 r + lane % 16, rows 32 ks + 8 (lane / 16) .. +8, of every part.
 template <int IN, int RT>
-__device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x4 (&vf)[RT][2], f32x4 (&acc)[RT][2],
-                                           int wave, int lane)
+__device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x4 (&vf)[RT][kParts<IN>],
+                                           f32x4 (&acc)[RT][2], int wave, int lane)
 {
     typedef short v4s __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) v4s lds_v4s;
@@ -511,14 +514,14 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
         const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
         zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
     }
-    // (an infinity in z times a value's second part, 0 or of the other sign, would
+    // (an infinity in z times a value's later part, 0 or of the other sign, would
     // be a NaN: such pieces are taken apart)
     if (__builtin_amdgcn_ballot_w64((has_special<IN>(zf[0]) | has_special<IN>(zf[1])) != 0)) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                add_special<IN>(zf[j], vf[r][0], vf[r][1], true, [&](auto type, u32x4 x, u32x4 y) {
+                add_special<IN>(zf[j], vf[r], true, [&](auto type, u32x4 x, u32x4 y) {
                     acc[r][j] = mfma16x16x32<type.value>(y, x, acc[r][j]);
                 });
         return;
@@ -526,7 +529,7 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kParts<IN>; ++h) {
             acc[r][0] = mfma16x16x32<IN>(vf[r][h], zf[0], acc[r][0]);
             acc[r][1] = mfma16x16x32<IN>(vf[r][h], zf[1], acc[r][1]);
         }
@@ -539,13 +542,14 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
 // once, in whole 256-byte row pieces, the next tile's loads in flight while a
 // tile is multiplied, the order of the one after that already there.  Sorted into
 // stretches of one adapter, partial sums need no atomics.  8192 rows, 12288
-// columns, rank 32 42 us (220 MB, 5.2 TB/s); 70 while each wave read v's parts for
-// itself, in 64-byte pieces.
+// columns, rank 32, bf16 48 us (220 MB, 4.5 TB/s; 42 with two of the three parts);
+// 70 while each wave read v's two parts for itself, in 64-byte pieces.
 template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {
     __shared__ __attribute__((aligned(16))) uint8_t zs[2][kGradRows * 256];
-    __shared__ u32x4 vs[2][RT * 256];
+    constexpr int NP = kParts<IN>, FRAGS = RT * NP * 128, VL = (FRAGS + 255) / 256;
+    __shared__ u32x4 vs[2][VL * 256];
     const int w = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int c0 = blockIdx.x * kGradCols;
@@ -570,7 +574,7 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
         // re-reads its last row or tile; rows are zeroed on their way to LDS): the waits
         // are then for some of the loads, not all.
         int row_at[2][4];
-        u32x4 zr[2][4], vr[2][RT];
+        u32x4 zr[2][4], vr[2][VL];
         auto load_order = [&](int (&rows)[4], int at) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -581,11 +585,13 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
             for (int i = 0; i < 4; ++i)
                 z[i] = *reinterpret_cast<const u32x4 *>(p.z[w] + (int64_t)rows[i] * p.ldz[w] + col);
         };
-        auto load_v = [&](u32x4 (&v)[RT], int at) {
+        auto load_v = [&](u32x4 (&v)[VL], int at) {
             const int64_t piece = (st.packed + min(at, last) - st.first) / 64;
 #pragma unroll
-            for (int r = 0; r < RT; ++r)          // (past rank_pad: not kept)
-                v[r] = p.pack[w][(piece * groups + min(rg / 16 + r, groups - 1)) * 256 + tid];
+            for (int i = 0; i < VL; ++i) {
+                const int f = min(i * 256 + tid, FRAGS - 1), r = f / (NP * 128);       // (past rank_pad: not kept)
+                v[i] = p.pack[w][(piece * groups + min(rg / 16 + r, groups - 1)) * (NP * 128) + f % (NP * 128)];
+            }
         };
         auto turn = [&](auto parity, int at) {
             constexpr int P = decltype(parity)::value;
@@ -595,8 +601,8 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
                     zr[P][i] = (u32x4){0u, 0u, 0u, 0u};
             store_z(zs[P], zr[P], tid);
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-                vs[P][r * 256 + tid] = vr[P][r];
+            for (int i = 0; i < VL; ++i)
+                vs[P][i * 256 + tid] = vr[P][i];
             load_order(row_at[1 - P], at + 3 * kGradRows);
             load(zr[P], row_at[P]);
             load_v(vr[P], at + 2 * kGradRows);
@@ -606,12 +612,12 @@ __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
             wg_barrier();
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                u32x4 vf[RT][2];
+                u32x4 vf[RT][NP];
 #pragma unroll
                 for (int r = 0; r < RT; ++r)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        vf[r][h] = vs[P][(r * 4 + ks * 2 + h) * 64 + lane];
+                    for (int h = 0; h < NP; ++h)
+                        vf[r][h] = vs[P][((r * 2 + ks) * NP + h) * 64 + lane];
                 multiply_z<IN, RT>(zs[P], ks, vf, acc, wave, lane);
             }
         };
@@ -761,17 +767,18 @@ __global__ __launch_bounds__(256) void lora_grad_few(GradArgs p)
                 __syncthreads();
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    u32x4 vf[RT][2];
+                    u32x4 vf[RT][kParts<IN>];
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
                         for (int d = 0; d < 4; ++d) {
                             const float *src = vs + (t - g0 + 32 * ks + 8 * (lane >> 4) + 2 * d) * PITCH + 16 * r + (lane & 15);
-                            uint16_t h0, l0, h1, l1;
-                            split16<IN>(src[0], h0, l0);
-                            split16<IN>(src[PITCH], h1, l1);
-                            vf[r][0][d] = (uint32_t)h0 | (uint32_t)h1 << 16;
-                            vf[r][1][d] = (uint32_t)l0 | (uint32_t)l1 << 16;
+                            uint16_t a[kParts<IN>], b[kParts<IN>];
+                            split_parts<IN>(src[0], a);
+                            split_parts<IN>(src[PITCH], b);
+#pragma unroll
+                            for (int h = 0; h < kParts<IN>; ++h)
+                                vf[r][h][d] = (uint32_t)a[h] | (uint32_t)b[h] << 16;
                         }
                     multiply_z<IN, RT>(zs[turn], ks, vf, acc, wave, lane);
                 }
@@ -1200,9 +1207,9 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.order = c.take<int32_t>(M);
     // stretches so long that column tiles x stretches give about two blocks a
     // compute unit, and no longer: each stretch writes a partial sum (gradients and
-    // their sums with two against four: 8192 rows, 12288 columns, rank 32 48 us
-    // against 52; 5918, 2256, 64 26 against 36; 2048, 4096, 16 12 against 13; but 7164,
-    // 10328, 24 48 against 45)
+    // their sums with two against four, v in two parts: 8192 rows, 12288 columns, rank
+    // 32 48 us against 52; 5918, 2256, 64 26 against 36; 2048, 4096, 16 12 against 13; but
+    // 7164, 10328, 24 48 against 45)
     const int64_t tiles = cdiv(K, 128) + cdiv(N, 128);
     const int64_t want = std::max<int64_t>(1, 2 * kNumCUs / tiles);
     g.chunk = (int)std::max<int64_t>(64, cdiv(cdiv(M, want), 64) * 64);
@@ -1211,7 +1218,7 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.first_stretch = c.take<int>(adapters + 1);
     const int64_t pieces = cdiv(M, 64) + adapters;     // each adapter's rows end inside one
     for (int i = 0; i < 2; ++i) {
-        g.pack[i] = c.take<u32x4>(pieces * (pad / 16) * 256);
+        g.pack[i] = c.take<u32x4>(pieces * (pad / 16) * (kParts<IN_BF16> * 128));
         g.part[i] = c.take<float>((int64_t)g.max_stretches * pad * g.cols[i]);
     }
     return w;

@@ -232,6 +232,29 @@ def test_backward_of_nothing(M, N, K, R, L):
     check(dx, ref["dx"][0], ref["dx"][0].abs() * 0.05 + 0.1, "dx of little")
 
 
+@pytest.mark.parametrize("M", [4, 1100])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_gradients_keep_the_low_rank_values(M, dt):
+    """Low-rank values of 21 bits, exact in FP32, meet one row of dy and x each: dA and
+    dB are single products, a few FP32 roundings off (2^-24 each)."""
+    import dense_gemm_nt_amd as g
+    N, K, R = 136, 64, 16
+    x, dy = torch.zeros(M, K, dtype=dt), torch.zeros(M, N, dtype=dt)
+    parts = torch.tensor([1.0, 2.0 ** -10, 2.0 ** -20])
+    x[1, :3], dy[1, :3] = parts.to(dt), parts.to(dt)
+    dy[1, 3:] = randn(N - 3, seed=3).to(dt)
+    x[1, 3:] = randn(K - 3, seed=4).to(dt)
+    A, B = torch.zeros(1, R, K, dtype=dt), torch.zeros(1, N, R, dtype=dt)
+    A[0, :, :3] = 1.0
+    B[0, :3, :] = 1.0
+    c = dict(x=x, W=torch.zeros(N, K, dtype=dt), A=A, B=B, ids=torch.zeros(M, dtype=torch.int32),
+             scale=torch.ones(1))
+    _, dA, dB = g.gemm_lora_backward(dy.to(DEV), **_dev(c))
+    ref = o.lora_backward(dy, **c)
+    check(dA, ref["dA"][0], ref["dA"][0].abs() * 2.0 ** -22, "dA")
+    check(dB, ref["dB"][0], ref["dB"][0].abs() * 2.0 ** -22, "dB")
+
+
 @pytest.mark.parametrize("M", [150, 1100])
 def test_backward_keeps_broken_rows_apart(M):
     import dense_gemm_nt_amd as g
