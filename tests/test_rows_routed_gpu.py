@@ -203,3 +203,34 @@ def test_expert_layer_together(captured):
         for name, terms, inner, rank, out in (("dx", D, D, R, dt), ("dA", 0, D, T, FP32), ("dB", 0, D, T, FP32)):
             r0, b0, l0 = back[name]
             check(q[name], r0, lora_bound(r0, b0, l0, terms, inner, rank, dt, out), name)
+
+
+def _far(t, ld):
+    """The same values in rows `ld` elements apart: offsets past 32 bits."""
+    wide = torch.empty(t.shape[0], ld, dtype=t.dtype, device=DEV)[:, :t.shape[1]]
+    return wide.copy_(t)
+
+
+def test_rows_more_than_32_bits_apart():
+    import dense_gemm_nt_amd as g
+    M, N, K, R, L, ld = 1100, 136, 72, 16, 3, (1 << 21) + 64
+    x, dy = randn(M, K, seed=1, dtype=BF16).to(DEV), randn(M, N, seed=2, dtype=BF16).to(DEV)
+    W, We = randn(N, K, seed=3, dtype=BF16).to(DEV), randn(2, N, K, seed=4, dtype=BF16).to(DEV)
+    A, B = randn(L, R, K, seed=5, dtype=BF16).to(DEV), randn(L, N, R, seed=6, dtype=BF16).to(DEV)
+    ids = (torch.arange(M, device=DEV) % (L + 1)).to(torch.int32) - 1
+    scale, off = torch.ones(L, device=DEV), torch.tensor([0, 300, M - 7], dtype=torch.int32, device=DEV)
+    fx, fdy = _far(x, ld), _far(dy, ld)
+    out = torch.zeros(M, ld, dtype=BF16, device=DEV)[:, :N]
+    assert torch.equal(g.gemm_lora(fx, W, A, B, ids, scale, out=out), g.gemm_lora(x, W, A, B, ids, scale))
+    for a, b in zip(g.gemm_lora_backward(fdy, fx, W, A, B, ids, scale), g.gemm_lora_backward(dy, x, W, A, B, ids, scale)):
+        assert torch.equal(a, b)
+    out.zero_()
+    assert torch.equal(g.gemm_routed(fx, We, off, out=out), g.gemm_routed(x, We, off))
+    out = out[:, :K].zero_()
+    assert torch.equal(g.gemm_routed(fdy, We.transpose(1, 2), off, out=out), g.gemm_routed(dy, We.transpose(1, 2), off))
+    assert torch.equal(g.gemm_routed_wgrad(fdy, fx, off), g.gemm_routed_wgrad(dy, x, off))
+    r, f = g.route_topk(dy, 4), g.route_topk(fdy, 4)
+    for a, b in zip(r, f):
+        assert a is b or torch.equal(a, b)
+    gw = torch.ones_like(r.weights)
+    assert torch.equal(g.route_topk_backward(fdy, f, gw), g.route_topk_backward(dy, r, gw))
