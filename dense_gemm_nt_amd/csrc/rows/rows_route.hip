@@ -343,7 +343,7 @@ __device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, i
         const bool chose = lane < found;
         float w = chose ? __expf(rank_value(my_key) - top) * inv : 0.0f;
         if (a.renorm && found)
-            w *= __builtin_amdgcn_rcpf(row_sum<64>(w));
+            w /= row_sum<64>(w);        // (a division: a single choice's weight is 1, not nearly 1)
         if (lane < a.k) {
             a.ids[t * a.k + lane] = my_e;
             a.weights[t * a.k + lane] = w;
@@ -398,14 +398,14 @@ __device__ __forceinline__ int route_rows_narrow(const RouteArgs &a, int64_t t0,
             }
         }
         chosen = row_sum<LPR>(chosen);
-        const float scale = a.renorm && found ? 1.0f / chosen : 1.0f;
+        const float share = a.renorm && found ? chosen : 1.0f;
         if (in) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (place_of[i] != 0xff) {
                     const int e = li * 4 + i;
                     a.ids[t * a.k + place_of[i]] = e;
-                    a.weights[t * a.k + place_of[i]] = x[0][i] * scale;
+                    a.weights[t * a.k + place_of[i]] = x[0][i] / share;
                     atomicAdd(&hist[e], 1);
                 }
             for (int j = found + li; j < a.k; j += LPR) {
@@ -549,7 +549,11 @@ __global__ __launch_bounds__(kGroupThreads) void route_place(RouteArgs a)
 // dlogit = p (dp - sum p dp), dp_e = g_loss E f_e / n + (the gradient of e's
 // weight, if chosen): p is recomputed from the logits, which are read once.  Lane j
 // of a row takes choice j's gradient, and LDS carries it to the lane that holds
-// the expert's column (a wave's own 256 Q values: no barrier).
+// the expert's column (a wave's own 256 Q values: no barrier).  Renormalized
+// weights' gradients are h_j = (g_j - sum_i g_i w_i) / S with sum_i w_i = 1: they are taken as
+// ((g_j - g_0) - sum_i (g_i - g_0) w_i) / S, which does not leave the rounding of
+// sum_i w_i times g where w_0 is nearly 1 or the only weight (it was 1e-7 of g / S then, in
+// FP32 1.5e-5 of dlogits with the loss's gradient beside it).
 template <int DT, int LPR, int Q>
 __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
 {
@@ -597,9 +601,10 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_wave_barrier();
             };
-            float mean = 0.0f, inv = 1.0f;
+            float mean = 0.0f, inv = 1.0f, g0 = 0.0f;
             if (a.renorm) {
-                // p where the choices are: their sum, and sum of g w
+                g0 = on ? a.grad_w[t * a.k] : 0.0f;
+                // p where the choices are: their sum, and sum of (g - g_0) w
 #pragma unroll
                 for (int q = 0; q < Q; ++q)
                     *reinterpret_cast<f32x4 *>(mine + li * 4 * Q + 4 * q) = x[q];
@@ -609,7 +614,7 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
                     const int e = on ? a.ids[t * a.k + j] : -1;
                     if ((uint32_t)e < (uint32_t)a.E) {
                         total += mine[e];
-                        mean += a.grad_w[t * a.k + j] * a.weights[t * a.k + j];
+                        mean += (a.grad_w[t * a.k + j] - g0) * a.weights[t * a.k + j];
                     }
                 }
                 total = row_sum<LPR>(total);
@@ -624,7 +629,7 @@ __global__ __launch_bounds__(256) void route_backward(RouteArgs a)
             for (int j = li; j < a.k; j += LPR) {
                 const int e = on ? a.ids[t * a.k + j] : -1;
                 if ((uint32_t)e < (uint32_t)a.E)
-                    mine[e] = (a.grad_w[t * a.k + j] - mean) * inv;
+                    mine[e] = (a.grad_w[t * a.k + j] - g0 - mean) * inv;
             }
             wave_sync();
 #pragma unroll

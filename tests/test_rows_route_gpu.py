@@ -229,3 +229,41 @@ def test_backward_refuses_a_routing_of_other_making():
         g.route_topk_backward(x, r._replace(weights=r.weights[:5]))
     with pytest.raises(ValueError):
         g.route_topk_backward(x, r._replace(counts=r.counts.cpu()))
+
+
+@pytest.mark.parametrize("T,E,k", [(5, 8, 1), (70, 40, 1), (130, 256, 1), (40, 600, 1), (300, 12, 2), (90, 60, 3),
+                                   (77, 200, 2), (50, 500, 4), (20, 1000, 3)])
+@pytest.mark.parametrize("dt", [FP32, BF16])
+def test_weights_that_sum_to_one_cancel_exactly(T, E, k, dt):
+    """Renormalized weights sum to 1, so with one choice they are 1 and have no gradient,
+    and with one choice far ahead theirs is small: near the formula's relative to
+    itself, not to grad_weights."""
+    import dense_gemm_nt_amd as g
+    x = randn(T, E, seed=T + E)
+    if k > 1:
+        x[torch.arange(T), torch.arange(T) % E] += 12.0                # far ahead of the others
+    x = x.to(dt)
+    r = g.route_topk(x.to(DEV), k)
+    ref = o.route(x, k, None, True)
+    gw, gl = randn(T, k, seed=1), torch.tensor(0.5)
+    got = g.route_topk_backward(x.to(DEV), r, gw.to(DEV))
+    if k == 1:
+        assert bool((r.weights == 1.0).all())
+        assert bool((got == 0).all())
+        both = g.route_topk_backward(x.to(DEV), r, gw.to(DEV), gl.to(DEV))
+        assert torch.equal(both, g.route_topk_backward(x.to(DEV), r, None, gl.to(DEV)))
+        return
+    d = o.route_backward(x, ref, True, gw, None)
+    w = ref["weights"]
+    total = ref["p"].gather(1, ref["ids"]).sum(1, keepdim=True)
+    # h_j = (d_j - sum_i d_i w_i) / S with d_j = g_j - g_0, the terms' errors being the
+    # weights' and S's (three and one of p's) and the roundings of k + 3 operations
+    far = (gw - gw[:, :1]).double().abs()
+    h = (far + (far * w).sum(1, keepdim=True)) / total
+    dp = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ref["ids"], h)
+    mag = ref["p"] * (dp + (ref["p"] * dp).sum(1, keepdim=True))
+    bound = (8 * _p_rel(x, E) + (E + 4 * k + 32) * 2.0 ** -23) * mag
+    if dt != FP32:
+        bound = bound + half_step(dt) * (d.abs() + bound) + 2.0 ** -133
+    err = (got.cpu().double() - d).abs()
+    assert bool((err <= bound + 1e-37).all()), float((err / (bound + 1e-37)).max())
