@@ -149,20 +149,56 @@ __device__ __forceinline__ void split16(float x, uint16_t &hi, uint16_t &lo)
 }
 
 // The same for the gradients' contraction over rows, whose FP32 results keep what
-// their operands hold: three bf16 parts (24 bits) or two fp16 ones (22).  With two
-// bf16 parts the adapters' gradients were 2.5e-6 off, with three as near as FP32
-// sums are; its MFMAs are few beside the bytes.
-template <int IN>
-constexpr int kParts = IN == IN_BF16 ? 3 : 2;
+// their operands hold: three bf16 parts, 24 bits, whatever the operands' type (with
+// two the adapters' gradients were 2.5e-6 off, with three as near as FP32 sums
+// are).  bf16 has FP32's range: two fp16 parts lose what is below 2^-25, and with it all of
+// a beginning adapter's gradients (dy and B of 1e-4: 12% off), and end at 65504.  So
+// FP16 operands are multiplied in bf16 as well, as two parts themselves
+// (bf16_halves).  The second of those is not multiplied with the third part (2^-26 of the
+// product), so a value that is not finite is held there alone: an infinity never meets
+// a second half of zero.  The low-rank values and gradients of 8192 rows, 12288 columns,
+// rank 32 take 115 us of FP16 operands and 100 of BF16 ones.
+constexpr int kParts = 3;
 
-template <int IN>
-__device__ __forceinline__ void split_parts(float x, uint16_t (&part)[kParts<IN>])
+__device__ __forceinline__ void split_parts(float x, uint16_t (&part)[kParts])
+{
+    const uint16_t hi = to16<IN_BF16>(x);
+    const bool finite = (hi & 0x7f80u) != 0x7f80u;
+    const float r = x - from16<IN_BF16>(hi);
+    const uint16_t mid = to16<IN_BF16>(r);
+    part[0] = finite ? hi : 0;
+    part[1] = finite ? mid : 0;
+    part[2] = finite ? to16<IN_BF16>(r - from16<IN_BF16>(mid)) : hi;
+}
+
+// What add_special takes as the first part of values held as split_parts makes them.
+__device__ __forceinline__ u32x4 first_part(const u32x4 (&part)[kParts])
+{
+    u32x4 y;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const uint32_t x = part[kParts - 1][d];
+        y[d] = part[0][d] | ((x & 0x7f80u) == 0x7f80u ? x & 0xffffu : 0u) |
+               ((x & 0x7f800000u) == 0x7f800000u ? x & 0xffff0000u : 0u);
+    }
+    return y;
+}
+
+// Eight finite fp16 values as sums of two bf16 ones, exactly: of 11 bits the first 8
+// (the FP32 value cut off) and the 3 left, in bf16's wider range.
+__device__ __forceinline__ void bf16_halves(u32x4 x, u32x4 &hi, u32x4 &lo)
 {
 #pragma unroll
-    for (int i = 0; i < kParts<IN>; ++i) {
-        part[i] = to16<IN>(x);
-        const float h = from16<IN>(part[i]);
-        x = __builtin_isfinite(h) ? x - h : 0.0f;
+    for (int d = 0; d < 4; ++d) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float v = from16<IN_FP16>((uint16_t)(x[d] >> (16 * i)));
+            h[i] = __builtin_bit_cast(uint32_t, v) & 0xffff0000u;
+            l[i] = __builtin_bit_cast(uint32_t, v - __builtin_bit_cast(float, h[i]));
+        }
+        hi[d] = h[0] >> 16 | h[1];
+        lo[d] = l[0] >> 16 | (l[1] & 0xffff0000u);
     }
 }
 
@@ -213,22 +249,21 @@ __device__ __forceinline__ u32x4 each16(u32x4 x, F f)
     return y;
 }
 
-// acc += x . (v[0] + v[1] + ...) where x holds infinities or NaNs: as the sum of x's finite
-// values (its others as +-1 to 2, by their exponents' highest bit: an infinite
-// hi then stays one, and a NaN a NaN)
-// and of what its others make, without any operand that could make a zero of
+// acc += x . v where x holds infinities or NaNs, and v is held as several parts: as the
+// sum of x's finite values (its others as +-1 to 2, by their exponents' highest bit: an
+// infinite v then stays one, and a NaN a NaN; finite(x) multiplies them by all parts)
+// and of what its others make, from v's first part hi, without any operand that could make a zero of
 // another row, or of a later part, into a NaN.  +-2^127 times +-2^127 (bf16) overflows to the infinity
 // that is due and is 0 where hi is masked to 0; a NaN (also that of infinity times 0) is
 // made as the sum of both infinities.  Where not `own`, v's parts are zeros that
-// are to add nothing.  mul(type, x, y) multiplies and adds to acc.  Rarely run, and
+// are to add nothing.  mul(x, y) multiplies bf16 values and adds to acc.  Rarely run, and
 // written for few registers: one operand pair at a time.
-template <int IN, int NP, typename F>
-__device__ __forceinline__ void add_special(u32x4 x, const u32x4 (&v)[NP], bool own, F mul)
+template <int IN, typename P, typename F>
+__device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, bool own, P finite, F mul)
 {
-    const u32x4 hi = v[0];
     constexpr uint32_t exp = IN == IN_BF16 ? 0x7f80u : 0x7c00u, big = 0x7f00u;
     auto step = [&](auto f, auto g, uint32_t flip) {
-        mul(std::integral_constant<int, IN_BF16>{}, each16(x, f), each16(hi, g) ^ flip);
+        mul(each16(x, f), each16(hi, g) ^ flip);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto is_nan = [](uint32_t v) { return (v & 0x7fffu) > exp ? big : 0u; };
@@ -244,9 +279,7 @@ __device__ __forceinline__ void add_special(u32x4 x, const u32x4 (&v)[NP], bool 
 #pragma unroll
         for (int d = 0; d < 4; ++d)
             y[d] = x[d] & ~((((x[d] & exps) + lowest) & 0x80008000u) >> 1);
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-            mul(std::integral_constant<int, IN>{}, y, v[i]);
+        finite(y);
         __builtin_amdgcn_sched_barrier(0);
     }
     step(inf, sign, 0u);
@@ -450,9 +483,13 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                     for (int fn = 0; fn < FN; ++fn) {
                         int again = s;                    // (a load of its own: registers)
                         asm volatile("" : "+s"(again));
-                        add_special<IN>(load_up(again, fn, rs), t, own, [&](auto type, u32x4 x, u32x4 y) {
-                            acc[fn][fm] = mfma32x32x16<type.value>(x, y, acc[fn][fm]);
-                        });
+                        add_special<IN>(
+                            load_up(again, fn, rs), t[0], own,
+                            [&](u32x4 x) {
+                                acc[fn][fm] = mfma32x32x16<IN>(x, t[0], acc[fn][fm]);
+                                acc[fn][fm] = mfma32x32x16<IN>(x, t[1], acc[fn][fm]);
+                            },
+                            [&](u32x4 x, u32x4 y) { acc[fn][fm] = mfma32x32x16<IN_BF16>(x, y, acc[fn][fm]); });
                     }
                 }
             }

@@ -416,11 +416,10 @@ __global__ __launch_bounds__(256) void lora_prepare(FlipArgs p, GradArgs a)
     }
 }
 
-// v's rows of a piece of 64 places of a stretch, scaled, split in two 16-bit values and
+// v's rows of a piece of 64 places of a stretch, scaled, split in bf16 parts and
 // transposed (zeros behind the stretch) to fragments as they go into the MFMA,
 // [piece][16 ranks][32 rows][part][lane] of 16 bytes: done once, where each column
 // tile of the gradient's kernel would do it again.
-template <int IN>
 __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
 {
     __shared__ float t[64][64 + 1];
@@ -452,7 +451,7 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
                 t[row][r + e] = v[e];
         }
         __syncthreads();
-        constexpr int NP = kParts<IN>;
+        constexpr int NP = kParts;
         u32x4 *out = p.pack[w] + (piece * (p.rank_pad / 16) + r0 / 16) * (NP * 128);
         // lane l of a fragment: rank l % 16, rows 8 (l / 16) .. +8 of its 32
         for (int i = tid; i < ranks * 8; i += 256) {
@@ -462,8 +461,8 @@ __global__ __launch_bounds__(256) void lora_pack(GradArgs p)
             for (int d = 0; d < 4; ++d) {
                 const float *src = &t[32 * ks + 8 * (lane >> 4) + 2 * d][16 * g + (lane & 15)];
                 uint16_t a[NP], b[NP];
-                split_parts<IN>(src[0], a);
-                split_parts<IN>(src[65], b);
+                split_parts(src[0], a);
+                split_parts(src[65], b);
 #pragma unroll
                 for (int h = 0; h < NP; ++h)
                     f[h][d] = (uint32_t)a[h] | (uint32_t)b[h] << 16;
@@ -496,7 +495,7 @@ __device__ __forceinline__ void store_z(uint8_t *zs, const u32x4 (&zr)[4], int t
 // acc[r][j] holds ranks 16 r .. +16 of columns 32 wave + 16 j .. +16.  vf: rank
 // 16 r + lane % 16, rows 32 ks + 8 (lane / 16) .. +8, of every part.
 template <int IN, int RT>
-__device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x4 (&vf)[RT][kParts<IN>],
+__device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x4 (&vf)[RT][kParts],
                                            f32x4 (&acc)[RT][2], int wave, int lane)
 {
     typedef short v4s __attribute__((ext_vector_type(4)));
@@ -514,6 +513,13 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
         const u32x2 lo = __builtin_bit_cast(u32x2, got[0]), hi = __builtin_bit_cast(u32x2, got[1]);
         zf[j] = (u32x4){lo[0], lo[1], hi[0], hi[1]};
     }
+    // z's finite values in one bf16 part or two, the second without v's last part
+    constexpr int ZP = IN == IN_FP16 ? 2 : 1;
+    auto parts_of = [](u32x4 x, u32x4 (&z)[2]) {
+        z[0] = x;
+        if constexpr (IN == IN_FP16)
+            bf16_halves(x, z[0], z[1]);
+    };
     // (an infinity in z times a value's later part, 0 or of the other sign, would
     // be a NaN: such pieces are taken apart)
     if (__builtin_amdgcn_ballot_w64((has_special<IN>(zf[0]) | has_special<IN>(zf[1])) != 0)) {
@@ -521,18 +527,32 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                add_special<IN>(zf[j], vf[r], true, [&](auto type, u32x4 x, u32x4 y) {
-                    acc[r][j] = mfma16x16x32<type.value>(y, x, acc[r][j]);
-                });
+                add_special<IN>(
+                    zf[j], first_part(vf[r]), true,
+                    [&](u32x4 x) {
+                        u32x4 z[2];
+                        parts_of(x, z);
+#pragma unroll
+                        for (int i = 0; i < ZP; ++i)
+#pragma unroll
+                            for (int h = 0; h < kParts - i; ++h)
+                                acc[r][j] = mfma16x16x32<IN_BF16>(vf[r][h], z[i], acc[r][j]);
+                    },
+                    [&](u32x4 x, u32x4 y) { acc[r][j] = mfma16x16x32<IN_BF16>(y, x, acc[r][j]); });
         return;
     }
+    u32x4 z[2][2];
+    parts_of(zf[0], z[0]);
+    parts_of(zf[1], z[1]);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int h = 0; h < kParts<IN>; ++h) {
-            acc[r][0] = mfma16x16x32<IN>(vf[r][h], zf[0], acc[r][0]);
-            acc[r][1] = mfma16x16x32<IN>(vf[r][h], zf[1], acc[r][1]);
-        }
+        for (int i = 0; i < ZP; ++i)
+#pragma unroll
+            for (int h = 0; h < kParts - i; ++h) {
+                acc[r][0] = mfma16x16x32<IN_BF16>(vf[r][h], z[0][i], acc[r][0]);
+                acc[r][1] = mfma16x16x32<IN_BF16>(vf[r][h], z[1][i], acc[r][1]);
+            }
 }
 
 // part[stretch][r][c] = sum over the stretch's rows m of s_a v[m][r] z[m][c]:
@@ -548,7 +568,7 @@ template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {
     __shared__ __attribute__((aligned(16))) uint8_t zs[2][kGradRows * 256];
-    constexpr int NP = kParts<IN>, FRAGS = RT * NP * 128, VL = (FRAGS + 255) / 256;
+    constexpr int NP = kParts, FRAGS = RT * NP * 128, VL = (FRAGS + 255) / 256;
     __shared__ u32x4 vs[2][VL * 256];
     const int w = blockIdx.z, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -767,17 +787,17 @@ __global__ __launch_bounds__(256) void lora_grad_few(GradArgs p)
                 __syncthreads();
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    u32x4 vf[RT][kParts<IN>];
+                    u32x4 vf[RT][kParts];
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
 #pragma unroll
                         for (int d = 0; d < 4; ++d) {
                             const float *src = vs + (t - g0 + 32 * ks + 8 * (lane >> 4) + 2 * d) * PITCH + 16 * r + (lane & 15);
-                            uint16_t a[kParts<IN>], b[kParts<IN>];
-                            split_parts<IN>(src[0], a);
-                            split_parts<IN>(src[PITCH], b);
+                            uint16_t a[kParts], b[kParts];
+                            split_parts(src[0], a);
+                            split_parts(src[PITCH], b);
 #pragma unroll
-                            for (int h = 0; h < kParts<IN>; ++h)
+                            for (int h = 0; h < kParts; ++h)
                                 vf[r][h][d] = (uint32_t)a[h] | (uint32_t)b[h] << 16;
                         }
                     multiply_z<IN, RT>(zs[turn], ks, vf, acc, wave, lane);
@@ -1218,7 +1238,7 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     g.first_stretch = c.take<int>(adapters + 1);
     const int64_t pieces = cdiv(M, 64) + adapters;     // each adapter's rows end inside one
     for (int i = 0; i < 2; ++i) {
-        g.pack[i] = c.take<u32x4>(pieces * (pad / 16) * (kParts<IN_BF16> * 128));
+        g.pack[i] = c.take<u32x4>(pieces * (pad / 16) * (kParts * 128));
         g.part[i] = c.take<float>((int64_t)g.max_stretches * pad * g.cols[i]);
     }
     return w;
@@ -1440,7 +1460,7 @@ gemm_status_t gemm_run_lora_backward(const void *dY, const void *X, const void *
                 return;
             }
             hipLaunchKernelGGL(lora_place, dim3(g.blocks + 1), dim3(kGroupThreads), 0, stream, g);
-            hipLaunchKernelGGL(lora_pack<in.value>, dim3(g.chunk / 64, g.max_stretches, 2), dim3(256), 0, stream, g);
+            hipLaunchKernelGGL(lora_pack, dim3(g.chunk / 64, g.max_stretches, 2), dim3(256), 0, stream, g);
             if (pad == 1)
                 hipLaunchKernelGGL((lora_grad<in.value, 1>), grid, dim3(256), 0, stream, g);
             else if (pad <= 3)

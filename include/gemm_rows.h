@@ -81,7 +81,8 @@ gemm_status_t gemm_run_lora(const void *X, const void *W, void *Y, int64_t M, in
  *   dX[m,:] = dY[m,:] W + s_a (dY[m,:] B_a) A_a          [M][K], dx_dtype
  *   dA_a    = s_a sum_{m: ids[m] = a} (dY[m,:] B_a)^T X[m,:]   [adapter][rank][K]
  *   dB_a    = s_a sum_{m: ids[m] = a} dY[m,:]^T (X[m,:] A_a^T) [adapter][N][rank]
- * dY B_a and X A_a^T are FP32 sums and enter the second products as above.
+ * dY B_a and X A_a^T are FP32 sums.  They enter dX as above; dA and dB take
+ * them, scaled, to 24 bits in FP32's range, whatever their size.
  * dA and dB are contiguous, of grad_dtype, and written whole: adapters without
  * a row get zeros.  dX may be NULL (not computed), and so may dA and dB, both
  * or neither.  K % 8 == 0, N % 8 == 0 and num_adapters <= 1024 (else

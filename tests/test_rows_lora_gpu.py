@@ -388,3 +388,64 @@ def test_python_refusals():
         g.gemm_lora_backward(torch.zeros(9, 24, device=DEV), **c)
     with pytest.raises(ValueError):
         g.gemm_lora_backward(torch.zeros(9, 23, dtype=BF16, device=DEV), **c)
+
+
+# ---- low-rank values of any size ----
+
+def _parts(rows, n, dt, seed):
+    """[rows, n] of dt whose rows begin with +-1, +-2^-9 and +-2^-18 and are zero behind: their
+    sum takes 19 bits, which no two bf16 values and, scaled down, no two fp16 ones hold."""
+    v = torch.zeros(rows, n)
+    sign = torch.randint(0, 2, (rows, 3), generator=torch.Generator().manual_seed(seed)) * 2.0 - 1.0
+    v[:, :3] = sign * torch.tensor([1.0, 2.0 ** -9, 2.0 ** -18])
+    return v.to(dt)
+
+
+def _signs(*shape, seed, dt):
+    return (torch.randint(0, 2, shape, generator=torch.Generator().manual_seed(seed)) * 2.0 - 1.0).to(dt)
+
+
+SCALES = [2.0 ** -40, 2.0 ** -24, 1.0, 2.0 ** 18, 2.0 ** 40]
+
+
+@pytest.mark.parametrize("M,R", [(4, 16), (200, 8), (300, 40), (250, 64), (1100, 16), (700, 64), (2300, 24), (1500, 128)])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_gradients_keep_low_rank_values_of_any_size(M, R, dt):
+    """Every adapter has one row that is not zero: its dA and dB are single products of low-rank
+    values of 19 bits, as above."""
+    import dense_gemm_nt_amd as g
+    N, K, L = 264, 328, 3
+    x, dy = torch.zeros(M, K, dtype=dt), torch.zeros(M, N, dtype=dt)
+    ids = torch.arange(M, dtype=torch.int32) % (L + 1) - 1
+    at = torch.tensor([int((ids == a).nonzero()[-1]) for a in range(L)])
+    x[at], dy[at] = _parts(L, K, dt, 1), _parts(L, N, dt, 2)
+    x[at, 3:], dy[at, 3:] = randn(L, K - 3, seed=3, dtype=dt), randn(L, N - 3, seed=4, dtype=dt)
+    c = dict(x=x, W=torch.zeros(N, K, dtype=dt), A=torch.zeros(L, R, K, dtype=dt),
+             B=torch.zeros(L, N, R, dtype=dt), ids=ids, scale=torch.ones(L))
+    c["A"][:, :, :3], c["B"][:, :3] = _signs(L, R, 3, seed=5, dt=dt), _signs(L, 3, R, seed=6, dt=dt)
+    ref = o.lora_backward(dy, **c)
+    for s in SCALES:
+        got = g.gemm_lora_backward(dy.to(DEV), **_dev({**c, "scale": torch.full((L,), s)}), need_dx=False)
+        for name, v in zip(("dA", "dB"), got[1:]):
+            want = ref[name][0] * s
+            check(v, want, want.abs() * 2.0 ** -20, "%s times %g" % (name, s))
+
+
+@pytest.mark.parametrize("M,R", [(300, 16), (1100, 32)])
+@pytest.mark.parametrize("std_dy,std_B", [(1e-4, 1e-4), (1e-3, 1e-4), (1e-2, 1e-3), (300.0, 30.0)])
+def test_fp16_gradients_of_a_beginning_adapter(M, R, std_dy, std_B):
+    """Adapters begin at B = 0: dA and dB against 64 bits in the 2-norm.  A rounding to FP32
+    is 2^-24 off; of the 1024 of a sum sqrt(1024) add up at random, and the bound is four
+    times that, 2^-17."""
+    import dense_gemm_nt_amd as g
+    N, K, L, dt = 1024, 512, 2, FP16
+    c = _case(M, N, K, R, L, "mixed", dt)
+    c["B"] = randn(L, N, R, seed=4, dtype=dt, std=std_B)
+    dy = randn(M, N, seed=9, dtype=dt, std=std_dy)
+    _, dA, dB = g.gemm_lora_backward(dy.to(DEV), **_dev(c), need_dx=False)
+    ref = o.lora_backward(dy, **c)
+    for name, v in (("dA", dA), ("dB", dB)):
+        r = ref[name][0]
+        off = float((v.cpu().double() - r).norm() / r.norm())
+        print("%s dy %g B %g: off %.3g" % (name, std_dy, std_B, off), flush=True)
+        assert off <= 2.0 ** -17
