@@ -4,7 +4,7 @@
 
 #define GNT_EXT_KERNEL(name) name##_lora
 #define GNT_EXT_ARGS LoraArgs
-#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) lora_add<IN, 1, true>(p, acc, r0, c0, split, lane);
+#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) lora_add<IN, 1, low_parts<IN, OUT> == 2, low_parts<IN, OUT>>(p, acc, r0, c0, split, lane);
 #include "../gemm_nt_pp2.hpp"
 
 #ifndef GNT_LORA_BNM

@@ -3,7 +3,7 @@
 
 #define GNT_EXT_KERNEL(name) name##_lora
 #define GNT_EXT_ARGS LoraArgs
-#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) lora_add<IN, 8, true>(p, acc, r0, c0, split, lane);
+#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) lora_add<IN, 8, true, low_parts<IN, OUT>>(p, acc, r0, c0, split, lane);
 #include "../gemm_nt_w4.hpp"
 
 namespace gnt {

@@ -132,21 +132,29 @@ __device__ __forceinline__ float from16(uint16_t h)
         return static_cast<float>(__builtin_bit_cast(_Float16, h));
 }
 
-// An FP32 value as the sum of two 16-bit ones, for the matrix cores: hi the
-// nearest, lo the nearest to what is left, so hi + lo is within 2^-16 (bf16) or
-// 2^-22 (fp16; 2^-25 absolute below its normal range) of x relative to it, where
-// one 16-bit value would be within 2^-8 or 2^-11.  The low-rank products are
-// intermediates that the caller never sees: rounding them to 16 bits would put an
-// error into an FP32 output that nothing else in it has.  It costs a second MFMA per rank-16 step, of which an
-// output tile has rank / 16 beside its K / 16.  An infinite hi (an infinity, or
-// past fp16's range) stands alone.
-template <int IN>
-__device__ __forceinline__ void split16(float x, uint16_t &hi, uint16_t &lo)
+// An FP32 value as the sum of NP 16-bit ones, for the matrix cores: each the nearest to what
+// the ones before it leave.  Two bf16 values are within 2^-17 of x relative to it, two
+// fp16 ones within 2^-23 while x is at least 2^-3 (the caller sees to that: below 2^-14 fp16's
+// steps no longer shrink), where one value would be within 2^-9 or 2^-12.  The low-rank
+// products are intermediates that the caller never sees: rounding them to 16 bits would
+// put an error into the output that nothing else in it has.  A result of 16 bits does not
+// show what two leave (a 64th of its own half step at most); an FP32 one of BF16 operands
+// does, and takes three (low_parts).  Each costs an MFMA per rank-16 step, of which an output
+// tile has rank / 16 beside its K / 16.  An infinite part (an infinity, or past fp16's
+// range) stands alone.
+template <int IN, int NP>
+__device__ __forceinline__ void split16(float x, uint16_t (&part)[NP])
 {
-    hi = to16<IN>(x);
-    const float h = from16<IN>(hi);
-    lo = __builtin_isfinite(h) ? to16<IN>(x - h) : (uint16_t)0;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        part[i] = to16<IN>(x);
+        const float h = from16<IN>(part[i]);
+        x = __builtin_isfinite(h) ? x - h : 0.0f;
+    }
 }
+
+template <int IN, int OUT>
+constexpr int low_parts = IN == IN_BF16 && OUT == OUT_FP32 ? 3 : 2;
 
 // The same for the gradients' contraction over rows, whose FP32 results keep what
 // their operands hold: three bf16 parts, 24 bits, whatever the operands' type (with
@@ -304,11 +312,18 @@ __device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, bool own, P finit
 // fragments are in flight together, and AHEAD the next ranks' low-rank values (as
 // the tile leaves registers for).  Rows without an adapter, and ids that name
 // none, add nothing.  Nothing here waits on the tile's own loads.
+//
+// fp16 parts of a low-rank value hold its bits only between 2^-3 and 2^15.  A row whose
+// largest value of a rank step lies outside has its accumulators and the values in units of a
+// power of two from then on, in which that value is just below 2^15 (2^-60 to 2^60: an
+// accumulator of FP16 products is below 2^63, so its units keep it in FP32's range), and
+// they are turned back at the end: multiplications by powers of two, in the rare tile.
+// Without it a value of 2^-25 was lost and one of 2^16 infinite, also in FP32 results.
 // In one launch each: 5001 x 8192 x 8192, rank 64, 4 adapters in runs 642 us against
 // 610 without adapters; 64 x 10240 x 8192, rank 16, 48 adapters 46.5 against 38.4; 1 x
 // 4096 x 4096, rank 16 13.2 in all.  What it adds is the round trips of ids,
 // low-rank values and up rows, one after the other, at the end of a tile.
-template <int IN, int NB, bool AHEAD, int FN, int FM>
+template <int IN, int NB, bool AHEAD, int NP, int FN, int FM>
 __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM], int r0, int c0, int split,
                                          int lane)
 {
@@ -392,7 +407,19 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
             }
         }
     };
-    float scale[FM];
+    float scale[FM];                   // (times the row's units)
+    bool units = false;                // some row's are not 1
+    auto shift_of = [&](int fm) {      // the units' exponent, without a register of its own
+        return id[fm] >= 0 ? __builtin_amdgcn_frexp_expf(scale[fm]) - __builtin_amdgcn_frexp_expf(p.scale[id[fm]]) : 0;
+    };
+    auto rescale = [&](int fm, int by) {
+        const float f = __builtin_ldexpf(1.0f, by);
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[fn][fm][e] *= f;
+    };
     start();
     fetch(0);
     if constexpr (AHEAD)
@@ -403,8 +430,8 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
     for (int rs = 0; rs < p.rank; rs += 16) {
         if constexpr (!AHEAD)
             fetch_low(rs);
-        // scaled, and split in two
-        u32x4 hi[FM], lo[FM];
+        // scaled, and split in parts
+        u32x4 part[NP][FM];
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm) {
             f32x4 v0 = low[fm][0], v1 = low[fm][1];
@@ -419,13 +446,41 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
             }
             v0 *= scale[fm];
             v1 *= scale[fm];
+            if constexpr (IN == IN_FP16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    top = fmaxf(top, fmaxf(__builtin_fabsf(v0[d]), __builtin_fabsf(v1[d])));
+                const unsigned bits = __builtin_bit_cast(unsigned, top);
+                const auto both = __builtin_amdgcn_permlane32_swap(bits, bits, false, false);
+                const unsigned lower = both[0], upper = both[1];   // (a row's 16 ranks are in two lanes)
+                top = fmaxf(__builtin_bit_cast(float, lower), __builtin_bit_cast(float, upper));
+                const bool out = top > 0.0f && __builtin_isfinite(top) && (top < 0.125f || top >= 32768.0f);
+                if (__builtin_amdgcn_ballot_w64(out)) {
+                    mfma_settle();
+                    // top in [2^(e - 1), 2^e): to just below 2^15; but units that a large
+                    // value has lowered are not raised again, over what it left in the sums
+                    const int e = __builtin_amdgcn_frexp_expf(top), was = shift_of(fm);
+                    const int to = max(-60, min(60, was + 15 - e));
+                    const int by = out && (to < was || was >= 0) ? to - was : 0;
+                    rescale(fm, by);
+                    scale[fm] = __builtin_ldexpf(scale[fm], by);
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        v0[d] = __builtin_ldexpf(v0[d], by);
+                        v1[d] = __builtin_ldexpf(v1[d], by);
+                    }
+                    units = true;
+                }
+            }
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
-                uint16_t h0, l0, h1, l1;
-                split16<IN>(d < 2 ? v0[2 * d] : v1[2 * d - 4], h0, l0);
-                split16<IN>(d < 2 ? v0[2 * d + 1] : v1[2 * d - 3], h1, l1);
-                hi[fm][d] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-                lo[fm][d] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+                uint16_t a[NP], b[NP];
+                split16<IN>(d < 2 ? v0[2 * d] : v1[2 * d - 4], a);
+                split16<IN>(d < 2 ? v0[2 * d + 1] : v1[2 * d - 3], b);
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+                    part[i][fm][d] = (uint32_t)a[i] | (uint32_t)b[i] << 16;
             }
         }
         // (the next ranks' values are on their way while these are multiplied)
@@ -451,11 +506,12 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                     const bool own = id[fm] == a[b];
                     if (__builtin_amdgcn_ballot_w64(own) == 0)
                         continue;
-                    const u32x4 th = own ? hi[fm] : zero, tl = own ? lo[fm] : zero;
 #pragma unroll
-                    for (int fn = 0; fn < FN; ++fn) {
-                        acc[fn][fm] = mfma32x32x16<IN>(up[b][fn], th, acc[fn][fm]);
-                        acc[fn][fm] = mfma32x32x16<IN>(up[b][fn], tl, acc[fn][fm]);
+                    for (int i = 0; i < NP; ++i) {
+                        const u32x4 t = own ? part[i][fm] : zero;
+#pragma unroll
+                        for (int fn = 0; fn < FN; ++fn)
+                            acc[fn][fm] = mfma32x32x16<IN>(up[b][fn], t, acc[fn][fm]);
                     }
                 }
             }
@@ -478,16 +534,16 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
                     const bool own = id[fm] == s;
                     if (__builtin_amdgcn_ballot_w64(own) == 0)
                         continue;
-                    const u32x4 t[2] = {own ? hi[fm] : zero, own ? lo[fm] : zero};
 #pragma unroll
                     for (int fn = 0; fn < FN; ++fn) {
                         int again = s;                    // (a load of its own: registers)
                         asm volatile("" : "+s"(again));
                         add_special<IN>(
-                            load_up(again, fn, rs), t[0], own,
+                            load_up(again, fn, rs), own ? part[0][fm] : zero, own,
                             [&](u32x4 x) {
-                                acc[fn][fm] = mfma32x32x16<IN>(x, t[0], acc[fn][fm]);
-                                acc[fn][fm] = mfma32x32x16<IN>(x, t[1], acc[fn][fm]);
+#pragma unroll
+                                for (int i = 0; i < NP; ++i)
+                                    acc[fn][fm] = mfma32x32x16<IN>(x, own ? part[i][fm] : zero, acc[fn][fm]);
                             },
                             [&](u32x4 x, u32x4 y) { acc[fn][fm] = mfma32x32x16<IN_BF16>(x, y, acc[fn][fm]); });
                     }
@@ -500,6 +556,10 @@ __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM
         }
     }
     mfma_settle();
+    if (units)
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+            rescale(fm, -shift_of(fm));
 }
 
 }  // namespace gnt

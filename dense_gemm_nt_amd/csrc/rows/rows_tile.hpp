@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
     }
     mfma_settle();
     if constexpr (!ROUTED) {
-        lora_add<IN, 4, true>(p, acc, m0 + wm, n0 + wn, split, lane);
+        lora_add<IN, 4, true, low_parts<IN, OUT>>(p, acc, m0 + wm, n0 + wn, split, lane);
         if (p.inreduce) {
             // (the ring is behind the barrier's last reader once the partials are out)
             if (!splitk_arrive<4, 2, 2>(p, acc, tm * p.tiles_n + tn, split, wave, lane,

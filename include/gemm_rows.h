@@ -67,8 +67,10 @@ typedef struct {
  * GEMM_FP32); epi as gemm_run_ex's (NULL: the identity).  The adapters' part is
  * added to the projection's FP32 sums, so Y is rounded once.  The low-rank
  * values X A_a^T are FP32 sums; scaled, they enter the second product as the
- * sum of two values of the operands' type (so FP16 operands need
- * |s_a X A_a^T| <= 65504; above it the result is infinite or NaN).
+ * sum of two values of the operands' type (three where BF16 operands have an FP32
+ * result), of FP16 operands in units of a power of two of each row's, so that small and
+ * large ones keep their bits: up to 2^75 (above it the result is infinite or NaN),
+ * and from 2^-40 of the row's largest one or 2^-85 on.
  *   K % 8 == 0 (else GEMM_ERR_UNSUPPORTED).  K = 0: the epilogue of zero. */
 gemm_status_t gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t num_adapters,
                                   int64_t rank, int64_t *bytes);

@@ -449,3 +449,41 @@ def test_fp16_gradients_of_a_beginning_adapter(M, R, std_dy, std_B):
         off = float((v.cpu().double() - r).norm() / r.norm())
         print("%s dy %g B %g: off %.3g" % (name, std_dy, std_B, off), flush=True)
         assert off <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("M,N,K,R,L", [(1, 136, 64, 16, 1), (40, 264, 72, 8, 3), (64, 1000, 512, 16, 9),
+                                       (100, 1000, 512, 32, 7), (256, 2048, 8192, 16, 20), (256, 8192, 8192, 24, 5),
+                                       (1500, 3200, 128, 40, 3), (2048, 4096, 64, 16, 4), (2050, 4100, 72, 64, 5)])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_forward_keeps_low_rank_values_of_any_size(M, N, K, R, L, dt):
+    """W is zero and every output one product s t[r] B[n, r] of a low-rank value t of 19 bits: in
+    FP32 it is off by the roundings of its parts' products as they are added (2^-23
+    each, at most six, and the conversions of the parts are exact)."""
+    import dense_gemm_nt_amd as g
+    c = dict(x=_parts(M, K, dt, 1), W=torch.zeros(N, K, dtype=dt), A=torch.zeros(L, R, K, dtype=dt),
+             B=torch.zeros(L, N, R, dtype=dt), ids=_ids(M, L, "mixed", 3), scale=torch.ones(L))
+    c["A"][:, :, :3] = _signs(L, R, 3, seed=2, dt=dt)
+    n = torch.arange(N)
+    c["B"][:, n, n % R] = randn(L, N, seed=4, dtype=dt)
+    y = o.lora(**c)[0]
+    for s in SCALES:
+        got = g.gemm_lora(**_dev({**c, "scale": torch.full((L,), s)}), out_dtype=FP32)
+        check(got, y * s, (y * s).abs() * 2.0 ** -20, "low-rank values times %g" % s)
+
+
+@pytest.mark.parametrize("M,N,K,R,L", [(3, 136, 64, 16, 2), (300, 256, 512, 40, 7), (777, 4096, 2048, 8, 3),
+                                       (1100, 264, 328, 24, 3), (2100, 512, 2048, 16, 2)])
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_input_gradient_keeps_low_rank_values_of_any_size(M, N, K, R, L, dt):
+    import dense_gemm_nt_amd as g
+    c = dict(x=torch.zeros(M, K, dtype=dt), W=torch.zeros(N, K, dtype=dt), A=torch.zeros(L, R, K, dtype=dt),
+             B=torch.zeros(L, N, R, dtype=dt), ids=_ids(M, L, "mixed", 3), scale=torch.ones(L))
+    c["B"][:, :3] = _signs(L, 3, R, seed=2, dt=dt)
+    k = torch.arange(K)
+    c["A"][:, k % R, k] = randn(L, K, seed=4, dtype=dt)
+    dy = _parts(M, N, dt, 1)
+    dx = o.lora_backward(dy, **c)["dx"][0]
+    for s in SCALES:
+        got = g.gemm_lora_backward(dy.to(DEV), **_dev({**c, "scale": torch.full((L,), s)}), dx_dtype=FP32,
+                                   need_adapters=False)[0]
+        check(got, dx * s, (dx * s).abs() * 2.0 ** -20, "input gradient times %g" % s)
