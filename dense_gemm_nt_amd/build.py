@@ -34,7 +34,8 @@ ROWS_SOURCES = [os.path.join(ROWS, f) for f in (
     "launch_lora_pp2_km.hip", "launch_routed_tiles.hip", "launch_routed_pp2.hip",
     "launch_routed_pp2_km.hip", "launch_routed_pp2_mm.hip", "launch_rows_tile.hip")]
 ROWS_HEADERS = [os.path.join(ROWS, f) for f in ("rows_common.hpp", "rows_group.hpp",
-                                                "rows_host.hpp", "rows_launch.hpp", "rows_tile.hpp")] + \
+                                                "rows_host.hpp", "rows_index.hpp", "rows_launch.hpp",
+                                                "rows_tile.hpp")] + \
     [os.path.join(ROOT, "include", "gemm_rows.h")]
 ROWS_LIB = os.path.join(PKG, "libgemm_rows.so")
 ARCH = "gfx950"

@@ -4,6 +4,7 @@
 // lora_add in rows_common.hpp.)
 #include "rows_group.hpp"
 #include "rows_host.hpp"
+#include "rows_index.hpp"
 #include "rows_launch.hpp"
 
 namespace gnt {
@@ -33,6 +34,13 @@ struct ShrinkPair {
     int num_counters;
 };
 
+__device__ __forceinline__ void clear_counters(const ShrinkPair &pair)
+{
+    const Walk w = clear_walk(blockIdx.x, blockIdx.y, blockIdx.z, gridDim.x, gridDim.y, gridDim.z, blockDim.x, threadIdx.x);
+    for (int64_t i = w.first; i < pair.num_counters; i += w.step)
+        pair.counters[i] = 0;
+}
+
 // low[s][m][r] = sum over split s of K of x[m][k] down_a[r][k], a = ids[m].
 //
 // One block takes 16 rows and one K split; its eight waves take K in steps
@@ -56,9 +64,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkPair pair
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    const int linear = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
-    for (int i = linear * (W * 64) + tid; i < pair.num_counters; i += gridDim.x * gridDim.y * gridDim.z * W * 64)
-        pair.counters[i] = 0;
+    clear_counters(pair);
 
     const int r0 = blockIdx.x * ROWS;
     const int m = r0 + (lane & (ROWS - 1));
@@ -156,9 +162,7 @@ __global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkPair pair)
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int linear = blockIdx.z * gridDim.x + blockIdx.x;
-    for (int i = linear * 256 + tid; i < pair.num_counters; i += gridDim.x * gridDim.z * 256)
-        pair.counters[i] = 0;
+    clear_counters(pair);
 
     const int r0 = blockIdx.x * 64, rows = min(64, p.M - r0);
     const int a_in = lane < rows ? p.ids[r0 + lane] : -1;

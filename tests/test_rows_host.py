@@ -213,3 +213,39 @@ def test_workspace_sizes(L):
         for fn in ("gemm_lora_workspace", "gemm_lora_backward_workspace"):
             st, n = b(fn, M, 4096, 4096, 8, 64)
             assert st == OK and n % 256 == 0 and n >= M * 64 * 4
+
+
+def test_cleared_words_of_the_largest_grid(L, tmp_path):
+    """Which counters a thread of the low-rank products' kernels clears, at the most rows that are
+    accepted (below 2^30; 64 a block of 256 threads, two products of K splits): a number past 2^31
+    must not come out negative, below every count, nor a step of 2^32 as zero."""
+    import subprocess
+    from dense_gemm_nt_amd import build
+    assert _lora(L, _adapters(), M=1 << 30) == UNSUPPORTED and _lora(L, _adapters(), M=(1 << 30) - 1) == INVALID
+    src = tmp_path / "walk.cpp"
+    src.write_text('''
+#include <cstdio>
+#include <initializer_list>
+#include "rows_index.hpp"
+int main()
+{
+    const uint32_t gx = ((1u << 30) - 1 + 63) / 64;
+    for (uint32_t gz : {1u, 2u, 8u, 32u})
+        for (uint32_t x : {0u, 1u << 23, gx - 1})
+            for (uint32_t z : {0u, gz - 1}) {
+                const gnt::Walk w = gnt::clear_walk(x, 0, z, gx, 1, gz, 256, 255);
+                printf("%u %u %u %lld %lld\\n", x, z, gz, (long long)w.first, (long long)w.step);
+            }
+}
+''')
+    exe = str(tmp_path / "walk")
+    subprocess.run(["g++", "-std=c++17", "-I" + build.ROWS, str(src), "-o", exe], check=True)
+    gx = (1 << 24)
+    out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split("\n")[:-1]
+    assert len(out) == 24
+    for line in out:
+        x, z, gz, first, step = map(int, line.split())
+        assert first == (z * gx + x) * 256 + 255 and step == gx * gz * 256
+    # and the kernels go by it: nothing else in them writes counters
+    text = open(os.path.join(build.ROWS, "rows_lora.hip")).read()
+    assert text.count("pair.counters[") == 1 and text.count("    clear_counters(pair);") == 2
