@@ -35,7 +35,8 @@ struct RoutedArgs : KernelArgs {
     int experts;
     int rows;                 // of the sorted arrays
     int tile_m;               // rows (weight gradient: rows of dW_e) of a tile
-    int tail;                 // rows behind the last expert's are set to zero
+    int tail;                 // rows of no expert (before the first's, behind the last's)
+                              // are set to zero
     int wgrad;                // dW_e [N][K] = dY_e^T X_e, else C_e = X_e op(W_e)
     int64_t b_stride;         // elements between experts' W
     int64_t c_stride;         // wgrad: elements between experts' dW
@@ -74,12 +75,13 @@ __device__ __forceinline__ bool routed_lookup(RoutedArgs &p, int &tm, int &tn)
     const int E = p.experts, rows = p.rows;
     auto at = [&](int e) { return min(max(p.offsets[e], 0), rows); };
     int top = 0, before = 0;                 // carried over the experts scanned
-    for (int e0 = 0; e0 <= E; e0 += 64) {
+    for (int e0 = 0; e0 <= E + 1; e0 += 64) {
         const int e = e0 + lane;
         const int lo = e <= E ? at(e) : 0, hi = e < E ? at(e + 1) : 0;
-        const int start = max(top, wave_scan(lo, lane, [](int a, int b) { return max(a, b); }));
-        // entry E is the tail's
-        const int count = e < E ? max(start, hi) - start : (e == E && p.tail ? rows - start : 0);
+        const int most = max(top, wave_scan(lo, lane, [](int a, int b) { return max(a, b); }));
+        // entry E is the rows behind the last expert's, entry E + 1 those before the first's
+        const int start = e <= E ? most : 0;
+        const int count = e < E ? max(start, hi) - start : !p.tail ? 0 : e == E ? rows - start : e == E + 1 ? at(0) : 0;
         const int tall = p.wgrad ? (e < E ? p.M : 0) : count;
         const int tiles = ((tall + p.tile_m - 1) / p.tile_m) * p.tiles_n;
         const int past = before + wave_scan(tiles, lane, [](int a, int b) { return a + b; });
@@ -98,7 +100,7 @@ __device__ __forceinline__ bool routed_lookup(RoutedArgs &p, int &tm, int &tn)
                 p.B += (int64_t)(g < E ? g : 0) * p.b_stride;
                 p.C = static_cast<uint8_t *>(p.C) + (int64_t)s * p.ldc * p.c_size;
                 p.M = n;
-                p.K = g < E ? p.K : 0;       // the tail: a sum over nothing
+                p.K = g < E ? p.K : 0;       // rows of no expert: a sum over nothing
             }
             p.tiles_m = (p.M + p.tile_m - 1) / p.tile_m;
             p.k_tiles = (p.K + 63) / 64;
@@ -108,7 +110,7 @@ __device__ __forceinline__ bool routed_lookup(RoutedArgs &p, int &tm, int &tn)
             tile_order(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
             return true;
         }
-        top = __builtin_amdgcn_readlane(start, 63);
+        top = __builtin_amdgcn_readlane(most, 63);
         before = __builtin_amdgcn_readlane(past, 63);
     }
     return false;

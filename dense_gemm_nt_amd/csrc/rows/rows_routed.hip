@@ -132,7 +132,8 @@ gemm_status_t gemm_run_routed(const void *X, const void *W, void *C, const int32
         fn = (a.tile_m == 256 ? kRouted_pp2 : a.tile_m == 128 ? kRouted_128 : kRouted_32)[in_dtype][out_dtype];
     }
     a.tiles_n = (int)cdiv(N, bn);
-    return launch(fn, a, tall(a.tile_m) * a.tiles_n, stream);
+    // (and a tile row more where rows before the first expert's are a run of their own)
+    return launch(fn, a, (tall(a.tile_m) + (a.tail ? 1 : 0)) * a.tiles_n, stream);
 }
 
 gemm_status_t gemm_run_routed_wgrad(const void *dY, const void *X, void *dW,

@@ -307,8 +307,8 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
     expert, W [E, N, K], offsets int32 [E + 1] on the device (route_topk's).  W[e]
     is K-major (unit stride along K) or a transposed view of [E, K, N] (unit
     stride along N): gemm_routed(dy, W.transpose(1, 2), offsets) is the gradient
-    in x of gemm_routed(x, W, offsets).  Rows behind offsets[E] are zero in a new
-    result, and left as they are in `out`."""
+    in x of gemm_routed(x, W, offsets).  Rows of no expert (before offsets[0], behind
+    offsets[E]) are zero in a new result, and left as they are in `out`."""
     import torch
     if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
         raise ValueError("x must be [S, K] and W [E, N, K], got %s and %s"

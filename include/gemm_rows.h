@@ -148,7 +148,8 @@ gemm_status_t gemm_run_route_backward(const void *logits, const gemm_routing_t *
                                       int64_t top_k, int renormalize, int dtype,
                                       hipStream_t stream);
 
-/* Rows behind the last expert's: left as they are, or set to zero. */
+/* Rows of no expert, before the first expert's and behind the last's: left as they
+ * are, or set to zero. */
 typedef enum { GEMM_TAIL_KEEP = 0, GEMM_TAIL_ZERO = 1 } gemm_tail_t;
 
 /* The experts' products over rows sorted by expert: for offsets[e] <= i <
@@ -158,8 +159,9 @@ typedef enum { GEMM_TAIL_KEEP = 0, GEMM_TAIL_ZERO = 1 } gemm_tail_t;
  * X the output gradient, the input gradient of the former).
  *   offsets  device, num_experts + 1 values; read as clamped to [0, rows] and
  *            to their running maximum, so a decreasing or too large one leaves
- *            its expert without rows; rows before offsets[0] are left alone
- *   tail     gemm_tail_t, for the rows behind the last expert's
+ *            its expert without rows
+ *   tail     gemm_tail_t, for the rows before offsets[0] and behind the last
+ *            expert's
  *   num_experts <= 1024; K % 8 == 0; rows = 0 or N = 0 enqueues nothing */
 gemm_status_t gemm_run_routed(const void *X, const void *W, void *C, const int32_t *offsets,
                               int64_t rows, int64_t N, int64_t K, int64_t num_experts, int64_t ldx,

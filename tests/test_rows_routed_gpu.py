@@ -234,3 +234,28 @@ def test_rows_more_than_32_bits_apart():
         assert a is b or torch.equal(a, b)
     gw = torch.ones_like(r.weights)
     assert torch.equal(g.route_topk_backward(fdy, f, gw), g.route_topk_backward(dy, r, gw))
+
+
+@pytest.mark.parametrize("S,E,N,K,mn", [(40, 8, 300, 136, False), (700, 7, 264, 328, False), (2000, 4, 700, 1032, False),
+                                        (2500, 3, 8300, 72, False), (700, 7, 264, 328, True), (2500, 3, 8304, 136, True),
+                                        (9, 70, 40, 16, False), (300, 64, 136, 64, False)])
+def test_rows_of_no_expert_are_zero_in_a_new_result(S, E, N, K, mn):
+    """A slice of a router's offsets (the experts held here) begins behind row 0: the rows before it
+    belong to no expert, as those behind the last do."""
+    import dense_gemm_nt_amd as g
+    x, W = randn(S, K, seed=1, dtype=BF16).to(DEV), randn(E, N, K, seed=2, dtype=BF16).to(DEV)
+    Wd = W.transpose(1, 2).contiguous().transpose(1, 2) if mn else W
+    for off in (_offsets(S, E, "late"), torch.full((E + 1,), S, dtype=torch.int32), _offsets(S, E, "wild", 3),
+                torch.full((E + 1,), 2 ** 31 - 1, dtype=torch.int32), torch.full((E + 1,), -7, dtype=torch.int32)):
+        ref, s = o.routed(x.cpu(), W.cpu(), off)
+        mine = torch.zeros(S, dtype=torch.bool)
+        for a, b in o.segments(off.tolist(), S)[0]:
+            mine[a:b] = True
+        stale = torch.full((S, N), 7.0, dtype=FP32, device=DEV)      # what the allocator gives next
+        del stale
+        got = g.gemm_routed(x, Wd, off.to(DEV), out_dtype=FP32).cpu()
+        assert bool((got[~mine] == 0).all())
+        check(got[mine], ref[mine], sum_bound(ref, s, K, FP32)[mine], "late offsets")
+        out = torch.full((S, N), 5.0, dtype=FP32, device=DEV)
+        g.gemm_routed(x, Wd, off.to(DEV), out=out)
+        assert torch.equal(out.cpu()[mine], got[mine]) and bool((out.cpu()[~mine] == 5.0).all())
