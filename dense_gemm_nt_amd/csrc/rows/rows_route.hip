@@ -154,6 +154,20 @@ __device__ __forceinline__ void store_logits(void *base, int64_t row, int c, int
     }
 }
 
+// e^d for d <= 0, NaN for NaN: 2^(d log2 e), with what the rounding of that product left put
+// back to first order.  Without it the result is off by 2^-24 for each unit of d: at
+// d = -80, 2^-18.  (An infinite d has no such rest; below -200 all is zero anyway.)
+__device__ __forceinline__ float exp_below(float d)
+{
+    constexpr float log2e = 1.44269504088896340736, ln2 = 0.69314718055994530942;
+    constexpr float log2e_rest = 1.44269504088896340736 - (double)log2e;
+    d = d < -200.0f ? -200.0f : d;
+    const float t = d * log2e;
+    const float rest = __builtin_fmaf(d, log2e_rest, __builtin_fmaf(d, log2e, -t));
+    const float r = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(r * rest, ln2, r);
+}
+
 // A row's softmax from its logits: p in place of x; false for a row without an
 // open expert.  key is the ranking value of each logit (NaN as the lowest
 // finite one).
@@ -170,16 +184,17 @@ __device__ __forceinline__ bool softmax_row(f32x4 (&x)[Q], f32x4 (&key)[Q])
         }
     top = row_max<LPR>(top);
     const bool open = top > -INFINITY;
+    top = open ? top : 0.0f;           // (a closed row's exponentials are then zeros)
     float sum = 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[q][i] = open ? __expf(x[q][i] - top) : 0.0f;
+            x[q][i] = exp_below(x[q][i] - top);
             sum += x[q][i];
         }
     sum = row_sum<LPR>(sum);
-    const float inv = open ? __builtin_amdgcn_rcpf(sum) : 0.0f;      // within an ulp
+    const float inv = open ? 1.0f / sum : 0.0f;
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
@@ -295,10 +310,10 @@ __device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, i
             float total = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v / 4][v % 4] = __expf(x[v / 4][v % 4] - top);
+                x[v / 4][v % 4] = exp_below(x[v / 4][v % 4] - top);
                 total += x[v / 4][v % 4];
             }
-            inv = __builtin_amdgcn_rcpf(row_sum<64>(total));
+            inv = 1.0f / row_sum<64>(total);
 #pragma unroll
             for (int q = 0; q < Q; ++q)
                 sum[q] += x[q] * inv;
@@ -341,7 +356,7 @@ __device__ __forceinline__ int route_rows_wide(const RouteArgs &a, int64_t t0, i
         }
         // lane j holds choice j: its weight from its logit, as p was made
         const bool chose = lane < found;
-        float w = chose ? __expf(rank_value(my_key) - top) * inv : 0.0f;
+        float w = chose ? exp_below(rank_value(my_key) - top) * inv : 0.0f;
         if (a.renorm && found)
             w /= row_sum<64>(w);        // (a division: a single choice's weight is 1, not nearly 1)
         if (lane < a.k) {

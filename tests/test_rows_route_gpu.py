@@ -267,3 +267,25 @@ def test_weights_that_sum_to_one_cancel_exactly(T, E, k, dt):
         bound = bound + half_step(dt) * (d.abs() + bound) + 2.0 ** -133
     err = (got.cpu().double() - d).abs()
     assert bool((err <= bound + 1e-37).all()), float((err / (bound + 1e-37)).max())
+
+
+@pytest.mark.parametrize("E", [8, 20, 100, 256])
+def test_small_probabilities_keep_their_bits(E):
+    """Logits a multiple of 1/8, so that their differences are exact: a probability is
+    off by its own exponential and those in the sum (2^-22 each), the sum (ten additions
+    deep) and four more roundings, however far it is below the largest."""
+    import dense_gemm_nt_amd as g
+    T, k = 64, 8
+    x = (torch.randint(-320, 321, (T, E), generator=torch.Generator().manual_seed(E)) / 8.0)
+    ref = o.route(x, k, None, False)
+    rel = 2 * 2.0 ** -22 + 14 * 2.0 ** -24
+    r = g.route_topk(x.to(DEV), k, renormalize=False)
+    err = (r.weights.cpu().double() - ref["weights"]).abs()
+    assert bool((err <= rel * ref["weights"] + 1e-37).all()), float((err / ref["weights"]).max())
+    # dlogits of one choice's weight with the other weights' gradients zero
+    gw = torch.zeros(T, k)
+    gw[:, k - 1] = 1.0
+    d = o.route_backward(x, ref, False, gw, None)
+    got = g.route_topk_backward(x.to(DEV), r, gw.to(DEV)).cpu().double()
+    # p_e (delta - p_j): p's error twice, two roundings
+    assert bool(((got - d).abs() <= (2 * rel + 3 * 2.0 ** -24) * d.abs() + 1e-37).all())
