@@ -235,24 +235,35 @@ def route_topk(logits, top_k, mask=None, renormalize=True):
     if mask is not None:
         _on(index, mask=_mask(mask, T))
     n = _workspace_bytes("gemm_route_workspace", T, E, k)
-    # One allocation, the workspace first (of the order of the results in size: it
-    # stays with them): each would be a tenth of a small call's time.
-    nk, words = T * k, n // 4
-    buf = torch.empty(words + 3 * nk + 2 * E + 3, dtype=torch.int32, device=logits.device)
-    _, ids, order, weights, counts, offsets, tokens, loss = buf.split_with_sizes(
-        (words, nk, nk, nk, E, E + 1, 1, 1))
-    ws = buf.data_ptr()
-    p = ws + n
-    at = p + 12 * nk
+    # Up to 256 KB in one allocation, the workspace first: two more are 3 us of a call whose
+    # kernels take no longer than the host (4099 tokens, 4 choices 19.2 us against 23.0).
+    # Beyond that the workspace, the results of T k values and those of E apart, so that who
+    # keeps one (a loss, the counts) does not keep the others' memory.
+    nk, words, few, dev = T * k, n // 4, 2 * E + 3, logits.device
+    if words + 3 * nk + few <= 65536:
+        buf = torch.empty(words + 3 * nk + few, dtype=torch.int32, device=dev)
+        ws = buf.data_ptr()
+        p = ws + n
+        at = p + 12 * nk
+        _, ids, order, weights, counts, offsets, tokens, loss = buf.split_with_sizes(
+            (words, nk, nk, nk, E, E + 1, 1, 1))
+    else:
+        space = torch.empty(words, dtype=torch.int32, device=dev)
+        most, small = (torch.empty(m, dtype=torch.int32, device=dev) for m in (3 * nk, few))
+        ws, p, at = space.data_ptr(), most.data_ptr(), small.data_ptr()
+        ids, order, weights = most.split_with_sizes((nk, nk, nk))
+        counts, offsets, tokens, loss = small.split_with_sizes((E, E + 1, 1, 1))
     c_out = _rows.GemmRouting(p, p + 8 * nk, at, at + 4 * E, p + 4 * nk, at + 8 * E + 4, at + 8 * E + 8)
     st = _rows.lib().gemm_run_route(logits.data_ptr(), _ptr(mask), T, E, ld, k, 1 if renormalize else 0,
                                     _code(logits.dtype), ctypes.byref(c_out), ws, n,
                                     torch._C._cuda_getCurrentRawStream(index))
     if st:
         _lib.check(st, "route_topk(T=%d, E=%d, k=%d)" % (T, E, k))
+    # (.data: tensors of their own, so that one changed in place is not taken by autograd for
+    # a change of the others)
     f32 = torch.float32
-    return Routing(ids.view(T, k), weights.view(f32).view(T, k), counts, offsets, order, tokens,
-                   loss.view(f32).view(()), bool(renormalize))
+    return Routing(ids.view(T, k).data, weights.view(f32).view(T, k).data, counts.data, offsets.data,
+                   order.data, tokens.data, loss.view(f32).view(()).data, bool(renormalize))
 
 
 def route_topk_backward(logits, routing, grad_weights=None, grad_loss=None, out=None):

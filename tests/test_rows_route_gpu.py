@@ -289,3 +289,21 @@ def test_small_probabilities_keep_their_bits(E):
     got = g.route_topk_backward(x.to(DEV), r, gw.to(DEV)).cpu().double()
     # p_e (delta - p_j): p's error twice, two roundings
     assert bool(((got - d).abs() <= (2 * rel + 3 * 2.0 ** -24) * d.abs() + 1e-37).all())
+
+
+def test_results_are_apart():
+    """A result changed in place leaves the others, and what autograd saved of them, alone."""
+    import dense_gemm_nt_amd as g
+    for T in (10, 20000):
+        r = g.route_topk(randn(T, 24, seed=1).to(DEV), 3)
+        p = torch.ones(T, 3, device=DEV, requires_grad=True)
+        y = (p * r.weights).sum()                              # saves weights
+        r.counts.zero_()
+        r.ids.clamp_(min=0)
+        y.backward()
+        assert torch.equal(p.grad, r.weights)
+        # what lives as long as one result does: the results of its size, and 64 KB
+        for t in (r.counts, r.offsets, r.tokens, r.loss):
+            assert t.untyped_storage().nbytes() <= 65536
+        for t in (r.ids, r.weights, r.order):
+            assert t.untyped_storage().nbytes() <= 3 * 3 * T * 4 + 65536
