@@ -169,6 +169,24 @@ __device__ __forceinline__ void load_lds16_policy(__amdgpu_buffer_rsrc_t rs, uin
         load_lds16(rs, voff, soff, lds_addr);
 }
 
+// load_lds16_policy for a kernel that keeps scalars in vector registers (spilled): a memory
+// instruction may read a scalar that a vector instruction (the v_readlane that brings it
+// back) wrote five wait states later at the earliest, and the compiler, which sees to that
+// before its own loads, does not look into an asm.  The wait states are part of it here.
+template <bool NT>
+__device__ __forceinline__ void load_lds16_settled(__amdgpu_buffer_rsrc_t rs, uint32_t voff, uint32_t soff,
+                                                   uint32_t lds_addr)
+{
+    if constexpr (NT)
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                     :
+                     : "v"(voff), "s"(rs), "s"(soff), "{m0}"(lds_addr));
+    else
+        asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                     :
+                     : "v"(voff), "s"(rs), "s"(soff), "{m0}"(lds_addr));
+}
+
 // One wave-wide 4-byte-per-lane load into LDS at lds_addr + 4 * lane (lanes
 // whose offset is out of range write zeros), completion tracked with vmcnt by
 // hand like load_lds16.  Also used to pull cache lines into L2 ahead of their

@@ -176,6 +176,12 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
             constexpr bool IS_A = decltype(is_a)::value;
             constexpr bool MN = IS_A ? AM : BNM;
             constexpr bool NT = decltype(nt)::value;
+            auto load16 = [](__amdgpu_buffer_rsrc_t rs, uint32_t v, uint32_t soff, uint32_t dst) {
+                if constexpr (PS == 1)               // (its scalars do not all fit)
+                    load_lds16_settled<NT>(rs, v, soff, dst);
+                else
+                    load_lds16_policy<NT>(rs, v, soff, dst);
+            };
             const int kt = kt0 + i;
             const uint32_t dst = lds0 + (uint32_t)(u * UNIT + (j * 4 + q) * 1024);
             if constexpr (MN) {
@@ -194,7 +200,7 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
                 const int cmax = ((IS_A ? rows_a : rows_b) - 1) & ~7;
                 const int col = min(row0 + 8 * mn_chunk, cmax);
                 const uint32_t v = (uint32_t)(4 * q + (lane >> 4)) * ld2 + (uint32_t)col * 2u;
-                load_lds16_policy<NT>(rs, v, (uint32_t)(16 * j) * ld2, dst);
+                load16(rs, v, (uint32_t)(16 * j) * ld2, dst);
             } else {
                 // Rows past the tile's valid rows read zeros.  In a grouped
                 // launch, an A load all of whose eight rows lie past M re-reads
@@ -213,7 +219,7 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
                 const bool some = !IS_A || !redirect_a || row + 8 * q < rows;   // wave-uniform
                 const uint32_t v = some ? ((kin && lrow0 + row < rows) ? (IS_A ? voffA : voffB) : kOutOfRange)
                                         : (kin ? voff0 : kOutOfRange);
-                load_lds16_policy<NT>(IS_A ? rsA : rsB, v, some ? koff + (uint32_t)row * ld2 : koff, dst);
+                load16(IS_A ? rsA : rsB, v, some ? koff + (uint32_t)row * ld2 : koff, dst);
             }
         };
         // The eight loads a wave issues in one memory phase, n = 0..7: group 0

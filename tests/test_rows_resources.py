@@ -148,3 +148,12 @@ def test_scalars_are_settled_before_loads(lib):
             if re.match(r"v_(readlane|readfirstlane|cmp)", op):
                 recent.append((5, _scalars(args.split(",")[0])))
     assert checked > 0
+
+
+@pytest.mark.skipif(not os.path.exists(k.OBJDUMP), reason="llvm-objdump not installed")
+def test_scalars_are_settled_before_loads_of_the_first_library():
+    """The same of libgemm_nt.so, whose persistent kernel keeps scalars in vector registers."""
+    from dense_gemm_nt_amd import build
+    if build.stale():
+        build.build()
+    test_scalars_are_settled_before_loads(build.LIB)
