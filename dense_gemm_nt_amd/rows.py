@@ -56,13 +56,15 @@ def _index(t):
 
 
 def _matrix(name, X, rows, cols):
-    """Leading dimension of a [rows, cols] tensor with unit stride along its columns."""
+    """Leading dimension of a [rows, cols] tensor with unit stride along its columns.  A single
+    row's stride is never used (and may be anything: the last token of a prompt is
+    such a view), so that it is not held to the limits of one."""
     if X.shape != (rows, cols):
         raise ValueError("%s must be [%d, %d], got %s" % (name, rows, cols, tuple(X.shape)))
     ld, step = X.stride()
     if step != 1 and cols > 1 and rows > 0:
         raise ValueError("%s needs unit stride along its columns" % name)
-    return ld if rows > 1 else max(cols, ld)
+    return ld if rows > 1 else cols
 
 
 def _vector(name, v, n, dtype):
@@ -106,9 +108,9 @@ def _adapters(A, B, ids, scale, M, N, K, dtype, index, torch):
     if (a_unit != 1 and K > 1 and A.numel()) or (b_unit != 1 and R > 1 and B.numel()):
         raise ValueError("A and B need unit stride along their last axis")
     if R <= 1:
-        a_ld = max(K, a_ld)
+        a_ld = K
     if N <= 1:
-        b_ld = max(R, b_ld)
+        b_ld = R
     if L <= 1:                         # a single adapter's stride is never used
         a_step = b_step = 0
     return _rows.GemmAdapters(A.data_ptr(), B.data_ptr(), scale.data_ptr(), ids.data_ptr(), L, R,
@@ -341,7 +343,7 @@ def gemm_routed(x, W, offsets, out=None, out_dtype=None):
     if W.numel() == 0:
         layout, ldw = _lib.GEMM_K_MAJOR, max(K, 1)
     elif w_col == 1 and (N == 1 or w_row >= K):
-        layout, ldw = _lib.GEMM_K_MAJOR, w_row if N > 1 else max(K, w_row)
+        layout, ldw = _lib.GEMM_K_MAJOR, w_row if N > 1 else K
     elif w_row == 1 and (K == 1 or w_col >= N):
         layout, ldw = _lib.GEMM_MN_MAJOR, w_col if K > 1 else max(N, w_col)
     else:

@@ -259,3 +259,29 @@ def test_rows_of_no_expert_are_zero_in_a_new_result(S, E, N, K, mn):
         out = torch.full((S, N), 5.0, dtype=FP32, device=DEV)
         g.gemm_routed(x, Wd, off.to(DEV), out=out)
         assert torch.equal(out.cpu()[mine], got[mine]) and bool((out.cpu()[~mine] == 5.0).all())
+
+
+def test_one_row_at_any_stride():
+    """A single row's stride is never used: the last token of a long prompt is such a row."""
+    import dense_gemm_nt_amd as g
+    K, N, E, R, L, dt = 72, 136, 3, 8, 2, BF16
+    W, We = randn(N, K, seed=1, dtype=dt).to(DEV), randn(E, N, K, seed=2, dtype=dt).to(DEV)
+    A, B = randn(L, R, K, seed=3, dtype=dt).to(DEV), randn(L, N, R, seed=4, dtype=dt).to(DEV)
+    ids, scale = torch.ones(1, dtype=torch.int32, device=DEV), torch.ones(L, device=DEV)
+    off = torch.tensor([0, 0, 1, 1], dtype=torch.int32, device=DEV)
+    for step in ((1 << 22) + 8, K + 3, 0):
+        def row(cols, seed):
+            wide = torch.zeros(step + cols, dtype=dt, device=DEV)
+            wide[:cols] = randn(cols, seed=seed, dtype=dt).to(DEV)
+            return wide.as_strided((1, cols), (step, 1)), wide[:cols].clone().view(1, cols)
+        (x, x1), (dy, dy1) = row(K, 5), row(N, 6)
+        out = torch.zeros(N + step, dtype=dt, device=DEV).as_strided((1, N), (step, 1))
+        assert torch.equal(g.gemm_lora(x, W, A, B, ids, scale, out=out), g.gemm_lora(x1, W, A, B, ids, scale))
+        for a, b in zip(g.gemm_lora_backward(dy, x, W, A, B, ids, scale),
+                        g.gemm_lora_backward(dy1, x1, W, A, B, ids, scale)):
+            assert torch.equal(a, b)
+        assert torch.equal(g.gemm_routed(x, We, off), g.gemm_routed(x1, We, off))
+        assert torch.equal(g.gemm_routed_wgrad(dy, x, off), g.gemm_routed_wgrad(dy1, x1, off))
+        r, r1 = g.route_topk(dy, 4), g.route_topk(dy1, 4)
+        assert all(torch.equal(a, b) for a, b in zip(r[:7], r1[:7]))
+        assert torch.equal(g.route_topk_backward(dy, r, r.weights), g.route_topk_backward(dy1, r1, r1.weights))
