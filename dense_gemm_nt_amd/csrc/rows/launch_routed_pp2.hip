@@ -1,5 +1,5 @@
-// The 256 x 256 ping-pong tile over a device-written problem list
-// (routed_lookup), by operand layout.
+// The 256 x 256 ping-pong tile over rows sorted by expert (routed_lookup), by operand
+// layout.
 #include "rows_launch.hpp"
 
 #define GNT_EXT_KERNEL(name) name##_routed

@@ -1,4 +1,4 @@
-// Kernel-template tiles over a device-written problem list (routed_lookup).
+// Kernel-template tiles over rows sorted by expert (routed_lookup).
 #include "rows_launch.hpp"
 
 #define GNT_EXT_KERNEL(name) name##_routed

@@ -321,10 +321,11 @@ __device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, bool own, P finit
 // accumulator of FP16 products is below 2^63, so its units keep it in FP32's range), and
 // they are turned back at the end: multiplications by powers of two, in the rare tile.
 // Without it a value of 2^-25 was lost and one of 2^16 infinite, also in FP32 results.
-// In one launch each: 5001 x 8192 x 8192, rank 64, 4 adapters in runs 642 us against
-// 610 without adapters; 64 x 10240 x 8192, rank 16, 48 adapters 46.5 against 38.4; 1 x
-// 4096 x 4096, rank 16 13.2 in all.  What it adds is the round trips of ids,
-// low-rank values and up rows, one after the other, at the end of a tile.
+// The projection's kernel with adapters and with ids that name none: 4096 x 8192 x 8192,
+// rank 64, 4 adapters in runs 450 us against 398; 64 x 10240 x 8192, rank 16, 48
+// adapters 48.3 against 37.0; 1 x 4096 x 4096, rank 16 13.5 against 12.4.  What it adds is
+// the round trips of ids, low-rank values and up rows, one after the other, at the end of
+// a tile.
 template <int IN, int NB, bool AHEAD, int NP, int FN, int FM>
 __device__ __forceinline__ void lora_add(const LoraArgs &p, f32x16 (&acc)[FN][FM], int r0, int c0, int split,
                                          int lane)

@@ -14,7 +14,8 @@ typedef routed_fn RoutedTable[2][3];
 // the tiles with the adapters added before anything leaves the accumulators
 extern LoraTable kLora_128_s4, kLora_128_s4_rot, kLora_128_s2, kLora_32_rot, kLora_w4, kLora_pp2,
     kLora_pp2_km, kLora_tile_km;
-// the tiles over a device-written problem list: both operands K-major (three
+// the tiles over rows sorted by expert (each block finds its tile's expert from the
+// offsets, routed_lookup): both operands K-major (three
 // tile heights), the weights MN-major (input gradient), both MN-major (weight
 // gradient)
 extern RoutedTable kRouted_32, kRouted_128, kRouted_pp2, kRouted_pp2_km, kRouted_pp2_mm;

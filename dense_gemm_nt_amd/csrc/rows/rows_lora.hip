@@ -150,8 +150,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(ShrinkPair pair
 // that a tile's adapters take few passes over its rows; a higher rank takes two
 // passes.  Wave w multiplies rows 16 w .. +16 with all 64 ranks, and keeps each row's
 // own adapter's.  Bytes bound it: 8 slabs, 64 KB of x, are in flight a compute unit.
-// 5001 x 8192, rank 64, 4 adapters 45 us (140 MB); 8192 x 4096 and 8192 x 8192 in one
-// launch, rank 32 51 us (208 MB, 4.1 TB/s; a device copy moves 4.85).
+// In calls whose projection's operands pass in between: 5001 x 8192, rank 64, 4 adapters
+// 47 to 49 us (138 MB); 8192 x 4096 and 8192 x 8192 in one launch, rank 32 53 to 55 us
+// (208 MB, 3.9 TB/s; a device copy moves 4.85).
 template <int IN>
 __global__ __launch_bounds__(256) void lora_shrink_rows(ShrinkPair pair)
 {
@@ -566,8 +567,8 @@ __device__ __forceinline__ void multiply_z(const uint8_t *zs, int ks, const u32x
 // once, in whole 256-byte row pieces, the next tile's loads in flight while a
 // tile is multiplied, the order of the one after that already there.  Sorted into
 // stretches of one adapter, partial sums need no atomics.  8192 rows, 12288
-// columns, rank 32, bf16 48 us (220 MB, 4.5 TB/s; 42 with two of the three parts);
-// 70 while each wave read v's two parts for itself, in 64-byte pieces.
+// columns, rank 32, bf16 50 us (236 MB, 4.8 TB/s); 70 while each wave read v's parts for
+// itself, in 64-byte pieces.
 template <int IN, int RT>
 __global__ __launch_bounds__(256) void lora_grad(GradArgs p)
 {
@@ -691,9 +692,12 @@ __device__ __forceinline__ void store_grad(void *out, int64_t at, float v, int d
 // values hold, scaled, in FP32; a lane splits what it multiplies.
 constexpr int kFewRows = 1024, kFewStage = 8192;
 
-// Measured for three adapters, in us: 777 rows, 6144 columns, rank 8 13 against 19
-// in four launches; 731, 4448, 24 26 against 22; with few rows three launches' time
-// less (18 rows, all of a backward call: 31 against 42).
+// A backward call without dX, in us, against four launches (BF16, rank 16; dy and x of 4096
+// and 2048 columns): 300 rows of 1, 3, 16, 64 adapters 22 / 21 / 32 / 70 against 29 / 29 / 41 /
+// 78; 1000 rows 47 / 33 / 58 / 102 against 30 / 38 / 69 / 109.  So one adapter of more than
+// about 500 rows, whose blocks are few and long, would be faster in four launches (at
+// 600 rows 33 against 30); the rule does not ask for it.  Past the bound on rows times
+// rank: 731 rows, 4448 columns, rank 24, 3 adapters 26 us of kernels against 22.
 __host__ __device__ constexpr bool few_rows(int64_t M, int64_t rank_pad)
 {
     return M <= kFewRows && M * rank_pad <= 16 * kFewRows;
@@ -887,8 +891,13 @@ ShrinkPlan plan_shrink(int64_t M, int64_t K, int64_t adapters, int64_t rank)
     const int64_t pad = cdiv(rank, 16);
     s.rt = pad >= 4 ? 4 : pad >= 2 ? 2 : 1;
     // Past 2048 rows 64-row tiles: there are enough of them, with K splits, for
-    // every compute unit (2048 x 4096, rank 16: 8.5 us against 6.7 on the 16-row
-    // tiles; 5001 x 8192, rank 64: 26 against 54; 8192 x 8192, rank 32: 33 against 54).
+    // every compute unit, and they take an adapter for fewer reads of its ranks.  The
+    // kernel alone in us, 16-row against 64-row tiles, x of three calls in turn:
+    //   8192 x 8192, rank 64: 1 adapter 85 / 37, 4 in runs 86 / 37, 64 in runs 154 / 58, 4
+    //   mixed 299 / 120, 64 mixed 1676 / 1588; rank 16: 1 adapter 43 / 35
+    //   4096 x 4096, rank 16: 1 adapter 11.0 / 11.4, 4 mixed 32 / 11, 64 mixed 125 / 108
+    // Up to 2048 rows neither always: 2048 x 4096, rank 16: 1 adapter 7.4 / 9.6, 64 mixed
+    // 62 / 84, but 4 mixed 17.8 / 10.7; 1024 x 4096, rank 16: 6.0 / 9.7, 33 / 82, 11.1 / 10.6.
     s.rows = M > 2048;
     if (s.rows) {
         s.tiles = (int)cdiv(M, 64);

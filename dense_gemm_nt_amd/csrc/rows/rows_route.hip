@@ -12,9 +12,9 @@
 // vector operations a choice, where maxima over all of a lane's columns and ballots
 // for each took about 45.
 //
-// 65536 x 256 FP32, 8 choices: forward 44 us (67 MB; about 350 vector operations
-// a row bound it), counts' scan 9.5, places 10, gradient 37 (141 MB, 3.8 TB/s).  16 x
-// 64, the one launch of a small call: 9 us, all of it round trips and reductions.
+// 65536 x 256 FP32, 8 choices: forward 49 us (67 MB; 366 vector operations
+// a row bound it), counts' scan 10, places 10, gradient 39 (141 MB, 3.6 TB/s).  16 x
+// 64, the one launch of a small call: 9.4 us, all of it round trips and reductions.
 #include <type_traits>
 
 #include "rows_group.hpp"

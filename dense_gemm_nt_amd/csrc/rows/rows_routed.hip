@@ -42,7 +42,8 @@ double expected_tiles(int64_t rows, int64_t E, int64_t height)
 
 // The height of K-major tiles: the least passes over the machine (a tile a
 // compute unit), weighed by what a pass takes, 18 : 24 : 62 us for 32 x 128, 128 x
-// 128 and 256 x 256 at a depth of 2048.  (A pass a tenth over counts as not over.)
+// 128 and 256 x 256 at a depth of 2048 (taken for every depth: their ratio is what
+// counts).  (A pass a tenth over counts as not over.)
 // Measured in us with 32 / 128 / 256 rows, depth 2048: 8 experts, N 2048: 320 rows
 // 21 / 25 / 42, 512 rows 31 / 26 / 43, 2400 rows 76 / 47 / 57; 16 experts, N 4096: 640 rows
 // 70 / 66 / 69, 1600 rows 116 / 84 / 73, 3200 rows 211 / 100 / 127, 7200 rows 415 / 202 / 166.
@@ -171,10 +172,10 @@ gemm_status_t gemm_run_routed_wgrad(const void *dY, const void *X, void *dW,
     fill_output(a, dW, K, out_dtype);
     // (each expert's array starts N K elements after the last one's: of 8 values)
     // One expert's tiles after the other's, so that their panels meet in the L2s.  16384
-    // rows of 32 uneven experts, 2048 x 4096, FP32 results 456 us, of which the
+    // rows of 32 uneven experts, 2048 x 4096, FP32 results 449 us, of which the
     // stores alone (no rows) take 179.  Experts' tiles taking turns, so that one's
-    // stores would run under another's products, was slower: 2, 4 and 8 at a time
-    // 395, 429 and 450 us against 380 in one session.
+    // stores would run under another's products, was slower: 2, 4 and 8 at a time by 4, 13
+    // and 18%.
     a.tiles_n = (int)cdiv(K, 256);
     return launch(kRouted_pp2_mm[in_dtype][out_dtype], a, num_experts * cdiv(N, 256) * a.tiles_n, stream);
 }
