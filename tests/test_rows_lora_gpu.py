@@ -487,3 +487,33 @@ def test_input_gradient_keeps_low_rank_values_of_any_size(M, N, K, R, L, dt):
         got = g.gemm_lora_backward(dy.to(DEV), **_dev({**c, "scale": torch.full((L,), s)}), dx_dtype=FP32,
                                    need_adapters=False)[0]
         check(got, dx * s, (dx * s).abs() * 2.0 ** -20, "input gradient times %g" % s)
+
+
+@pytest.mark.parametrize("M", [40, 120, 256, 2048])
+@pytest.mark.parametrize("s", [2.0 ** -30, 2.0 ** 20])
+def test_broken_adapters_meet_rows_of_other_units(M, s):
+    """Infinities and NaNs in an adapter where FP16 low-rank values are small or large, in both
+    directions: where the formula has them, and the other values as near as ever."""
+    import dense_gemm_nt_amd as g
+    N, K, R, L = {40: (256, 64), 120: (256, 64), 256: (2048, 8192), 2048: (4096, 64)}[M] + (16, 5)
+    c = _case(M, N, K, R, L, "mixed", FP16)
+    c["W"].zero_()
+    c["scale"].fill_(s)
+    c["B"][1, 3, 2], c["B"][1, 7, 5], c["B"][1, 7, 6] = float("nan"), float("inf"), float("-inf")
+    c["B"][1, 9, 1], c["B"][1, 130, 0] = float("-inf"), float("inf")
+    c["A"][4, 3] = 0
+    c["B"][4, 11, 3] = float("inf")                    # zero times infinity
+    y, sb, sl = o.lora(**c)
+    zero = torch.zeros_like(sb)
+    got = g.gemm_lora(**_dev(c), out_dtype=FP32)
+    check(got, y, lora_bound(y, zero, torch.where(torch.isfinite(sl), sl, zero), K, K, R, FP16, FP32), "units")
+    assert not bool(torch.isfinite(y).all())
+    d = _case(M, N, K, R, L, "mixed", FP16)
+    d["W"].zero_()
+    d["scale"].fill_(s)
+    d["A"][1, 3, 5], d["A"][1, 7, 9] = float("nan"), float("inf")
+    dy = randn(M, N, seed=9, dtype=FP16)
+    got = g.gemm_lora_backward(dy.to(DEV), **_dev(d), dx_dtype=FP32, need_adapters=False)[0]
+    r, sb, sl = o.lora_backward(dy, **d)["dx"]
+    zero = torch.zeros_like(sb)
+    check(got, r, lora_bound(r, zero, torch.where(torch.isfinite(sl), sl, zero), N, N, R, FP16, FP32), "units dx")
