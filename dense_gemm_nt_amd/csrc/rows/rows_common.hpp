@@ -136,9 +136,9 @@ __device__ __forceinline__ float from16(uint16_t h)
 
 // An FP32 value as the sum of NP 16-bit ones, for the matrix cores: each the nearest to what
 // the ones before it leave.  Two bf16 values are within 2^-17 of x relative to it, two
-// fp16 ones within 2^-23 while x is at least 2^-3 (the caller sees to that: below 2^-14 fp16's
-// steps no longer shrink), where one value would be within 2^-9 or 2^-12.  The low-rank
-// products are intermediates that the caller never sees: rounding them to 16 bits would
+// fp16 ones within 2^-23 from 2^-2 on and 2^-25 absolute below (fp16's steps no longer shrink
+// below 2^-14: the caller keeps x up), where one value would be within 2^-8 or 2^-11.  The
+// low-rank products are intermediates that the caller never sees: rounding them to 16 bits would
 // put an error into the output that nothing else in it has.  A result of 16 bits does not
 // show what two leave (a 64th of its own half step at most); an FP32 one of BF16 operands
 // does, and takes three (low_parts).  Each costs an MFMA per rank-16 step, of which an output
@@ -319,7 +319,9 @@ __device__ __forceinline__ void add_special(u32x4 x, u32x4 hi, bool own, P finit
 // largest value of a rank step lies outside has its accumulators and the values in units of a
 // power of two from then on, in which that value is just below 2^15 (2^-60 to 2^60: an
 // accumulator of FP16 products is below 2^63, so its units keep it in FP32's range), and
-// they are turned back at the end: multiplications by powers of two, in the rare tile.
+// they are turned back at the end: multiplications by powers of two, in the rare tile.  A
+// value is then off by 2^-22 of its step's largest at most, or 2^-40 of the row's largest
+// in the steps before.
 // Without it a value of 2^-25 was lost and one of 2^16 infinite, also in FP32 results.
 // The projection's kernel with adapters and with ids that name none: 4096 x 8192 x 8192,
 // rank 64, 4 adapters in runs 450 us against 398; 64 x 10240 x 8192, rank 16, 48

@@ -69,8 +69,8 @@ typedef struct {
  * values X A_a^T are FP32 sums; scaled, they enter the second product as the
  * sum of two values of the operands' type (three where BF16 operands have an FP32
  * result), of FP16 operands in units of a power of two of each row's, so that small and
- * large ones keep their bits: up to 2^75 (above it the result is infinite or NaN),
- * and from 2^-40 of the row's largest one or 2^-85 on.
+ * large ones keep their bits: to 2^-22 of the largest of their 16 ranks (2^-40 of the row's
+ * largest, and 2^-85), and up to 2^75 (above it the result is infinite or NaN).
  *   K % 8 == 0 (else GEMM_ERR_UNSUPPORTED).  K = 0: the epilogue of zero. */
 gemm_status_t gemm_lora_workspace(int64_t M, int64_t N, int64_t K, int64_t num_adapters,
                                   int64_t rank, int64_t *bytes);
