@@ -957,8 +957,11 @@ Plan plan_projection(int64_t M, int64_t N, int64_t K)
 {
     // ... but for 33 to 64 rows where two rows of 32 x 128 tiles, too many to
     // split K, leave compute units idle that one row of 128 x 128 tiles with K
-    // splits does not: 64 x 10240 x 8192 (160 blocks against 240) 53.9 us against
-    // 38.4 without adapters.
+    // splits does not.  The plain product on either tile, in us, where the rule takes the
+    // latter: 64 x 10240 x 8192 (160 blocks against 240) 52 / 38, 64 x 8704 x 8192 51 / 34,
+    // 40 x 8704 x 4096 28 / 22, 64 x 6144 x 8192 32 / 28, 64 x 6144 x 4096 18.5 / 19.7; and where
+    // not: 64 x 8192 x 4096 19 / 22, 40 x 8192 x 8192 31 / 33, 64 x 16384 x 4096 30 / 31, but 64 x
+    // 12288 x 8192 (as many blocks on both) 52 / 44.
     if (M > 32 && M <= 64) {
         const Plan p = make_plan(M, N, K, kPartialBytes, -1, -1, 0);
         const Plan q = make_plan(M, N, K, kPartialBytes, CFG_T128x128, -1, 0);

@@ -124,6 +124,7 @@ typedef struct {
  * top_k open experts has -1 in the places left.  mask (one byte per token, 0:
  * padding; NULL: none) takes tokens out; they, and tokens without an open
  * expert, are not routed: ids -1, weights 0, p = 0.
+ * (p is FP32: below 2^-126 it may be zero.)
  *   weights = p of the choice, divided by the choices' sum where renormalize
  *   loss    = E sum_e f_e P_e, f_e = counts[e] / (n top_k),
  *             P_e = (sum over routed tokens of p_e) / n; 0 for n = 0
