@@ -38,6 +38,17 @@ ROWS_HEADERS = [os.path.join(ROWS, f) for f in ("rows_common.hpp", "rows_group.h
                                                 "rows_tile.hpp")] + \
     [os.path.join(ROOT, "include", "gemm_rows.h")]
 ROWS_LIB = os.path.join(PKG, "libgemm_rows.so")
+# the products of a feed-forward layer (include/gemm_layer.h), likewise
+LAYER = os.path.join(CSRC, "layer")
+LAYER_SOURCES = [os.path.join(LAYER, f) for f in (
+    "layer_gated.hip", "layer_int8.hip", "launch_gated_tiles.hip", "launch_gated_tiles_b.hip",
+    "launch_gategrad_tiles.hip", "launch_gategrad_tiles_b.hip", "launch_gated_w4.hip",
+    "launch_gategrad_w4.hip", "launch_gated_pp2.hip", "launch_gategrad_pp2.hip", "launch_gated_dx.hip",
+    "launch_gated_dw.hip", "launch_int8_tiles.hip", "launch_int8_pp2.hip")]
+LAYER_HEADERS = [os.path.join(LAYER, f) for f in ("layer_common.hpp", "layer_host.hpp", "layer_launch.hpp",
+                                                  "paired_ext.hpp", "int8_ext.hpp")] + \
+    [os.path.join(ROOT, "include", "gemm_layer.h")]
+LAYER_LIB = os.path.join(PKG, "libgemm_layer.so")
 ARCH = "gfx950"
 
 
@@ -100,6 +111,18 @@ def build_rows(verbose: bool = False, jobs: int = 0) -> str:
     return build(verbose, jobs, ROWS_LIB, sources=ROWS_SOURCES)
 
 
+def build_layer(verbose: bool = False, jobs: int = 0) -> str:
+    """The library of a feed-forward layer's products."""
+    return build(verbose, jobs, LAYER_LIB, sources=LAYER_SOURCES)
+
+
+def stale_layer() -> bool:
+    if not os.path.exists(LAYER_LIB):
+        return True
+    t = os.path.getmtime(LAYER_LIB)
+    return any(os.path.getmtime(f) > t for f in LAYER_SOURCES + LAYER_HEADERS + ROWS_HEADERS + HEADERS)
+
+
 def stale_rows() -> bool:
     if not os.path.exists(ROWS_LIB):
         return True
@@ -117,3 +140,4 @@ def stale() -> bool:
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
     print(build_rows(verbose="-v" in sys.argv))
+    print(build_layer(verbose="-v" in sys.argv))

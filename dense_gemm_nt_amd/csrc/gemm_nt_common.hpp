@@ -15,11 +15,15 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // Input formats: the 16-bit ones, and the FP8 pairs IN_F8 + 2 * (A is E5M2) +
-// (B is E5M2), each operand E4M3 or E5M2 (OCP 8-bit floating point).
-enum : int { IN_BF16 = 0, IN_FP16 = 1, IN_F8 = 2 };
+// (B is E5M2), each operand E4M3 or E5M2 (OCP 8-bit floating point).  IN_I8: 8-bit
+// integers, two to a 16-bit element of the tiles (an MFMA's fragment is 16 bytes of a row of
+// either), whose accumulators hold INT32 sums in their bits until GNT_EXT_ACC converts them.
+enum : int { IN_BF16 = 0, IN_FP16 = 1, IN_F8 = 2, IN_I8 = 6 };
 enum : int { OUT_BF16 = 0, OUT_FP16 = 1, OUT_FP32 = 2 };
 
 // One problem of a grouped launch ("CUTLASS Deep Dive", "Grouped GEMM -- MoE's
@@ -223,6 +227,10 @@ __device__ __forceinline__ f32x16 mfma32x32x16(u32x4 a, u32x4 b, f32x16 c)
     if constexpr (IN == IN_BF16)
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else if constexpr (IN == IN_I8)
+        return __builtin_bit_cast(f32x16, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                                              __builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b),
+                                              __builtin_bit_cast(i32x16, c), 0, 0, 0));
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

@@ -1,6 +1,6 @@
 // gemm_nt_ext.hpp -- extension points of the tile kernels.  Not set by this
 // library's own translation units: its kernels have the names and the argument
-// block below and nothing added.  A translation unit of rows/ that needs a tile
+// block below and nothing added.  A translation unit of rows/ or layer/ that needs a tile
 // with an addition defines them before it includes a tile header:
 //   GNT_EXT_KERNEL(name)  the kernel's name (its own, so that the two libraries'
 //                         kernels stay apart)
@@ -12,6 +12,18 @@
 //   GNT_EXT_ACC(p, acc, r0, c0, split, lane)  adds to a wave's accumulators,
 //                         whose block starts at row r0 and column c0, once the
 //                         main loop is done and before anything leaves them
+//   GNT_EXT_MAP(p, tm, tn, split)  in place of the block map where every block has a
+//                         tile; may move p's pointers
+//   GNT_EXT_STORE(p, acc, r0, c0, stage, lane)  in place of a whole sum's store (after a
+//                         reduction in the kernel; partials of a second pass are stored as
+//                         ever), through the wave's share of the idle LDS
+//   GNT_EXT_PAIRED 1      B's rows alternate in groups of eight between two arrays of
+//                         GNT_EXT_COLS(p) rows each: row R of B is row 8 (R / 16) + R mod 8 of
+//                         array (R / 8) mod 2, which GNT_EXT_B(p, w) and GNT_EXT_LDB(p, w)
+//                         name.  Eight rows are what one wave-wide load of a K-major B
+//                         brings (and two of an MN-major one, four each), so a wave loads
+//                         from one of the arrays only, and what belongs together ends up in
+//                         one lane's accumulators (registers 8 u + 0..3 and 8 u + 4..7).
 // (Included by every tile header, so without an include guard of its own.)
 #ifndef GNT_EXT_KERNEL
 #define GNT_EXT_KERNEL(name) name
@@ -19,4 +31,10 @@
 #endif
 #ifndef GNT_EXT_ACC
 #define GNT_EXT_ACC(p, acc, r0, c0, split, lane)
+#endif
+#ifndef GNT_EXT_PAIRED
+#define GNT_EXT_PAIRED 0
+#define GNT_EXT_COLS(p) 0
+#define GNT_EXT_B(p, w) p.B
+#define GNT_EXT_LDB(p, w) p.ldb
 #endif

@@ -61,6 +61,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     constexpr int WTM = BM / WM, WTN = BN / WN;
     constexpr int FM = WTM / 32, FN = WTN / 32;
     constexpr int KSTEPS = BK / 16;
+    constexpr bool PAIRED = GNT_EXT_PAIRED;   // B's rows from two arrays in turn
+    static_assert(!PAIRED || (RPI == 8 && NWAVES % 2 == 0), "a wave's loads are of one array");
     static_assert(CH == 8 || CH == 4, "BK must be 32 or 64");
     static_assert(A_LOADS * RPI * NWAVES == BM && B_LOADS * RPI * NWAVES == BN, "tile/load mismatch");
     static_assert(FM >= 1 && FN >= 1 && WTM % 32 == 0 && WTN % 32 == 0, "wave tile");
@@ -77,6 +79,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     split = 0;
     if (!GNT_EXT_LOOKUP(p, tm, tn))
         return;
+#elif defined(GNT_EXT_MAP)
+    GNT_EXT_MAP(p, tm, tn, split);
 #else
     if (p.inreduce)       // the K splits of a tile adjacent in launch order (splitk_arrive)
         map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
@@ -90,11 +94,14 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     const SlabOrder<ROT> order = slab_order<ROT>(kt_begin, kt_end - kt_begin, p.k_tiles, p.K % BK != 0, n0);
 
     const int rows_a = min(BM, p.M - m0);
-    const int rows_b = min(BN, p.N - n0);
+    const int rows_b = PAIRED ? min(BN / 2, GNT_EXT_COLS(p) - n0 / 2) : min(BN, p.N - n0);
+    // (of paired arrays the one that this wave's loads are of)
+    const int ldb = GNT_EXT_LDB(p, wave & 1);
     const __amdgpu_buffer_rsrc_t rsA =
         make_rsrc(p.A + (int64_t)m0 * p.lda, (uint32_t)rows_a * (uint32_t)p.lda * 2u);
     const __amdgpu_buffer_rsrc_t rsB =
-        make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)rows_b * (uint32_t)p.ldb * 2u);
+        make_rsrc(GNT_EXT_B(p, wave & 1) + (int64_t)(PAIRED ? n0 / 2 : n0) * ldb,
+                  (uint32_t)rows_b * (uint32_t)ldb * 2u);
 
     // Load j of this wave covers LDS rows (j * NWAVES + wave) * RPI .. +RPI.  A
     // row's swizzle key depends on the row mod 16 only, which is the same for
@@ -106,7 +113,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     constexpr int RSTEP = NWAVES * RPI;
     const int lrow0 = wave * RPI + lane / CH;
     const int lc = (lane % CH) ^ row_key<CH>(lrow0);
-    const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
+    const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)ldb * 2u;
+    const int lrowB = PAIRED ? (wave >> 1) * RPI + lane / CH : lrow0;
+    constexpr int RSTEPB = PAIRED ? RSTEP / 2 : RSTEP;
 
     const uint32_t lds_base = (uint32_t)(uintptr_t)smem;
     const uint32_t ldsA = lds_base;
@@ -125,7 +134,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
             load_lds16(rsA, v, koff, ldsA + s * A_BYTES + (j * NWAVES + wave) * 1024);
         } else {
             const int jb = j - A_LOADS;
-            const uint32_t r = (uint32_t)min(lrow0 + jb * RSTEP, rows_b - 1);
+            const uint32_t r = (uint32_t)min(lrowB + jb * RSTEPB, rows_b - 1);
             const uint32_t v = kin ? r * ldb2 + (uint32_t)lc * 16u : kOutOfRange;
             load_lds16_policy<decltype(nt)::value>(rsB, v, koff,
                                                    ldsB + s * B_BYTES + (jb * NWAVES + wave) * 1024);
@@ -285,6 +294,15 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
             p.splits = 1;
         }
     }
+
+#ifdef GNT_EXT_STORE
+    if (p.splits == 1) {
+        wg_barrier();                        // the ring's last fragments have been read
+        GNT_EXT_STORE(p, acc, m0 + wave_m * WTM, n0 + wave_n * WTN,
+                      smem + wave * (STAGES * (A_BYTES + B_BYTES) / NWAVES), lane);
+        return;
+    }
+#endif
 
     // Epilogue without a fused epilogue: each wave's block through its share of
     // the (now idle) LDS ring, stored row-contiguously (C, or this split's

@@ -81,7 +81,8 @@ template <int IN, int OUT, bool AM = false, bool BNM = false, int SC = 0, bool G
           int PS = 0>
 __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_ARGS p0)
 {
-    constexpr bool F8 = IN >= IN_F8;
+    constexpr bool F8 = IN >= IN_F8 && IN < IN_I8;
+    constexpr bool PAIRED = GNT_EXT_PAIRED;  // B's rows from two arrays in turn
     constexpr int ESZ = F8 ? 1 : 2;          // bytes per element
     static_assert(!(F8 && (AM || BNM)), "FP8 operands are K-major");
     static_assert(SC == 0 || F8, "blockwise scales are for FP8 inputs");
@@ -140,13 +141,15 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
         const int nk = streamk ? sk_nk : min(p.k_tiles, kt0 + p.kt_per_split) - kt0;
 
         const int rows_a = min(BM, p.M - m0);
-        const int rows_b = min(BN, p.N - n0);
+        const int rows_b = PAIRED && !BNM ? min(BN / 2, GNT_EXT_COLS(p) - n0 / 2) : min(BN, p.N - n0);
         const uint8_t *Ab = reinterpret_cast<const uint8_t *>(p.A);
-        const uint8_t *Bb = reinterpret_cast<const uint8_t *>(p.B);
+        // (of paired arrays the one that this wave's loads are of)
+        const uint8_t *Bb = reinterpret_cast<const uint8_t *>(GNT_EXT_B(p, q & 1));
+        const int ldb = GNT_EXT_LDB(p, q & 1);
         const __amdgpu_buffer_rsrc_t rsA =
             make_rsrc(Ab + (int64_t)m0 * p.lda * ESZ, (uint32_t)rows_a * (uint32_t)p.lda * ESZ);
         const __amdgpu_buffer_rsrc_t rsB =
-            make_rsrc(Bb + (int64_t)n0 * p.ldb * ESZ, (uint32_t)rows_b * (uint32_t)p.ldb * ESZ);
+            make_rsrc(Bb + (int64_t)(PAIRED ? n0 / 2 : n0) * ldb * ESZ, (uint32_t)rows_b * (uint32_t)ldb * ESZ);
 
         // Load slots: within a 128-row unit, load j (0..3) of wave q covers rows
         // 32 j + 8 q .. +8 (one 1 KB wave-wide load, 8 rows x 128 bytes).  The
@@ -154,10 +157,11 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
         // swizzled chunk are the same for every j and every unit.
         const int lrow0 = q * 8 + lane / CH;
         const int lc = (lane % CH) ^ row_key<CH>(lrow0);
-        const uint32_t lda2 = (uint32_t)p.lda * ESZ, ldb2 = (uint32_t)p.ldb * ESZ;   // row pitch, bytes
+        const uint32_t lda2 = (uint32_t)p.lda * ESZ, ldb2 = (uint32_t)ldb * ESZ;   // row pitch, bytes
+        const int lrowB = PAIRED ? (q >> 1) * 8 + lane / CH : lrow0;
         const uint32_t voffA = (uint32_t)lrow0 * lda2 + (uint32_t)lc * 16u;
         const uint32_t voff0 = (uint32_t)lc * 16u;      // the same chunk of the tile's row 0
-        const uint32_t voffB = (uint32_t)lrow0 * ldb2 + (uint32_t)lc * 16u;
+        const uint32_t voffB = (uint32_t)lrowB * ldb2 + (uint32_t)lc * 16u;
         const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
         // Load number j (0..3) of the 128-row unit starting at tile row `row0` of
@@ -185,22 +189,23 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
             const int kt = kt0 + i;
             const uint32_t dst = lds0 + (uint32_t)(u * UNIT + (j * 4 + q) * 1024);
             if constexpr (MN) {
-                const uint16_t *X = IS_A ? p.A : p.B;
-                const int ld = IS_A ? p.lda : p.ldb;
+                constexpr bool PB = PAIRED && !IS_A;    // 32 k-rows a slab of each array
+                const uint16_t *X = IS_A ? p.A : GNT_EXT_B(p, q >> 1);
+                const int ld = IS_A ? p.lda : GNT_EXT_LDB(p, q >> 1);
                 const int col0 = IS_A ? m0 : n0;
-                const int rows_left = min(BK, p.K - kt * BK);
+                const int rows_left = PB ? min(BK / 2, GNT_EXT_COLS(p) - kt * (BK / 2)) : min(BK, p.K - kt * BK);
                 // the slab's k-rows as whole rows of ld elements (the operand
                 // occupies K such rows), seen from the tile's first column
                 const __amdgpu_buffer_rsrc_t rs =
-                    make_rsrc(X + (int64_t)kt * BK * ld + col0,
+                    make_rsrc(X + (int64_t)kt * (PB ? BK / 2 : BK) * ld + col0,
                               (uint32_t)(((int64_t)rows_left * ld - col0) * 2));
                 const uint32_t ld2 = (uint32_t)ld * 2u;
                 // chunks wholly past column M (N) re-read the last valid chunk:
                 // they only feed output rows (columns) that are never stored
                 const int cmax = ((IS_A ? rows_a : rows_b) - 1) & ~7;
                 const int col = min(row0 + 8 * mn_chunk, cmax);
-                const uint32_t v = (uint32_t)(4 * q + (lane >> 4)) * ld2 + (uint32_t)col * 2u;
-                load16(rs, v, (uint32_t)(16 * j) * ld2, dst);
+                const uint32_t v = (uint32_t)(4 * (PB ? q & 1 : q) + (lane >> 4)) * ld2 + (uint32_t)col * 2u;
+                load16(rs, v, (uint32_t)((PB ? 8 : 16) * j) * ld2, dst);
             } else {
                 // Rows past the tile's valid rows read zeros.  In a grouped
                 // launch, an A load all of whose eight rows lie past M re-reads
@@ -213,11 +218,12 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
                 // zero reads.
                 const uint32_t koff = (uint32_t)kt * (uint32_t)(BK * ESZ);
                 const bool kin = lc * 16 < (p.K - kt * BK) * ESZ;
-                const int row = row0 + 32 * j;
+                const int row = PAIRED && !IS_A ? (row0 + 32 * j) / 2 : row0 + 32 * j;
+                const int lrow = IS_A ? lrow0 : lrowB;
                 const int rows = IS_A ? rows_a : rows_b;
                 const uint32_t ld2 = IS_A ? lda2 : ldb2;
                 const bool some = !IS_A || !redirect_a || row + 8 * q < rows;   // wave-uniform
-                const uint32_t v = some ? ((kin && lrow0 + row < rows) ? (IS_A ? voffA : voffB) : kOutOfRange)
+                const uint32_t v = some ? ((kin && lrow + row < rows) ? (IS_A ? voffA : voffB) : kOutOfRange)
                                         : (kin ? voff0 : kOutOfRange);
                 load16(IS_A ? rsA : rsB, v, some ? koff + (uint32_t)row * ld2 : koff, dst);
             }
@@ -548,6 +554,12 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
             }
         }
         uint8_t *stage = smem + wave * 16384;
+#ifdef GNT_EXT_STORE
+        if (p.splits == 1) {
+            GNT_EXT_STORE(p, acc, m0 + wm0, n0 + wn0, stage, lane);
+            return;
+        }
+#endif
         if constexpr (streamk) {
             // a whole 256 x 256 slot per segment, ragged tiles included
             float *ws = p.partials + (int64_t)sk_slot * (BM * BN);
@@ -675,11 +687,15 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
             wg_barrier();
         }
     } else {
+#ifdef GNT_EXT_MAP
+        GNT_EXT_MAP(p, tm, tn, split);
+#else
         if (p.inreduce)
             map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn,
                                   split);
         else
             map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+#endif
         tile(tm, tn, split);
     }
 }

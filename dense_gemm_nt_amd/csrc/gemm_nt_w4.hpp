@@ -188,6 +188,7 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
     constexpr int LA = BM / 32, LB = BN / 32; // loads per wave and slab
     constexpr int MF = FN * FM;               // MFMAs per k-step
     constexpr int NR = FM + FN;               // fragment reads per k-step
+    constexpr bool PAIRED = GNT_EXT_PAIRED;   // B's rows from two arrays in turn
     static_assert(BN == 128, "the 256 x 128 tile is the instantiated and tested one");
     static_assert(NUA == 3 && NUB == 4, "the load schedule below is written for 3 A and 4 B units");
     static_assert(NUA * UA + NUB * UBB <= 160 * 1024, "LDS budget");
@@ -200,20 +201,27 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
     const int wm = wave >> 1, wn = wave & 1;
 
     int tm, tn, split;
+#ifdef GNT_EXT_MAP
+    GNT_EXT_MAP(p, tm, tn, split);
+#else
     if (p.inreduce)
         map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
     else
         map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+#endif
     const int m0 = tm * BM, n0 = tn * BN;
     const int kt0 = split * p.kt_per_split;
     const int nk = min(p.k_tiles, kt0 + p.kt_per_split) - kt0;
 
     const int rows_a = min(BM, p.M - m0);
-    const int rows_b = min(BN, p.N - n0);
+    const int rows_b = PAIRED ? min(BN / 2, GNT_EXT_COLS(p) - n0 / 2) : min(BN, p.N - n0);
+    // (of paired arrays the one that this wave's loads are of)
+    const int ldb = GNT_EXT_LDB(p, wave & 1);
     const __amdgpu_buffer_rsrc_t rsA =
         make_rsrc(p.A + (int64_t)m0 * p.lda, (uint32_t)rows_a * (uint32_t)p.lda * 2u);
     const __amdgpu_buffer_rsrc_t rsB =
-        make_rsrc(p.B + (int64_t)n0 * p.ldb, (uint32_t)rows_b * (uint32_t)p.ldb * 2u);
+        make_rsrc(GNT_EXT_B(p, wave & 1) + (int64_t)(PAIRED ? n0 / 2 : n0) * ldb,
+                  (uint32_t)rows_b * (uint32_t)ldb * 2u);
 
     // Load j of wave w for one operand covers tile rows 32 j + 8 w + lane / 8:
     // lane l fills physical chunk l % 8 of its row, which holds logical chunk
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
     // the same for every load of the wave.
     const int lr = lane >> 3;
     const int lc = (lane & 7) ^ row_key<CH>(8 * wave + lr);
-    const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)p.ldb * 2u;
+    const uint32_t lda2 = (uint32_t)p.lda * 2u, ldb2 = (uint32_t)ldb * 2u;
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     // Load j of operand `op` (0: A into A unit u, 1: B into B unit u) of local
@@ -242,7 +250,8 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
             const uint32_t v = kin ? (uint32_t)min(row, rows_a - 1) * lda2 + (uint32_t)lc * 16u : kOutOfRange;
             load_lds16(rsA, v, kb, lds0 + (uint32_t)(u * UA + (row - lr) * PITCH));
         } else {
-            const uint32_t v = kin ? (uint32_t)min(row, rows_b - 1) * ldb2 + (uint32_t)lc * 16u : kOutOfRange;
+            const int row_b = PAIRED ? 16 * j + 8 * (wave >> 1) + lr : row;
+            const uint32_t v = kin ? (uint32_t)min(row_b, rows_b - 1) * ldb2 + (uint32_t)lc * 16u : kOutOfRange;
             load_lds16_policy<decltype(nt)::value>(rsB, v, kb, lds0 + (uint32_t)(NUA * UA + u * UBB + (row - lr) * PITCH));
         }
     };
@@ -400,6 +409,12 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
     uint8_t *stage = smem + wave * 32768;
     wait_vmcnt<0>();
     wg_barrier();
+#ifdef GNT_EXT_STORE
+    if (p.splits == 1) {
+        GNT_EXT_STORE(p, acc, r0, c0, stage, lane);
+        return;
+    }
+#endif
     if (full && p.splits == 1 && p.rows16 && !p.epi) {
         if constexpr (OUT == OUT_BF16)
             store_wave_block_staged<__bf16, FN, true>(

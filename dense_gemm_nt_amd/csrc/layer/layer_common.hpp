@@ -1,0 +1,369 @@
+// layer_common.hpp -- pieces shared by the kernels of a feed-forward layer's products:
+// argument blocks, activations with their slopes, and what the tiles do with their sums.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../gemm_nt_common.hpp"
+
+namespace gnt {
+
+enum : int { GATE_RELU = 1, GATE_GELU = 2, GATE_SILU = 3 };
+
+// The gated block's products.  B and B2 are the gate's and the up projection's weights,
+// `cols` rows each, in turn groups of eight (GNT_EXT_PAIRED): N, or the contraction of the
+// input gradient, counts both, 2 cols rounded up to whole groups.
+struct PairedArgs : KernelArgs {
+    const uint16_t *B2;
+    int ldb2;
+    int cols;
+    const uint16_t *dh;         // backward: the block's output gradient [M][cols]
+    int lddh;
+    int dh16;                   // its rows start 16-byte aligned
+    const uint32_t *most;       // FP16 backward: kMostParts partial maxima of |dh| (its bits)
+    void *C2;                   // weight gradients: C is the gate's, C2 the up projection's
+};
+
+constexpr int kMostParts = 256;
+
+// An opaque copy of the lane id: what an epilogue derives from it is computed there, and
+// not held across the main loop, whose registers are all taken.
+__device__ __forceinline__ int fresh_lane(int lane)
+{
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+__device__ __forceinline__ float from_bits16(int in, uint32_t h)
+{
+    return in == IN_BF16 ? __builtin_bit_cast(float, h << 16)
+                         : static_cast<float>(__builtin_bit_cast(_Float16, (uint16_t)h));
+}
+
+// Phi(x) and phi(x), the normal distribution and its density.  Phi(-|x|) = exp(-x^2 / 2)
+// t q(t), t = 1 / (1 + 0.3 |x|): erfcx(|x| / sqrt 2) / 2 is smooth in t, and q is its quotient by
+// t as a polynomial fitted here (Chebyshev nodes on 0 <= |x| <= 14.5, relative error
+// made even by reweighting): 1.7e-7 of Phi, 5e-7 evaluated in FP32.  So the tail keeps its
+// relative accuracy, and the slope takes the same exponential.
+__device__ __forceinline__ void normal_cdf(float x, float &cdf, float &pdf)
+{
+    const float a = fabsf(x);
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3f * a);
+    float q = 0.0354238897562027f;
+    q = q * t - 0.15615904331207275f;
+    q = q * t + 0.20455773174762726f;
+    q = q * t - 0.05203482508659363f;
+    q = q * t + 0.12769216299057007f;
+    q = q * t + 0.10017584264278412f;
+    q = q * t + 0.12071215361356735f;
+    q = q * t + 0.11963200569152832f;
+    const float e = __expf(-0.5f * x * x);
+    const float low = e * (t * q);
+    cdf = x < 0.0f ? low : 1.0f - low;
+    pdf = 0.39894228040143268f * e;
+}
+
+// act(v); with `slope` also act'(v) (0 at ReLU's corner).  A NaN stays one.
+template <bool SLOPE>
+__device__ __forceinline__ float gate_value(int act, float v, float &slope)
+{
+    if (act == GATE_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
+        if constexpr (SLOPE)
+            slope = s + v * s * (1.0f - s);
+        return v * s;
+    }
+    if (act == GATE_GELU) {
+        float cdf, pdf;
+        normal_cdf(v, cdf, pdf);
+        if constexpr (SLOPE)
+            slope = cdf + v * pdf;
+        return v * cdf;
+    }
+    if constexpr (SLOPE)
+        slope = v <= 0.0f ? 0.0f : v > 0.0f ? 1.0f : v;
+    return v <= 0.0f ? 0.0f : v;
+}
+
+template <int OUT>
+__device__ __forceinline__ uint32_t to_bits16(float x)
+{
+    if constexpr (OUT == OUT_BF16)
+        return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+    else
+        return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+
+// `count` (1 .. 8, or 4 of FP32) consecutive values of a row at C, element index idx: one
+// 16-byte store where all are there and rows allow it.
+template <int OUT, int V>
+__device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)[V], bool wide, int count)
+{
+    if constexpr (OUT == OUT_FP32) {
+        float *c = static_cast<float *>(C) + idx;
+        if (wide && count >= V) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<f32x4 *>(c + i) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < count)
+                    c[i] = x[i];
+        }
+    } else {
+        static_assert(V == 8, "16 bytes");
+        uint16_t *c = static_cast<uint16_t *>(C) + idx;
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = to_bits16<OUT>(x[2 * i]) | to_bits16<OUT>(x[2 * i + 1]) << 16;
+        if (wide && count >= V) {
+            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < count)
+                    c[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// The gated block's output: act(gate) * up of a wave's accumulators (gate and up in one
+// lane, registers 8 u + e and 8 u + 4 + e) into C [M][cols], whose columns are half the
+// tile's.  The wave's block is staged as FP32 rows of 16 FN values in its own LDS, chunk c of
+// row r at c ^ (r mod the chunks), and read back as 16-byte pieces of rows.
+template <int OUT, int FN, int FM>
+__device__ __forceinline__ void store_gated(const PairedArgs &p, const f32x16 (&acc)[FN][FM], int r0, int c0,
+                                            uint8_t *stage, int lane_id)
+{
+    const int lane = fresh_lane(lane_id);
+    constexpr int CPR = 4 * FN, ROWB = 16 * CPR, KEYM = CPR - 1;
+    const int h = lane >> 5;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int r = fm * 32 + (lane & 31), c = 4 * fn + 2 * u + h;
+                f32x4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float slope;
+                    y[e] = gate_value<false>(p.act, acc[fn][fm][8 * u + e], slope) * acc[fn][fm][8 * u + 4 + e];
+                }
+                *reinterpret_cast<f32x4 *>(stage + r * ROWB + ((c ^ (r & KEYM)) * 16)) = y;
+            }
+    wait_lgkmcnt0();
+    constexpr int V = OUT == OUT_FP32 ? 4 : 8;        // values per lane
+    constexpr int LPR = 16 * FN / V, RPS = 64 / LPR;  // lanes per row, rows per step
+#pragma unroll
+    for (int j = 0; j < 32 * FM / RPS; ++j) {
+        const int r = j * RPS + lane / LPR, c = (lane % LPR) * (V / 4);
+        const int m = r0 + r, n = c0 / 2 + 4 * c;
+        float y[V];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const f32x4 v = *reinterpret_cast<const f32x4 *>(stage + r * ROWB + (((c + i) ^ (r & KEYM)) * 16));
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[4 * i + e] = v[e];
+        }
+        if (m < p.M && n < p.cols)
+            store_run<OUT, V>(p.C, (int64_t)m * p.ldc + n, y, p.rows16 != 0, p.cols - n);
+    }
+}
+
+// 2^-floor(log2 max|dh|) as an exponent, from the partial maxima (every lane's result is the
+// same): what FP16 gradients of the pre-activations are multiplied by, so that they
+// neither end below fp16's smallest step nor lose bits there whatever the scale of dh.
+__device__ __forceinline__ int most_shift(const uint32_t *most, int lane)
+{
+    uint32_t b = 0;
+#pragma unroll
+    for (int i = 0; i < kMostParts / 64; ++i)
+        b = max(b, most[64 * i + lane]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        b = max(b, (uint32_t)__shfl_xor((int)b, o));
+    b = __builtin_amdgcn_readfirstlane(b);
+    if (b == 0 || b >= 0x7c00u)                       // nothing, or not finite
+        return 0;
+    return b >= 0x400u ? 15 - (int)(b >> 10) : 24 - (31 - __builtin_clz(b));
+}
+
+// The gradients of the pre-activations from their sums, dg = dh u act'(g) and du = dh act(g),
+// into C [M][N] in the sums' own layout (N = 2 cols rounded up, rows 16-byte aligned).  The
+// wave's part of dh, 16 FN columns of 32 rows a pass, comes through its LDS in 16-byte
+// pieces of rows (read in the accumulators' layout a load would touch 32 rows for 8 bytes
+// each), and the results leave the same way.  Columns at or past `cols` (the last group's
+// rest) get zeros.
+template <int IN, int FN, int FM>
+__device__ __forceinline__ void store_gate_gradients(const PairedArgs &p, const f32x16 (&acc)[FN][FM], int r0,
+                                                     int c0, uint8_t *stage, int lane_id)
+{
+    constexpr int CPR = 2 * FN, ROWB = 16 * CPR, KEYM = CPR - 1, RPS = 64 / CPR;     // dh
+    constexpr int CPO = 4 * FN, ROWO = 16 * CPO, KEYO = CPO - 1, RPO = 64 / CPO;     // results
+    const int lane = fresh_lane(lane_id);
+    const int h = lane >> 5, f0 = c0 / 2;
+    uint8_t *out = stage + 32 * ROWB;
+    float scale = 1.0f;
+    if constexpr (IN == IN_FP16)
+        scale = __builtin_ldexpf(1.0f, most_shift(p.most, lane));
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+        for (int j = 0; j < 32 / RPS; ++j) {
+            const int r = j * RPS + lane / CPR, c = lane % CPR;
+            const int m = r0 + fm * 32 + r, n = f0 + 8 * c;
+            u32x4 w = {0u, 0u, 0u, 0u};
+            if (m < p.M && n < p.cols) {
+                const uint16_t *src = p.dh + (int64_t)m * p.lddh + n;
+                if (p.dh16 && n + 8 <= p.cols) {
+                    w = *reinterpret_cast<const u32x4 *>(src);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (n + i < p.cols)
+                            w[i >> 1] |= (uint32_t)src[i] << (16 * (i & 1));
+                }
+            }
+            *reinterpret_cast<u32x4 *>(stage + r * ROWB + ((c ^ (r & KEYM)) * 16)) = w;
+        }
+        wait_lgkmcnt0();
+        const int r = lane & 31;
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int ch = 2 * fn + u, n = f0 + 8 * ch + 4 * h;
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(stage + r * ROWB + ((ch ^ (r & KEYM)) * 16) + 8 * h);
+                uint32_t dg[4], du[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float d = scale * from_bits16(IN, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                    float slope;
+                    const float a = gate_value<true>(p.act, acc[fn][fm][8 * u + e], slope);
+                    const bool in = n + e < p.cols;
+                    dg[e] = in ? to_bits16<IN>(d * acc[fn][fm][8 * u + 4 + e] * slope) : 0u;
+                    du[e] = in ? to_bits16<IN>(d * a) : 0u;
+                }
+                // column 32 fn + 16 u + 4 h of dg and, eight on, of du
+                uint8_t *at = out + r * ROWO + 8 * h;
+                *reinterpret_cast<u32x2 *>(at + (((2 * ch) ^ (r & KEYO)) * 16)) = (u32x2){dg[0] | dg[1] << 16, dg[2] | dg[3] << 16};
+                *reinterpret_cast<u32x2 *>(at + (((2 * ch + 1) ^ (r & KEYO)) * 16)) = (u32x2){du[0] | du[1] << 16, du[2] | du[3] << 16};
+            }
+        wait_lgkmcnt0();
+#pragma unroll
+        for (int j = 0; j < 32 / RPO; ++j) {
+            const int ro = j * RPO + lane / CPO, c = lane % CPO;
+            const int m = r0 + fm * 32 + ro, n = c0 + 8 * c;
+            const u32x4 v = *reinterpret_cast<const u32x4 *>(out + ro * ROWO + ((c ^ (ro & KEYO)) * 16));
+            if (m < p.M && n < p.N)
+                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.C) + (int64_t)m * p.ldc + n) = v;
+        }
+        wait_lgkmcnt0();
+    }
+}
+
+// Takes FP16 gradients' scale back out of sums over them.
+template <int IN, int FN, int FM>
+__device__ __forceinline__ void unscale(const PairedArgs &p, f32x16 (&acc)[FN][FM], int lane)
+{
+    if constexpr (IN == IN_FP16) {
+        const float f = __builtin_ldexpf(1.0f, -most_shift(p.most, lane));
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[fn][fm][e] *= f;
+    }
+}
+
+// The weight gradients' store: tile row R is row 8 (R / 16) + R mod 8 of the gate's array
+// (C) or the up projection's (C2), by R / 8 mod 2.  Staged as FP32, 32 rows a pass, and
+// read back as 16-byte pieces of rows.
+template <int OUT, int FN, int FM>
+__device__ __forceinline__ void store_paired_rows(const PairedArgs &p, const f32x16 (&acc)[FN][FM], int r0, int c0,
+                                                  uint8_t *stage, int lane_id)
+{
+    const int lane = fresh_lane(lane_id);
+    constexpr int CPR = 8 * FN, ROWB = 16 * CPR, KEYM = CPR < 16 ? CPR - 1 : 15;
+    constexpr int V = OUT == OUT_FP32 ? 4 : 8;
+    constexpr int LPR = 32 * FN / V, RPS = 64 / LPR;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = lane & 31, c = 8 * fn + 2 * q + (lane >> 5);
+                const f32x4 v = {acc[fn][fm][4 * q], acc[fn][fm][4 * q + 1], acc[fn][fm][4 * q + 2],
+                                 acc[fn][fm][4 * q + 3]};
+                *reinterpret_cast<f32x4 *>(stage + r * ROWB + ((c ^ (r & KEYM)) * 16)) = v;
+            }
+        wait_lgkmcnt0();
+#pragma unroll
+        for (int j = 0; j < 32 / RPS; ++j) {
+            const int r = j * RPS + lane / LPR, c = (lane % LPR) * (V / 4);
+            const int R = r0 + fm * 32 + r, f = (R >> 4) * 8 + (R & 7), n = c0 + 4 * c;
+            float y[V];
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(stage + r * ROWB + (((c + i) ^ (r & KEYM)) * 16));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[4 * i + e] = v[e];
+            }
+            if (f < p.cols && n < p.N)
+                store_run<OUT, V>((R >> 3) & 1 ? p.C2 : p.C, (int64_t)f * p.ldc + n, y, p.rows16 != 0, p.N - n);
+        }
+        wait_lgkmcnt0();
+    }
+}
+
+// The product in 8-bit integers: a scale for each row of A and each row of B (or one for
+// all: step 0).
+struct Int8Args : KernelArgs {
+    const float *sa;
+    const float *sb;
+    int sa_step, sb_step;
+};
+
+// INT32 sums to FP32 ones in the values' units: (sum * s_m) * t_n, one rounding of the
+// sum (2^-24 of it) and one of each product, in this order so that a sum of zero stays
+// zero whatever the scales' product.  K splits add up what this gives.
+template <int FN, int FM>
+__device__ __forceinline__ void int8_scale(const Int8Args &p, f32x16 (&acc)[FN][FM], int r0, int c0, int lane_id)
+{
+    const int lane = fresh_lane(lane_id);
+    float s[FM];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+        s[fm] = p.sa[(int64_t)min(r0 + fm * 32 + (lane & 31), p.M - 1) * p.sa_step];
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int n = c0 + fn * 32 + 8 * q + 4 * (lane >> 5);
+            float t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                t[e] = p.sb[(int64_t)min(n + e, p.N - 1) * p.sb_step];
+#pragma unroll
+            for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[fn][fm][4 * q + e] =
+                        (static_cast<float>(__builtin_bit_cast(int, (float)acc[fn][fm][4 * q + e])) * s[fm]) * t[e];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+}
+
+}  // namespace gnt

@@ -1,0 +1,102 @@
+/*
+ * gemm_layer.h -- C ABI of the MI355X (gfx950) products of a feed-forward layer:
+ * the gated block and its gradients, the product in 8-bit integers with a
+ * scale for each token and output channel, and the orthogonalized update of a
+ * weight.  Built as libgemm_layer.so, beside gemm_nt.h's library, whose types,
+ * status codes and epilogue it uses.
+ *
+ * Storage, types, rounding: row-major with element strides; operands BF16 or
+ * FP16 (all of one call's 16-bit operands share the type) or INT8; FP32 or INT32
+ * sums; results rounded once to nearest even.  Limits: rows below 2^30, sizes
+ * below 2^31, fewer than 2^23 output tiles, leading dimensions of operands
+ * below 2^22 and multiples of 8 (INT8: below 2^23, of 16), operand bases
+ * 16-byte aligned; outputs, and dH, need their element's alignment.  For given
+ * arguments every call on the same device returns the same bits.
+ *
+ * Workspaces: no handle; a call that needs one takes a device workspace of the
+ * caller's, 256-byte aligned and at least as large as the matching *_workspace
+ * function says for the same sizes.  Nothing needs to be in it before a call, and
+ * nothing is kept in it between calls.  Two calls that may run concurrently
+ * (different streams, two graphs' replays) need workspaces of their own.  A
+ * call allocates nothing, reads nothing on the host and only enqueues work on
+ * `stream`, for the device that is current; it can be captured into a HIP graph.
+ *
+ * Errors: GEMM_ERR_INVALID_ARG for null pointers, negative sizes, leading
+ * dimensions that are too small, unknown modes and a workspace that is too
+ * small; GEMM_ERR_UNSUPPORTED for types and sizes outside the limits;
+ * GEMM_ERR_MISALIGNED; GEMM_ERR_HIP.  On an error nothing is enqueued, but for
+ * GEMM_ERR_HIP, after which part of a call's launches may be.
+ */
+#ifndef GEMM_LAYER_H
+#define GEMM_LAYER_H
+
+#include <stdint.h>
+
+#include "gemm_nt.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* The gate's activation: max(0, x), x Phi(x) (the exact form), x / (1 + exp(-x)). */
+typedef enum { GEMM_GATE_RELU = 1, GEMM_GATE_GELU = 2, GEMM_GATE_SILU = 3 } gemm_gate_t;
+
+/* The gated block: H = act(X Wg^T) * (X Wu^T), X [M][K], Wg and Wu [F][K], H [M][F] of
+ * out_dtype (GEMM_BF16, GEMM_FP16, GEMM_FP32).  Both sums, the activation and the product
+ * are FP32, in one kernel; H is rounded once.
+ *   K % 8 == 0; F below 2^21.  K = 0: act(0) * 0. */
+gemm_status_t gemm_gated_workspace(int64_t M, int64_t F, int64_t K, int64_t *bytes);
+gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void *H, int64_t M,
+                             int64_t F, int64_t K, int64_t ldx, int64_t ldwg, int64_t ldwu,
+                             int64_t ldh, int in_dtype, int out_dtype, int activation,
+                             void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of H = act(g) * u, g = X Wg^T, u = X Wu^T, for dH [M][F] of the operands'
+ * type (any leading dimension >= F):
+ *   dg = dH u act'(g), du = dH act(g)
+ *   dX = dg Wg + du Wu     [M][K], dx_dtype
+ *   dWg = dg^T X, dWu = du^T X     [F][K] contiguous, grad_dtype, written whole
+ * Nothing of the forward call is needed: g and u are computed again, in FP32, and
+ * so are dg and du, which are then rounded to the operands' type once (relative to the value 2^-9
+ * at most for BF16; FP16 2^-12, in units of the power of two that brings dH's largest magnitude to
+ * 1 .. 2: dg and du must stay below 2^16 and lose bits below 2^-14 in them).  So an
+ * FP32 result is no more exact than that.
+ * dX may be NULL (not computed), and so may dWg and dWu, both or neither.  act' of ReLU
+ * is 0 at 0.  M = 0 writes zeros to dWg and dWu, F = 0 to dX. */
+gemm_status_t gemm_gated_backward_workspace(int64_t M, int64_t F, int64_t K, int64_t *bytes);
+gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void *Wg,
+                                      const void *Wu, void *dX, void *dWg, void *dWu, int64_t M,
+                                      int64_t F, int64_t K, int64_t lddh, int64_t ldx,
+                                      int64_t ldwg, int64_t ldwu, int64_t lddx, int in_dtype,
+                                      int dx_dtype, int grad_dtype, int activation,
+                                      void *workspace, int64_t workspace_bytes,
+                                      hipStream_t stream);
+
+/* Rows of X [M][K] (GEMM_BF16, GEMM_FP16 or GEMM_FP32; any leading dimension >= K) in 8-bit
+ * integers: scale[m] = max |X[m,:]| / 127, codes[m][k] = X[m][k] / scale[m] to the nearest
+ * integer, even at a tie, in -127 .. 127; both quotients are FP32 numbers, rounded to
+ * nearest.  A row of zeros has scale 0 and codes 0; one that holds an infinity or a NaN
+ * has scale NaN and codes 0.  codes [M][ldq], any ldq >= K; columns K .. ldq - 1 are left as they
+ * are. */
+gemm_status_t gemm_run_quantize_int8(const void *X, void *codes, float *scale, int64_t M,
+                                     int64_t K, int64_t ldx, int64_t ldq, int in_dtype,
+                                     hipStream_t stream);
+
+/* C = act(alpha y + beta C_old + bias), y[m][n] = scale_a[m] scale_b[n] sum_k A[m][k]
+ * B[n][k], A [M][K] and B [N][K] INT8 (-128 .. 127), C [M][N] of out_dtype; epi as gemm_run_ex's
+ * (NULL: the identity).  The sum is exact (INT32; of a K split, each split's), taken to
+ * FP32, multiplied by scale_a[m] and then by scale_b[n].
+ *   scales_a  M, or 1: one scale for all rows;  scales_b  N, or 1
+ *   K % 16 == 0, K < 2^17 */
+gemm_status_t gemm_int8_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes);
+gemm_status_t gemm_run_int8(const void *A, const void *B, void *C, int64_t M, int64_t N, int64_t K,
+                            int64_t lda, int64_t ldb, int64_t ldc, int out_dtype,
+                            const float *scale_a, int64_t scales_a, const float *scale_b,
+                            int64_t scales_b, const gemm_epilogue_t *epi, void *workspace,
+                            int64_t workspace_bytes, hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GEMM_LAYER_H */
