@@ -13,7 +13,7 @@ from ._lib import (GEMM_BF16, GEMM_FP16, GEMM_FP32, GEMM_FP8_E4M3, GEMM_FP8_E5M2
                    gemm_create, gemm_destroy, gemm_plan, gemm_run, gemm_status_string,
                    gemm_validate)
 from .api import Gemm, default_handle, gemm_fp8, gemm_grouped, gemm_nt
-from .layer import gemm_gated, gemm_gated_backward, gemm_int8, quantize_int8
+from .layer import gemm_gated, gemm_gated_backward, gemm_int8, orthogonalize, quantize_int8
 from .rows import (Routing, gemm_lora, gemm_lora_backward, gemm_routed, gemm_routed_wgrad,
                    route_topk, route_topk_backward)
 
@@ -21,4 +21,5 @@ __all__ = ["GEMM_BF16", "GEMM_FP16", "GEMM_FP32", "GEMM_FP8_E4M3", "GEMM_FP8_E5M
            "Gemm", "default_handle", "gemm_fp8", "gemm_grouped", "gemm_nt", "gemm_create", "gemm_destroy",
            "gemm_plan", "gemm_run", "gemm_status_string", "gemm_validate", "Routing", "gemm_lora",
            "gemm_lora_backward", "gemm_routed", "gemm_routed_wgrad", "route_topk",
-           "route_topk_backward", "gemm_gated", "gemm_gated_backward", "gemm_int8", "quantize_int8"]
+           "route_topk_backward", "gemm_gated", "gemm_gated_backward", "gemm_int8", "quantize_int8",
+           "orthogonalize"]

@@ -12,7 +12,8 @@ GATES = {"relu": 1, "gelu": 2, "silu": 3}
 
 # Every symbol include/gemm_layer.h declares.
 EXPORTS = ("gemm_gated_workspace", "gemm_run_gated", "gemm_gated_backward_workspace",
-           "gemm_run_gated_backward", "gemm_run_quantize_int8", "gemm_int8_workspace", "gemm_run_int8")
+           "gemm_run_gated_backward", "gemm_run_quantize_int8", "gemm_int8_workspace", "gemm_run_int8",
+           "gemm_orthogonalize_workspace", "gemm_run_orthogonalize")
 
 _lib = None
 
@@ -37,6 +38,9 @@ def lib():
     L.gemm_int8_workspace.argtypes = [i64] * 3 + [out64]
     L.gemm_run_int8.argtypes = [vp] * 3 + [i64] * 6 + [ci, vp, i64, vp, i64, ctypes.POINTER(GemmEpilogue),
                                                        vp, i64, vp]
+    L.gemm_orthogonalize_workspace.argtypes = [i64] * 3 + [out64]
+    L.gemm_run_orthogonalize.argtypes = [vp] * 2 + [i64] * 7 + [ci] * 2 + [i64, ctypes.POINTER(ctypes.c_float),
+                                                                          ctypes.c_double, vp, i64, vp]
     for name in EXPORTS:
         getattr(L, name).restype = ci
     _lib = L

@@ -13,7 +13,8 @@
 //                         whose block starts at row r0 and column c0, once the
 //                         main loop is done and before anything leaves them
 //   GNT_EXT_MAP(p, tm, tn, split)  in place of the block map where every block has a
-//                         tile; may move p's pointers
+//                         tile; may move p.A and p.B
+//   GNT_EXT_TILE(p, tm, tn)  the tile's number in the launch (its partials and counter)
 //   GNT_EXT_STORE(p, acc, r0, c0, stage, lane)  in place of a whole sum's store (after a
 //                         reduction in the kernel; partials of a second pass are stored as
 //                         ever), through the wave's share of the idle LDS
@@ -31,6 +32,9 @@
 #endif
 #ifndef GNT_EXT_ACC
 #define GNT_EXT_ACC(p, acc, r0, c0, split, lane)
+#endif
+#ifndef GNT_EXT_TILE
+#define GNT_EXT_TILE(p, tm, tn) ((tm) * p.tiles_n + (tn))
 #endif
 #ifndef GNT_EXT_PAIRED
 #define GNT_EXT_PAIRED 0

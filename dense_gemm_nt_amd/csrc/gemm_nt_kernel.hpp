@@ -87,7 +87,7 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     else
         map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
 #endif
-    const int tile = tm * p.tiles_n + tn;
+    const int tile = GNT_EXT_TILE(p, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     const int kt_begin = split * p.kt_per_split;
     const int kt_end = min(p.k_tiles, kt_begin + p.kt_per_split);

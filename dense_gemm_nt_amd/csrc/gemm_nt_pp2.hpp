@@ -547,7 +547,7 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
                 // two K splits: the second to arrive holds the sum and stores it
                 // as an unsplit tile (the flag lives in unit 8, past the staging
                 // area)
-                if (!splitk2_arrive<8, FN, FM>(p, acc, tm * p.tiles_n + tn, split, wave, lane,
+                if (!splitk2_arrive<8, FN, FM>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
                                                reinterpret_cast<uint32_t *>(smem + 8 * UNIT)))
                     return;
                 p.splits = 1;

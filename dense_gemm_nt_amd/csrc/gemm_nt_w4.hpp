@@ -397,7 +397,7 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
         // two K splits: the second to arrive holds the sum and stores it as an
         // unsplit tile
         wait_vmcnt<0>();
-        if (!splitk2_arrive<4, FN, FM>(p, acc, tm * p.tiles_n + tn, split, wave, lane,
+        if (!splitk2_arrive<4, FN, FM>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
                                        reinterpret_cast<uint32_t *>(smem)))
             return;
         p.splits = 1;

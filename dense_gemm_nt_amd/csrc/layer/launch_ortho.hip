@@ -1,0 +1,49 @@
+// The tiles of the orthogonalized update: both operands K-major (the squares) on the 128 x
+// 128 and the ping-pong tile, and the second MN-major (the step) on the ping-pong tile and
+// the 128 x 128 one of rows_tile.hpp.
+#include "layer_launch.hpp"
+#include "ortho_common.hpp"
+#include "ortho_ext.hpp"
+#include "../gemm_nt_kernel.hpp"
+#include "../gemm_nt_pp2.hpp"
+#include "../rows/rows_tile.hpp"
+
+namespace gnt {
+
+template <>
+struct TileHooks<OrthoArgs> {
+    static constexpr bool kLookup = false, kPaired = false, kStore = true;
+    template <int IN, int OUT>
+    static __device__ __forceinline__ void add(OrthoArgs &, f32x16 (&)[2][2], int, int, int, int)
+    {
+    }
+    static __device__ __forceinline__ const uint16_t *b(const OrthoArgs &p, int) { return p.B; }
+    static __device__ __forceinline__ int ldb(const OrthoArgs &p, int) { return p.ldb; }
+    static __device__ __forceinline__ int cols(const OrthoArgs &) { return 0; }
+    static __device__ __forceinline__ void map(OrthoArgs &p, int &tm, int &tn, int &split)
+    {
+        ortho_map(p, tm, tn, split);
+    }
+    static __device__ __forceinline__ int tile(const OrthoArgs &p, int tm, int tn) { return ortho_tile(p, tm, tn); }
+    static __device__ __forceinline__ void store(const OrthoArgs &p, const f32x16 (&acc)[2][2], int r0, int c0,
+                                                 uint8_t *stage, int lane)
+    {
+        store_ortho(p, acc, r0, c0, stage, lane);
+    }
+};
+
+hipError_t launch_ortho(const OrthoArgs &a, int tile, bool mn_major, unsigned grid, hipStream_t s)
+{
+    if (tile == 256 && mn_major)
+        hipLaunchKernelGGL((gemm_nt_pp2_ortho<IN_FP16, OUT_FP16, false, true>), dim3(grid), dim3(512), 0, s, a);
+    else if (tile == 256)
+        hipLaunchKernelGGL((gemm_nt_pp2_ortho<IN_FP16, OUT_FP16>), dim3(grid), dim3(512), 0, s, a);
+    else if (mn_major)
+        hipLaunchKernelGGL((rows_tile<IN_FP16, OUT_FP16, OrthoArgs>), dim3(grid), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((gemm_nt_kernel_ortho<128, 128, 64, 2, 4, 4, IN_FP16, OUT_FP16, false, false>),
+                           dim3(grid), dim3(512), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace gnt

@@ -27,12 +27,46 @@ namespace gnt {
 
 constexpr int kTileStages = 5, kTileOperand = 8192;
 
-// `args` is LoraArgs (a plan's tile and K split, adapters added) or RoutedArgs
-// (an expert's tile).
+// What a tile's argument block brings: LoraArgs a plan's tile and K split, to whose sums adapters
+// are added, RoutedArgs an expert's tile; others (outside this folder) specialize it.
+//   kLookup  finds the block's tile (false: none) without K splits, in place of the plan's map
+//   kPaired  B's k-rows alternate in groups of eight between two arrays
+//   tile     the tile's number in the launch
+//   kStore   store(p, acc, r0, c0, stage, lane) in place of a whole sum's store
+template <typename Args>
+struct TileHooks {
+    static constexpr bool kLookup = false, kPaired = false, kStore = false;
+    template <int IN, int OUT>
+    static __device__ __forceinline__ void add(Args &p, f32x16 (&acc)[2][2], int r0, int c0, int split, int lane)
+    {
+        lora_add<IN, 4, true, low_parts<IN, OUT>>(p, acc, r0, c0, split, lane);
+    }
+    static __device__ __forceinline__ const uint16_t *b(const Args &p, int) { return p.B; }
+    static __device__ __forceinline__ int ldb(const Args &p, int) { return p.ldb; }
+    static __device__ __forceinline__ int cols(const Args &) { return 0; }
+    static __device__ __forceinline__ int tile(const Args &p, int tm, int tn) { return tm * p.tiles_n + tn; }
+    static __device__ __forceinline__ void map(Args &p, int &tm, int &tn, int &split)
+    {
+        if (p.inreduce)
+            map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
+        else
+            map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+    }
+};
+
+template <>
+struct TileHooks<RoutedArgs> {
+    static constexpr bool kLookup = true, kPaired = false, kStore = false;
+    static __device__ __forceinline__ const uint16_t *b(const RoutedArgs &p, int) { return p.B; }
+    static __device__ __forceinline__ int ldb(const RoutedArgs &p, int) { return p.ldb; }
+    static __device__ __forceinline__ int cols(const RoutedArgs &) { return 0; }
+};
+
 template <int IN, int OUT, typename Args>
 __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
 {
-    constexpr bool ROUTED = std::is_same_v<Args, RoutedArgs>;
+    using Hooks = TileHooks<Args>;
+    constexpr bool ROUTED = Hooks::kLookup, PAIRED = Hooks::kPaired;
     constexpr int BM = 128, BN = 128, BK = 32, ST = kTileStages, OPER = kTileOperand, NL = 4;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[ST * 2 * OPER];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -43,17 +77,15 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
     if constexpr (ROUTED) {
         if (!routed_lookup(p, tm, tn))
             return;
-    } else if (p.inreduce) {
-        map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
     } else {
-        map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+        Hooks::map(p, tm, tn, split);
     }
     const int m0 = tm * BM, n0 = tn * BN;
     // (k_tiles and kt_per_split count 64-deep slabs, as the plans do)
     const int k_begin = split * p.kt_per_split * 64;
     const int k_end = min(p.K, k_begin + p.kt_per_split * 64);
     const int nk = (k_end - k_begin + BK - 1) / BK;
-    const bool whole = (k_end - k_begin) % BK == 0;
+    const bool whole = (k_end - k_begin) % BK == 0 && (!PAIRED || Hooks::cols(p) % (BK / 2) == 0);
     const int rows_a = min(BM, p.M - m0), rows_b = min(BN, p.N - n0);
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
@@ -74,14 +106,16 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
         }
         // B's k-rows of the slab as whole rows of ldb elements, from the tile's
         // first column
-        const int k_rows = min(BK, k_end - k0);
+        const int k_rows = PAIRED ? min(BK / 2, Hooks::cols(p) - k0 / 2) : min(BK, k_end - k0);
+        const int ldb = Hooks::ldb(p, wave >> 1);
         const __amdgpu_buffer_rsrc_t rs_b =
-            make_rsrc(p.B + (int64_t)k0 * p.ldb + n0, (uint32_t)(((int64_t)k_rows * p.ldb - n0) * 2));
+            make_rsrc(Hooks::b(p, wave >> 1) + (int64_t)(PAIRED ? k0 / 2 : k0) * ldb + n0,
+                      (uint32_t)(((int64_t)k_rows * ldb - n0) * 2));
         const int col = min(8 * chunk, (rows_b - 1) & ~7);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int row = 16 * j + 4 * wave + kr;
-            const uint32_t v = row < k_rows ? (uint32_t)row * (uint32_t)p.ldb * 2u + (uint32_t)col * 2u : kOutOfRange;
+            const int row = PAIRED ? 8 * j + 4 * (wave & 1) + kr : 16 * j + 4 * wave + kr;
+            const uint32_t v = row < k_rows ? (uint32_t)row * (uint32_t)ldb * 2u + (uint32_t)col * 2u : kOutOfRange;
             load_lds16(rs_b, v, 0, at + OPER + (uint32_t)(16 * j + 4 * wave) * 256u);
         }
     };
@@ -145,10 +179,10 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
     }
     mfma_settle();
     if constexpr (!ROUTED) {
-        lora_add<IN, 4, true, low_parts<IN, OUT>>(p, acc, m0 + wm, n0 + wn, split, lane);
+        Hooks::template add<IN, OUT>(p, acc, m0 + wm, n0 + wn, split, lane);
         if (p.inreduce) {
             // (the ring is behind the barrier's last reader once the partials are out)
-            if (!splitk_arrive<4, 2, 2>(p, acc, tm * p.tiles_n + tn, split, wave, lane,
+            if (!splitk_arrive<4, 2, 2>(p, acc, Hooks::tile(p, tm, tn), split, wave, lane,
                                         reinterpret_cast<uint32_t *>(smem)))
                 return;
             p.splits = 1;
@@ -161,6 +195,10 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
     wait_lgkmcnt0();
     wg_barrier();
     const int r0 = m0 + wm, c0 = n0 + wn;
+    if constexpr (Hooks::kStore) {
+        Hooks::store(p, acc, r0, c0, smem + wave * 16384, lane);
+        return;
+    }
     const bool partial = !ROUTED && p.splits > 1;
     const bool wide = !partial && p.rows16 && !p.epi && r0 + 64 <= p.M && c0 + 64 <= p.N;
     if (!wide) {

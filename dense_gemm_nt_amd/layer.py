@@ -3,7 +3,8 @@
 - the gated block act(x Wg^T) * (x Wu^T) and its gradients: ``gemm_gated``,
   ``gemm_gated_backward``;
 - the product in 8-bit integers with a scale for each token and output channel:
-  ``quantize_int8``, ``gemm_int8``.
+  ``quantize_int8``, ``gemm_int8``;
+- the orthogonalized update of a weight (Newton-Schulz products): ``orthogonalize``.
 
 Every call runs on the tensors' device, on its current stream, with workspaces and
 results from torch's allocator, so calls on several streams do not share any
@@ -184,4 +185,59 @@ def gemm_int8(A, B, scale_a, scale_b, out=None, out_dtype=None, alpha=1.0, beta=
         torch._C._cuda_getCurrentRawStream(index))
     if st:
         _lib.check(st, "gemm_int8(M=%d, N=%d, K=%d)" % (M, N, K))
+    return out
+
+
+@functools.lru_cache(maxsize=16)
+def _coefficients(flat):
+    return (ctypes.c_float * len(flat))(*flat)
+
+
+def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, out_dtype=None):
+    """The orthogonalized update of G [m, n] or of a stack [B, m, n] (bfloat16, float16 or
+    float32, unit stride along the last axis): X = G / (||G|| + eps), then `steps` times
+    X = a X + b (X X^T) X + c (X X^T)^2 X, which takes every singular value s to
+    a s + b s^3 + c s^5 and leaves the singular vectors.  `coefficients` is (a, b, c), or
+    one such triple a step.  Of out_dtype (default bfloat16).  X is kept in float32 and
+    multiplied in float16: about 1e-3 of the exact iteration off (relative) where the
+    coefficients keep the singular values below 2."""
+    import torch
+    if G.dim() not in (2, 3):
+        raise ValueError("G must be [m, n] or [B, m, n]")
+    index = _index(G)
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return orthogonalize(G, steps, coefficients, eps, out, out_dtype)
+    steps = int(steps)
+    if steps < 0:
+        raise ValueError("steps must not be negative")
+    flat = tuple(coefficients)
+    if len(flat) == 3 and not hasattr(flat[0], "__len__"):
+        flat = flat * steps
+    elif len(flat) == steps and all(hasattr(t, "__len__") and len(t) == 3 for t in flat):
+        flat = tuple(v for t in flat for v in t)
+    else:
+        raise ValueError("coefficients must be (a, b, c) or %d such triples" % steps)
+    B = G.shape[0] if G.dim() == 3 else 1
+    m, n = G.shape[-2:]
+
+    def strides(name, t):
+        if B and m and n and t.stride(-1) != 1 and n > 1:
+            raise ValueError("%s needs unit stride along its last axis" % name)
+        return t.stride(-2) if m > 1 else n, t.stride(0) if G.dim() == 3 and B > 1 else 0
+    ldg, g_step = strides("G", G)
+    if out is None:
+        out = torch.empty(G.shape, dtype=out_dtype or torch.bfloat16, device=G.device)
+    else:
+        _out("out", out, G.shape, G.device)
+    ldu, u_step = strides("out", out)
+    if B > 1 and m and n and u_step < (m - 1) * ldu + n:
+        raise ValueError("out's matrices overlap")
+    ws_bytes = _workspace_bytes("gemm_orthogonalize_workspace", B, m, n)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=G.device) if ws_bytes else None
+    st = _layer.lib().gemm_run_orthogonalize(
+        G.data_ptr(), out.data_ptr(), B, m, n, ldg, ldu, g_step, u_step, _code(G.dtype), _code(out.dtype), steps,
+        _coefficients(flat), eps, _ptr(ws), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        _lib.check(st, "orthogonalize(B=%d, m=%d, n=%d)" % (B, m, n))
     return out
