@@ -12,12 +12,15 @@
 //   GNT_EXT_ACC(p, acc, r0, c0, split, lane)  adds to a wave's accumulators,
 //                         whose block starts at row r0 and column c0, once the
 //                         main loop is done and before anything leaves them
-//   GNT_EXT_MAP(p, tm, tn, split)  in place of the block map where every block has a
-//                         tile; may move p.A and p.B
+//   GNT_EXT_MAP(p, tm, tn, split)  in place of the block map, K splits among it; false where
+//                         the block has no tile; may move p.A and p.B
 //   GNT_EXT_TILE(p, tm, tn)  the tile's number in the launch (its partials and counter)
 //   GNT_EXT_STORE(p, acc, r0, c0, stage, lane)  in place of a whole sum's store (after a
 //                         reduction in the kernel; partials of a second pass are stored as
 //                         ever), through the wave's share of the idle LDS
+//   GNT_EXT_AHEAD 1       a wave with one 32 x 32 block reads all of a slab's fragments before its
+//                         first MFMA (gemm_nt_kernel.hpp): with one MFMA a k-step, reading one
+//                         k-step ahead leaves most of each read's latency to be waited for
 //   GNT_EXT_PAIRED 1      B's rows alternate in groups of eight between two arrays of
 //                         GNT_EXT_COLS(p) rows each: row R of B is row 8 (R / 16) + R mod 8 of
 //                         array (R / 8) mod 2, which GNT_EXT_B(p, w) and GNT_EXT_LDB(p, w)
@@ -32,6 +35,9 @@
 #endif
 #ifndef GNT_EXT_ACC
 #define GNT_EXT_ACC(p, acc, r0, c0, split, lane)
+#endif
+#ifndef GNT_EXT_AHEAD
+#define GNT_EXT_AHEAD 0
 #endif
 #ifndef GNT_EXT_TILE
 #define GNT_EXT_TILE(p, tm, tn) ((tm) * p.tiles_n + (tn))

@@ -80,7 +80,8 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     if (!GNT_EXT_LOOKUP(p, tm, tn))
         return;
 #elif defined(GNT_EXT_MAP)
-    GNT_EXT_MAP(p, tm, tn, split);
+    if (!GNT_EXT_MAP(p, tm, tn, split))
+        return;
 #else
     if (p.inreduce)       // the K splits of a tile adjacent in launch order (splitk_arrive)
         map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
@@ -166,7 +167,9 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     // vector memory unit accepts at about one 1 KB load per 25 cycles, can run
     // beside the matrix cores instead of ahead of them.
     auto compute_slab = [&](const uint8_t *sa, const uint8_t *sb, int kvalid, auto load) {
-        u32x4 af[2][FM], bf[2][FN];
+        constexpr bool AHEAD = GNT_EXT_AHEAD && FM * FN == 1;    // all of the slab's fragments first
+        constexpr int SLOTS = AHEAD ? KSTEPS : 2;
+        u32x4 af[SLOTS][FM], bf[SLOTS][FN];
         auto fetch = [&](int ks, int slot) {
 #pragma unroll
             for (int fm = 0; fm < FM; ++fm)
@@ -176,10 +179,16 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
                 bf[slot][fn] = *reinterpret_cast<const u32x4 *>(sb + fn * 32 * PITCH + roff[ks]);
         };
         fetch(0, 0);
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int ks = 1; ks < KSTEPS; ++ks)
+                fetch(ks, ks);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
         for (int ks = 0; ks < KSTEPS; ++ks) {
-            const int cur = ks & 1;
-            if (ks + 1 < KSTEPS)
+            const int cur = AHEAD ? ks : ks & 1;
+            if (!AHEAD && ks + 1 < KSTEPS)
                 fetch(ks + 1, cur ^ 1);
             if constexpr (KMASK) {
                 const int nvalid = kvalid - (2 * ks + (lane >> 5)) * 8;

@@ -688,7 +688,8 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
         }
     } else {
 #ifdef GNT_EXT_MAP
-        GNT_EXT_MAP(p, tm, tn, split);
+        if (!GNT_EXT_MAP(p, tm, tn, split))
+            return;
 #else
         if (p.inreduce)
             map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn,

@@ -202,7 +202,8 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
 
     int tm, tn, split;
 #ifdef GNT_EXT_MAP
-    GNT_EXT_MAP(p, tm, tn, split);
+    if (!GNT_EXT_MAP(p, tm, tn, split))
+        return;
 #else
     if (p.inreduce)
         map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);

@@ -1,6 +1,5 @@
-// The tiles of the orthogonalized update: both operands K-major (the squares) on the 128 x
-// 128 and the ping-pong tile, and the second MN-major (the step) on the ping-pong tile and
-// the 128 x 128 one of rows_tile.hpp.
+// The tiles of the orthogonalized update: both operands K-major on three tile sizes, and the
+// second MN-major (the step) on the ping-pong tile and the 128 x 128 one of rows_tile.hpp.
 #include "layer_launch.hpp"
 #include "ortho_common.hpp"
 #include "ortho_ext.hpp"
@@ -22,9 +21,9 @@ struct TileHooks<OrthoArgs> {
     static __device__ __forceinline__ int cols(const OrthoArgs &) { return 0; }
     static __device__ __forceinline__ void map(OrthoArgs &p, int &tm, int &tn, int &split)
     {
-        ortho_map(p, tm, tn, split);
+        ortho_map(p, tm, tn, split);          // (a step's tiles are all there)
     }
-    static __device__ __forceinline__ int tile(const OrthoArgs &p, int tm, int tn) { return ortho_tile(p, tm, tn); }
+    static __device__ __forceinline__ int tile(const OrthoArgs &p, int, int) { return ortho_tile(p); }
     static __device__ __forceinline__ void store(const OrthoArgs &p, const f32x16 (&acc)[2][2], int r0, int c0,
                                                  uint8_t *stage, int lane)
     {
@@ -32,17 +31,31 @@ struct TileHooks<OrthoArgs> {
     }
 };
 
-hipError_t launch_ortho(const OrthoArgs &a, int tile, bool mn_major, unsigned grid, hipStream_t s)
+hipError_t launch_ortho(const OrthoArgs &a, OrthoTile tile, unsigned grid, hipStream_t s)
 {
-    if (tile == 256 && mn_major)
+    switch (tile) {
+    case ORTHO_256_MN:
         hipLaunchKernelGGL((gemm_nt_pp2_ortho<IN_FP16, OUT_FP16, false, true>), dim3(grid), dim3(512), 0, s, a);
-    else if (tile == 256)
+        break;
+    case ORTHO_256:
         hipLaunchKernelGGL((gemm_nt_pp2_ortho<IN_FP16, OUT_FP16>), dim3(grid), dim3(512), 0, s, a);
-    else if (mn_major)
+        break;
+    case ORTHO_128_MN:
         hipLaunchKernelGGL((rows_tile<IN_FP16, OUT_FP16, OrthoArgs>), dim3(grid), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((gemm_nt_kernel_ortho<128, 128, 64, 2, 4, 4, IN_FP16, OUT_FP16, false, false>),
-                           dim3(grid), dim3(512), 0, s, a);
+        break;
+    case ORTHO_128:
+        hipLaunchKernelGGL((gemm_nt_kernel_ortho<128, 128, 64, 2, 4, 4, IN_FP16, OUT_FP16, false, false>), dim3(grid),
+                           dim3(512), 0, s, a);
+        break;
+    case ORTHO_128_S2:
+        hipLaunchKernelGGL((gemm_nt_kernel_ortho<128, 128, 64, 2, 4, 2, IN_FP16, OUT_FP16, false, false>), dim3(grid),
+                           dim3(512), 0, s, a);
+        break;
+    case ORTHO_64:
+        hipLaunchKernelGGL((gemm_nt_kernel_ortho<64, 64, 64, 2, 2, 4, IN_FP16, OUT_FP16, false, false>), dim3(grid),
+                           dim3(256), 0, s, a);
+        break;
+    }
     return hipGetLastError();
 }
 

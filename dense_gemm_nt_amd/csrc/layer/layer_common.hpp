@@ -98,8 +98,9 @@ __device__ __forceinline__ uint32_t to_bits16(float x)
 }
 
 // `count` (1 .. 8, or 4 of FP32) consecutive values of a row at C, element index idx: one
-// 16-byte store where all are there and rows allow it.
-template <int OUT, int V>
+// 16-byte store where all are there and rows allow it, of 16-bit values with the
+// non-temporal policy where NT (results; what the next launch reads stays in the caches).
+template <int OUT, int V, bool NT = true>
 __device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)[V], bool wide, int count)
 {
     if constexpr (OUT == OUT_FP32) {
@@ -122,7 +123,10 @@ __device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)
         for (int i = 0; i < 4; ++i)
             w[i] = to_bits16<OUT>(x[2 * i]) | to_bits16<OUT>(x[2 * i + 1]) << 16;
         if (wide && count >= V) {
-            __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
+            if constexpr (NT)
+                __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
+            else
+                *reinterpret_cast<u32x4 *>(c) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)

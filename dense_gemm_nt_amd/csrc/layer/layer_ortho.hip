@@ -19,7 +19,7 @@
 
 namespace gnt {
 
-hipError_t launch_ortho(const OrthoArgs &a, int tile, bool mn_major, unsigned grid, hipStream_t s);
+hipError_t launch_ortho(const OrthoArgs &a, OrthoTile tile, unsigned grid, hipStream_t s);
 
 constexpr int kOrthoParts = 1024;          // partial sums of squares of a stack, at most
 
@@ -27,6 +27,27 @@ __device__ __forceinline__ float read_any(const void *x, int64_t i, int dtype)
 {
     return dtype == OUT_FP32 ? static_cast<const float *>(x)[i]
                              : from_bits16(dtype, static_cast<const uint16_t *>(x)[i]);
+}
+
+// Eight values from element i on, of which the first `left` are there; zeros behind them.
+__device__ __forceinline__ void read_eight(const void *x, int64_t i, int dtype, bool wide, int left, float (&v)[8])
+{
+    if (wide && left >= 8 && dtype == OUT_FP32) {
+        const f32x4 *s = reinterpret_cast<const f32x4 *>(static_cast<const float *>(x) + i);
+        const f32x4 a = s[0], b = s[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = a[e], v[4 + e] = b[e];
+    } else if (wide && left >= 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(x) + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = from_bits16(dtype, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = e < left ? read_any(x, i + e, dtype) : 0.0f;
+    }
 }
 
 __device__ __forceinline__ double block_sum(double v, double *part)
@@ -41,18 +62,34 @@ __device__ __forceinline__ double block_sum(double v, double *part)
 }
 
 // Partial sums of squares, in FP64 (an FP32 gradient's squares leave FP32's range on both
-// sides): block (i, b) takes every gridDim.x-th row of matrix b.
+// sides): the threads of matrix b's blocks (x, b) take eight values of a row each in turn, four
+// loads of them at a time (one at a time 2 TB/s, of a long row 5.6).  The arrival counters of
+// the products to come are cleared on the way.
 __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n, int64_t ld, int64_t step, int dtype,
-                                                     double *parts)
+                                                     int wide, double *parts, unsigned *counters, int num_counters)
 {
     __shared__ double part[4];
+    const int id = blockIdx.x * 256 + threadIdx.x, threads = gridDim.x * 256;
+    if (blockIdx.y == 0)
+        for (int i = id; i < num_counters; i += threads)
+            counters[i] = 0u;
+    const int runs = (n + 7) / 8;
+    const int64_t all = (int64_t)m * runs, from = blockIdx.y * step;
     double s = 0.0;
-    for (int r = blockIdx.x; r < m; r += gridDim.x) {
-        const int64_t row = blockIdx.y * step + (int64_t)r * ld;
-        for (int c = threadIdx.x; c < n; c += 256) {
-            const double v = read_any(G, row + c, dtype);
-            s += v * v;
+    for (int64_t i = id; i < all; i += 4 * (int64_t)threads) {
+        float v[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t at = i + j * (int64_t)threads;
+            const int64_t r = at / runs;
+            const int c = (int)(at - r * runs) * 8;
+            read_eight(G, from + r * ld + c, dtype, wide != 0, at < all ? n - c : 0, v[j]);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s += (double)v[j][e] * (double)v[j][e];
     }
     s = block_sum(s, part);
     if (threadIdx.x == 0)
@@ -60,38 +97,54 @@ __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n
 }
 
 // X = G / (||G|| + eps) in FP32 and, times s, in FP16, [rows8][cols8] with zeros past the
-// matrix; a tall G (flip) is transposed on the way.  A block has 64 x 64 values.
+// matrix, and with xt the latter transposed, [cols8][rows8]; a tall G (flip) is transposed on the
+// way.  A block has 64 x 64 values.
 __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, int64_t ld, int64_t step, int dtype,
-                                                   int flip, const double *parts, int num_parts, double eps, float s,
-                                                   float *x, uint16_t *xh, int rows8, int cols8)
+                                                   int wide, int flip, const double *parts, int num_parts, double eps,
+                                                   float s, float *x, uint16_t *xh, uint16_t *xt, int rows8, int cols8)
 {
     __shared__ double part[4];
     __shared__ float tile[64][65];
+    const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;         // of X
+    const int g_r0 = flip ? c0 : r0, g_c0 = flip ? r0 : c0;       // of G
+    float v[2][8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = threadIdx.x + 256 * i, r = g_r0 + (t >> 3), c = g_c0 + 8 * (t & 7);
+        read_eight(G, blockIdx.z * step + (int64_t)r * ld + c, dtype, wide != 0, r < m ? n - c : 0, v[i]);
+    }
     double sum = 0.0;
     for (int i = threadIdx.x; i < num_parts; i += 256)
         sum += parts[blockIdx.z * num_parts + i];
     const double inv = 1.0 / (__builtin_sqrt(block_sum(sum, part)) + eps);
-    const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;         // of X
-    const int g_r0 = flip ? c0 : r0, g_c0 = flip ? r0 : c0;       // of G
-    const int64_t from = blockIdx.z * step;
-    for (int i = threadIdx.x; i < 4096; i += 256) {
-        const int r = g_r0 + (i >> 6), c = g_c0 + (i & 63);
-        tile[i >> 6][i & 63] = r < m && c < n ? (float)(read_any(G, from + (int64_t)r * ld + c, dtype) * inv) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = threadIdx.x + 256 * i;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            tile[t >> 3][8 * (t & 7) + e] = (float)((double)v[i][e] * inv);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 512; i += 256) {
-        const int r = i >> 3, c = (i & 7) * 8;
-        if (r0 + r >= rows8 || c0 + c >= cols8)
-            continue;
-        const int64_t at = (int64_t)blockIdx.z * rows8 * cols8 + (int64_t)(r0 + r) * cols8 + c0 + c;
-        float y[8], h[8];
+    const int64_t at = (int64_t)blockIdx.z * rows8 * cols8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            y[e] = flip ? tile[c + e][r] : tile[r][c + e];
-            h[e] = s * y[e];
+    for (int i = 0; i < 2; ++i) {
+        const int t = threadIdx.x + 256 * i, r = t >> 3, c = (t & 7) * 8;
+        float y[8], h[8];
+        if (r0 + r < rows8 && c0 + c < cols8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] = flip ? tile[c + e][r] : tile[r][c + e];
+                h[e] = s * y[e];
+            }
+            store_run<OUT_FP32, 8>(x, at + (int64_t)(r0 + r) * cols8 + c0 + c, y, true, 8);
+            store_run<OUT_FP16, 8, false>(xh, at + (int64_t)(r0 + r) * cols8 + c0 + c, h, true, 8);
         }
-        store_run<OUT_FP32, 8>(x, at, y, true, 8);
-        store_run<OUT_FP16, 8>(xh, at, h, true, 8);
+        if (xt && c0 + r < cols8 && r0 + c < rows8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                h[e] = s * (flip ? tile[r][c + e] : tile[c + e][r]);
+            store_run<OUT_FP16, 8, false>(xt, at + (int64_t)(c0 + r) * rows8 + r0 + c, h, true, 8);
+        }
     }
 }
 
@@ -114,59 +167,132 @@ __global__ __launch_bounds__(256) void ortho_copy(const float *x, int rows8, int
 
 namespace {
 
-struct OrthoPlan {
-    int tile, splits;
-    Plan plan;               // of one of the stack's matrices
-    int64_t blocks;          // of the stack
+// One launch of a product: its tile and K splits, and which of the stack's tiles.
+struct OrthoLaunch {
+    OrthoTile tile;
+    int size;                // of a tile
+    int first, quarters;     // OrthoArgs'
+    int splits, kt_per_split;
+    int64_t blocks;
 };
 
-// Tile and K splits of a stack's product.  A pass of the machine takes about 10 + 1.5 us a
-// 64-deep slab on the ping-pong tile and 5 + 0.62 on the 128 x 128 one; splits are summed in
-// the kernel (two on the ping-pong tile), in about 6 and 3 + s / 2 us, and keep 4 slabs.
-OrthoPlan plan_ortho(int64_t batch, int64_t M, int64_t N, int64_t K)
+struct OrthoPlan {
+    int half;                // a square's lower half only: the size of its tiles
+    int tiles;               // of a matrix
+    int tiles_m, tiles_n, k_tiles;
+    int count;
+    OrthoLaunch part[2];
+    int64_t partials;        // values
+    int64_t counters;
+};
+
+// What a pass of the machine takes, in us: begin + slab a 64-deep slab (alone: with one block a
+// compute unit where two fit); the most splits (summed in the kernel), and us a split.  From
+// the kernels' times: steps of 12 matrices of 768 x 2048 and of one of 4096 x 8192 (12 and 64 slabs)
+// on 256_MN 41 and 132 a pass, 128_MN 26 and 87, 128_S2 28 and 86, 128 19 and 47, 64 12 and 32;
+// squares of 4096 on 256 91 (64 slabs) and 160 (128), of 12 x 768 on 128 17 (12) and 28 (32), of 1000 on 64
+// 9.5 (16) and 28 (125).
+struct OrthoKind {
+    OrthoTile tile;
+    int size, at_once, splits;
+    bool mn;
+    double begin, slab, alone, split;
+};
+constexpr OrthoKind kOrthoKinds[] = {
+    {ORTHO_256, 256, 1, 2, false, 18.0, 1.3, 1.3, 8.0},   {ORTHO_256_MN, 256, 1, 2, true, 19.0, 1.75, 1.75, 8.0},
+    {ORTHO_128, 128, 1, 16, false, 11.5, 0.52, 0.52, 1.0}, {ORTHO_128_S2, 128, 2, 1, false, 15.0, 1.1, 0.6, 0.0},
+    {ORTHO_128_MN, 128, 2, 16, true, 11.0, 1.2, 0.85, 1.0}, {ORTHO_64, 64, 2, 16, false, 6.5, 0.4, 0.22, 0.7},
+};
+
+double cost_of(const OrthoKind &k, int64_t blocks, int64_t slabs, int64_t splits)
+{
+    const double slab = blocks <= kNumCUs ? k.alone : k.slab;
+    return (double)cdiv(blocks, kNumCUs * k.at_once) * (k.begin + slab * (double)slabs) +
+           (splits > 1 ? 2.0 + k.split * (double)splits : 0.0);
+}
+
+// Splits of `slabs` that keep four slabs each and fill `s` whole; 0: not that many.
+int64_t slabs_per(int64_t slabs, int64_t s)
+{
+    const int64_t per = cdiv(slabs, s);
+    return s == 1 ? per : slabs / s >= 4 && cdiv(slabs, per) == s ? per : 0;
+}
+
+// The launches of a stack's product [M][N] over K, the least by what they are expected to take:
+// `square` (M = N, symmetric, both operands K-major: the lower half of its tiles) or the step.
+OrthoPlan plan_ortho(int64_t batch, int64_t M, int64_t N, int64_t K, bool square)
 {
     OrthoPlan best{};
-    double least = 0.0;
+    double least = -1.0;
     const int64_t slabs = cdiv(K, 64);
-    for (int tile : {256, 128}) {
-        const int64_t tm = cdiv(M, tile), tn = cdiv(N, tile), tiles = tm * tn * batch;
-        for (int64_t s = 1; s <= (tile == 256 ? 2 : 16) && (s == 1 || slabs / s >= 4); ++s) {
-            const int64_t per = cdiv(slabs, s), splits = slabs ? cdiv(slabs, per) : 1;
-            if (splits != s || (s > 1 && (tiles * s * tile * tile * 4 > kPartialBytes * 4 || tiles * s > 4 * kNumCUs)))
+    auto fits = [&](int64_t blocks, int64_t s, int size) {
+        return s == 1 || (blocks * size * size * 4 <= 2 * kPartialBytes && blocks <= 4 * kNumCUs);
+    };
+    auto begin = [&](const OrthoKind &k) {
+        OrthoPlan p{};
+        p.tiles_m = (int)cdiv(M, k.size), p.tiles_n = (int)cdiv(N, k.size);
+        p.k_tiles = (int)slabs;
+        p.half = square ? k.size : 0;
+        p.tiles = square ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+        return p;
+    };
+    auto add = [&](OrthoPlan &p, const OrthoKind &k, int64_t first, bool quarters, int64_t tiles, int64_t s) {
+        const int64_t blocks = tiles * s;
+        p.part[p.count++] = {k.tile, k.size, (int)first, quarters, (int)s, (int)slabs_per(slabs, s), blocks};
+        if (s > 1) {
+            p.partials = std::max<int64_t>(p.partials, blocks * k.size * k.size);
+            p.counters = std::max<int64_t>(p.counters, tiles);
+        }
+    };
+    for (const OrthoKind &k : kOrthoKinds) {
+        if (square ? k.mn : k.tile == ORTHO_256)
+            continue;
+        for (int64_t s = 1; s <= k.splits; ++s) {
+            const int64_t per = slabs_per(slabs, s);
+            OrthoPlan p = begin(k);
+            const int64_t all = batch * p.tiles;
+            if ((slabs && !per) || !fits(all * s, s, k.size))
                 continue;
-            const double passes = (double)cdiv(tiles * s, kNumCUs);
-            const double cost = tile == 256 ? passes * (10 + 1.5 * per) + (s > 1 ? 6 : 0)
-                                            : passes * (5 + 0.62 * per) + (s > 1 ? 3 + 0.5 * s : 0);
-            if (best.tile == 0 || cost < least) {
-                least = cost;
-                best.tile = tile;
-                best.splits = (int)s;
-                Plan &p = best.plan;
-                p = Plan{};
-                p.tiles_m = (int)tm, p.tiles_n = (int)tn;
-                p.k_tiles = (int)slabs;
-                p.splits = (int)s;
-                p.kt_per_split = (int)per;
-                p.group_m = std::min<int>(4, p.tiles_m);
-                p.inreduce = s > 1;
-                p.ws_bytes = s > 1 ? tiles * s * tile * tile * 4 : 0;
-                p.grid = tiles * s;
+            add(p, k, 0, false, all, s);
+            const double cost = cost_of(k, all * s, per, s);
+            if (least < 0.0 || cost < least)
+                least = cost, best = p;
+        }
+    }
+    // A square's 256 x 256 tiles that fill whole passes of the machine, and the quarters of the
+    // rest on the 128 x 128 tile, with splits: two matrices of 4096 rows (272 tiles) 3.29 ms for
+    // the update, on the one tile 3.53.  (Whole passes of tiles split in two did not pay: one
+    // matrix of 4096 x 8192, 128 tiles twice and 8 over, 3.18 against 3.14.)
+    if (square) {
+        const OrthoKind &k = kOrthoKinds[0], &q = kOrthoKinds[2];
+        OrthoPlan p = begin(k);
+        const int64_t all = batch * p.tiles, whole = all / kNumCUs * kNumCUs, rest = 4 * (all - whole);
+        if (whole > 0 && rest > 0) {
+            int64_t rs = 1;
+            double rest_cost = cost_of(q, rest, slabs, 1);
+            for (int64_t t = 2; t <= q.splits; ++t)
+                if (slabs_per(slabs, t) && fits(rest * t, t, q.size) && cost_of(q, rest * t, slabs_per(slabs, t), t) < rest_cost)
+                    rest_cost = cost_of(q, rest * t, slabs_per(slabs, t), t), rs = t;
+            if (cost_of(k, whole, slabs, 1) + rest_cost < least) {
+                add(p, k, 0, false, whole, 1);
+                add(p, q, whole, true, rest, rs);
+                best = p;
             }
         }
     }
-    best.blocks = best.plan.grid;
     return best;
 }
 
 struct OrthoWs {
     int64_t r, k, r8, k8;
     int parts;               // partial sums a matrix
+    bool turned;             // the step reads X transposed
     OrthoPlan plan[3];
     double *sums;
     float *x, *partials;
-    uint16_t *xh, *a, *b;
+    uint16_t *xh, *xt, *a, *b;
     unsigned *counters;
-    int num_counters[3];
+    int num_counters;
     int64_t bytes;
 };
 
@@ -175,26 +301,30 @@ OrthoWs carve_ortho(int64_t batch, int64_t m, int64_t n, void *base)
     OrthoWs w{};
     Carver c{static_cast<uint8_t *>(base)};
     w.r = std::min(m, n), w.k = std::max(m, n);
-    w.r8 = cdiv(w.r, 8) * 8, w.k8 = cdiv(w.k, 8) * 8;
-    w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(m, kOrthoParts / std::max<int64_t>(1, batch)));
-    w.plan[ORTHO_SQUARE] = plan_ortho(batch, w.r8, w.r8, w.k8);
-    w.plan[ORTHO_POLY] = plan_ortho(batch, w.r8, w.r8, w.r8);
-    w.plan[ORTHO_STEP] = plan_ortho(batch, w.r8, w.k8, w.r8);
+    // whole 128-byte lines a row: 1000 x 2047 with rows of 1000 and 2048 took 19.8 us a step,
+    // 1024 x 2048 14.9
+    w.r8 = cdiv(w.r, 64) * 64, w.k8 = cdiv(w.k, 64) * 64;
+    w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(cdiv(m * cdiv(n, 8), 1024), kOrthoParts / std::max<int64_t>(1, batch)));
+    w.plan[ORTHO_SQUARE] = plan_ortho(batch, w.r8, w.r8, w.k8, true);
+    w.plan[ORTHO_POLY] = plan_ortho(batch, w.r8, w.r8, w.r8, true);
+    w.plan[ORTHO_STEP] = plan_ortho(batch, w.r8, w.k8, w.r8, false);
+    const int64_t size = batch * w.r8 * w.k8;
     w.sums = c.take<double>(batch * w.parts);
-    w.x = c.take<float>(batch * w.r8 * w.k8);
-    w.xh = c.take<uint16_t>(2 * batch * w.r8 * w.k8);      // two, in turn: a step reads one and writes the other
+    w.x = c.take<float>(size);
+    w.xh = c.take<uint16_t>(2 * size);       // two, in turn: a step reads one and writes the other
+    const OrthoTile step = w.plan[ORTHO_STEP].part[0].tile;
+    w.turned = step != ORTHO_256_MN && step != ORTHO_128_MN;
+    w.xt = c.take<uint16_t>(w.turned ? 2 * size : 0);
     w.a = c.take<uint16_t>(batch * w.r8 * w.r8);
     w.b = c.take<uint16_t>(batch * w.r8 * w.r8);
     int64_t partial = 0, counters = 0;
-    for (int i = 0; i < 3; ++i) {
-        const Plan &p = w.plan[i].plan;
-        partial = std::max(partial, p.ws_bytes / 4);
-        w.num_counters[i] = p.inreduce ? (int)(batch * p.tiles_m * p.tiles_n) : 0;
-        counters = std::max<int64_t>(counters, w.num_counters[i]);
+    for (const OrthoPlan &p : w.plan) {
+        partial = std::max(partial, p.partials);
+        counters = std::max(counters, p.counters);
     }
     w.partials = c.take<float>(partial);
     w.counters = c.take<unsigned>(counters);               // (each call of a tile leaves them zero)
-    w.num_counters[0] = (int)counters;
+    w.num_counters = (int)counters;
     w.bytes = c.used;
     return w;
 }
@@ -254,21 +384,21 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != GEMM_OK)
         return st;
     const bool flip = m > n;
+    const int wide = (ldg * size_of(in_dtype)) % 16 == 0 && (g_step * size_of(in_dtype)) % 16 == 0 &&
+                     (uintptr_t)G % 16 == 0;
     for (const OrthoPlan &p : w.plan)
-        if (p.blocks <= 0 || p.blocks >= kMaxBlocks)
-            return GEMM_ERR_UNSUPPORTED;
+        for (int i = 0; i < p.count; ++i)
+            if (p.part[i].blocks <= 0 || p.part[i].blocks >= kMaxBlocks)
+                return GEMM_ERR_UNSUPPORTED;
 
     hipLaunchKernelGGL(ortho_squares, dim3(w.parts, (unsigned)batch), dim3(256), 0, stream, G, (int)m, (int)n, ldg,
-                       g_step, in_dtype, w.sums);
+                       g_step, in_dtype, wide, w.sums, w.counters, w.num_counters);
     hipError_t e = hipGetLastError();
-    const SplitWs counters{w.partials, w.counters, w.num_counters[0]};
-    if (e == hipSuccess)
-        e = clear_counters(&counters, 1, stream);
     const float s = std::exp2(std::round(0.5f * std::log2((float)w.k))), t = 64.0f;
     if (e == hipSuccess) {
         hipLaunchKernelGGL(ortho_begin, dim3((unsigned)cdiv(w.k8, 64), (unsigned)cdiv(w.r8, 64), (unsigned)batch), dim3(256),
-                           0, stream, G, (int)m, (int)n, ldg, g_step, in_dtype, (int)flip, w.sums, w.parts, eps, s, w.x,
-                           w.xh, (int)w.r8, (int)w.k8);
+                           0, stream, G, (int)m, (int)n, ldg, g_step, in_dtype, wide, (int)flip, w.sums, w.parts, eps,
+                           s, w.x, w.xh, w.turned ? w.xt : nullptr, (int)w.r8, (int)w.k8);
         e = hipGetLastError();
     }
     OrthoArgs last{};
@@ -290,24 +420,32 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
         const float ca = coefficients[3 * i], cb = coefficients[3 * i + 1], cc = coefficients[3 * i + 2];
         const float sigma = i >= 2 ? 1.0f : 0.0f;
         uint16_t *xh = w.xh + (i & 1) * batch * x_step, *next = w.xh + ((i + 1) & 1) * batch * x_step;
-        const SplitWs split{w.partials, w.counters, 0};
+        const uint16_t *xt = w.turned ? w.xt + (i & 1) * batch * x_step : nullptr;
         for (int mode = ORTHO_SQUARE; mode <= ORTHO_STEP && e == hipSuccess; ++mode) {
             const OrthoPlan &plan = w.plan[mode];
             OrthoArgs a = mode == ORTHO_STEP && i + 1 == steps ? last : OrthoArgs{};
             a.mode = mode;
-            a.all_splits = plan.splits;
+            a.tiles = plan.tiles;
+            a.half = plan.half;
             const bool step = mode == ORTHO_STEP;
-            fill_args(a, plan.plan, split, mode == ORTHO_SQUARE ? w.a : mode == ORTHO_POLY ? w.b : next, w.r8,
-                      step ? w.k8 : w.r8, mode == ORTHO_SQUARE ? w.k8 : w.r8, step ? w.k8 : w.r8, GEMM_FP16);
+            a.C = mode == ORTHO_SQUARE ? w.a : mode == ORTHO_POLY ? w.b : next;
+            a.M = (int)w.r8, a.N = (int)(step ? w.k8 : w.r8), a.K = (int)(mode == ORTHO_SQUARE ? w.k8 : w.r8);
+            a.ldc = a.N;
+            a.tiles_m = plan.tiles_m, a.tiles_n = plan.tiles_n, a.k_tiles = plan.k_tiles;
+            a.group_m = std::min(4, plan.tiles_m);
+            a.partials = w.partials;
+            a.counters = w.counters;
             a.A = mode == ORTHO_SQUARE ? xh : mode == ORTHO_POLY ? w.a : w.b;
-            a.B = mode == ORTHO_SQUARE ? xh : mode == ORTHO_POLY ? w.a : xh;
+            a.B = mode == ORTHO_SQUARE ? xh : mode == ORTHO_POLY ? w.a : w.turned ? xt : xh;
             a.lda = (int)(mode == ORTHO_SQUARE ? w.k8 : w.r8);
-            a.ldb = (int)(mode == ORTHO_POLY ? w.r8 : w.k8);
+            a.ldb = (int)(mode == ORTHO_POLY || (step && w.turned) ? w.r8 : w.k8);
             a.a_step = mode == ORTHO_SQUARE ? x_step : sq_step;
             a.b_step = mode == ORTHO_POLY ? sq_step : x_step;
             a.c_step = step ? x_step : sq_step;
             a.old = w.a;
             a.x = w.x;
+            a.xt = step && w.turned ? w.xt + ((i + 1) & 1) * batch * x_step : nullptr;
+            a.ldt = (int)w.r8;
             if (mode == ORTHO_SQUARE) {
                 a.alpha = t / (s * s);
                 a.shift = t * sigma;
@@ -319,7 +457,15 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
                 a.beta = (float)((double)ca + (double)sigma * ((double)cb + (double)cc));
                 a.scale = s;
             }
-            e = launch_ortho(a, plan.tile, step, (unsigned)plan.blocks, stream);
+            for (int j = 0; j < plan.count && e == hipSuccess; ++j) {
+                const OrthoLaunch &l = plan.part[j];
+                a.first = l.first;
+                a.quarters = l.quarters;
+                a.splits = a.all_splits = l.splits;
+                a.kt_per_split = l.kt_per_split;
+                a.inreduce = l.splits > 1;
+                e = launch_ortho(a, l.tile, (unsigned)l.blocks, stream);
+            }
         }
     }
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;

@@ -1,5 +1,6 @@
 // paired_ext.hpp -- the tiles' extension points for B in two arrays (before a tile header):
 // the gated block, or with GNT_GATE_GRAD its pre-activations' gradients.
+#define GNT_EXT_AHEAD 1
 #define GNT_EXT_ARGS PairedArgs
 #define GNT_EXT_PAIRED 1
 #define GNT_EXT_COLS(p) (p.cols)
