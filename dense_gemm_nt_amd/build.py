@@ -44,7 +44,7 @@ LAYER_SOURCES = [os.path.join(LAYER, f) for f in (
     "layer_gated.hip", "layer_int8.hip", "launch_gated_tiles.hip", "launch_gated_tiles_b.hip",
     "launch_gategrad_tiles.hip", "launch_gategrad_tiles_b.hip", "launch_gated_w4.hip",
     "launch_gategrad_w4.hip", "launch_gated_pp2.hip", "launch_gategrad_pp2.hip", "launch_gated_dx.hip",
-    "launch_gated_dw.hip", "launch_int8_tiles.hip", "launch_int8_pp2.hip", "layer_ortho.hip",
+    "launch_gated_dx_tile.hip", "launch_gated_dw.hip", "launch_int8_tiles.hip", "launch_int8_pp2.hip", "layer_ortho.hip",
     "launch_ortho.hip")]
 LAYER_HEADERS = [os.path.join(LAYER, f) for f in ("layer_common.hpp", "layer_host.hpp", "layer_launch.hpp",
                                                   "paired_ext.hpp", "int8_ext.hpp", "ortho_common.hpp",

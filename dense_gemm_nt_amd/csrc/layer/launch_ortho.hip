@@ -10,15 +10,12 @@
 namespace gnt {
 
 template <>
-struct TileHooks<OrthoArgs> {
-    static constexpr bool kLookup = false, kPaired = false, kStore = true;
+struct TileHooks<OrthoArgs> : PlanTile<OrthoArgs> {
+    static constexpr bool kStore = true;
     template <int IN, int OUT>
     static __device__ __forceinline__ void add(OrthoArgs &, f32x16 (&)[2][2], int, int, int, int)
     {
     }
-    static __device__ __forceinline__ const uint16_t *b(const OrthoArgs &p, int) { return p.B; }
-    static __device__ __forceinline__ int ldb(const OrthoArgs &p, int) { return p.ldb; }
-    static __device__ __forceinline__ int cols(const OrthoArgs &) { return 0; }
     static __device__ __forceinline__ void map(OrthoArgs &p, int &tm, int &tn, int &split)
     {
         ortho_map(p, tm, tn, split);          // (a step's tiles are all there)

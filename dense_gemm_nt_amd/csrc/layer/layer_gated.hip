@@ -55,13 +55,13 @@ __global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int
 }
 
 struct ClearList {
-    unsigned *at[3];
-    int count[3];
+    unsigned *at[4];
+    int count[4];
 };
 
 __global__ __launch_bounds__(256) void clear_words(ClearList l)
 {
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 4; ++i)
         for (int j = blockIdx.x * 256 + threadIdx.x; j < l.count[i]; j += gridDim.x * 256)
             l.at[i][j] = 0u;
 }
@@ -152,20 +152,38 @@ gemm_status_t check_sizes(int64_t M, int64_t F, int64_t K, int in_dtype, int out
     return GEMM_OK;
 }
 
-Plan plan_gated(int64_t M, int64_t F, int64_t K) { return make_plan(M, both(F), K, kPartialBytes, -1, -1, 0); }
-Plan plan_dx(int64_t M, int64_t F, int64_t K)
-{
-    return make_plan(M, K, both(F), kPartialBytes, CFG_PP2_256x256, -1, 0);
-}
+GradPlan plan_dx(int64_t M, int64_t F, int64_t K) { return plan_mn_major(M, K, both(F), kPartialBytes); }
 // (the contraction runs over rows, which the MN-major operands take in any number)
 Plan plan_dw(int64_t M, int64_t F, int64_t K)
 {
     return make_plan(both(F), K, cdiv(M, 8) * 8, kPartialBytes, CFG_PP2_256x256, -1, 0);
 }
 
+// The workspaces of the two sums' pieces.
+struct SumsWs {
+    Pieces pieces;
+    SplitWs split[2];
+};
+
+SumsWs carve_sums(Carver &c, int64_t M, int64_t F, int64_t K)
+{
+    SumsWs w;
+    w.pieces = plan_pieces(M, both(F), K);
+    for (int i = 0; i < w.pieces.count; ++i)
+        w.split[i] = carve_splits(c, w.pieces.at[i].plan);
+    return w;
+}
+
+bool launchable(const Pieces &p)
+{
+    return launchable(p.at[0].plan) && (p.count == 1 || launchable(p.at[1].plan));
+}
+
 struct BackwardWs {
-    Plan plan[3];                       // the pre-activations' gradients, dx, dW
-    SplitWs split[3];
+    SumsWs sums;
+    GradPlan dx;
+    Plan plan[2];                       // dx, dW
+    SplitWs split[2];
     uint16_t *d;                        // [M][both(F)]
     uint32_t *most;
     int64_t bytes;
@@ -177,13 +195,27 @@ BackwardWs carve_backward(int64_t M, int64_t F, int64_t K, void *base)
     Carver c{static_cast<uint8_t *>(base)};
     w.d = c.take<uint16_t>(M * both(F));
     w.most = c.take<uint32_t>(kMostParts);
-    w.plan[0] = plan_gated(M, F, K);
-    w.plan[1] = plan_dx(M, F, K);
-    w.plan[2] = plan_dw(M, F, K);
-    for (int i = 0; i < 3; ++i)
+    w.sums = carve_sums(c, M, F, K);
+    w.dx = plan_dx(M, F, K);
+    w.plan[0] = w.dx.plan;
+    w.plan[1] = plan_dw(M, F, K);
+    for (int i = 0; i < 2; ++i)
         w.split[i] = carve_splits(c, w.plan[i]);
     w.bytes = c.used;
     return w;
+}
+
+// The arguments of the sums' rows from `row` on and `cols` of the block's columns (F counts
+// the last ones) from `col` on.
+PairedArgs piece(PairedArgs a, int64_t row, int64_t col, int64_t cols)
+{
+    a.A += row * a.lda;
+    a.B += col * a.ldb;
+    a.B2 += col * a.ldb2;
+    a.cols = (int)std::min<int64_t>(a.cols - col, cols);
+    if (a.dh)
+        a.dh += row * a.lddh + col;
+    return a;
 }
 
 template <int MODE, int IN, int OUT>
@@ -218,7 +250,7 @@ gemm_status_t gemm_gated_workspace(int64_t M, int64_t F, int64_t K, int64_t *byt
         return st;
     Carver c{nullptr};
     if (M > 0 && F > 0)
-        carve_splits(c, plan_gated(M, F, K));
+        carve_sums(c, M, F, K);
     *bytes = c.used;
     return GEMM_OK;
 }
@@ -238,35 +270,42 @@ gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void
     if (K > 0 && ((st = check_operand(X, K, ldx)) != GEMM_OK || (st = check_operand(Wg, K, ldwg)) != GEMM_OK ||
                   (st = check_operand(Wu, K, ldwu)) != GEMM_OK))
         return st;
-    const Plan p = plan_gated(M, F, K);
     Carver c{static_cast<uint8_t *>(workspace)};
-    const SplitWs w = carve_splits(c, p);
+    const SumsWs w = carve_sums(c, M, F, K);
     if ((st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
         return st;
-    if (!launchable(p))
+    if (!launchable(w.pieces))
         return GEMM_ERR_UNSUPPORTED;
+    if (clear_counters(w.split, w.pieces.count, stream) != hipSuccess)
+        return GEMM_ERR_HIP;
     PairedArgs a{};
-    fill_args(a, p, w, H, M, both(F), K, ldh, out_dtype);
     a.A = static_cast<const uint16_t *>(X);
     a.B = static_cast<const uint16_t *>(Wg);
     a.B2 = static_cast<const uint16_t *>(Wu);
     a.lda = (int)ldx, a.ldb = (int)ldwg, a.ldb2 = (int)ldwu;
     a.cols = (int)F;
     a.act = activation;
-    if (clear_counters(&w, 1, stream) != hipSuccess)
-        return GEMM_ERR_HIP;
-    const bool rot = rotate_slabs(1, M);
-    paired_fn fn;
-    switch (p.cfg) {
-    case CFG_T128x128: fn = (rot ? kGated_128_s4_rot : kGated_128_s4)[in_dtype][out_dtype]; break;
-    case CFG_T128x128_S2: fn = kGated_128_s2[in_dtype][out_dtype]; break;
-    case CFG_T32x128: fn = kGated_32_rot[in_dtype][out_dtype]; break;
-    case CFG_W4_256x128: fn = kGated_w4[in_dtype][out_dtype]; break;
-    default: fn = kGated_pp2[in_dtype][out_dtype];
+    const int64_t size = size_of(out_dtype);
+    hipError_t e = hipSuccess;
+    for (int i = 0; i < w.pieces.count && e == hipSuccess; ++i) {
+        const auto &q = w.pieces.at[i];
+        const Plan &p = q.plan;
+        PairedArgs b = piece(a, q.row, q.col / 2, q.cols / 2);
+        fill_args(b, p, w.split[i], static_cast<uint8_t *>(H) + (q.row * ldh + q.col / 2) * size, q.rows, q.cols, K, ldh,
+                  out_dtype);
+        const bool rot = rotate_slabs(1, q.rows);
+        paired_fn fn;
+        switch (p.cfg) {
+        case CFG_T128x128: fn = (rot ? kGated_128_s4_rot : kGated_128_s4)[in_dtype][out_dtype]; break;
+        case CFG_T128x128_S2: fn = kGated_128_s2[in_dtype][out_dtype]; break;
+        case CFG_T32x128: fn = kGated_32_rot[in_dtype][out_dtype]; break;
+        case CFG_W4_256x128: fn = kGated_w4[in_dtype][out_dtype]; break;
+        default: fn = kGated_pp2[in_dtype][out_dtype];
+        }
+        e = fn(b, (unsigned)p.grid, stream);
+        if (e == hipSuccess && p.splits > 1 && !p.inreduce)
+            e = run_sum_out<SUM_GATED>(b, out_dtype, stream);
     }
-    hipError_t e = fn(a, (unsigned)p.grid, stream);
-    if (e == hipSuccess && p.splits > 1 && !p.inreduce)
-        e = run_sum_out<SUM_GATED>(a, out_dtype, stream);
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
@@ -318,16 +357,10 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
     if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != GEMM_OK)
         return st;
     const bool inner = M > 0 && F > 0;
-    if ((inner && !launchable(w.plan[0])) || (want_dx && !launchable(w.plan[1])) || (want_dw && !launchable(w.plan[2])))
+    if ((inner && !launchable(w.sums.pieces)) || (want_dx && !launchable(w.plan[0])) || (want_dw && !launchable(w.plan[1])))
         return GEMM_ERR_UNSUPPORTED;
-    SplitWs split[3] = {w.split[0], w.split[1], w.split[2]};
-    if (!inner)
-        split[0].num_counters = 0;
-    if (!want_dx)
-        split[1].num_counters = 0;
-    if (!want_dw)
-        split[2].num_counters = 0;
-    hipError_t e = clear_counters(split, 3, stream);
+    SplitWs split[4] = {w.split[0], w.split[1], w.sums.split[0], w.sums.split[1]};
+    hipError_t e = clear_counters(split, inner ? 2 + w.sums.pieces.count : 2, stream);
     const int64_t both_cols = both(F);
     PairedArgs a{};
     a.B = static_cast<const uint16_t *>(Wg);
@@ -344,13 +377,15 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
                            a.dh16, w.most);
         e = hipGetLastError();
     }
-    if (e == hipSuccess && inner) {
-        const Plan &p = w.plan[0];
+    for (int i = 0; inner && i < w.sums.pieces.count && e == hipSuccess; ++i) {
+        const auto &q = w.sums.pieces.at[i];
+        const Plan &p = q.plan;
         PairedArgs b = a;
-        fill_args(b, p, w.split[0], w.d, M, both_cols, K, both_cols, in_dtype);
         b.A = static_cast<const uint16_t *>(X);
         b.lda = (int)ldx;
-        const bool rot = rotate_slabs(1, M);
+        b = piece(b, q.row, q.col / 2, q.cols / 2);
+        fill_args(b, p, w.sums.split[i], w.d + q.row * both_cols + q.col, q.rows, q.cols, K, both_cols, in_dtype);
+        const bool rot = rotate_slabs(1, q.rows);
         paired_fn fn;
         switch (p.cfg) {
         case CFG_T128x128: fn = (rot ? kGateGrad_128_s4_rot : kGateGrad_128_s4)[in_dtype]; break;
@@ -365,12 +400,12 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
                                       : run_sum<SUM_GRAD, IN_FP16, OUT_FP16>(b, stream);
     }
     if (e == hipSuccess && want_dx) {
-        const Plan &p = w.plan[1];
+        const Plan &p = w.plan[0];
         PairedArgs b = a;
-        fill_args(b, p, w.split[1], dX, M, K, both_cols, lddx, dx_dtype);
+        fill_args(b, p, w.split[0], dX, M, K, both_cols, lddx, dx_dtype);
         b.A = w.d;
         b.lda = (int)both_cols;
-        e = kGatedDx_pp2[in_dtype][dx_dtype](b, (unsigned)p.grid, stream);
+        e = (w.dx.tile ? kGatedDx_tile : kGatedDx_pp2)[in_dtype][dx_dtype](b, (unsigned)p.grid, stream);
         if (e == hipSuccess && p.splits > 1 && !p.inreduce) {
             const KernelArgs &k = b;
             const unsigned grid = (unsigned)cdiv(M * (K / 4), 256);
@@ -384,9 +419,9 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         }
     }
     if (e == hipSuccess && want_dw) {
-        const Plan &p = w.plan[2];
+        const Plan &p = w.plan[1];
         PairedArgs b = a;
-        fill_args(b, p, w.split[2], dWg, both_cols, K, M, K, grad_dtype);
+        fill_args(b, p, w.split[1], dWg, both_cols, K, M, K, grad_dtype);
         b.rows16 = b.rows16 && (uintptr_t)dWu % 16 == 0;
         b.vec_store = b.vec_store && (uintptr_t)dWu % (4 * size_of(grad_dtype)) == 0;
         b.C2 = dWu;

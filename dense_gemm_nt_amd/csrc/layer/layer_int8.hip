@@ -126,6 +126,70 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
     }
 }
 
+// A few tokens' product without the tiles: all of it is the stream of B, which the lanes take 16
+// bytes each straight into registers and multiply with v_dot4.  A block has four rows of B, its
+// waves every fourth KB of them, two KB of each row in flight; exact sums, so their order does
+// not matter.  No K splits, hence no counters and no second launch.  One and two rows, in us,
+// against the tiles: 8192 x 8192 14.2 and 14.9 / 19.6, 28672 x 8192 36.0 and 37.0 / 38.8, 1024 x 4096 11.3 / 16.7,
+// 8192 x 1024 11.5 / 11.4 (so from 2048 on); with four rows the loads of A, as many as B's, take over:
+// 28672 x 8192 44.4 / 38.8.
+constexpr int kFewRows = 2;
+
+template <int OUT, int MR>
+__global__ __launch_bounds__(256) void int8_few(Int8Args p, int K, int lda, int ldb)
+{
+    constexpr int R = 4;
+    __shared__ int part[4][R][MR];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n0 = blockIdx.x * R;
+    const int8_t *A = reinterpret_cast<const int8_t *>(p.A);
+    const int8_t *B = reinterpret_cast<const int8_t *>(p.B);
+    int acc[R][MR];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+            acc[r][m] = 0;
+#pragma unroll 2
+    for (int k = wave * 1024 + lane * 16; k < K; k += 4096) {
+        i32x4 b[R], a[MR];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            b[r] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(B + (int64_t)min(n0 + r, p.N - 1) * ldb + k));
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+            a[m] = *reinterpret_cast<const i32x4 *>(A + (int64_t)min(m, p.M - 1) * lda + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int m = 0; m < MR; ++m)
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+                    acc[r][m] = __builtin_amdgcn_sdot4(a[m][d], b[r][d], acc[r][m], false);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1)
+                acc[r][m] += __shfl_xor(acc[r][m], o);
+            if (lane == 0)
+                part[wave][r][m] = acc[r][m];
+        }
+    __syncthreads();
+    const int m = threadIdx.x;
+    if (m >= p.M)
+        return;
+    f32x4 y;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int sum = (part[0][r][m] + part[1][r][m]) + (part[2][r][m] + part[3][r][m]);
+        y[r] = (static_cast<float>(sum) * p.sa[m * p.sa_step]) * p.sb[(int64_t)min(n0 + r, p.N - 1) * p.sb_step];
+    }
+    store_result<OUT>(p, 0, m, n0, y);
+}
+
 namespace {
 
 gemm_status_t check_sizes(int64_t M, int64_t N, int64_t K)
@@ -136,7 +200,42 @@ gemm_status_t check_sizes(int64_t M, int64_t N, int64_t K)
     return M >= kMaxRows || N >= kMaxSize || K >= (1 << 17) || K % 16 ? GEMM_ERR_UNSUPPORTED : GEMM_OK;
 }
 
-Plan plan_int8(int64_t M, int64_t N, int64_t K) { return make_plan(M, N, K / 2, kPartialBytes, -1, -1, 0); }
+// The workspaces of a product's pieces.
+struct Int8Ws {
+    Pieces pieces;
+    SplitWs split[2];
+};
+
+Int8Ws carve_int8(Carver &c, int64_t M, int64_t N, int64_t K)
+{
+    Int8Ws w;
+    w.pieces = plan_pieces(M, N, K / 2);
+    for (int i = 0; i < w.pieces.count; ++i)
+        w.split[i] = carve_splits(c, w.pieces.at[i].plan);
+    return w;
+}
+
+template <int MR>
+hipError_t run_few_of(const Int8Args &a, int K, int lda, int ldb, int out_dtype, hipStream_t stream)
+{
+    const dim3 grid((unsigned)cdiv(a.N, 4));
+    if (out_dtype == GEMM_BF16)
+        hipLaunchKernelGGL((int8_few<OUT_BF16, MR>), grid, dim3(256), 0, stream, a, K, lda, ldb);
+    else if (out_dtype == GEMM_FP16)
+        hipLaunchKernelGGL((int8_few<OUT_FP16, MR>), grid, dim3(256), 0, stream, a, K, lda, ldb);
+    else
+        hipLaunchKernelGGL((int8_few<OUT_FP32, MR>), grid, dim3(256), 0, stream, a, K, lda, ldb);
+    return hipGetLastError();
+}
+
+hipError_t run_few(const Int8Args &a, int K, int lda, int ldb, int out_dtype, hipStream_t stream)
+{
+    return a.M == 1 ? run_few_of<1>(a, K, lda, ldb, out_dtype, stream)
+                    : run_few_of<2>(a, K, lda, ldb, out_dtype, stream);
+}
+
+// (a launch has fewer than 2^32 threads)
+bool few_rows(int64_t M, int64_t N, int64_t K) { return M <= kFewRows && K >= 2048 && N < (1 << 25); }
 
 gemm_status_t check_codes(const void *p, int64_t row, int64_t ld)
 {
@@ -197,8 +296,8 @@ gemm_status_t gemm_int8_workspace(int64_t M, int64_t N, int64_t K, int64_t *byte
     if (st != GEMM_OK)
         return st;
     Carver c{nullptr};
-    if (M > 0 && N > 0)
-        carve_splits(c, plan_int8(M, N, K));
+    if (M > 0 && N > 0 && !few_rows(M, N, K))
+        carve_int8(c, M, N, K);
     *bytes = c.used;
     return GEMM_OK;
 }
@@ -225,51 +324,77 @@ gemm_status_t gemm_run_int8(const void *A, const void *B, void *C, int64_t M, in
         return GEMM_ERR_MISALIGNED;
     if (K > 0 && ((st = check_codes(A, K, lda)) != GEMM_OK || (st = check_codes(B, K, ldb)) != GEMM_OK))
         return st;
-    const Plan p = plan_int8(M, N, K);
+    const bool few = few_rows(M, N, K);
     Carver c{static_cast<uint8_t *>(workspace)};
-    const SplitWs w = carve_splits(c, p);
-    if ((st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
-        return st;
-    if (!launchable(p))
-        return GEMM_ERR_UNSUPPORTED;
+    Int8Ws w{};
+    if (!few) {
+        w = carve_int8(c, M, N, K);
+        if ((st = check_workspace(workspace, workspace_bytes, c.used)) != GEMM_OK)
+            return st;
+    }
+    for (int i = 0; i < w.pieces.count; ++i)
+        if (!launchable(w.pieces.at[i].plan))
+            return GEMM_ERR_UNSUPPORTED;
     Int8Args a{};
-    fill_args(a, p, w, C, M, N, K / 2, ldc, out_dtype);
     a.A = static_cast<const uint16_t *>(A);
     a.B = static_cast<const uint16_t *>(B);
     a.lda = (int)(lda / 2), a.ldb = (int)(ldb / 2);
     a.sa = scale_a, a.sb = scale_b;
     a.sa_step = scales_a != 1, a.sb_step = scales_b != 1;
-    if (epi) {
+    auto epilogue = [&](int64_t row, int64_t col) {       // after fill_args
+        if (!epi)
+            return;
         a.alpha = epi->alpha;
         a.beta = epi->beta;
-        a.bias = epi->bias_along != GEMM_BIAS_NONE ? epi->bias : nullptr;
+        a.bias = epi->bias_along == GEMM_BIAS_N ? epi->bias + col : epi->bias_along == GEMM_BIAS_M ? epi->bias + row : nullptr;
         a.bias_along = epi->bias_along;
         a.act = epi->activation;
         a.bias_vec = (uintptr_t)a.bias % 16 == 0;
         a.epi = !(a.alpha == 1.0f && a.beta == 0.0f && a.bias_along == GEMM_BIAS_NONE && a.act == GEMM_ACT_NONE);
+    };
+    if (few) {
+        Plan none{};
+        none.tiles_m = none.tiles_n = none.splits = 1;
+        fill_args(a, none, SplitWs{}, C, M, N, K / 2, ldc, out_dtype);
+        epilogue(0, 0);
+        return run_few(a, (int)K, (int)lda, (int)ldb, out_dtype, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
     }
-    if (clear_counters(&w, 1, stream) != hipSuccess)
+    if (clear_counters(w.split, w.pieces.count, stream) != hipSuccess)
         return GEMM_ERR_HIP;
-    const bool rot = rotate_slabs(1, M);
-    int8_fn fn;
-    switch (p.cfg) {
-    case CFG_T128x128: fn = (rot ? kInt8_128_s4_rot : kInt8_128_s4)[out_dtype]; break;
-    case CFG_T128x128_S2: fn = kInt8_128_s2[out_dtype]; break;
-    case CFG_T32x128: fn = kInt8_32_rot[out_dtype]; break;
-    case CFG_W4_256x128: fn = kInt8_w4[out_dtype]; break;
-    default: fn = kInt8_pp2[out_dtype];
-    }
-    hipError_t e = fn(a, (unsigned)p.grid, stream);
-    if (e == hipSuccess && p.splits > 1 && !p.inreduce) {
-        const KernelArgs &k = a;
-        const unsigned grid = (unsigned)cdiv(M * ((N + 3) / 4), 256);
-        if (out_dtype == GEMM_BF16)
-            hipLaunchKernelGGL(splitk_sum<OUT_BF16>, dim3(grid), dim3(256), 0, stream, k);
-        else if (out_dtype == GEMM_FP16)
-            hipLaunchKernelGGL(splitk_sum<OUT_FP16>, dim3(grid), dim3(256), 0, stream, k);
-        else
-            hipLaunchKernelGGL(splitk_sum<OUT_FP32>, dim3(grid), dim3(256), 0, stream, k);
-        e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    const Int8Args whole = a;
+    for (int i = 0; i < w.pieces.count && e == hipSuccess; ++i) {
+        const auto &q = w.pieces.at[i];
+        const Plan &p = q.plan;
+        a = whole;
+        a.A += q.row * a.lda;
+        a.B += q.col * a.ldb;
+        a.sa += q.row * a.sa_step;
+        a.sb += q.col * a.sb_step;
+        fill_args(a, p, w.split[i], static_cast<uint8_t *>(C) + (q.row * ldc + q.col) * size_of(out_dtype), q.rows,
+                  q.cols, K / 2, ldc, out_dtype);
+        epilogue(q.row, q.col);
+        const bool rot = rotate_slabs(1, q.rows);
+        int8_fn fn;
+        switch (p.cfg) {
+        case CFG_T128x128: fn = (rot ? kInt8_128_s4_rot : kInt8_128_s4)[out_dtype]; break;
+        case CFG_T128x128_S2: fn = kInt8_128_s2[out_dtype]; break;
+        case CFG_T32x128: fn = kInt8_32_rot[out_dtype]; break;
+        case CFG_W4_256x128: fn = kInt8_w4[out_dtype]; break;
+        default: fn = kInt8_pp2[out_dtype];
+        }
+        e = fn(a, (unsigned)p.grid, stream);
+        if (e == hipSuccess && p.splits > 1 && !p.inreduce) {
+            const KernelArgs &k = a;
+            const unsigned grid = (unsigned)cdiv(q.rows * ((q.cols + 3) / 4), 256);
+            if (out_dtype == GEMM_BF16)
+                hipLaunchKernelGGL(splitk_sum<OUT_BF16>, dim3(grid), dim3(256), 0, stream, k);
+            else if (out_dtype == GEMM_FP16)
+                hipLaunchKernelGGL(splitk_sum<OUT_FP16>, dim3(grid), dim3(256), 0, stream, k);
+            else
+                hipLaunchKernelGGL(splitk_sum<OUT_FP32>, dim3(grid), dim3(256), 0, stream, k);
+            e = hipGetLastError();
+        }
     }
     return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }

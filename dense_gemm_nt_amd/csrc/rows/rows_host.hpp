@@ -66,6 +66,43 @@ inline gemm_status_t check_output(const void *p, int64_t row, int64_t ld, int dt
     return (uintptr_t)p % size_of(dt) ? GEMM_ERR_MISALIGNED : GEMM_OK;
 }
 
+// The plan of a product whose B is MN-major (an input gradient's): the ping-pong tile, or
+// (`tile`) the 128 x 128 one of rows_tile.hpp, with partials of at most `bound` bytes.
+struct GradPlan {
+    Plan plan;
+    bool tile;
+};
+inline GradPlan plan_mn_major(int64_t M, int64_t N, int64_t K, int64_t bound)
+{
+    GradPlan g{make_plan(M, N, K, bound, CFG_PP2_256x256, -1, 0), false};
+    // The ping-pong tiles from a quarter of the machine on (product and gradient
+    // parts, 4096 deep: 777 x 2048, 32 tiles, 51 us against 42 on the smaller tile;
+    // 1024 x 4096, 64 tiles, 62 against 58; 2048 x 4096, 128 tiles, 84 against 91).
+    if (cdiv(M, 256) * cdiv(N, 256) >= kNumCUs / 4)
+        return g;
+    Plan &p = g.plan;
+    g.tile = true;
+    p = Plan{};
+    p.tiles_m = (int)cdiv(M, 128);
+    p.tiles_n = (int)cdiv(N, 128);
+    p.k_tiles = (int)cdiv(K, 64);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    // K splits while all blocks, two to a compute unit, run at once; at least 8
+    // slabs each
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kNumCUs / tiles, p.k_tiles / 8));
+    while (splits > 1 && (tiles * splits * 128 * 128 * 4 > bound || tiles * 4 > GEMM_COUNTER_BYTES))
+        --splits;
+    p.kt_per_split = (int)cdiv(p.k_tiles, splits);
+    p.splits = p.k_tiles ? (int)cdiv(p.k_tiles, p.kt_per_split) : 1;
+    p.group_m = std::min(4, p.tiles_m);
+    p.grid = tiles * p.splits;
+    if (p.splits > 1) {
+        p.inreduce = 1;
+        p.ws_bytes = p.grid * 128 * 128 * 4;
+    }
+    return g;
+}
+
 inline gemm_status_t check_epilogue(const gemm_epilogue_t *epi)
 {
     if (!epi)

@@ -970,43 +970,6 @@ Plan plan_projection(int64_t M, int64_t N, int64_t K)
     }
     return make_plan(M, N, K, kPartialBytes, -1, -1, 0);
 }
-// The input gradient's: the ping-pong tile, or (`tile`) the 128 x 128 one of
-// rows_tile.hpp.
-struct GradPlan {
-    Plan plan;
-    bool tile;
-};
-GradPlan plan_mn_major(int64_t M, int64_t N, int64_t K)
-{
-    GradPlan g{make_plan(M, N, K, kPartialBytes, CFG_PP2_256x256, -1, 0), false};
-    // The ping-pong tiles from a quarter of the machine on (product and gradient
-    // parts, 4096 deep: 777 x 2048, 32 tiles, 51 us against 42 on the smaller tile;
-    // 1024 x 4096, 64 tiles, 62 against 58; 2048 x 4096, 128 tiles, 84 against 91).
-    if (cdiv(M, 256) * cdiv(N, 256) >= kNumCUs / 4)
-        return g;
-    Plan &p = g.plan;
-    g.tile = true;
-    p = Plan{};
-    p.tiles_m = (int)cdiv(M, 128);
-    p.tiles_n = (int)cdiv(N, 128);
-    p.k_tiles = (int)cdiv(K, 64);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    // K splits while all blocks, two to a compute unit, run at once; at least 8
-    // slabs each
-    int64_t splits = std::max<int64_t>(1, std::min<int64_t>(2 * kNumCUs / tiles, p.k_tiles / 8));
-    while (splits > 1 && (tiles * splits * 128 * 128 * 4 > kPartialBytes || tiles * 4 > GEMM_COUNTER_BYTES))
-        --splits;
-    p.kt_per_split = (int)cdiv(p.k_tiles, splits);
-    p.splits = p.k_tiles ? (int)cdiv(p.k_tiles, p.kt_per_split) : 1;
-    p.group_m = std::min(4, p.tiles_m);
-    p.grid = tiles * p.splits;
-    if (p.splits > 1) {
-        p.inreduce = 1;
-        p.ws_bytes = p.grid * 128 * 128 * 4;
-    }
-    return g;
-}
-
 // A product's rows in one launch, or in two: where the ping-pong tiles' last pass
 // over the machine is at most half full, the rows of the full passes, and then the
 // rest, with K splits that give the idle units a share.  5001 x 8192 x 8192 (640
@@ -1221,7 +1184,7 @@ BackwardWs carve_backward(Carver &c, int64_t M, int64_t N, int64_t K, int64_t ad
     w.t = plan_shrink(M, K, adapters, rank);
     w.u = plan_shrink(M, N, adapters, rank);
     if (M > 0 && K > 0)
-        w.dx = plan_mn_major(M, K, N);
+        w.dx = plan_mn_major(M, K, N, kPartialBytes);
     w.proj = carve_projection(c, w.dx.plan);
     if (!has_adapters(adapters, rank) || M == 0 || N == 0 || K == 0)
         return w;      // nothing but a product, or less

@@ -28,19 +28,14 @@ namespace gnt {
 constexpr int kTileStages = 5, kTileOperand = 8192;
 
 // What a tile's argument block brings: LoraArgs a plan's tile and K split, to whose sums adapters
-// are added, RoutedArgs an expert's tile; others (outside this folder) specialize it.
+// are added (add), RoutedArgs an expert's tile; others (outside this folder) specialize it.
 //   kLookup  finds the block's tile (false: none) without K splits, in place of the plan's map
 //   kPaired  B's k-rows alternate in groups of eight between two arrays
 //   tile     the tile's number in the launch
 //   kStore   store(p, acc, r0, c0, stage, lane) in place of a whole sum's store
 template <typename Args>
-struct TileHooks {
+struct PlanTile {
     static constexpr bool kLookup = false, kPaired = false, kStore = false;
-    template <int IN, int OUT>
-    static __device__ __forceinline__ void add(Args &p, f32x16 (&acc)[2][2], int r0, int c0, int split, int lane)
-    {
-        lora_add<IN, 4, true, low_parts<IN, OUT>>(p, acc, r0, c0, split, lane);
-    }
     static __device__ __forceinline__ const uint16_t *b(const Args &p, int) { return p.B; }
     static __device__ __forceinline__ int ldb(const Args &p, int) { return p.ldb; }
     static __device__ __forceinline__ int cols(const Args &) { return 0; }
@@ -54,12 +49,21 @@ struct TileHooks {
     }
 };
 
+template <typename Args>
+struct TileHooks;
+
 template <>
-struct TileHooks<RoutedArgs> {
-    static constexpr bool kLookup = true, kPaired = false, kStore = false;
-    static __device__ __forceinline__ const uint16_t *b(const RoutedArgs &p, int) { return p.B; }
-    static __device__ __forceinline__ int ldb(const RoutedArgs &p, int) { return p.ldb; }
-    static __device__ __forceinline__ int cols(const RoutedArgs &) { return 0; }
+struct TileHooks<LoraArgs> : PlanTile<LoraArgs> {
+    template <int IN, int OUT>
+    static __device__ __forceinline__ void add(LoraArgs &p, f32x16 (&acc)[2][2], int r0, int c0, int split, int lane)
+    {
+        lora_add<IN, 4, true, low_parts<IN, OUT>>(p, acc, r0, c0, split, lane);
+    }
+};
+
+template <>
+struct TileHooks<RoutedArgs> : PlanTile<RoutedArgs> {
+    static constexpr bool kLookup = true;
 };
 
 template <int IN, int OUT, typename Args>

@@ -15,6 +15,7 @@ SIZES = [
     (1, 1, 8), (1, 520, 64), (1, 512, 4096), (3, 77, 1032), (33, 1001, 264), (64, 9000, 72), (70, 515, 2056),
     (128, 4096, 136), (200, 1027, 4104), (256, 333, 264), (300, 4100, 264), (512, 1024, 8192), (257, 2049, 520),
     (777, 1408, 2048), (640, 129, 1400), (1025, 2500, 72), (700, 2800, 328), (1600, 700, 2600), (260, 8, 2600),
+    (1868, 4739, 576), (1113, 6538, 528),       # the last pass's rows, and columns, apart
 ]
 
 

@@ -32,7 +32,8 @@ def test_quantize(M, K, dt):
 
 SIZES = [(1, 1, 16), (1, 8192, 8192), (3, 77, 1040), (33, 1001, 272), (64, 9000, 80), (70, 515, 4112), (128, 4096, 144),
          (200, 1027, 8208), (256, 333, 272), (300, 4100, 528), (512, 1024, 16384), (257, 2049, 1040), (777, 1408, 2048),
-         (640, 129, 1392), (1025, 5000, 80), (700, 5600, 656), (2, 3, 131056)]
+         (640, 129, 1392), (1025, 5000, 80), (700, 5600, 656), (2, 3, 131056), (2, 1030, 2064),
+         (1868, 9480, 1152), (1113, 13080, 1056)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
