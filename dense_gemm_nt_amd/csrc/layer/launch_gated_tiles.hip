@@ -21,6 +21,9 @@ GNT_GATED_TILE(128_s4_rot, 128, 2, 4, 4, true)
 #else
 GNT_GATED_TILE(128_s2, 128, 2, 4, 2, false)
 GNT_GATED_TILE(32_rot, 32, 1, 4, 6, true)
+#ifndef GNT_GATE_GRAD
+GNT_GATED_TILE(128_s2_rot, 128, 2, 4, 2, true)
+#endif
 #endif
 
 }  // namespace gnt

@@ -18,6 +18,7 @@ namespace gnt {
 GNT_INT8_TILE(128_s4, 128, 2, 4, 4, false)
 GNT_INT8_TILE(128_s4_rot, 128, 2, 4, 4, true)
 GNT_INT8_TILE(128_s2, 128, 2, 4, 2, false)
+GNT_INT8_TILE(128_s2_rot, 128, 2, 4, 2, true)
 GNT_INT8_TILE(32_rot, 32, 1, 4, 6, true)
 
 }  // namespace gnt

@@ -13,6 +13,20 @@ namespace gnt {
 
 enum : int { GATE_RELU = 1, GATE_GELU = 2, GATE_SILU = 3 };
 
+// Words that a launch sets to zero.
+struct ClearList {
+    unsigned *at[4];
+    int count[4];
+};
+
+__device__ __forceinline__ void clear_list(const ClearList &l, int id, int threads)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        for (int j = id; j < l.count[i]; j += threads)
+            l.at[i][j] = 0u;
+}
+
 // The gated block's products.  B and B2 are the gate's and the up projection's weights,
 // `cols` rows each, in turn groups of eight (GNT_EXT_PAIRED): N, or the contraction of the
 // input gradient, counts both, 2 cols rounded up to whole groups.
@@ -25,6 +39,7 @@ struct PairedArgs : KernelArgs {
     int dh16;                   // its rows start 16-byte aligned
     const uint32_t *most;       // FP16 backward: kMostParts partial maxima of |dh| (its bits)
     void *C2;                   // weight gradients: C is the gate's, C2 the up projection's
+    ClearList clear;            // gradients of the sums: cleared on the way
 };
 
 constexpr int kMostParts = 256;
@@ -215,6 +230,7 @@ __device__ __forceinline__ void store_gate_gradients(const PairedArgs &p, const 
     const int lane = fresh_lane(lane_id);
     const int h = lane >> 5, f0 = c0 / 2;
     uint8_t *out = stage + 32 * ROWB;
+    clear_list(p.clear, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
     float scale = 1.0f;
     if constexpr (IN == IN_FP16)
         scale = __builtin_ldexpf(1.0f, most_shift(p.most, lane));

@@ -54,27 +54,27 @@ __global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int
         most[blockIdx.x] = max(max(part[0], part[1]), max(part[2], part[3]));
 }
 
-struct ClearList {
-    unsigned *at[4];
-    int count[4];
-};
-
 __global__ __launch_bounds__(256) void clear_words(ClearList l)
 {
-    for (int i = 0; i < 4; ++i)
-        for (int j = blockIdx.x * 256 + threadIdx.x; j < l.count[i]; j += gridDim.x * 256)
-            l.at[i][j] = 0u;
+    clear_list(l, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
+}
+
+ClearList clear_of(const SplitWs *w, int count)
+{
+    ClearList l{};
+    for (int i = 0; i < count; ++i) {
+        l.at[i] = w[i].counters;
+        l.count[i] = w[i].num_counters;
+    }
+    return l;
 }
 
 hipError_t clear_counters(const SplitWs *w, int count, hipStream_t stream)
 {
-    ClearList l{};
+    const ClearList l = clear_of(w, count);
     int most = 0;
-    for (int i = 0; i < count; ++i) {
-        l.at[i] = w[i].counters;
-        l.count[i] = w[i].num_counters;
-        most = std::max(most, l.count[i]);
-    }
+    for (int n : l.count)
+        most = std::max(most, n);
     if (most == 0)
         return hipSuccess;
     hipLaunchKernelGGL(clear_words, dim3((unsigned)std::min<int64_t>(32, cdiv(most, 256))), dim3(256), 0, stream, l);
@@ -297,7 +297,7 @@ gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void
         paired_fn fn;
         switch (p.cfg) {
         case CFG_T128x128: fn = (rot ? kGated_128_s4_rot : kGated_128_s4)[in_dtype][out_dtype]; break;
-        case CFG_T128x128_S2: fn = kGated_128_s2[in_dtype][out_dtype]; break;
+        case CFG_T128x128_S2: fn = (rot ? kGated_128_s2_rot : kGated_128_s2)[in_dtype][out_dtype]; break;
         case CFG_T32x128: fn = kGated_32_rot[in_dtype][out_dtype]; break;
         case CFG_W4_256x128: fn = kGated_w4[in_dtype][out_dtype]; break;
         default: fn = kGated_pp2[in_dtype][out_dtype];
@@ -360,7 +360,11 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
     if ((inner && !launchable(w.sums.pieces)) || (want_dx && !launchable(w.plan[0])) || (want_dw && !launchable(w.plan[1])))
         return GEMM_ERR_UNSUPPORTED;
     SplitWs split[4] = {w.split[0], w.split[1], w.sums.split[0], w.sums.split[1]};
-    hipError_t e = clear_counters(split, inner ? 2 + w.sums.pieces.count : 2, stream);
+    const int splits = inner ? 2 + w.sums.pieces.count : 2;
+    // what the later products count on is cleared by the first's blocks, each of which stores a
+    // tile, or where those are split themselves by a launch
+    const bool clear_first = inner && w.sums.pieces.at[0].plan.splits == 1;
+    hipError_t e = clear_first ? hipSuccess : clear_counters(split, splits, stream);
     const int64_t both_cols = both(F);
     PairedArgs a{};
     a.B = static_cast<const uint16_t *>(Wg);
@@ -384,6 +388,8 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         b.A = static_cast<const uint16_t *>(X);
         b.lda = (int)ldx;
         b = piece(b, q.row, q.col / 2, q.cols / 2);
+        if (clear_first && i == 0)
+            b.clear = clear_of(split, splits);
         fill_args(b, p, w.sums.split[i], w.d + q.row * both_cols + q.col, q.rows, q.cols, K, both_cols, in_dtype);
         const bool rot = rotate_slabs(1, q.rows);
         paired_fn fn;

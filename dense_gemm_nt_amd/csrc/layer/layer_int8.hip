@@ -378,7 +378,7 @@ gemm_status_t gemm_run_int8(const void *A, const void *B, void *C, int64_t M, in
         int8_fn fn;
         switch (p.cfg) {
         case CFG_T128x128: fn = (rot ? kInt8_128_s4_rot : kInt8_128_s4)[out_dtype]; break;
-        case CFG_T128x128_S2: fn = kInt8_128_s2[out_dtype]; break;
+        case CFG_T128x128_S2: fn = (rot ? kInt8_128_s2_rot : kInt8_128_s2)[out_dtype]; break;
         case CFG_T32x128: fn = kInt8_32_rot[out_dtype]; break;
         case CFG_W4_256x128: fn = kInt8_w4[out_dtype]; break;
         default: fn = kInt8_pp2[out_dtype];

@@ -13,7 +13,7 @@ typedef paired_fn PairedInTable[2];        // [in dtype]
 typedef int8_fn Int8Table[3];              // [out dtype]
 
 // the gated block: act(gate) * up of the tile's sums
-extern PairedTable kGated_128_s4, kGated_128_s4_rot, kGated_128_s2, kGated_32_rot, kGated_w4, kGated_pp2;
+extern PairedTable kGated_128_s4, kGated_128_s4_rot, kGated_128_s2, kGated_128_s2_rot, kGated_32_rot, kGated_w4, kGated_pp2;
 // its pre-activations' gradients from the same sums
 extern PairedInTable kGateGrad_128_s4, kGateGrad_128_s4_rot, kGateGrad_128_s2, kGateGrad_32_rot, kGateGrad_w4,
     kGateGrad_pp2;
@@ -21,7 +21,7 @@ extern PairedInTable kGateGrad_128_s4, kGateGrad_128_s4_rot, kGateGrad_128_s2, k
 // MN-major)
 extern PairedTable kGatedDx_pp2, kGatedDx_tile, kGatedDw_pp2;
 // the product in 8-bit integers
-extern Int8Table kInt8_128_s4, kInt8_128_s4_rot, kInt8_128_s2, kInt8_32_rot, kInt8_w4, kInt8_pp2;
+extern Int8Table kInt8_128_s4, kInt8_128_s4_rot, kInt8_128_s2, kInt8_128_s2_rot, kInt8_32_rot, kInt8_w4, kInt8_pp2;
 
 }  // namespace gnt
 

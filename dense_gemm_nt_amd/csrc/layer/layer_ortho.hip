@@ -4,11 +4,12 @@
 //   A = X X^T,  X = a X + (b A + c A^2) X
 // which takes every singular value s of X to a s + b s^3 + c s^5.
 //
-// Numbers.  The products run on FP16 operands with FP32 sums; X itself is kept in FP32, and
-// its FP16 copy (in units of 1 / s, s the power of two near sqrt(k), so that entries of
-// 1 / sqrt(r k) are not below fp16's steps) only enters the products, so an X of steep spectrum, whose
-// small singular values the first steps multiply by a alone, keeps them: with X in FP16
-// a spectrum falling as 1 / i ended 2.9e-3 off, so 0.5e-3.  From the third step on, when the singular
+// Numbers.  The products run on FP16 operands with FP32 sums.  X is the sum of two FP16 values (in
+// units of 1 / s, s the power of two near 16 sqrt(k), so that entries of 1 / sqrt(r k) have 22 bits in
+// them), of which only the first enters the products; so an X of steep spectrum, whose small
+// singular values the first steps multiply by a alone, keeps them: with X in one FP16 value
+// a spectrum falling as 1 / i ended 2.9e-3 off, so 0.5e-3.  (In FP32 beside the copy for the
+// products it was as exact, for 12 bytes a value and step to move where this has 8: @@.)  From the third step on, when the singular
 // values are near 1, the squares are held as what they differ from the identity by:
 //   A = I + A':  b A + c A^2 = (b + c) I + (b + 2 c) A' + c A'^2
 // whose diagonal does not fill FP16's bits with what is known already; the multiple of I goes
@@ -96,67 +97,79 @@ __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n
         parts[blockIdx.y * gridDim.x + blockIdx.x] = s;
 }
 
-// X = G / (||G|| + eps) in FP32 and, times s, in FP16, [rows8][cols8] with zeros past the
-// matrix, and with xt the latter transposed, [cols8][rows8]; a tall G (flip) is transposed on the
-// way.  A block has 64 x 64 values.
+// s X = s G / (||G|| + eps) as two FP16 values, [rows8][cols8] with zeros past the matrix, and
+// with xt the first also transposed, [cols8][rows8]; a tall G (flip) is transposed on the way.
+// A block has 64 x 64 values.
 __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, int64_t ld, int64_t step, int dtype,
                                                    int wide, int flip, const double *parts, int num_parts, double eps,
-                                                   float s, float *x, uint16_t *xh, uint16_t *xt, int rows8, int cols8)
+                                                   float s, uint16_t *hi, uint16_t *lo, uint16_t *xt, int rows8, int cols8)
 {
     __shared__ double part[4];
     __shared__ float tile[64][65];
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;         // of X
     const int g_r0 = flip ? c0 : r0, g_c0 = flip ? r0 : c0;       // of G
+    // eight values a load where rows allow it, else one (64 a row)
+    const int64_t from = blockIdx.z * step;
     float v[2][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i, r = g_r0 + (t >> 3), c = g_c0 + 8 * (t & 7);
-        read_eight(G, blockIdx.z * step + (int64_t)r * ld + c, dtype, wide != 0, r < m ? n - c : 0, v[i]);
+        if (wide)
+            read_eight(G, from + (int64_t)r * ld + c, dtype, true, r < m ? n - c : 0, v[i]);
+        else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int u = threadIdx.x + 256 * (8 * i + e), ur = g_r0 + (u >> 6), uc = g_c0 + (u & 63);
+                v[i][e] = ur < m && uc < n ? read_any(G, from + (int64_t)ur * ld + uc, dtype) : 0.0f;
+            }
     }
     double sum = 0.0;
     for (int i = threadIdx.x; i < num_parts; i += 256)
         sum += parts[blockIdx.z * num_parts + i];
-    const double inv = 1.0 / (__builtin_sqrt(block_sum(sum, part)) + eps);
+    const double inv = (double)s / (__builtin_sqrt(block_sum(sum, part)) + eps);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            tile[t >> 3][8 * (t & 7) + e] = (float)((double)v[i][e] * inv);
+        for (int e = 0; e < 8; ++e) {
+            const int u = threadIdx.x + 256 * (8 * i + e);
+            tile[wide ? t >> 3 : u >> 6][wide ? 8 * (t & 7) + e : u & 63] = (float)((double)v[i][e] * inv);
+        }
     }
     __syncthreads();
     const int64_t at = (int64_t)blockIdx.z * rows8 * cols8;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i, r = t >> 3, c = (t & 7) * 8;
-        float y[8], h[8];
+        float y[8], z[8];
         if (r0 + r < rows8 && c0 + c < cols8) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 8; ++e)
                 y[e] = flip ? tile[c + e][r] : tile[r][c + e];
-                h[e] = s * y[e];
-            }
-            store_run<OUT_FP32, 8>(x, at + (int64_t)(r0 + r) * cols8 + c0 + c, y, true, 8);
-            store_run<OUT_FP16, 8, false>(xh, at + (int64_t)(r0 + r) * cols8 + c0 + c, h, true, 8);
+            two_halves(y, z);
+            store_run<OUT_FP16, 8, false>(hi, at + (int64_t)(r0 + r) * cols8 + c0 + c, y, true, 8);
+            store_run<OUT_FP16, 8, false>(lo, at + (int64_t)(r0 + r) * cols8 + c0 + c, z, true, 8);
         }
         if (xt && c0 + r < cols8 && r0 + c < rows8) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                h[e] = s * (flip ? tile[r][c + e] : tile[c + e][r]);
-            store_run<OUT_FP16, 8, false>(xt, at + (int64_t)(c0 + r) * rows8 + r0 + c, h, true, 8);
+                y[e] = flip ? tile[r][c + e] : tile[c + e][r];
+            store_run<OUT_FP16, 8, false>(xt, at + (int64_t)(c0 + r) * rows8 + r0 + c, y, true, 8);
         }
     }
 }
 
 // The update of no steps at all: X as it begins.
-__global__ __launch_bounds__(256) void ortho_copy(const float *x, int rows8, int cols8, OrthoArgs p)
+__global__ __launch_bounds__(256) void ortho_copy(const uint16_t *hi, const uint16_t *lo, float unit, int rows8, int cols8,
+                                                  OrthoArgs p)
 {
     const int m = p.flip ? p.update_cols : p.update_rows, n = p.flip ? p.update_rows : p.update_cols;
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= (int64_t)m * n)
         return;
     const int r = (int)(t / n), c = (int)(t - (int64_t)r * n);
-    const float v = x[(int64_t)blockIdx.y * rows8 * cols8 + (p.flip ? (int64_t)c * cols8 + r : (int64_t)r * cols8 + c)];
+    const int64_t i = (int64_t)blockIdx.y * rows8 * cols8 + (p.flip ? (int64_t)c * cols8 + r : (int64_t)r * cols8 + c);
+    const float v = unit * (from_bits16(IN_FP16, hi[i]) + from_bits16(IN_FP16, lo[i]));
     const int64_t at = blockIdx.y * p.update_step + (int64_t)r * p.ldu + c;
     if (p.update_dtype == OUT_FP32)
         static_cast<float *>(p.update)[at] = v;
@@ -289,8 +302,8 @@ struct OrthoWs {
     bool turned;             // the step reads X transposed
     OrthoPlan plan[3];
     double *sums;
-    float *x, *partials;
-    uint16_t *xh, *xt, *a, *b;
+    float *partials;
+    uint16_t *hi, *lo, *xt, *a, *b;
     unsigned *counters;
     int num_counters;
     int64_t bytes;
@@ -310,8 +323,8 @@ OrthoWs carve_ortho(int64_t batch, int64_t m, int64_t n, void *base)
     w.plan[ORTHO_STEP] = plan_ortho(batch, w.r8, w.k8, w.r8, false);
     const int64_t size = batch * w.r8 * w.k8;
     w.sums = c.take<double>(batch * w.parts);
-    w.x = c.take<float>(size);
-    w.xh = c.take<uint16_t>(2 * size);       // two, in turn: a step reads one and writes the other
+    w.hi = c.take<uint16_t>(2 * size);       // two, in turn: a step reads one and writes the other
+    w.lo = c.take<uint16_t>(size);
     const OrthoTile step = w.plan[ORTHO_STEP].part[0].tile;
     w.turned = step != ORTHO_256_MN && step != ORTHO_128_MN;
     w.xt = c.take<uint16_t>(w.turned ? 2 * size : 0);
@@ -394,11 +407,11 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     hipLaunchKernelGGL(ortho_squares, dim3(w.parts, (unsigned)batch), dim3(256), 0, stream, G, (int)m, (int)n, ldg,
                        g_step, in_dtype, wide, w.sums, w.counters, w.num_counters);
     hipError_t e = hipGetLastError();
-    const float s = std::exp2(std::round(0.5f * std::log2((float)w.k))), t = 64.0f;
+    const float s = 16.0f * std::exp2(std::round(0.5f * std::log2((float)w.k))), t = 64.0f;
     if (e == hipSuccess) {
         hipLaunchKernelGGL(ortho_begin, dim3((unsigned)cdiv(w.k8, 64), (unsigned)cdiv(w.r8, 64), (unsigned)batch), dim3(256),
                            0, stream, G, (int)m, (int)n, ldg, g_step, in_dtype, wide, (int)flip, w.sums, w.parts, eps,
-                           s, w.x, w.xh, w.turned ? w.xt : nullptr, (int)w.r8, (int)w.k8);
+                           s, w.hi, w.lo, w.turned ? w.xt : nullptr, (int)w.r8, (int)w.k8);
         e = hipGetLastError();
     }
     OrthoArgs last{};
@@ -411,15 +424,15 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     const int64_t size = size_of(out_dtype);
     last.update16 = (ldu * size) % 16 == 0 && (uintptr_t)U % 16 == 0 && (batch == 1 || (u_step * size) % 16 == 0);
     if (e == hipSuccess && steps == 0) {
-        hipLaunchKernelGGL(ortho_copy, dim3((unsigned)cdiv(m * n, 256), (unsigned)batch), dim3(256), 0, stream, w.x,
-                           (int)w.r8, (int)w.k8, last);
+        hipLaunchKernelGGL(ortho_copy, dim3((unsigned)cdiv(m * n, 256), (unsigned)batch), dim3(256), 0, stream, w.hi,
+                           w.lo, 1.0f / s, (int)w.r8, (int)w.k8, last);
         e = hipGetLastError();
     }
     const int64_t x_step = w.r8 * w.k8, sq_step = w.r8 * w.r8;
     for (int64_t i = 0; i < steps && e == hipSuccess; ++i) {
         const float ca = coefficients[3 * i], cb = coefficients[3 * i + 1], cc = coefficients[3 * i + 2];
         const float sigma = i >= 2 ? 1.0f : 0.0f;
-        uint16_t *xh = w.xh + (i & 1) * batch * x_step, *next = w.xh + ((i + 1) & 1) * batch * x_step;
+        uint16_t *xh = w.hi + (i & 1) * batch * x_step, *next = w.hi + ((i + 1) & 1) * batch * x_step;
         const uint16_t *xt = w.turned ? w.xt + (i & 1) * batch * x_step : nullptr;
         for (int mode = ORTHO_SQUARE; mode <= ORTHO_STEP && e == hipSuccess; ++mode) {
             const OrthoPlan &plan = w.plan[mode];
@@ -443,7 +456,8 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
             a.b_step = mode == ORTHO_POLY ? sq_step : x_step;
             a.c_step = step ? x_step : sq_step;
             a.old = w.a;
-            a.x = w.x;
+            a.hi = xh;
+            a.lo = w.lo;
             a.xt = step && w.turned ? w.xt + ((i + 1) & 1) * batch * x_step : nullptr;
             a.ldt = (int)w.r8;
             if (mode == ORTHO_SQUARE) {
@@ -453,9 +467,10 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
                 a.alpha = cc / t;
                 a.beta = cb + 2.0f * cc * sigma;
             } else {
-                a.alpha = 1.0f / (t * s);
-                a.beta = (float)((double)ca + (double)sigma * ((double)cb + (double)cc));
-                a.scale = s;
+                // (of s X; the last step's X itself)
+                const float unit = a.update ? 1.0f / s : 1.0f;
+                a.alpha = unit / t;
+                a.beta = unit * (float)((double)ca + (double)sigma * ((double)cb + (double)cc));
             }
             for (int j = 0; j < plan.count && e == hipSuccess; ++j) {
                 const OrthoLaunch &l = plan.part[j];

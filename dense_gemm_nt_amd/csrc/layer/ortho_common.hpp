@@ -9,7 +9,8 @@ namespace gnt {
 // past the matrix):
 //   SQUARE  t (X X^T - sigma I), FP16
 //   POLY    t (b' A + c A^2) from A, FP16
-//   STEP    a' X + B X: X in FP32 again, and s X in FP16; in the last step the update
+//   STEP    a' X + B X: s X as the sum of two FP16 values, of which the first is what the products
+//           take; in the last step the update
 // The products' tiles: all but the _MN ones have both operands K-major; _S2 is the 128 x 128
 // tile with a two-stage ring, and so two blocks a compute unit.
 enum OrthoTile : int { ORTHO_256, ORTHO_256_MN, ORTHO_128, ORTHO_128_S2, ORTHO_128_MN, ORTHO_64 };
@@ -27,8 +28,8 @@ struct OrthoArgs : KernelArgs {
     int64_t a_step, b_step, c_step;    // elements between a stack's matrices (16-bit ones)
     const uint16_t *old;               // POLY: A (c_step apart)
     float shift;                       // SQUARE: t sigma
-    float scale;                       // STEP: s
-    float *x;                          // STEP: X in FP32 (c_step apart, rows of ldc)
+    const uint16_t *hi;                // STEP: s X, the first parts, and the second ones, which the
+    uint16_t *lo;                      // step replaces (c_step apart, rows of ldc)
     uint16_t *xt;                      // STEP: s X transposed as well (rows of ldt), or null
     int ldt;
     void *update;                      // the last STEP's result (else null), rows of ldu
@@ -93,6 +94,23 @@ __device__ __forceinline__ int ortho_tile(const OrthoArgs &p)
     return ortho_number(p, split);
 }
 
+__device__ __forceinline__ float half_at(u32x4 w, int i)
+{
+    return from_bits16(IN_FP16, (w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
+}
+
+// x as the sum of two FP16 values: y (the nearest to x) and what it leaves.  22 bits where s x
+// is above 2^-3, and 2^-25 absolute below.
+__device__ __forceinline__ void two_halves(float (&x)[8], float (&rest)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float h = static_cast<float>(static_cast<_Float16>(x[i]));
+        rest[i] = x[i] - h;
+        x[i] = h;
+    }
+}
+
 // Eight consecutive values from element idx of an array of `dtype`, the first `count` of them.
 __device__ __forceinline__ void store_values(void *at, int64_t idx, int dtype, const float (&y)[8], bool wide,
                                              int count)
@@ -118,7 +136,8 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
     const int64_t b = ortho_matrix(p);
     uint16_t *C = static_cast<uint16_t *>(p.C) + b * p.c_step;
     const uint16_t *old = p.old + b * p.c_step;
-    float *x = p.x + b * p.c_step;
+    const uint16_t *hi = p.hi + b * p.c_step;
+    uint16_t *lo = p.lo + b * p.c_step;
     // where the transposed values go: a square's other half, X's transposed copy, or a tall
     // update
     void *turned = nullptr;
@@ -150,8 +169,7 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
         wait_lgkmcnt0();
 #pragma unroll 1
         for (int g = 0; g < STEPS; g += GROUP) {
-            f32x4 xl[GROUP], xr[GROUP];
-            u32x4 w[GROUP];
+            u32x4 v[GROUP], w[GROUP];
             auto at = [&](int j, int &m, int &n) {
                 m = r0 + fm * 32 + (g + j) * RPS + lane / LPR;
                 n = c0 + 8 * (lane % LPR);
@@ -163,8 +181,8 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
                     int m, n;
                     const int64_t idx = at(j, m, n);
                     if (m < p.M && n < p.N) {
-                        xl[j] = *reinterpret_cast<const f32x4 *>(x + idx);
-                        xr[j] = *reinterpret_cast<const f32x4 *>(x + idx + 4);
+                        v[j] = *reinterpret_cast<const u32x4 *>(hi + idx);
+                        w[j] = *reinterpret_cast<const u32x4 *>(lo + idx);
                     }
                 }
             } else if (p.mode == ORTHO_POLY) {
@@ -182,8 +200,8 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
                 int m, n;
                 const int64_t idx = at(j, m, n);
                 uint8_t *at0 = stage + r * ROWB + ((c ^ (r & KEYM)) * 16), *at1 = stage + r * ROWB + (((c + 1) ^ (r & KEYM)) * 16);
-                const f32x4 lo = *reinterpret_cast<const f32x4 *>(at0), hi = *reinterpret_cast<const f32x4 *>(at1);
-                float y[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                const f32x4 y0 = *reinterpret_cast<const f32x4 *>(at0), y1 = *reinterpret_cast<const f32x4 *>(at1);
+                float y[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
                 if (m >= p.M || n >= p.N)
                     continue;
                 if (p.mode == ORTHO_SQUARE) {
@@ -194,19 +212,17 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
                 } else if (p.mode == ORTHO_POLY) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        y[i] = p.alpha * y[i] + p.beta * from_bits16(IN_FP16, (w[j][i >> 1] >> (16 * (i & 1))) & 0xffffu);
+                        y[i] = p.alpha * y[i] + p.beta * half_at(w[j], i);
                     store_run<OUT_FP16, 8, false>(C, idx, y, true, 8);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        y[i] = p.alpha * y[i] + p.beta * (i < 4 ? xl[j][i] : xr[j][i - 4]);
+                        y[i] = p.alpha * y[i] + p.beta * (half_at(v[j], i) + half_at(w[j], i));
                     if (!p.update) {
-                        *reinterpret_cast<f32x4 *>(x + idx) = (f32x4){y[0], y[1], y[2], y[3]};
-                        *reinterpret_cast<f32x4 *>(x + idx + 4) = (f32x4){y[4], y[5], y[6], y[7]};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            y[i] *= p.scale;
+                        float z[8];
+                        two_halves(y, z);
                         store_run<OUT_FP16, 8, false>(C, idx, y, true, 8);
+                        store_run<OUT_FP16, 8, false>(lo, idx, z, true, 8);
                     } else if (!turned && m < p.update_rows && n < p.update_cols) {
                         store_values(p.update, b * p.update_step + (int64_t)m * p.ldu + n, p.update_dtype, y,
                                      p.update16 != 0, p.update_cols - n);
