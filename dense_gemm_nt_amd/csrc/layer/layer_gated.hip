@@ -191,16 +191,22 @@ struct BackwardWs {
 
 BackwardWs carve_backward(int64_t M, int64_t F, int64_t K, void *base)
 {
-    BackwardWs w;
+    BackwardWs w{};
     Carver c{static_cast<uint8_t *>(base)};
     w.d = c.take<uint16_t>(M * both(F));
     w.most = c.take<uint32_t>(kMostParts);
-    w.sums = carve_sums(c, M, F, K);
-    w.dx = plan_dx(M, F, K);
-    w.plan[0] = w.dx.plan;
-    w.plan[1] = plan_dw(M, F, K);
-    for (int i = 0; i < 2; ++i)
-        w.split[i] = carve_splits(c, w.plan[i]);
+    // (a product of no rows or columns has no plan)
+    if (M > 0 && F > 0)
+        w.sums = carve_sums(c, M, F, K);
+    if (M > 0 && K > 0) {
+        w.dx = plan_dx(M, F, K);
+        w.plan[0] = w.dx.plan;
+        w.split[0] = carve_splits(c, w.plan[0]);
+    }
+    if (F > 0 && K > 0) {
+        w.plan[1] = plan_dw(M, F, K);
+        w.split[1] = carve_splits(c, w.plan[1]);
+    }
     w.bytes = c.used;
     return w;
 }

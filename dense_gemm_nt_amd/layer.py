@@ -198,9 +198,9 @@ def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     float32, unit stride along the last axis): X = G / (||G|| + eps), then `steps` times
     X = a X + b (X X^T) X + c (X X^T)^2 X, which takes every singular value s to
     a s + b s^3 + c s^5 and leaves the singular vectors.  `coefficients` is (a, b, c), or
-    one such triple a step.  Of out_dtype (default bfloat16).  X is kept in float32 and
+    one such triple a step.  Of out_dtype (default bfloat16).  X is kept to 22 bits and
     multiplied in float16: about 1e-3 of the exact iteration off (relative) where the
-    coefficients keep the singular values below 2."""
+    coefficients keep the singular values below 2.  `out` may be G itself."""
     import torch
     if G.dim() not in (2, 3):
         raise ValueError("G must be [m, n] or [B, m, n]")
@@ -231,7 +231,7 @@ def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     else:
         _out("out", out, G.shape, G.device)
     ldu, u_step = strides("out", out)
-    if B > 1 and m and n and u_step < (m - 1) * ldu + n:
+    if B > 1 and m and n and u_step < (m - 1) * ldu + n and not (u_step >= n and ldu >= (B - 1) * u_step + n):
         raise ValueError("out's matrices overlap")
     ws_bytes = _workspace_bytes("gemm_orthogonalize_workspace", B, m, n)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=G.device) if ws_bytes else None

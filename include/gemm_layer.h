@@ -101,10 +101,10 @@ gemm_status_t gemm_run_int8(const void *A, const void *B, void *C, int64_t M, in
  *   X = a X + b (X X^T) X + c (X X^T)^2 X,   (a, b, c) = coefficients[3 i .. 3 i + 2]
  * (for m > n with X^T X on the other side, which is the same), so that every singular
  * value s of X becomes a s + b s^3 + c s^5.  U [m][n] of out_dtype, rows of ldu, matrices u_step
- * apart; its matrices must not overlap.  `coefficients` is a host array, read in the call.
+ * apart; its matrices must not overlap (it may be G).  `coefficients` is a host array, read in the call.
  *
- * The norm is an FP64 sum; X is kept in FP32; the products run on FP16 copies with
- * FP32 sums.  With coefficients that keep the singular values below 2, U is about
+ * The norm is an FP64 sum; X is kept as the sum of two FP16 values (22 bits, scaled); the
+ * products run on the first of them with FP32 sums.  With coefficients that keep the singular values below 2, U is about
  * 1e-3 of the exact iteration off (relative, of the whole matrix; 4e-3 where half of the
  * singular values are zero), so that an FP32 U is no more exact than that.  An infinity or NaN in G makes its
  * matrix NaN.  steps = 0: X.  batch <= 65535, m and n at most 2^20; any ldg >= n, ldu >= n. */
