@@ -359,8 +359,10 @@ __device__ __forceinline__ bool splitk2_arrive(const KernelArgs &p, f32x16 (&acc
     wg_barrier();
     if (wave == 0 && lane == 0)
         *flag = __hip_atomic_fetch_add(p.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    wg_barrier();
+    wait_lgkmcnt0();                                      // (a barrier does not wait for LDS: unwaited, a
+    wg_barrier();                                         // wave on another SIMD read the word's old value)
     const uint32_t arrived = __builtin_amdgcn_readfirstlane(*flag);
+    wait_lgkmcnt0();
     wg_barrier();                                         // every wave has read the flag
     if (arrived == 0)
         return false;
@@ -426,8 +428,10 @@ __device__ __forceinline__ bool splitk_arrive(const KernelArgs &p, f32x16 (&acc)
     wg_barrier();
     if (wave == 0 && lane == 0)
         *flag = __hip_atomic_fetch_add(p.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    wg_barrier();
+    wait_lgkmcnt0();                                      // (a barrier does not wait for LDS: unwaited, a
+    wg_barrier();                                         // wave on another SIMD read the word's old value)
     const uint32_t arrived = __builtin_amdgcn_readfirstlane(*flag);
+    wait_lgkmcnt0();
     wg_barrier();                                         // every wave has read the flag
     if (arrived != (uint32_t)(S - 1))
         return false;
