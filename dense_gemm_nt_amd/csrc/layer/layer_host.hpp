@@ -93,7 +93,7 @@ inline Plan plan_product(int64_t M, int64_t N, int64_t K)
 // A product in one launch, or in two: where the ping-pong tiles' last pass over the machine would be
 // mostly empty, the rows (or columns) of the whole passes, and then the rest on a plan of its
 // own.  8111 x 8200 x 4096 (1056 tiles, 33 in a row) 523 us in one launch, whose fifth pass has 32,
-// 450 in two; 1500 x 10928 x 4096 (258 tiles) 187, and @@ as 42 columns of tiles and the rest.
+// 450 in two; 1500 x 10928 x 4096 (258 tiles) 185, and 138 as 42 columns of tiles and the rest.
 struct Pieces {
     struct {
         int64_t row, rows, col, cols;

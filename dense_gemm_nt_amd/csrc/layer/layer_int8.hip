@@ -94,23 +94,40 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
     if (t == 0)
         scale[m] = s;
     const bool some = finite && s > 0.0f;
+    // x times the reciprocal is within 127 * 2^-22 = 3.1e-5 of the quotient (s and its reciprocal
+    // normal numbers, two roundings and the quotient's own), so further than that from a half it
+    // rounds to the same integer; the eight values that hold a nearer one are divided.  Adding
+    // 1.5 * 2^23 rounds to the integer, even at a tie, which is then in the low byte.
+    // 8111 x 8192 FP16 40 us (4.9 TB/s), with eight divisions 53.
+    constexpr float kRound = 12582912.0f;
+    const bool quick = some && s > 1e-35f && s < 1e35f;
+    const float inv = quick ? 1.0f / s : 0.0f;
     auto put = [&](int k, const float (&y)[8]) {
-        int8_t q[8];
+        uint32_t q[8];
+        float far = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            q[e] = some ? (int8_t)fminf(fmaxf(__builtin_rintf(y[e] / s), -127.0f), 127.0f) : (int8_t)0;
-        int8_t *dst = codes + m * ldq + k;
-        if (wide_q && k + 8 <= K) {
-            u32x2 w = {0u, 0u};
+        for (int e = 0; e < 8; ++e) {
+            const float t = y[e] * inv, r = t + kRound;
+            far = fmaxf(far, fabsf(t - (r - kRound)));
+            q[e] = __builtin_bit_cast(uint32_t, r);
+        }
+        if (!quick || far > 0.4999f) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                w[e >> 2] |= (uint32_t)(uint8_t)q[e] << (8 * (e & 3));
+                q[e] = some ? (uint32_t)(int)fminf(fmaxf(__builtin_rintf(y[e] / s), -127.0f), 127.0f) : 0u;
+        }
+        int8_t *dst = codes + m * ldq + k;
+        if (wide_q && k + 8 <= K) {
+            u32x2 w;
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+                w[d] = (q[4 * d] & 0xffu) | (q[4 * d + 1] & 0xffu) << 8 | (q[4 * d + 2] & 0xffu) << 16 | q[4 * d + 3] << 24;
             *reinterpret_cast<u32x2 *>(dst) = w;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (k + e < K)
-                    dst[e] = q[e];
+                    dst[e] = (int8_t)q[e];
         }
     };
 #pragma unroll

@@ -27,18 +27,18 @@ CALLS, WARM, COPY_MB = 33, 3, 512
 SIMDS, XCDS = 1024, 8
 
 
-def cases_module():
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+def cases_module(name="operators"):
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     return m
 
 
-def run():
+def run(cases="operators"):
     if ROOT not in sys.path:
         sys.path.insert(0, ROOT)
     import torch
-    m = cases_module()
+    m = cases_module(cases)
     m.own = True
     for case in m.listed():
         states = [m.prepare(case, seed) for seed in range(3)]
@@ -100,13 +100,13 @@ def _blocks(r):
     return "x".join(str(int(r["Grid_Size_" + a]) // int(r["Workgroup_Size_" + a])) for a in "XYZ")
 
 
-def table(folder):
+def table(folder, cases="operators"):
     """The lines of the table: per case and kernel its median time and mean counters."""
     files = {n: dispatches(os.path.join(folder, "%s_%s.csv" % (n, kind))) for n, kind in (
         ("trace", "kernel_trace"), ("fetch", "counter_collection"), ("write", "counter_collection"),
         ("sq", "counter_collection"))}
     runs = {n: segments(ds) for n, ds in files.items()}
-    cases = cases_module().listed()
+    cases = cases_module(cases).listed()
     for n, s in runs.items():
         if [len(x) for x in s] != [len(x) for x in runs["trace"]] or len(s) != len(cases):
             raise SystemExit("%s holds other dispatches than the trace or the cases" % n)
