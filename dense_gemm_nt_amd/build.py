@@ -48,7 +48,7 @@ LAYER_SOURCES = [os.path.join(LAYER, f) for f in (
     "launch_ortho.hip")]
 LAYER_HEADERS = [os.path.join(LAYER, f) for f in ("layer_common.hpp", "layer_host.hpp", "layer_launch.hpp",
                                                   "paired_ext.hpp", "int8_ext.hpp", "ortho_common.hpp",
-                                                  "ortho_ext.hpp")] + \
+                                                  "ortho_ext.hpp", "tile64.hpp")] + \
     [os.path.join(ROOT, "include", "gemm_layer.h")]
 LAYER_LIB = os.path.join(PKG, "libgemm_layer.so")
 ARCH = "gfx950"

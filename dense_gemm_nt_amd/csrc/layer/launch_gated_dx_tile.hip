@@ -1,15 +1,15 @@
-// The gated block's input gradient on the 128 x 128 tile for MN-major weights (rows_tile.hpp),
-// whose k-rows come from the two weights in turn.
+// The gated block's input gradient on the 128 x 128 tile for MN-major weights (rows_tile.hpp) and
+// the 64 x 64 one (tile64.hpp); their k-rows come from the two weights in turn.
 #include "layer_launch.hpp"
-#include "../rows/rows_tile.hpp"
+#include "tile64.hpp"
 
 namespace gnt {
 
 template <>
 struct TileHooks<PairedArgs> : PlanTile<PairedArgs> {
     static constexpr bool kPaired = true;
-    template <int IN, int OUT>
-    static __device__ __forceinline__ void add(PairedArgs &p, f32x16 (&acc)[2][2], int, int, int, int lane)
+    template <int IN, int OUT, int FN, int FM>
+    static __device__ __forceinline__ void add(PairedArgs &p, f32x16 (&acc)[FN][FM], int, int, int, int lane)
     {
         unscale<IN>(p, acc, lane);
     }
@@ -25,6 +25,14 @@ static hipError_t launch_dx(const PairedArgs &a, unsigned grid, hipStream_t s)
     return hipGetLastError();
 }
 
+template <int IN, int OUT>
+static hipError_t launch_dx_64(const PairedArgs &a, unsigned grid, hipStream_t s)
+{
+    hipLaunchKernelGGL((tile64<IN, OUT, PairedArgs>), dim3(grid), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 PairedTable kGatedDx_tile = GNT_LAYER_TABLE(launch_dx);
+PairedTable kGatedDx_64 = GNT_LAYER_TABLE(launch_dx_64);
 
 }  // namespace gnt

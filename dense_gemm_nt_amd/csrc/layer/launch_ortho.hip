@@ -6,22 +6,24 @@
 #include "../gemm_nt_kernel.hpp"
 #include "../gemm_nt_pp2.hpp"
 #include "../rows/rows_tile.hpp"
+#include "tile64.hpp"
 
 namespace gnt {
 
 template <>
 struct TileHooks<OrthoArgs> : PlanTile<OrthoArgs> {
     static constexpr bool kStore = true;
-    template <int IN, int OUT>
-    static __device__ __forceinline__ void add(OrthoArgs &, f32x16 (&)[2][2], int, int, int, int)
+    template <int IN, int OUT, int FN, int FM>
+    static __device__ __forceinline__ void add(OrthoArgs &, f32x16 (&)[FN][FM], int, int, int, int)
     {
     }
-    static __device__ __forceinline__ void map(OrthoArgs &p, int &tm, int &tn, int &split)
+    static __device__ __forceinline__ bool map(OrthoArgs &p, int &tm, int &tn, int &split)
     {
-        ortho_map(p, tm, tn, split);          // (a step's tiles are all there)
+        return ortho_map(p, tm, tn, split);
     }
     static __device__ __forceinline__ int tile(const OrthoArgs &p, int, int) { return ortho_tile(p); }
-    static __device__ __forceinline__ void store(const OrthoArgs &p, const f32x16 (&acc)[2][2], int r0, int c0,
+    template <int FN, int FM>
+    static __device__ __forceinline__ void store(const OrthoArgs &p, const f32x16 (&acc)[FN][FM], int r0, int c0,
                                                  uint8_t *stage, int lane)
     {
         store_ortho(p, acc, r0, c0, stage, lane);
@@ -51,6 +53,9 @@ hipError_t launch_ortho(const OrthoArgs &a, OrthoTile tile, unsigned grid, hipSt
     case ORTHO_64:
         hipLaunchKernelGGL((gemm_nt_kernel_ortho<64, 64, 64, 2, 2, 4, IN_FP16, OUT_FP16, false, false>), dim3(grid),
                            dim3(256), 0, s, a);
+        break;
+    case ORTHO_64_MN:
+        hipLaunchKernelGGL((tile64<IN_FP16, OUT_FP16, OrthoArgs>), dim3(grid), dim3(256), 0, s, a);
         break;
     }
     return hipGetLastError();

@@ -152,7 +152,36 @@ gemm_status_t check_sizes(int64_t M, int64_t F, int64_t K, int in_dtype, int out
     return GEMM_OK;
 }
 
-GradPlan plan_dx(int64_t M, int64_t F, int64_t K) { return plan_mn_major(M, K, both(F), kPartialBytes); }
+// The input gradient's plan: the library's for an MN-major B, or (`small`) the 64 x 64 tile where its
+// tiles all run at once, two a compute unit, split along K to be as many, with at most 64
+// slabs each.  In us, the sums' part with it (the 128 x 128 tile's first): 64 rows, F 1408, K 2048
+// 31 and 24; 777 rows 52 and 50; 1024 x 2048 x 1024 54 and 44; 64 x 14336 x 4096 (8 splits of 56 slabs)
+// 120 and 104; but 512 x 5632 x 2048 (2 of 88) 88 and 86, 777 x 5461 x 2048 (171 slabs) 137 and 163.
+struct DxPlan : GradPlan {
+    bool small;
+};
+DxPlan plan_dx(int64_t M, int64_t F, int64_t K)
+{
+    DxPlan g{plan_mn_major(M, K, both(F), kPartialBytes), false};
+    Plan p{};
+    p.tiles_m = (int)cdiv(M, 64);
+    p.tiles_n = (int)cdiv(K, 64);
+    p.k_tiles = (int)cdiv(both(F), 64);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = 2 * kNumCUs;
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(most / tiles, p.k_tiles / 8));
+    p.kt_per_split = (int)cdiv(p.k_tiles, splits);
+    if (tiles > most || p.kt_per_split > 64)
+        return g;
+    p.splits = p.k_tiles ? (int)cdiv(p.k_tiles, p.kt_per_split) : 1;
+    p.group_m = std::min(4, p.tiles_m);
+    p.grid = tiles * p.splits;
+    if (p.splits > 1) {
+        p.inreduce = 1;
+        p.ws_bytes = p.grid * 64 * 64 * 4;
+    }
+    g.plan = p, g.small = true;
+    return g;
+}
 // (the contraction runs over rows, which the MN-major operands take in any number)
 Plan plan_dw(int64_t M, int64_t F, int64_t K)
 {
@@ -181,7 +210,7 @@ bool launchable(const Pieces &p)
 
 struct BackwardWs {
     SumsWs sums;
-    GradPlan dx;
+    DxPlan dx;
     Plan plan[2];                       // dx, dW
     SplitWs split[2];
     uint16_t *d;                        // [M][both(F)]
@@ -417,7 +446,7 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         fill_args(b, p, w.split[0], dX, M, K, both_cols, lddx, dx_dtype);
         b.A = w.d;
         b.lda = (int)both_cols;
-        e = (w.dx.tile ? kGatedDx_tile : kGatedDx_pp2)[in_dtype][dx_dtype](b, (unsigned)p.grid, stream);
+        e = (w.dx.small ? kGatedDx_64 : w.dx.tile ? kGatedDx_tile : kGatedDx_pp2)[in_dtype][dx_dtype](b, (unsigned)p.grid, stream);
         if (e == hipSuccess && p.splits > 1 && !p.inreduce) {
             const KernelArgs &k = b;
             const unsigned grid = (unsigned)cdiv(M * (K / 4), 256);

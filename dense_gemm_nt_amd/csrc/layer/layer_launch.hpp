@@ -19,7 +19,7 @@ extern PairedInTable kGateGrad_128_s4, kGateGrad_128_s4_rot, kGateGrad_128_s2, k
     kGateGrad_pp2;
 // the gradients in the input (the weights MN-major) and in the weights (both operands
 // MN-major)
-extern PairedTable kGatedDx_pp2, kGatedDx_tile, kGatedDw_pp2;
+extern PairedTable kGatedDx_pp2, kGatedDx_tile, kGatedDx_64, kGatedDw_pp2;
 // the product in 8-bit integers
 extern Int8Table kInt8_128_s4, kInt8_128_s4_rot, kInt8_128_s2, kInt8_128_s2_rot, kInt8_32_rot, kInt8_w4, kInt8_pp2;
 

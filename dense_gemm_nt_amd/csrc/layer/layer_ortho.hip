@@ -9,8 +9,9 @@
 // them), of which only the first enters the products; so an X of steep spectrum, whose small
 // singular values the first steps multiply by a alone, keeps them: with X in one FP16 value
 // a spectrum falling as 1 / i ended 2.9e-3 off, so 0.5e-3.  (In FP32 beside the copy for the
-// products it was as exact, for 12 bytes a value and step to move where this has 8: @@.)  From the third step on, when the singular
-// values are near 1, the squares are held as what they differ from the identity by:
+// products it was as exact, for 12 bytes a value and step to move where this has 8: 12 of 2048 x
+// 768 564 us against 504, 4096 x 8192 2543 against 2445.)  From the third step on, when the
+// singular values are near 1, the squares are held as what they differ from the identity by:
 //   A = I + A':  b A + c A^2 = (b + c) I + (b + 2 c) A' + c A'^2
 // whose diagonal does not fill FP16's bits with what is known already; the multiple of I goes
 // into X's factor, exactly (a random 512 x 512: 1.5e-3 off without, 0.9e-3 with).  A BF16
@@ -202,9 +203,10 @@ struct OrthoPlan {
 // What a pass of the machine takes, in us: begin + slab a 64-deep slab (alone: with one block a
 // compute unit where two fit); the most splits (summed in the kernel), and us a split.  From
 // the kernels' times: steps of 12 matrices of 768 x 2048 and of one of 4096 x 8192 (12 and 64 slabs)
-// on 256_MN 41 and 132 a pass, 128_MN 26 and 87, 128_S2 28 and 86, 128 19 and 47, 64 12 and 32;
-// squares of 4096 on 256 91 (64 slabs) and 160 (128), of 12 x 768 on 128 17 (12) and 28 (32), of 1000 on 64
-// 9.5 (16) and 28 (125).
+// on 256_MN 32 and 117 a pass, 128_MN 19 and 83, 128_S2 21 and 86, 128 16 and 45; squares of 4096 on
+// 256 88 (64 slabs) and 155 (128), of 12 x 768 on 128 16 (12) and 26 (32), of 1000 on 64 9 (16), 11 (32) and
+// 28 (125); steps of 1000 on 64_MN 8.  Over twenty-two shapes the choices were within 4% of the best
+// tile and split of each product.
 struct OrthoKind {
     OrthoTile tile;
     int size, at_once, splits;
@@ -212,9 +214,10 @@ struct OrthoKind {
     double begin, slab, alone, split;
 };
 constexpr OrthoKind kOrthoKinds[] = {
-    {ORTHO_256, 256, 1, 2, false, 18.0, 1.3, 1.3, 8.0},   {ORTHO_256_MN, 256, 1, 2, true, 19.0, 1.75, 1.75, 8.0},
-    {ORTHO_128, 128, 1, 16, false, 11.5, 0.52, 0.52, 1.0}, {ORTHO_128_S2, 128, 2, 1, false, 15.0, 1.1, 0.6, 0.0},
-    {ORTHO_128_MN, 128, 2, 16, true, 11.0, 1.2, 0.85, 1.0}, {ORTHO_64, 64, 2, 16, false, 6.5, 0.4, 0.22, 0.7},
+    {ORTHO_256, 256, 1, 2, false, 18.0, 1.3, 1.3, 16.0},  {ORTHO_256_MN, 256, 1, 2, true, 11.0, 1.62, 1.62, 16.0},
+    {ORTHO_128, 128, 1, 16, false, 11.5, 0.52, 0.52, 5.0}, {ORTHO_128_S2, 128, 2, 1, false, 15.0, 1.1, 0.6, 0.0},
+    {ORTHO_128_MN, 128, 2, 16, true, 7.0, 1.05, 1.0, 3.0}, {ORTHO_64, 64, 2, 16, false, 5.5, 0.55, 0.28, 0.8},
+    {ORTHO_64_MN, 64, 2, 16, true, 3.0, 0.55, 0.28, 0.8},
 };
 
 double cost_of(const OrthoKind &k, int64_t blocks, int64_t slabs, int64_t splits)
@@ -258,7 +261,8 @@ OrthoPlan plan_ortho(int64_t batch, int64_t M, int64_t N, int64_t K, bool square
         }
     };
     for (const OrthoKind &k : kOrthoKinds) {
-        if (square ? k.mn : k.tile == ORTHO_256)
+        // (a step's 64 x 64 tiles read X as it is: 1000 x 2047 189 us, with X transposed 203)
+        if (square ? k.mn : k.tile == ORTHO_256 || k.tile == ORTHO_64)
             continue;
         for (int64_t s = 1; s <= k.splits; ++s) {
             const int64_t per = slabs_per(slabs, s);
@@ -326,7 +330,7 @@ OrthoWs carve_ortho(int64_t batch, int64_t m, int64_t n, void *base)
     w.hi = c.take<uint16_t>(2 * size);       // two, in turn: a step reads one and writes the other
     w.lo = c.take<uint16_t>(size);
     const OrthoTile step = w.plan[ORTHO_STEP].part[0].tile;
-    w.turned = step != ORTHO_256_MN && step != ORTHO_128_MN;
+    w.turned = step == ORTHO_128 || step == ORTHO_128_S2;
     w.xt = c.take<uint16_t>(w.turned ? 2 * size : 0);
     w.a = c.take<uint16_t>(batch * w.r8 * w.r8);
     w.b = c.take<uint16_t>(batch * w.r8 * w.r8);

@@ -13,7 +13,7 @@ namespace gnt {
 //           take; in the last step the update
 // The products' tiles: all but the _MN ones have both operands K-major; _S2 is the 128 x 128
 // tile with a two-stage ring, and so two blocks a compute unit.
-enum OrthoTile : int { ORTHO_256, ORTHO_256_MN, ORTHO_128, ORTHO_128_S2, ORTHO_128_MN, ORTHO_64 };
+enum OrthoTile : int { ORTHO_256, ORTHO_256_MN, ORTHO_128, ORTHO_128_S2, ORTHO_128_MN, ORTHO_64, ORTHO_64_MN };
 
 enum : int { ORTHO_SQUARE = 0, ORTHO_POLY = 1, ORTHO_STEP = 2 };
 

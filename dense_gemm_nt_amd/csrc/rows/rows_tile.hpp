@@ -31,7 +31,7 @@ constexpr int kTileStages = 5, kTileOperand = 8192;
 // are added (add), RoutedArgs an expert's tile; others (outside this folder) specialize it.
 //   kLookup  finds the block's tile (false: none) without K splits, in place of the plan's map
 //   kPaired  B's k-rows alternate in groups of eight between two arrays
-//   tile     the tile's number in the launch
+//   map, tile  the block's tile and split (false: none), and its number in the launch
 //   kStore   store(p, acc, r0, c0, stage, lane) in place of a whole sum's store
 template <typename Args>
 struct PlanTile {
@@ -40,12 +40,13 @@ struct PlanTile {
     static __device__ __forceinline__ int ldb(const Args &p, int) { return p.ldb; }
     static __device__ __forceinline__ int cols(const Args &) { return 0; }
     static __device__ __forceinline__ int tile(const Args &p, int tm, int tn) { return tm * p.tiles_n + tn; }
-    static __device__ __forceinline__ void map(Args &p, int &tm, int &tn, int &split)
+    static __device__ __forceinline__ bool map(Args &p, int &tm, int &tn, int &split)
     {
         if (p.inreduce)
             map_block_split_minor(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, p.splits, tm, tn, split);
         else
             map_block(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, p.group_m, tm, tn, split);
+        return true;
     }
 };
 
@@ -81,8 +82,8 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
     if constexpr (ROUTED) {
         if (!routed_lookup(p, tm, tn))
             return;
-    } else {
-        Hooks::map(p, tm, tn, split);
+    } else if (!Hooks::map(p, tm, tn, split)) {
+        return;
     }
     const int m0 = tm * BM, n0 = tn * BN;
     // (k_tiles and kt_per_split count 64-deep slabs, as the plans do)

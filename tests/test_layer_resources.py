@@ -39,6 +39,8 @@ def test_every_family_is_built(kernels):
     # the update's tiles; the 128 x 128 tile for MN-major B: the update's, and the input gradient's
     assert _count(kernels, "gemm_nt_kernel_ortho") == 3 and _count(kernels, "gemm_nt_pp2_ortho") == 2
     assert _count(kernels, "rows_tile") == 1 + 6
+    # and the 64 x 64 one
+    assert _count(kernels, "tile64") == 1 + 6
 
 
 def test_no_scratch_no_spills(kernels):
@@ -53,9 +55,9 @@ def test_lds_and_register_budget(kernels):
         assert m[".group_segment_fixed_size"] <= k.LDS_BYTES, n
         waves = -(-m[".max_flat_workgroup_size"] // 64)
         assert -(-waves // 4) * m[".vgpr_count"] <= k.REGS_PER_SIMD_LANE, n
-    # the two-stage ring, the 64 x 64 tile and the tile for MN-major B run two blocks a compute unit
-    two = [n for n in kernels if ("gemm_nt_kernel" in n and ("Li4ELi2E" in n or "Li64ELi64ELi64E" in n)) or "rows_tile" in n]
-    assert len(two) == (2 * 6 + 2) + 2 * 3 + 2 + 7
+    # the two-stage ring, the 64 x 64 tiles and the tile for MN-major B run two blocks a compute unit
+    two = [n for n in kernels if ("gemm_nt_kernel" in n and ("Li4ELi2E" in n or "Li64ELi64ELi64E" in n)) or "rows_tile" in n or "tile64" in n]
+    assert len(two) == (2 * 6 + 2) + 2 * 3 + 2 + 7 + 7
     for n in two:
         waves = kernels[n][".max_flat_workgroup_size"] // 64
         assert 2 * kernels[n][".group_segment_fixed_size"] <= k.LDS_BYTES, n
