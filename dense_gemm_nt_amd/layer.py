@@ -147,8 +147,8 @@ def gemm_int8(A, B, scale_a, scale_b, out=None, out_dtype=None, alpha=1.0, beta=
               bias_along="n", activation="none"):
     """C = act(alpha * y + beta * C_old + bias), y[m, n] = scale_a[m] scale_b[n] (A[m] . B[n]), for
     int8 A [M, K] (quantize_int8's codes) and B [N, K], scales float32 [M] and [N] (or one
-    value each): [M, N] of out_dtype (default bfloat16).  The integer sums are
-    exact.  K a multiple of 16 below 2^17; the epilogue as gemm_nt's."""
+    value each): [M, N] of out_dtype (default bfloat16).  The integer sums (of a K split,
+    each split's) are exact.  K a multiple of 16 below 2^17; the epilogue as gemm_nt's."""
     import torch
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("A must be [M, K] and B [N, K], got %s and %s" % (tuple(A.shape), tuple(B.shape)))
@@ -189,8 +189,25 @@ def gemm_int8(A, B, scale_a, scale_b, out=None, out_dtype=None, alpha=1.0, beta=
 
 
 @functools.lru_cache(maxsize=16)
-def _coefficients(flat):
-    return (ctypes.c_float * len(flat))(*flat)
+def _floats(values):
+    return (ctypes.c_float * len(values))(*values)
+
+
+def _coefficients(coefficients, steps):
+    """The steps' triples as a host array."""
+    flat = tuple(coefficients)
+    if len(flat) == 3 and not any(map(_is_triple, flat)):
+        flat = flat * steps
+    elif len(flat) == steps and all(map(_is_triple, flat)):
+        flat = tuple(v for t in flat for v in t)
+    else:
+        raise ValueError("coefficients must be (a, b, c) or %d such triples" % steps)
+    # (numbers, not what holds them: a tensor's element may change between calls)
+    return _floats(tuple(map(float, flat)))
+
+
+def _is_triple(t):
+    return getattr(t, "shape", None) == (3,) or isinstance(t, (tuple, list)) and len(t) == 3
 
 
 def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, out=None, out_dtype=None):
@@ -211,13 +228,7 @@ def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     steps = int(steps)
     if steps < 0:
         raise ValueError("steps must not be negative")
-    flat = tuple(coefficients)
-    if len(flat) == 3 and not hasattr(flat[0], "__len__"):
-        flat = flat * steps
-    elif len(flat) == steps and all(hasattr(t, "__len__") and len(t) == 3 for t in flat):
-        flat = tuple(v for t in flat for v in t)
-    else:
-        raise ValueError("coefficients must be (a, b, c) or %d such triples" % steps)
+    values = _coefficients(coefficients, steps)
     B = G.shape[0] if G.dim() == 3 else 1
     m, n = G.shape[-2:]
 
@@ -237,7 +248,7 @@ def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, 
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=G.device) if ws_bytes else None
     st = _layer.lib().gemm_run_orthogonalize(
         G.data_ptr(), out.data_ptr(), B, m, n, ldg, ldu, g_step, u_step, _code(G.dtype), _code(out.dtype), steps,
-        _coefficients(flat), eps, _ptr(ws), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
+        values, eps, _ptr(ws), ws_bytes, torch._C._cuda_getCurrentRawStream(index))
     if st:
         _lib.check(st, "orthogonalize(B=%d, m=%d, n=%d)" % (B, m, n))
     return out

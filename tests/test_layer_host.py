@@ -201,3 +201,19 @@ def test_calls_refuse_what_is_not_theirs():
         g.orthogonalize(torch.zeros(3))
     with pytest.raises(ValueError):
         g.orthogonalize(torch.zeros(3, 4))
+
+
+def test_coefficients_are_taken_as_numbers():
+    from dense_gemm_nt_amd import layer
+    t = torch.tensor([1.0, 2.0, 3.0])
+    assert list(layer._coefficients(t, 2)) == [1, 2, 3, 1, 2, 3]
+    scalars = list(t)                                       # (views: the same objects with other values)
+    assert list(layer._coefficients(scalars, 1)) == [1, 2, 3]
+    t += 1
+    assert list(layer._coefficients(scalars, 1)) == [2, 3, 4] and list(layer._coefficients(t, 1)) == [2, 3, 4]
+    assert list(layer._coefficients([(1, 2, 3), [4, 5, 6], t], 3)) == [1, 2, 3, 4, 5, 6, 2, 3, 4]
+    assert list(layer._coefficients(torch.ones(3, 3), 3)) == [1] * 9
+    assert list(layer._coefficients((1, 2, 3), 0)) == [] and list(layer._coefficients([], 0)) == []
+    for bad, steps in (((1, 2), 2), ((1, 2, 3, 4), 4), ([(1, 2, 3)], 2), ([(1, 2)] * 2, 2), ([(1, 2, 3), 1, 2], 3)):
+        with pytest.raises(ValueError):
+            layer._coefficients(bad, steps)
