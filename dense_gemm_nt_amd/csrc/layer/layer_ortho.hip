@@ -279,7 +279,8 @@ OrthoPlan plan_ortho(int64_t batch, int64_t M, int64_t N, int64_t K, bool square
     // A square's 256 x 256 tiles that fill whole passes of the machine, and the quarters of the
     // rest on the 128 x 128 tile, with splits: two matrices of 4096 rows (272 tiles) 3.29 ms for
     // the update, on the one tile 3.53.  (Whole passes of tiles split in two did not pay: one
-    // matrix of 4096 x 8192, 128 tiles twice and 8 over, 3.18 against 3.14.)
+    // matrix of 4096 x 8192, 128 tiles twice and 8 over, 3.18 against 3.14; nor did 192 x 192 tiles, four
+    // waves of 96 x 96: there 253 of them fill the machine and took 1.1 us a slab, 2.52 against 2.56.)
     if (square) {
         const OrthoKind &k = kOrthoKinds[0], &q = kOrthoKinds[2];
         OrthoPlan p = begin(k);
@@ -330,7 +331,8 @@ OrthoWs carve_ortho(int64_t batch, int64_t m, int64_t n, void *base)
     w.hi = c.take<uint16_t>(2 * size);       // two, in turn: a step reads one and writes the other
     w.lo = c.take<uint16_t>(size);
     const OrthoTile step = w.plan[ORTHO_STEP].part[0].tile;
-    w.turned = step == ORTHO_128 || step == ORTHO_128_S2;
+    // (every tile but those reads B by rows of K)
+    w.turned = step != ORTHO_256_MN && step != ORTHO_128_MN && step != ORTHO_64_MN;
     w.xt = c.take<uint16_t>(w.turned ? 2 * size : 0);
     w.a = c.take<uint16_t>(batch * w.r8 * w.r8);
     w.b = c.take<uint16_t>(batch * w.r8 * w.r8);
