@@ -201,7 +201,8 @@ struct OrthoPlan {
 };
 
 // What a pass of the machine takes, in us: begin + slab a 64-deep slab (alone: with one block a
-// compute unit where two fit); the most splits (summed in the kernel), and us a split.  From
+// compute unit where two fit); the most splits (summed in the kernel), and us a split
+// (a step's K is the smaller side, too short to split: 1000 x 2047 210 us in two, 183 whole).  From
 // the kernels' times: steps of 12 matrices of 768 x 2048 and of one of 4096 x 8192 (12 and 64 slabs)
 // on 256_MN 32 and 117 a pass, 128_MN 19 and 83, 128_S2 21 and 86, 128 16 and 45; squares of 4096 on
 // 256 88 (64 slabs) and 155 (128), of 12 x 768 on 128 16 (12) and 26 (32), of 1000 on 64 9 (16), 11 (32) and
@@ -214,10 +215,10 @@ struct OrthoKind {
     double begin, slab, alone, split;
 };
 constexpr OrthoKind kOrthoKinds[] = {
-    {ORTHO_256, 256, 1, 2, false, 18.0, 1.3, 1.3, 16.0},  {ORTHO_256_MN, 256, 1, 2, true, 11.0, 1.62, 1.62, 16.0},
+    {ORTHO_256, 256, 1, 2, false, 18.0, 1.3, 1.3, 16.0},  {ORTHO_256_MN, 256, 1, 1, true, 11.0, 1.62, 1.62, 0.0},
     {ORTHO_128, 128, 1, 16, false, 11.5, 0.52, 0.52, 5.0}, {ORTHO_128_S2, 128, 2, 1, false, 15.0, 1.1, 0.6, 0.0},
-    {ORTHO_128_MN, 128, 2, 16, true, 7.0, 1.05, 1.0, 3.0}, {ORTHO_64, 64, 2, 16, false, 5.5, 0.55, 0.28, 0.8},
-    {ORTHO_64_MN, 64, 2, 16, true, 3.0, 0.55, 0.28, 0.8},
+    {ORTHO_128_MN, 128, 2, 1, true, 7.0, 1.05, 1.0, 0.0}, {ORTHO_64, 64, 2, 16, false, 5.5, 0.55, 0.28, 0.8},
+    {ORTHO_64_MN, 64, 2, 1, true, 3.0, 0.55, 0.28, 0.0},
 };
 
 double cost_of(const OrthoKind &k, int64_t blocks, int64_t slabs, int64_t splits)

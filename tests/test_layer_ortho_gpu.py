@@ -151,3 +151,9 @@ def test_signed_permutations_are_exact(B, m, n):
     out = g.orthogonalize(G.to(DEV), steps=4, coefficients=[(1.0, 0.0, 0.0), (2.0, 0.0, 0.0), (1.0, 0.0, 0.0), (0.5, 0.0, 0.0)],
                           eps=0.0, out_dtype=BF16)
     assert torch.equal(out.cpu().float(), G * s)
+
+
+@pytest.mark.parametrize("B,m,n", [(4, 1024, 1024), (3, 1024, 4096), (2, 4096, 4096), (2, 6000, 4096)])
+def test_tiles_of_larger_updates_are_exact(B, m, n):
+    """The same on 128 x 128 tiles, whole and split, and on 256 x 256 ones with the last pass's in quarters."""
+    test_signed_permutations_are_exact(B, m, n)
