@@ -29,6 +29,30 @@ def _workspace_bytes(fn, *sizes):
     return n
 
 
+def _span(t, unit):
+    """(first byte, bytes from there to the last one's end, bytes of a row, from row to row or 0 with
+    one row) of a matrix or vector of unit stride."""
+    rows, row = (t.shape[0], t.shape[1] * unit) if t.dim() == 2 else (1, t.numel() * unit)
+    step = t.stride(0) * unit if rows > 1 else 0
+    return t.data_ptr(), (rows - 1) * step + row if rows and row else 0, row, step
+
+
+def _apart(out, **operands):
+    """Refuses an `out` that shares memory with an operand, which blocks still read when others
+    store.  (Column ranges of one buffer's rows are apart.)"""
+    at, size, row, step = _span(out, out.element_size())
+    for name, t in operands.items():
+        if t is None:
+            continue
+        at2, size2, row2, step2 = _span(t, t.element_size())
+        if not size or not size2 or at + size <= at2 or at2 + size2 <= at:
+            continue
+        every = step or step2
+        if every and (step2 or step) == every and (at2 - at) % every >= row and (at - at2) % every >= row2:
+            continue
+        raise ValueError("out overlaps %s" % name)
+
+
 def _gate(activation):
     code = _layer.GATES.get(activation)
     if code is None:
@@ -67,6 +91,7 @@ def gemm_gated(x, Wg, Wu, activation="silu", out=None, out_dtype=None):
         ldh = F
     else:
         ldh = _matrix("out", _out("out", out, (M, F), x.device), M, F)
+        _apart(out, x=x, Wg=Wg, Wu=Wu)
     n = _workspace_bytes("gemm_gated_workspace", M, F, K)
     ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
     st = _layer.lib().gemm_run_gated(
@@ -171,6 +196,7 @@ def gemm_int8(A, B, scale_a, scale_b, out=None, out_dtype=None, alpha=1.0, beta=
         ldc = N
     else:
         ldc = _matrix("out", _out("out", out, (M, N), A.device), M, N)
+        _apart(out, A=A, B=B, scale_a=scale_a, scale_b=scale_b, bias=bias)
     epi = None
     if not (alpha == 1.0 and beta == 0.0 and bias is None and activation == "none"):
         if bias is not None:

@@ -10,8 +10,10 @@
  * sums; results rounded once to nearest even.  Limits: rows below 2^30, sizes
  * below 2^31, fewer than 2^23 output tiles, leading dimensions of operands
  * below 2^22 and multiples of 8 (INT8: below 2^23, of 16), operand bases
- * 16-byte aligned; outputs, and dH, need their element's alignment.  For given
- * arguments every call on the same device returns the same bits.
+ * 16-byte aligned; outputs, and dH, need their element's alignment.  Outputs
+ * and the workspace must not overlap the operands or each other (not checked
+ * here; but for U, which may be G).  For given arguments every call on the same
+ * device returns the same bits.
  *
  * Workspaces: no handle; a call that needs one takes a device workspace of the
  * caller's, 256-byte aligned and at least as large as the matching *_workspace

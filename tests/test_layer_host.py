@@ -217,3 +217,20 @@ def test_coefficients_are_taken_as_numbers():
     for bad, steps in (((1, 2), 2), ((1, 2, 3, 4), 4), ([(1, 2, 3)], 2), ([(1, 2)] * 2, 2), ([(1, 2, 3), 1, 2], 3)):
         with pytest.raises(ValueError):
             layer._coefficients(bad, steps)
+
+
+def test_outputs_that_overlap_operands_are_refused():
+    from dense_gemm_nt_amd import layer
+    buf = torch.zeros(8, 64)
+    a, b = buf[:, :24], buf[:, 24:56]
+    layer._apart(a, x=b)                                    # columns of the same rows
+    layer._apart(b, x=a, y=None, z=torch.zeros(3))
+    layer._apart(buf[:4], x=buf[4:])
+    layer._apart(buf[:1, :8], x=buf[0, 8:16], y=buf[1, :8])
+    layer._apart(buf[:, 16:24], x=buf[1:, :16])
+    layer._apart(buf[3:4, :8], x=buf[:, 8:16]), layer._apart(buf[:, 8:16], x=buf[3, :8])
+    layer._apart(buf[:0], x=buf), layer._apart(buf[:, :0], x=buf)
+    for out, x in ((a, a), (a, buf[:, 23:30]), (buf[:, 23:30], a), (buf[:4], buf[3:]), (buf[1:3, 8:], buf[2:, :9]),
+                   (buf.view(16, 32)[2:5], buf[1]), (buf[2:3], buf[:, 5:6]), (buf[:, 5:6], buf[2:3])):
+        with pytest.raises(ValueError):
+            layer._apart(out, x=x)
