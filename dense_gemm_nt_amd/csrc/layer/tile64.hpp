@@ -4,11 +4,12 @@
 //
 // Four waves (2 x 2 blocks of 32 x 32), two blocks a compute unit; a ring of four stages of
 // 64-deep slabs (8 KB an operand) filled by direct-to-LDS loads, and all of a slab's fragments
-// read before its first MFMA.  A slab's time is its barrier, the LDS reads' latency and the
-// loads': 0.28 us with one block on a compute unit, 0.5 with two.  (Two groups of four waves a tile, each with half of its K and their sums joined
-// in LDS, one such block a compute unit: level at one tile a compute unit, 1000 x 2048 x 1000, and
-// behind from there on.  A K-major B's fragments read all at once, too: 178 us for the update of a
-// 1000 x 2047 with the plan tile's order, 191 with this.)
+// read before its first MFMA.  Of few blocks a launch's beginning and end (its first loads, the
+// stores) take 6 to 8 us and a slab 0.15; of 416 blocks of 44 slabs (23 us) a slab 0.37, its
+// loads from the L2s at 17 TB/s.  Level with this: fragments read a slab ahead, loads between the
+// MFMAs, eight stages.  Slower: two groups of four waves a tile with half of K each (one block a
+// compute unit; 1000 x 2047's update 202 us, 189 with this), and a K-major B the same way (191,
+// 178 with the plan tile's order of reads and loads).
 //
 //   A: 64 rows of 128 bytes, a load 8 rows; chunk c of row r at c ^ row_key<8>(r)
 //   B: 64 k-rows of 64 columns, a load 8 k-rows; chunk c of k-row r at c ^ 4 (r / 2 mod 2), so
