@@ -36,7 +36,6 @@ struct PairedArgs : KernelArgs {
     int cols;
     const uint16_t *dh;         // backward: the block's output gradient [M][cols]
     int lddh;
-    int dh16;                   // its rows start 16-byte aligned
     const uint32_t *most;       // FP16 backward: kMostParts partial maxima of |dh| (its bits)
     void *C2;                   // weight gradients: C is the gate's, C2 the up projection's
     ClearList clear;            // gradients of the sums: cleared on the way
@@ -112,18 +111,25 @@ __device__ __forceinline__ uint32_t to_bits16(float x)
         return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
 }
 
+// 16 bytes of values at the alignment of one: the memory unit takes them at any address, so rows
+// of odd lengths need no other path (with one of single values for them, the gated block of 1500
+// rows and 5461 FP16 columns 143 us, 130 with this; quantizing 4000 x 4095 BF16 29 and 16, FP32
+// 38 and 16).
+typedef uint32_t run16_t __attribute__((ext_vector_type(4), aligned(2)));
+typedef float run32_t __attribute__((ext_vector_type(4), aligned(4)));
+
 // `count` (1 .. 8, or 4 of FP32) consecutive values of a row at C, element index idx: one
-// 16-byte store where all are there and rows allow it, of 16-bit values with the
-// non-temporal policy where NT (results; what the next launch reads stays in the caches).
+// 16-byte store where all are there, of 16-bit values with the non-temporal policy where
+// NT (results; what the next launch reads stays in the caches).
 template <int OUT, int V, bool NT = true>
-__device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)[V], bool wide, int count)
+__device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)[V], int count)
 {
     if constexpr (OUT == OUT_FP32) {
         float *c = static_cast<float *>(C) + idx;
-        if (wide && count >= V) {
+        if (count >= V) {
 #pragma unroll
             for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<f32x4 *>(c + i) = (f32x4){x[i], x[i + 1], x[i + 2], x[i + 3]};
+                *reinterpret_cast<run32_t *>(c + i) = (run32_t){x[i], x[i + 1], x[i + 2], x[i + 3]};
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -133,15 +139,15 @@ __device__ __forceinline__ void store_run(void *C, int64_t idx, const float (&x)
     } else {
         static_assert(V == 8, "16 bytes");
         uint16_t *c = static_cast<uint16_t *>(C) + idx;
-        u32x4 w;
+        run16_t w;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = to_bits16<OUT>(x[2 * i]) | to_bits16<OUT>(x[2 * i + 1]) << 16;
-        if (wide && count >= V) {
+        if (count >= V) {
             if constexpr (NT)
-                __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(c));
+                __builtin_nontemporal_store(w, reinterpret_cast<run16_t *>(c));
             else
-                *reinterpret_cast<u32x4 *>(c) = w;
+                *reinterpret_cast<run16_t *>(c) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i)
@@ -193,7 +199,7 @@ __device__ __forceinline__ void store_gated(const PairedArgs &p, const f32x16 (&
                 y[4 * i + e] = v[e];
         }
         if (m < p.M && n < p.cols)
-            store_run<OUT, V>(p.C, (int64_t)m * p.ldc + n, y, p.rows16 != 0, p.cols - n);
+            store_run<OUT, V>(p.C, (int64_t)m * p.ldc + n, y, p.cols - n);
     }
 }
 
@@ -243,8 +249,8 @@ __device__ __forceinline__ void store_gate_gradients(const PairedArgs &p, const 
             u32x4 w = {0u, 0u, 0u, 0u};
             if (m < p.M && n < p.cols) {
                 const uint16_t *src = p.dh + (int64_t)m * p.lddh + n;
-                if (p.dh16 && n + 8 <= p.cols) {
-                    w = *reinterpret_cast<const u32x4 *>(src);
+                if (n + 8 <= p.cols) {
+                    w = *reinterpret_cast<const run16_t *>(src);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -342,7 +348,7 @@ __device__ __forceinline__ void store_paired_rows(const PairedArgs &p, const f32
                     y[4 * i + e] = v[e];
             }
             if (f < p.cols && n < p.N)
-                store_run<OUT, V>((R >> 3) & 1 ? p.C2 : p.C, (int64_t)f * p.ldc + n, y, p.rows16 != 0, p.N - n);
+                store_run<OUT, V>((R >> 3) & 1 ? p.C2 : p.C, (int64_t)f * p.ldc + n, y, p.N - n);
         }
         wait_lgkmcnt0();
     }

@@ -25,7 +25,7 @@
 namespace gnt {
 
 // The partial maxima of |dh| (16-bit patterns without the sign, which order as the values do).
-__global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int F, int ld, int wide, uint32_t *most)
+__global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int F, int ld, uint32_t *most)
 {
     __shared__ uint32_t part[4];
     uint32_t b = 0;
@@ -34,11 +34,10 @@ __global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int
     for (int64_t m = blockIdx.x; m < M; m += step) {
         const uint16_t *row = x + m * ld;
         int n = threadIdx.x * 8;
-        if (wide)
-            for (; n + 8 <= F; n += 2048) {
-                const u32x4 w = *reinterpret_cast<const u32x4 *>(row + n);
-                take(w[0]), take(w[1]), take(w[2]), take(w[3]);
-            }
+        for (; n + 8 <= F; n += 2048) {
+            const u32x4 w = *reinterpret_cast<const run16_t *>(row + n);
+            take(w[0]), take(w[1]), take(w[2]), take(w[3]);
+        }
         for (; n < F; n += 2048)
             for (int i = 0; i < 8; ++i)
                 if (n + i < F)
@@ -409,11 +408,10 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
     a.act = activation;
     a.dh = static_cast<const uint16_t *>(dH);
     a.lddh = (int)lddh;
-    a.dh16 = lddh % 8 == 0 && (uintptr_t)dH % 16 == 0;
     a.most = w.most;
     if (e == hipSuccess && in_dtype == GEMM_FP16) {
         hipLaunchKernelGGL(most_of, dim3(kMostParts), dim3(256), 0, stream, a.dh, F > 0 ? M : 0, (int)F, a.lddh,
-                           a.dh16, w.most);
+                           w.most);
         e = hipGetLastError();
     }
     for (int i = 0; inner && i < w.sums.pieces.count && e == hipSuccess; ++i) {
@@ -463,7 +461,6 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         const Plan &p = w.plan[1];
         PairedArgs b = a;
         fill_args(b, p, w.split[1], dWg, both_cols, K, M, K, grad_dtype);
-        b.rows16 = b.rows16 && (uintptr_t)dWu % 16 == 0;
         b.vec_store = b.vec_store && (uintptr_t)dWu % (4 * size_of(grad_dtype)) == 0;
         b.C2 = dWu;
         b.A = w.d;

@@ -19,17 +19,17 @@ __device__ __forceinline__ float read_value(const void *x, int64_t i)
 
 // Eight values from element i on; those at or past K are zero.
 template <int IN>
-__device__ __forceinline__ void read8(const void *x, int64_t i, bool wide, int left, float (&v)[8])
+__device__ __forceinline__ void read8(const void *x, int64_t i, int left, float (&v)[8])
 {
-    if (wide && left >= 8) {
+    if (left >= 8) {
         if constexpr (IN == OUT_FP32) {
-            const f32x4 *s = reinterpret_cast<const f32x4 *>(static_cast<const float *>(x) + i);
+            const run32_t *s = reinterpret_cast<const run32_t *>(static_cast<const float *>(x) + i);
             const f32x4 a = s[0], b = s[1];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 v[e] = a[e], v[4 + e] = b[e];
         } else {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(x) + i);
+            const u32x4 w = *reinterpret_cast<const run16_t *>(static_cast<const uint16_t *>(x) + i);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 v[e] = from_bits16(IN, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
@@ -41,6 +41,8 @@ __device__ __forceinline__ void read8(const void *x, int64_t i, bool wide, int l
     }
 }
 
+typedef uint32_t codes8_t __attribute__((ext_vector_type(2), aligned(1)));    // of rows of any length
+
 // Codes and scale of a row: s = max |x| / 127, q = the nearest integer (even at a tie) to x / s,
 // both quotients rounded to FP32 as IEEE division does.  A row of zeros: scale 0, codes 0; a row
 // with an infinity or NaN: scale NaN, codes 0, so that its products are NaN.  TPR threads a
@@ -48,7 +50,7 @@ __device__ __forceinline__ void read8(const void *x, int64_t i, bool wide, int l
 // longer is read again (from L2).
 template <int IN, int TPR>
 __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *codes, float *scale, int64_t M, int K,
-                                                     int64_t ldx, int64_t ldq, int wide, int wide_q)
+                                                     int64_t ldx, int64_t ldq)
 {
     constexpr int ROWS = 256 / TPR, HELD = 4;
     __shared__ uint32_t part[4];
@@ -68,13 +70,13 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
         for (int i = 0; i < HELD; ++i) {
             const int k = (i * TPR + t) * 8;
             if (k < K) {
-                read8<IN>(x, row + k, wide, K - k, v[i]);
+                read8<IN>(x, row + k, K - k, v[i]);
                 most(v[i]);
             }
         }
         for (int k = (HELD * TPR + t) * 8; k < K; k += TPR * 8) {
             float y[8];
-            read8<IN>(x, row + k, wide, K - k, y);
+            read8<IN>(x, row + k, K - k, y);
             most(y);
         }
     }
@@ -117,12 +119,12 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
                 q[e] = some ? (uint32_t)(int)fminf(fmaxf(__builtin_rintf(y[e] / s), -127.0f), 127.0f) : 0u;
         }
         int8_t *dst = codes + m * ldq + k;
-        if (wide_q && k + 8 <= K) {
-            u32x2 w;
+        if (k + 8 <= K) {
+            codes8_t w;
 #pragma unroll
             for (int d = 0; d < 2; ++d)
                 w[d] = (q[4 * d] & 0xffu) | (q[4 * d + 1] & 0xffu) << 8 | (q[4 * d + 2] & 0xffu) << 16 | q[4 * d + 3] << 24;
-            *reinterpret_cast<u32x2 *>(dst) = w;
+            *reinterpret_cast<codes8_t *>(dst) = w;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
     }
     for (int k = (HELD * TPR + t) * 8; k < K; k += TPR * 8) {
         float y[8];
-        read8<IN>(x, row + k, wide, K - k, y);
+        read8<IN>(x, row + k, K - k, y);
         put(k, y);
     }
 }
@@ -284,17 +286,15 @@ gemm_status_t gemm_run_quantize_int8(const void *X, void *codes, float *scale, i
     const int64_t size = size_of(in_dtype);
     if ((uintptr_t)scale % 4 || (uintptr_t)X % size)
         return GEMM_ERR_MISALIGNED;
-    const int wide = (ldx * size) % 16 == 0 && (uintptr_t)X % 16 == 0;
-    const int wide_q = ldq % 8 == 0 && (uintptr_t)codes % 8 == 0;
     const bool wave = K <= 2048;
     const unsigned grid = (unsigned)cdiv(M, wave ? 4 : 1);
     auto launch = [&](auto in) {
         if (wave)
             hipLaunchKernelGGL((quantize_rows<in.value, 64>), dim3(grid), dim3(256), 0, stream, X,
-                               static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq, wide, wide_q);
+                               static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq);
         else
             hipLaunchKernelGGL((quantize_rows<in.value, 256>), dim3(grid), dim3(256), 0, stream, X,
-                               static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq, wide, wide_q);
+                               static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq);
     };
     if (in_dtype == GEMM_BF16)
         launch(std::integral_constant<int, OUT_BF16>{});

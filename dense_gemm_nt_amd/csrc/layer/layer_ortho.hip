@@ -32,16 +32,16 @@ __device__ __forceinline__ float read_any(const void *x, int64_t i, int dtype)
 }
 
 // Eight values from element i on, of which the first `left` are there; zeros behind them.
-__device__ __forceinline__ void read_eight(const void *x, int64_t i, int dtype, bool wide, int left, float (&v)[8])
+__device__ __forceinline__ void read_eight(const void *x, int64_t i, int dtype, int left, float (&v)[8])
 {
-    if (wide && left >= 8 && dtype == OUT_FP32) {
-        const f32x4 *s = reinterpret_cast<const f32x4 *>(static_cast<const float *>(x) + i);
+    if (left >= 8 && dtype == OUT_FP32) {
+        const run32_t *s = reinterpret_cast<const run32_t *>(static_cast<const float *>(x) + i);
         const f32x4 a = s[0], b = s[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             v[e] = a[e], v[4 + e] = b[e];
-    } else if (wide && left >= 8) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(x) + i);
+    } else if (left >= 8) {
+        const u32x4 w = *reinterpret_cast<const run16_t *>(static_cast<const uint16_t *>(x) + i);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             v[e] = from_bits16(dtype, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
@@ -68,7 +68,7 @@ __device__ __forceinline__ double block_sum(double v, double *part)
 // loads of them at a time (one at a time 2 TB/s, of a long row 5.6).  The arrival counters of
 // the products to come are cleared on the way.
 __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n, int64_t ld, int64_t step, int dtype,
-                                                     int wide, double *parts, unsigned *counters, int num_counters)
+                                                     double *parts, unsigned *counters, int num_counters)
 {
     __shared__ double part[4];
     const int id = blockIdx.x * 256 + threadIdx.x, threads = gridDim.x * 256;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n
             const int64_t at = i + j * (int64_t)threads;
             const int64_t r = at / runs;
             const int c = (int)(at - r * runs) * 8;
-            read_eight(G, from + r * ld + c, dtype, wide != 0, at < all ? n - c : 0, v[j]);
+            read_eight(G, from + r * ld + c, dtype, at < all ? n - c : 0, v[j]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -102,27 +102,19 @@ __global__ __launch_bounds__(256) void ortho_squares(const void *G, int m, int n
 // with xt the first also transposed, [cols8][rows8]; a tall G (flip) is transposed on the way.
 // A block has 64 x 64 values.
 __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, int64_t ld, int64_t step, int dtype,
-                                                   int wide, int flip, const double *parts, int num_parts, double eps,
+                                                   int flip, const double *parts, int num_parts, double eps,
                                                    float s, uint16_t *hi, uint16_t *lo, uint16_t *xt, int rows8, int cols8)
 {
     __shared__ double part[4];
     __shared__ float tile[64][65];
     const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;         // of X
     const int g_r0 = flip ? c0 : r0, g_c0 = flip ? r0 : c0;       // of G
-    // eight values a load where rows allow it, else one (64 a row)
     const int64_t from = blockIdx.z * step;
     float v[2][8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i, r = g_r0 + (t >> 3), c = g_c0 + 8 * (t & 7);
-        if (wide)
-            read_eight(G, from + (int64_t)r * ld + c, dtype, true, r < m ? n - c : 0, v[i]);
-        else
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int u = threadIdx.x + 256 * (8 * i + e), ur = g_r0 + (u >> 6), uc = g_c0 + (u & 63);
-                v[i][e] = ur < m && uc < n ? read_any(G, from + (int64_t)ur * ld + uc, dtype) : 0.0f;
-            }
+        read_eight(G, from + (int64_t)r * ld + c, dtype, r < m ? n - c : 0, v[i]);
     }
     double sum = 0.0;
     for (int i = threadIdx.x; i < num_parts; i += 256)
@@ -132,10 +124,8 @@ __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, 
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int u = threadIdx.x + 256 * (8 * i + e);
-            tile[wide ? t >> 3 : u >> 6][wide ? 8 * (t & 7) + e : u & 63] = (float)((double)v[i][e] * inv);
-        }
+        for (int e = 0; e < 8; ++e)
+            tile[t >> 3][8 * (t & 7) + e] = (float)((double)v[i][e] * inv);
     }
     __syncthreads();
     const int64_t at = (int64_t)blockIdx.z * rows8 * cols8;
@@ -148,14 +138,14 @@ __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, 
             for (int e = 0; e < 8; ++e)
                 y[e] = flip ? tile[c + e][r] : tile[r][c + e];
             two_halves(y, z);
-            store_run<OUT_FP16, 8, false>(hi, at + (int64_t)(r0 + r) * cols8 + c0 + c, y, true, 8);
-            store_run<OUT_FP16, 8, false>(lo, at + (int64_t)(r0 + r) * cols8 + c0 + c, z, true, 8);
+            store_run<OUT_FP16, 8, false>(hi, at + (int64_t)(r0 + r) * cols8 + c0 + c, y, 8);
+            store_run<OUT_FP16, 8, false>(lo, at + (int64_t)(r0 + r) * cols8 + c0 + c, z, 8);
         }
         if (xt && c0 + r < cols8 && r0 + c < rows8) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 y[e] = flip ? tile[r][c + e] : tile[c + e][r];
-            store_run<OUT_FP16, 8, false>(xt, at + (int64_t)(c0 + r) * rows8 + r0 + c, y, true, 8);
+            store_run<OUT_FP16, 8, false>(xt, at + (int64_t)(c0 + r) * rows8 + r0 + c, y, 8);
         }
     }
 }
@@ -404,20 +394,18 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != GEMM_OK)
         return st;
     const bool flip = m > n;
-    const int wide = (ldg * size_of(in_dtype)) % 16 == 0 && (g_step * size_of(in_dtype)) % 16 == 0 &&
-                     (uintptr_t)G % 16 == 0;
     for (const OrthoPlan &p : w.plan)
         for (int i = 0; i < p.count; ++i)
             if (p.part[i].blocks <= 0 || p.part[i].blocks >= kMaxBlocks)
                 return GEMM_ERR_UNSUPPORTED;
 
     hipLaunchKernelGGL(ortho_squares, dim3(w.parts, (unsigned)batch), dim3(256), 0, stream, G, (int)m, (int)n, ldg,
-                       g_step, in_dtype, wide, w.sums, w.counters, w.num_counters);
+                       g_step, in_dtype, w.sums, w.counters, w.num_counters);
     hipError_t e = hipGetLastError();
     const float s = 16.0f * std::exp2(std::round(0.5f * std::log2((float)w.k))), t = 64.0f;
     if (e == hipSuccess) {
         hipLaunchKernelGGL(ortho_begin, dim3((unsigned)cdiv(w.k8, 64), (unsigned)cdiv(w.r8, 64), (unsigned)batch), dim3(256),
-                           0, stream, G, (int)m, (int)n, ldg, g_step, in_dtype, wide, (int)flip, w.sums, w.parts, eps,
+                           0, stream, G, (int)m, (int)n, ldg, g_step, in_dtype, (int)flip, w.sums, w.parts, eps,
                            s, w.hi, w.lo, w.turned ? w.xt : nullptr, (int)w.r8, (int)w.k8);
         e = hipGetLastError();
     }
@@ -428,8 +416,6 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     last.ldu = (int)ldu;
     last.update_rows = (int)w.r, last.update_cols = (int)w.k;
     last.flip = flip;
-    const int64_t size = size_of(out_dtype);
-    last.update16 = (ldu * size) % 16 == 0 && (uintptr_t)U % 16 == 0 && (batch == 1 || (u_step * size) % 16 == 0);
     if (e == hipSuccess && steps == 0) {
         hipLaunchKernelGGL(ortho_copy, dim3((unsigned)cdiv(m * n, 256), (unsigned)batch), dim3(256), 0, stream, w.hi,
                            w.lo, 1.0f / s, (int)w.r8, (int)w.k8, last);

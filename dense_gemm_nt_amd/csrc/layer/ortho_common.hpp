@@ -36,7 +36,7 @@ struct OrthoArgs : KernelArgs {
     int64_t update_step;
     int update_dtype, ldu;
     int update_rows, update_cols;      // of X's shape; `flip`: stored transposed
-    int flip, update16;                // update16: its rows allow 16-byte stores
+    int flip;
 };
 
 // Tile t of the lower half: tile row tm has tm + 1 of them.
@@ -112,15 +112,14 @@ __device__ __forceinline__ void two_halves(float (&x)[8], float (&rest)[8])
 }
 
 // Eight consecutive values from element idx of an array of `dtype`, the first `count` of them.
-__device__ __forceinline__ void store_values(void *at, int64_t idx, int dtype, const float (&y)[8], bool wide,
-                                             int count)
+__device__ __forceinline__ void store_values(void *at, int64_t idx, int dtype, const float (&y)[8], int count)
 {
     if (dtype == OUT_FP32)
-        store_run<OUT_FP32, 8>(at, idx, y, wide, count);
+        store_run<OUT_FP32, 8>(at, idx, y, count);
     else if (dtype == OUT_FP16)
-        store_run<OUT_FP16, 8>(at, idx, y, wide, count);
+        store_run<OUT_FP16, 8>(at, idx, y, count);
     else
-        store_run<OUT_BF16, 8>(at, idx, y, wide, count);
+        store_run<OUT_BF16, 8>(at, idx, y, count);
 }
 
 // A wave's sums, 32 rows a pass through its LDS as FP32 (chunk c of row r at c ^ (r mod
@@ -141,7 +140,7 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
     // where the transposed values go: a square's other half, X's transposed copy, or a tall
     // update
     void *turned = nullptr;
-    int ldt = p.ldc, rows_t = p.M, cols_t = p.N, dtype_t = OUT_FP16, wide_t = 1;
+    int ldt = p.ldc, rows_t = p.M, cols_t = p.N, dtype_t = OUT_FP16;
     int64_t base_t = 0;
     if (p.mode != ORTHO_STEP) {
         if (p.half && r0 / p.half != c0 / p.half)
@@ -149,7 +148,7 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
     } else if (p.update) {
         if (p.flip)
             turned = p.update, base_t = b * p.update_step, ldt = p.ldu, rows_t = p.update_rows, cols_t = p.update_cols,
-            dtype_t = p.update_dtype, wide_t = p.update16;
+            dtype_t = p.update_dtype;
     } else if (p.xt) {
         turned = p.xt + b * p.c_step, ldt = p.ldt;
     }
@@ -208,12 +207,12 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         y[i] = p.alpha * y[i] - (m == n + i ? p.shift : 0.0f);
-                    store_run<OUT_FP16, 8, false>(C, idx, y, true, 8);
+                    store_run<OUT_FP16, 8, false>(C, idx, y, 8);
                 } else if (p.mode == ORTHO_POLY) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         y[i] = p.alpha * y[i] + p.beta * half_at(w[j], i);
-                    store_run<OUT_FP16, 8, false>(C, idx, y, true, 8);
+                    store_run<OUT_FP16, 8, false>(C, idx, y, 8);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -221,11 +220,11 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
                     if (!p.update) {
                         float z[8];
                         two_halves(y, z);
-                        store_run<OUT_FP16, 8, false>(C, idx, y, true, 8);
-                        store_run<OUT_FP16, 8, false>(lo, idx, z, true, 8);
+                        store_run<OUT_FP16, 8, false>(C, idx, y, 8);
+                        store_run<OUT_FP16, 8, false>(lo, idx, z, 8);
                     } else if (!turned && m < p.update_rows && n < p.update_cols) {
                         store_values(p.update, b * p.update_step + (int64_t)m * p.ldu + n, p.update_dtype, y,
-                                     p.update16 != 0, p.update_cols - n);
+                                     p.update_cols - n);
                     }
                 }
                 if (turned) {
@@ -248,7 +247,7 @@ __device__ __forceinline__ void store_ortho(const OrthoArgs &p, const f32x16 (&a
                     y[i] = *reinterpret_cast<const float *>(stage + r * ROWB + (((c >> 2) ^ (r & KEYM)) * 16) + (c & 3) * 4);
                 }
                 if (m < rows_t && n < cols_t)
-                    store_values(turned, base_t + (int64_t)n * ldt + m, dtype_t, y, wide_t != 0, rows_t - m);
+                    store_values(turned, base_t + (int64_t)n * ldt + m, dtype_t, y, rows_t - m);
             }
             wait_lgkmcnt0();
         }
