@@ -1,8 +1,11 @@
 """Compile-time resources of the layer library's kernels (no device work), as
 tests/test_kernel_resources.py reads them: no scratch, no spilled vector
 registers, registers that fit the occupancy the LDS allows; and the wait
-states before memory instructions that read scalars."""
+states before memory instructions that read scalars or store results."""
 import os
+import re
+import subprocess
+import tempfile
 
 import pytest
 
@@ -67,3 +70,35 @@ def test_lds_and_register_budget(kernels):
 @pytest.mark.skipif(not os.path.exists(k.OBJDUMP), reason="llvm-objdump not installed")
 def test_scalars_are_settled_before_loads(lib):
     r.test_scalars_are_settled_before_loads(lib)
+
+
+@pytest.mark.skipif(not os.path.exists(k.OBJDUMP), reason="llvm-objdump not installed")
+def test_waits_before_results_are_stored(lib):
+    """No LDS or memory store stands within the wait states of a matrix instruction whose result
+    it stores (text order, every kernel)."""
+    checked = 0
+    for co in k._code_objects(lib):
+        with tempfile.TemporaryDirectory() as d:
+            path = os.path.join(d, "co.o")
+            open(path, "wb").write(co)
+            text = subprocess.run([k.OBJDUMP, "-d", "--no-show-raw-insn", path], check=True, capture_output=True,
+                                  text=True).stdout
+        recent = []
+        for line in text.splitlines():
+            s = line.split("//")[0].strip()
+            if re.match(r"^[0-9a-f]+ <(\S+)>:$", line):
+                recent = []
+                continue
+            if not s:
+                continue
+            op = s.split()[0]
+            args = s[len(op):]
+            recent = [(left - 1, regs) for left, regs in recent if left > 1]
+            if op.startswith("v_mfma"):
+                recent.append((20, r._registers(args.split(",")[0])))      # 16 passes and 3, at most
+                checked += 1
+            elif op == "s_nop":
+                recent = [(left - int(args), regs) for left, regs in recent if left > int(args)]
+            elif re.match(r"(ds_write|ds_store|global_store|buffer_store)", op):
+                assert not [regs for _, regs in recent if regs & r._registers(args)], s
+    assert checked > 0
