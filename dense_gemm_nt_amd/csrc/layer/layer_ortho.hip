@@ -119,7 +119,9 @@ __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, 
     double sum = 0.0;
     for (int i = threadIdx.x; i < num_parts; i += 256)
         sum += parts[blockIdx.z * num_parts + i];
-    const double inv = (double)s / (__builtin_sqrt(block_sum(sum, part)) + eps);
+    // (an infinity alone would leave the other values 0: what is not finite takes the whole matrix)
+    const double squares = block_sum(sum, part);
+    const double inv = __builtin_isfinite(squares) ? (double)s / (__builtin_sqrt(squares) + eps) : __builtin_nan("");
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = threadIdx.x + 256 * i;
