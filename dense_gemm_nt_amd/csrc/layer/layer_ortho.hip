@@ -152,23 +152,25 @@ __global__ __launch_bounds__(256) void ortho_begin(const void *G, int m, int n, 
     }
 }
 
-// The update of no steps at all: X as it begins.
+// The update of no steps at all: X as it begins.  (A launch has fewer than 2^32 threads:
+// kCopyBlocks a matrix at most, which take its values in turn.)
+constexpr int64_t kCopyBlocks = (int64_t)1 << 20;
+
 __global__ __launch_bounds__(256) void ortho_copy(const uint16_t *hi, const uint16_t *lo, float unit, int rows8, int cols8,
                                                   OrthoArgs p)
 {
     const int m = p.flip ? p.update_cols : p.update_rows, n = p.flip ? p.update_rows : p.update_cols;
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (t >= (int64_t)m * n)
-        return;
-    const int r = (int)(t / n), c = (int)(t - (int64_t)r * n);
-    const int64_t i = (int64_t)blockIdx.y * rows8 * cols8 + (p.flip ? (int64_t)c * cols8 + r : (int64_t)r * cols8 + c);
-    const float v = unit * (from_bits16(IN_FP16, hi[i]) + from_bits16(IN_FP16, lo[i]));
-    const int64_t at = blockIdx.y * p.update_step + (int64_t)r * p.ldu + c;
-    if (p.update_dtype == OUT_FP32)
-        static_cast<float *>(p.update)[at] = v;
-    else
-        static_cast<uint16_t *>(p.update)[at] =
-            (uint16_t)(p.update_dtype == OUT_BF16 ? to_bits16<OUT_BF16>(v) : to_bits16<OUT_FP16>(v));
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < (int64_t)m * n; t += (int64_t)gridDim.x * 256) {
+        const int r = (int)(t / n), c = (int)(t - (int64_t)r * n);
+        const int64_t i = (int64_t)blockIdx.y * rows8 * cols8 + (p.flip ? (int64_t)c * cols8 + r : (int64_t)r * cols8 + c);
+        const float v = unit * (from_bits16(IN_FP16, hi[i]) + from_bits16(IN_FP16, lo[i]));
+        const int64_t at = blockIdx.y * p.update_step + (int64_t)r * p.ldu + c;
+        if (p.update_dtype == OUT_FP32)
+            static_cast<float *>(p.update)[at] = v;
+        else
+            static_cast<uint16_t *>(p.update)[at] =
+                (uint16_t)(p.update_dtype == OUT_BF16 ? to_bits16<OUT_BF16>(v) : to_bits16<OUT_FP16>(v));
+    }
 }
 
 namespace {
@@ -419,8 +421,8 @@ gemm_status_t gemm_run_orthogonalize(const void *G, void *U, int64_t batch, int6
     last.update_rows = (int)w.r, last.update_cols = (int)w.k;
     last.flip = flip;
     if (e == hipSuccess && steps == 0) {
-        hipLaunchKernelGGL(ortho_copy, dim3((unsigned)cdiv(m * n, 256), (unsigned)batch), dim3(256), 0, stream, w.hi,
-                           w.lo, 1.0f / s, (int)w.r8, (int)w.k8, last);
+        hipLaunchKernelGGL(ortho_copy, dim3((unsigned)std::min(cdiv(m * n, 256), kCopyBlocks), (unsigned)batch), dim3(256), 0,
+                           stream, w.hi, w.lo, 1.0f / s, (int)w.r8, (int)w.k8, last);
         e = hipGetLastError();
     }
     const int64_t x_step = w.r8 * w.k8, sq_step = w.r8 * w.r8;

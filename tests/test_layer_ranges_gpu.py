@@ -4,6 +4,7 @@ import math
 import pytest
 import torch
 
+from oracle import layer as o
 from tests.rows_util import randn
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +26,34 @@ def test_an_update_of_what_is_not_finite(steps, value):
         got = g.orthogonalize(S.to(DEV), steps=steps, out_dtype=FP32).cpu()
         assert bool(got[1].isnan().all())
         assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+
+
+# ------------------------------------------------- more values than a launch has threads
+
+@pytest.mark.parametrize("M,K", [((1 << 26) + 3, 8), ((1 << 22) + 5, 24), ((1 << 20) + 5, 2056)])
+def test_quantize_rows_of_more_than_a_launch(M, K):
+    """Past 2^32 threads at a thread a value or so, and past the blocks of one launch."""
+    import dense_gemm_nt_amd as g
+    rows = randn(257, K, seed=1, dtype=BF16).to(DEV)
+    x = rows.repeat(-(-M // 257), 1)[:M]
+    codes, scale = g.quantize_int8(x)
+    rc, rs = o.quantize(rows.cpu())
+    rc, rs = rc.to(DEV), rs.to(DEV)
+    whole = M // 257 * 257
+    assert bool((codes[:whole].view(-1, 257, K) == rc).all()) and bool((scale[:whole].view(-1, 257) == rs).all())
+    assert torch.equal(codes[whole:], rc[:M - whole]) and torch.equal(scale[whole:], rs[:M - whole])
+
+
+def test_update_of_more_values_than_a_launch():
+    """No steps: the scaled matrix itself, 2^32 values and some."""
+    import dense_gemm_nt_amd as g
+    m, n = 4097, 1 << 20
+    G = torch.zeros(m, n, dtype=BF16, device=DEV)
+    G[0, 0], G[m - 1, n - 1], G[2048, 77], G[m - 1, 0] = 1.0, -2.0, 2.0, 4.0      # of norm 5
+    U = g.orthogonalize(G, steps=0, eps=0.0, out_dtype=FP32)
+    want = {(0, 0): 0.2, (m - 1, n - 1): -0.4, (2048, 77): 0.4, (m - 1, 0): 0.8}
+    for at, v in want.items():
+        assert abs(float(U[at]) - v) <= 2.0 ** -21 * abs(v), at
+        U[at] = 0.0
+    for i in range(0, m, 512):
+        assert not bool(U[i:i + 512].any())
