@@ -22,7 +22,8 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 // Input formats: the 16-bit ones, and the FP8 pairs IN_F8 + 2 * (A is E5M2) +
 // (B is E5M2), each operand E4M3 or E5M2 (OCP 8-bit floating point).  IN_I8: 8-bit
 // integers, two to a 16-bit element of the tiles (an MFMA's fragment is 16 bytes of a row of
-// either), whose accumulators hold INT32 sums in their bits until GNT_EXT_ACC converts them.
+// either), whose accumulators and K splits' partials hold INT32 sums in their bits until the sum is
+// whole (GNT_EXT_ACC, GNT_EXT_SUM).
 enum : int { IN_BF16 = 0, IN_FP16 = 1, IN_F8 = 2, IN_I8 = 6 };
 enum : int { OUT_BF16 = 0, OUT_FP16 = 1, OUT_FP32 = 2 };
 
@@ -315,6 +316,12 @@ __device__ __forceinline__ void map_block_split_minor(int bid, int G, int tiles_
     tile_order(t, tiles_m, tiles_n, group_m, tm, tn);
 }
 
+// The sum of two INT32 values that FP32 registers hold in their bits.
+__device__ __forceinline__ float add_bits(float a, float b)
+{
+    return __builtin_bit_cast(float, __builtin_bit_cast(int, a) + __builtin_bit_cast(int, b));
+}
+
 // Two K splits reduced inside the GEMM kernel ("A Blackwell GEMM by Hand in
 // CuTe DSL", section 9: split-K for decode, here with the partials combined by
 // the two CTAs themselves instead of a second pass).  Each split of tile t
@@ -330,7 +337,8 @@ __device__ __forceinline__ void map_block_split_minor(int bid, int G, int tiles_
 // which blocks are resident.  `flag` is a word of LDS no wave is using; every
 // wave of the block calls this with its own accumulators (NW waves, G register
 // groups of four per lane).
-template <int NW, int FN, int FM>
+// (INT: the values are INT32 sums in FP32 registers, and so are the partials.)
+template <int NW, bool INT = false, int FN, int FM>
 __device__ __forceinline__ bool splitk2_arrive(const KernelArgs &p, f32x16 (&acc)[FN][FM], int tile, int split,
                                                int wave, int lane, uint32_t *flag)
 {
@@ -377,8 +385,17 @@ __device__ __forceinline__ bool splitk2_arrive(const KernelArgs &p, f32x16 (&acc
                 const f32x4 o = __builtin_bit_cast(
                     f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, vo + g * 1024u, other, SC1));
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[fn][fm][4 * q + e] = 0.0f + (acc[fn][fm][4 * q + e] + o[e]);
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (INT) {
+                        // (held where it stands: integer sums sink to their use, past the
+                        // loads after them, and the registers do not suffice)
+                        float sum = add_bits(acc[fn][fm][4 * q + e], o[e]);
+                        asm volatile("" : "+v"(sum));
+                        acc[fn][fm][4 * q + e] = sum;
+                    } else {
+                        acc[fn][fm][4 * q + e] = 0.0f + (acc[fn][fm][4 * q + e] + o[e]);
+                    }
+                }
                 // eight loads in flight at a time: enough to cover the latency,
                 // few enough registers to keep every accumulator in place
                 if ((g & 7) == 7)
@@ -399,8 +416,9 @@ __device__ __forceinline__ bool splitk2_arrive(const KernelArgs &p, f32x16 (&acc
 // in flight at a time.  That is the order, hence the bits, of the second pass
 // (splitk_sum), whichever split came last.  It resets the counter for the
 // next call and returns true; the others return false and are done.  No block
-// waits for another.  `flag` is a word of LDS no wave is using.
-template <int NW, int FN, int FM>
+// waits for another.  `flag` is a word of LDS no wave is using.  (INT: INT32 sums
+// and partials, as in splitk2_arrive.)
+template <int NW, bool INT = false, int FN, int FM>
 __device__ __forceinline__ bool splitk_arrive(const KernelArgs &p, f32x16 (&acc)[FN][FM], int tile, int split,
                                               int wave, int lane, uint32_t *flag)
 {
@@ -465,7 +483,14 @@ __device__ __forceinline__ bool splitk_arrive(const KernelArgs &p, f32x16 (&acc)
                         const int g = (fn * FM + fm) * 4 + q;
                         const f32x4 own = {acc[fn][fm][4 * q], acc[fn][fm][4 * q + 1], acc[fn][fm][4 * q + 2],
                                            acc[fn][fm][4 * q + 3]};
-                        tot[g] += s == split ? own : buf[c][g];
+                        const f32x4 part = s == split ? own : buf[c][g];
+                        if constexpr (INT) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                tot[g][e] = add_bits(tot[g][e], part[e]);
+                        } else {
+                            tot[g] += part;
+                        }
                     }
         }
     }

@@ -12,6 +12,7 @@
 //   GNT_EXT_ACC(p, acc, r0, c0, split, lane)  adds to a wave's accumulators,
 //                         whose block starts at row r0 and column c0, once the
 //                         main loop is done and before anything leaves them
+//   GNT_EXT_SUM(p, acc, r0, c0, lane)  changes the sum of K splits after its reduction in the kernel
 //   GNT_EXT_MAP(p, tm, tn, split)  in place of the block map, K splits among it; false where
 //                         the block has no tile; may move p.A and p.B
 //   GNT_EXT_TILE(p, tm, tn)  the tile's number in the launch (its partials and counter)
@@ -35,6 +36,9 @@
 #endif
 #ifndef GNT_EXT_ACC
 #define GNT_EXT_ACC(p, acc, r0, c0, split, lane)
+#endif
+#ifndef GNT_EXT_SUM
+#define GNT_EXT_SUM(p, acc, r0, c0, lane)
 #endif
 #ifndef GNT_EXT_AHEAD
 #define GNT_EXT_AHEAD 0

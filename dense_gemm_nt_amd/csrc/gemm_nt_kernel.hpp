@@ -297,10 +297,11 @@ __global__ __launch_bounds__(WM *WN * 64, 1) void GNT_EXT_KERNEL(gemm_nt_kernel)
     // has no registers for the reduction's buffers.
     if constexpr (STAGES > 2) {
         if (p.inreduce) {
-            if (!splitk_arrive<NWAVES, FN, FM>(p, acc, tile, split, wave, lane,
-                                               reinterpret_cast<uint32_t *>(smem)))
+            if (!splitk_arrive<NWAVES, IN == IN_I8>(p, acc, tile, split, wave, lane,
+                                                    reinterpret_cast<uint32_t *>(smem)))
                 return;
             p.splits = 1;
+            GNT_EXT_SUM(p, acc, m0 + wave_m * WTM, n0 + wave_n * WTN, lane)
         }
     }
 

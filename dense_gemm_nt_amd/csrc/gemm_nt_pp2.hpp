@@ -547,10 +547,11 @@ __global__ __launch_bounds__(512, 1) void GNT_EXT_KERNEL(gemm_nt_pp2)(GNT_EXT_AR
                 // two K splits: the second to arrive holds the sum and stores it
                 // as an unsplit tile (the flag lives in unit 8, past the staging
                 // area)
-                if (!splitk2_arrive<8, FN, FM>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
-                                               reinterpret_cast<uint32_t *>(smem + 8 * UNIT)))
+                if (!splitk2_arrive<8, IN == IN_I8>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
+                                                    reinterpret_cast<uint32_t *>(smem + 8 * UNIT)))
                     return;
                 p.splits = 1;
+                GNT_EXT_SUM(p, acc, m0 + wm0, n0 + wn0, lane)
             }
         }
         uint8_t *stage = smem + wave * 16384;

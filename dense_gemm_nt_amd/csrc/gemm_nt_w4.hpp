@@ -398,10 +398,11 @@ __global__ __launch_bounds__(256, 1) void GNT_EXT_KERNEL(gemm_nt_w4)(GNT_EXT_ARG
         // two K splits: the second to arrive holds the sum and stores it as an
         // unsplit tile
         wait_vmcnt<0>();
-        if (!splitk2_arrive<4, FN, FM>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
-                                       reinterpret_cast<uint32_t *>(smem)))
+        if (!splitk2_arrive<4, IN == IN_I8>(p, acc, GNT_EXT_TILE(p, tm, tn), split, wave, lane,
+                                            reinterpret_cast<uint32_t *>(smem)))
             return;
         p.splits = 1;
+        GNT_EXT_SUM(p, acc, m0 + wm * 128, n0 + wn * (BN / 2), lane)
     }
     // Epilogue.  Every wave is past its last fragment read and every load has
     // landed; after the barrier the ring is free for staging (32 KB per wave).

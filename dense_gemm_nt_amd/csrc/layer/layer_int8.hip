@@ -2,7 +2,8 @@
 //
 // y[m][n] = s_m t_n sum_k q[m][k] w[n][k].  v_mfma_i32_32x32x32_i8 takes 16 bytes of a row per
 // lane, as the 16-bit MFMA does, and sums exactly in 32 bits, so the tiles run as they are on
-// K / 2 elements of 16 bits; the scales come in when the sum is whole (int8_scale).
+// K / 2 elements of 16 bits; the scales come in when the sum is whole, K splits and all
+// (int8_scale, int8_sum).
 #include "layer_host.hpp"
 #include "layer_launch.hpp"
 
@@ -210,6 +211,41 @@ __global__ __launch_bounds__(256) void int8_few(Int8Args p, int K, int lda, int 
     store_result<OUT>(p, 0, m, n0, y);
 }
 
+// The second pass of a product split along K (tiles whose splits are not summed in the
+// kernel): the integer partials, the scales as int8_scale has them, the epilogue.
+template <int OUT>
+__global__ __launch_bounds__(256) void int8_sum(Int8Args p)
+{
+    const int nvec = (p.N + 3) >> 2;
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= (int64_t)p.M * nvec)
+        return;
+    const int m = (int)(t / nvec);
+    const int n = (int)(t - (int64_t)m * nvec) * 4;
+    const int valid = min(p.N - n, 4);
+    const int64_t plane = (int64_t)p.M * p.N;
+    const int *src = reinterpret_cast<const int *>(p.partials) + (int64_t)m * p.N + n;
+    i32x4 sum = {0, 0, 0, 0};
+    if ((p.N & 3) == 0) {
+        for (int s = 0; s < p.splits; ++s)
+            sum += *reinterpret_cast<const i32x4 *>(src + s * plane);
+    } else {
+        for (int s = 0; s < p.splits; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < valid)
+                    sum[i] += src[s * plane + i];
+    }
+    const float sa = p.sa[(int64_t)m * p.sa_step];
+    f32x4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        y[i] = (static_cast<float>(sum[i]) * sa) * p.sb[(int64_t)min(n + i, p.N - 1) * p.sb_step];
+    if (p.epi)
+        y = epilogue4<OUT>(p, m, n, y, valid);
+    store4<OUT>(p.C, (int64_t)m * p.ldc + n, y, p.vec_store != 0, valid);
+}
+
 namespace {
 
 gemm_status_t check_sizes(int64_t M, int64_t N, int64_t K)
@@ -403,14 +439,13 @@ gemm_status_t gemm_run_int8(const void *A, const void *B, void *C, int64_t M, in
         }
         e = fn(a, (unsigned)p.grid, stream);
         if (e == hipSuccess && p.splits > 1 && !p.inreduce) {
-            const KernelArgs &k = a;
             const unsigned grid = (unsigned)cdiv(q.rows * ((q.cols + 3) / 4), 256);
             if (out_dtype == GEMM_BF16)
-                hipLaunchKernelGGL(splitk_sum<OUT_BF16>, dim3(grid), dim3(256), 0, stream, k);
+                hipLaunchKernelGGL(int8_sum<OUT_BF16>, dim3(grid), dim3(256), 0, stream, a);
             else if (out_dtype == GEMM_FP16)
-                hipLaunchKernelGGL(splitk_sum<OUT_FP16>, dim3(grid), dim3(256), 0, stream, k);
+                hipLaunchKernelGGL(int8_sum<OUT_FP16>, dim3(grid), dim3(256), 0, stream, a);
             else
-                hipLaunchKernelGGL(splitk_sum<OUT_FP32>, dim3(grid), dim3(256), 0, stream, k);
+                hipLaunchKernelGGL(int8_sum<OUT_FP32>, dim3(grid), dim3(256), 0, stream, a);
             e = hipGetLastError();
         }
     }

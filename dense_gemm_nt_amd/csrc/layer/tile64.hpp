@@ -131,7 +131,7 @@ __global__ __launch_bounds__(256, 2) void tile64(Args p)
     wg_barrier();                          // the ring is idle
     Hooks::template add<IN, OUT>(p, acc, m0 + wm, n0 + wn, split, lane);
     if (p.inreduce) {
-        if (!splitk_arrive<4, 1, 1>(p, acc, Hooks::tile(p, tm, tn), split, wave, lane, reinterpret_cast<uint32_t *>(smem)))
+        if (!splitk_arrive<4>(p, acc, Hooks::tile(p, tm, tn), split, wave, lane, reinterpret_cast<uint32_t *>(smem)))
             return;
         p.splits = 1;
     }

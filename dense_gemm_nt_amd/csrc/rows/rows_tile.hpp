@@ -187,7 +187,7 @@ __global__ __launch_bounds__(256, 2) void rows_tile(Args p)
         Hooks::template add<IN, OUT>(p, acc, m0 + wm, n0 + wn, split, lane);
         if (p.inreduce) {
             // (the ring is behind the barrier's last reader once the partials are out)
-            if (!splitk_arrive<4, 2, 2>(p, acc, Hooks::tile(p, tm, tn), split, wave, lane,
+            if (!splitk_arrive<4>(p, acc, Hooks::tile(p, tm, tn), split, wave, lane,
                                         reinterpret_cast<uint32_t *>(smem)))
                 return;
             p.splits = 1;

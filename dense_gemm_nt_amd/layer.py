@@ -172,8 +172,8 @@ def gemm_int8(A, B, scale_a, scale_b, out=None, out_dtype=None, alpha=1.0, beta=
               bias_along="n", activation="none"):
     """C = act(alpha * y + beta * C_old + bias), y[m, n] = scale_a[m] scale_b[n] (A[m] . B[n]), for
     int8 A [M, K] (quantize_int8's codes) and B [N, K], scales float32 [M] and [N] (or one
-    value each): [M, N] of out_dtype (default bfloat16).  The integer sums (of a K split,
-    each split's) are exact.  K a multiple of 16 below 2^17; the epilogue as gemm_nt's."""
+    value each): [M, N] of out_dtype (default bfloat16).  The integer sums are exact, and taken
+    to FP32 once.  K a multiple of 16 below 2^17; the epilogue as gemm_nt's."""
     import torch
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("A must be [M, K] and B [N, K], got %s and %s" % (tuple(A.shape), tuple(B.shape)))

@@ -86,8 +86,8 @@ gemm_status_t gemm_run_quantize_int8(const void *X, void *codes, float *scale, i
 
 /* C = act(alpha y + beta C_old + bias), y[m][n] = scale_a[m] scale_b[n] sum_k A[m][k]
  * B[n][k], A [M][K] and B [N][K] INT8 (-128 .. 127), C [M][N] of out_dtype; epi as gemm_run_ex's
- * (NULL: the identity).  The sum is exact (INT32; of a K split, each split's), taken to
- * FP32, multiplied by scale_a[m] and then by scale_b[n].
+ * (NULL: the identity).  The sum is exact (INT32, K splits and all), taken to FP32, multiplied
+ * by scale_a[m] and then by scale_b[n].
  *   scales_a  M, or 1: one scale for all rows;  scales_b  N, or 1
  *   K % 16 == 0, K < 2^17 */
 gemm_status_t gemm_int8_workspace(int64_t M, int64_t N, int64_t K, int64_t *bytes);

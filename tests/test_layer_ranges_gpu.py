@@ -6,10 +6,44 @@ import torch
 
 from oracle import layer as o
 from tests.rows_util import randn
+from tests.test_layer_int8_gpu import SIZES as INT8_SIZES
+from tests.test_layer_int8_gpu import _codes, _scales
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ------------------------------------------------------------ the integer product
+
+def _exact(A, B, sa, sb):
+    """The definition: the exact sum to FP32, times scale_a, times scale_b."""
+    s = A.double() @ B.double().t()                      # (below 2^31: exact)
+    return s.float() * sa[:, None] * sb
+
+
+@pytest.mark.parametrize("M,N,K", INT8_SIZES)
+def test_int8_is_the_exact_sum_whatever_the_splits(M, N, K):
+    import dense_gemm_nt_amd as g
+    A, B, sa, sb = _codes(M, K, seed=1), _codes(N, K, seed=2), _scales(M, 3), _scales(N, 4)
+    y = g.gemm_int8(A.to(DEV), B.to(DEV), sa.to(DEV), sb.to(DEV), out_dtype=FP32)
+    assert torch.equal(y.cpu(), _exact(A, B, sa, sb))
+
+
+@pytest.mark.parametrize("M", [1, 3, 70, 200, 300])
+def test_int8_splits_of_a_sum_that_cancels(M):
+    """The halves of K cancel up to a few codes; with scales of 1e29 either half is past FP32's end."""
+    import dense_gemm_nt_amd as g
+    N, K = 300, 16384
+    A = torch.full((M, K), 127, dtype=torch.int8)
+    B = torch.full((N, K), 127, dtype=torch.int8)
+    B[:, K // 2:] = -127
+    B[:, 5] = _codes(N, seed=1)
+    sa, sb = torch.full((M,), 1e29), torch.full((N,), 100.0)
+    y = g.gemm_int8(A.to(DEV), B.to(DEV), sa.to(DEV), sb.to(DEV), out_dtype=FP32)
+    assert bool(torch.isfinite(y).all()) and torch.equal(y.cpu(), _exact(A, B, sa, sb))
+    y = g.gemm_int8(A.to(DEV), B.to(DEV), torch.full((1,), math.inf, device=DEV), sb.to(DEV), out_dtype=FP32)
+    assert torch.equal(y.cpu().nan_to_num(nan=0.5), _exact(A, B, torch.full((M,), math.inf), sb).nan_to_num(nan=0.5))
 
 
 # ------------------------------------------------------------------- the update
