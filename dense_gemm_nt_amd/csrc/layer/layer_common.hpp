@@ -203,7 +203,7 @@ __device__ __forceinline__ void store_gated(const PairedArgs &p, const f32x16 (&
     }
 }
 
-// 2^-floor(log2 max|dh|) as an exponent, from the partial maxima (every lane's result is the
+// 2^-floor(log2 max|dh|) as an exponent, from the finite values' partial maxima (every lane's result is the
 // same): what FP16 gradients of the pre-activations are multiplied by, so that they
 // neither end below fp16's smallest step nor lose bits there whatever the scale of dh.
 __device__ __forceinline__ int most_shift(const uint32_t *most, int lane)
@@ -216,7 +216,7 @@ __device__ __forceinline__ int most_shift(const uint32_t *most, int lane)
     for (int o = 32; o > 0; o >>= 1)
         b = max(b, (uint32_t)__shfl_xor((int)b, o));
     b = __builtin_amdgcn_readfirstlane(b);
-    if (b == 0 || b >= 0x7c00u)                       // nothing, or not finite
+    if (b == 0)
         return 0;
     return b >= 0x400u ? 15 - (int)(b >> 10) : 24 - (31 - __builtin_clz(b));
 }

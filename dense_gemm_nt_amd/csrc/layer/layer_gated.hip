@@ -24,12 +24,15 @@
 
 namespace gnt {
 
-// The partial maxima of |dh| (16-bit patterns without the sign, which order as the values do).
+// The partial maxima of |dh| (16-bit patterns without the sign, which order as the values do), of
+// its finite values: what is not finite has its own row and column only, and no say in the rest's
+// scale.
 __global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int F, int ld, uint32_t *most)
 {
     __shared__ uint32_t part[4];
     uint32_t b = 0;
-    auto take = [&](uint32_t w) { b = max(b, max(w & 0x7fffu, (w >> 16) & 0x7fffu)); };
+    auto take1 = [&](uint32_t v) { b = max(b, v < 0x7c00u ? v : 0u); };
+    auto take = [&](uint32_t w) { take1(w & 0x7fffu), take1((w >> 16) & 0x7fffu); };
     const int64_t step = gridDim.x;
     for (int64_t m = blockIdx.x; m < M; m += step) {
         const uint16_t *row = x + m * ld;

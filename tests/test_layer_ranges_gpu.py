@@ -6,12 +6,37 @@ import torch
 
 from oracle import layer as o
 from tests.rows_util import randn
+from tests.test_layer_gated_gpu import _operands
 from tests.test_layer_int8_gpu import SIZES as INT8_SIZES
 from tests.test_layer_int8_gpu import _codes, _scales
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ------------------------------------------------------------------ FP16 gradients
+
+@pytest.mark.parametrize("std", [1e-6, 1.0, 1e4])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_fp16_gradients_beside_a_value_that_is_not_finite(std, value):
+    """A NaN or infinity in dh reaches its own row of dx and its own column's weights, and leaves
+    every other bit as it was."""
+    import dense_gemm_nt_amd as g
+    M, F, K = 70, 136, 72
+    x, Wg, Wu = _operands(M, F, K, FP16)
+    dh = randn(M, F, seed=4, std=std).clamp(-4 * std, 4 * std).to(FP16)
+    bad = dh.clone()
+    bad[5, 20] = value
+    plain = dh.clone()
+    plain[5, 20] = 0.0
+    kw = dict(activation="silu", grad_dtype=FP32, dx_dtype=FP32)
+    dx, a, b = (t.cpu() for t in g.gemm_gated_backward(*(t.to(DEV) for t in (plain, x, Wg, Wu)), **kw))
+    bx, ba, bb = (t.cpu() for t in g.gemm_gated_backward(*(t.to(DEV) for t in (bad, x, Wg, Wu)), **kw))
+    rows, cols = [m for m in range(M) if m != 5], [f for f in range(F) if f != 20]
+    assert torch.equal(bx[rows], dx[rows]) and not bool(torch.isfinite(bx[5]).any())
+    assert torch.equal(ba[cols], a[cols]) and torch.equal(bb[cols], b[cols])
+    assert not bool(torch.isfinite(ba[20]).any()) and not bool(torch.isfinite(bb[20]).any())
 
 
 # ------------------------------------------------------------ the integer product
