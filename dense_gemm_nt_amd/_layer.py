@@ -12,8 +12,9 @@ GATES = {"relu": 1, "gelu": 2, "silu": 3}
 
 # Every symbol include/gemm_layer.h declares.
 EXPORTS = ("gemm_gated_workspace", "gemm_run_gated", "gemm_gated_backward_workspace",
-           "gemm_run_gated_backward", "gemm_run_quantize_int8", "gemm_int8_workspace", "gemm_run_int8",
-           "gemm_orthogonalize_workspace", "gemm_run_orthogonalize")
+           "gemm_gated_backward_workspace_of", "gemm_run_gated_backward", "gemm_run_quantize_int8",
+           "gemm_int8_workspace", "gemm_run_int8", "gemm_orthogonalize_workspace",
+           "gemm_run_orthogonalize")
 
 _lib = None
 
@@ -33,6 +34,7 @@ def lib():
     L.gemm_gated_workspace.argtypes = [i64] * 3 + [out64]
     L.gemm_run_gated.argtypes = [vp] * 4 + [i64] * 7 + [ci] * 3 + [vp, i64, vp]
     L.gemm_gated_backward_workspace.argtypes = [i64] * 3 + [out64]
+    L.gemm_gated_backward_workspace_of.argtypes = [i64] * 3 + [ci, out64]
     L.gemm_run_gated_backward.argtypes = [vp] * 7 + [i64] * 8 + [ci] * 4 + [vp, i64, vp]
     L.gemm_run_quantize_int8.argtypes = [vp] * 3 + [i64] * 4 + [ci, vp]
     L.gemm_int8_workspace.argtypes = [i64] * 3 + [out64]

@@ -5,7 +5,7 @@
 
 #define GNT_EXT_KERNEL(name) name##_gated_dw
 #define GNT_EXT_ARGS PairedArgs
-#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) unscale<IN>(p, acc, lane);
+#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) unscale<IN, true>(p, acc, r0, lane);
 #define GNT_EXT_STORE(p, acc, r0, c0, stage, lane) store_paired_rows<OUT>(p, acc, r0, c0, stage, lane)
 #include "../gemm_nt_pp2.hpp"
 

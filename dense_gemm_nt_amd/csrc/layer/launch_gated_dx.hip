@@ -8,7 +8,7 @@
 #define GNT_EXT_COLS(p) (p.cols)
 #define GNT_EXT_B(p, w) ((w) ? p.B2 : p.B)
 #define GNT_EXT_LDB(p, w) ((w) ? p.ldb2 : p.ldb)
-#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) unscale<IN>(p, acc, lane);
+#define GNT_EXT_ACC(p, acc, r0, c0, split, lane) unscale<IN, false>(p, acc, r0, lane);
 #include "../gemm_nt_pp2.hpp"
 
 namespace gnt {

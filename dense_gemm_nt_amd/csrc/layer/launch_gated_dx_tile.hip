@@ -9,9 +9,9 @@ template <>
 struct TileHooks<PairedArgs> : PlanTile<PairedArgs> {
     static constexpr bool kPaired = true;
     template <int IN, int OUT, int FN, int FM>
-    static __device__ __forceinline__ void add(PairedArgs &p, f32x16 (&acc)[FN][FM], int, int, int, int lane)
+    static __device__ __forceinline__ void add(PairedArgs &p, f32x16 (&acc)[FN][FM], int r0, int, int, int lane)
     {
-        unscale<IN>(p, acc, lane);
+        unscale<IN, false>(p, acc, r0, lane);
     }
     static __device__ __forceinline__ const uint16_t *b(const PairedArgs &p, int w) { return w ? p.B2 : p.B; }
     static __device__ __forceinline__ int ldb(const PairedArgs &p, int w) { return w ? p.ldb2 : p.ldb; }

@@ -36,12 +36,22 @@ struct PairedArgs : KernelArgs {
     int cols;
     const uint16_t *dh;         // backward: the block's output gradient [M][cols]
     int lddh;
-    const uint32_t *most;       // FP16 backward: kMostParts partial maxima of |dh| (its bits)
-    void *C2;                   // weight gradients: C is the gate's, C2 the up projection's
+    // FP16 backward, what the units of rows and columns are made of (gate_units): the finite |dh|'s
+    // largest bits of each row [M] and of each chunk of rows' columns [col_chunks][col_step], and
+    // kNormParts partial maxima of the squared norms of X's rows and of the weights' rows; and the
+    // units' reciprocals [M] and [cols], which the sums' gradients leave for the products over
+    // them (null: no units)
+    const uint16_t *row_most;
+    const uint16_t *col_most;
+    int col_chunks, col_step;
+    const float *norms;
+    float *row_back, *col_back;
+    void *C2;                   // weight gradients: C is the gate's, C2 the up projection's; FP16
+                                // gradients of the sums: C in its rows' units (or null), C2 its columns'
     ClearList clear;            // gradients of the sums: cleared on the way
 };
 
-constexpr int kMostParts = 256;
+constexpr int kNormParts = 512;
 
 // An opaque copy of the lane id: what an epilogue derives from it is computed there, and
 // not held across the main loop, whose registers are all taken.
@@ -203,22 +213,52 @@ __device__ __forceinline__ void store_gated(const PairedArgs &p, const f32x16 (&
     }
 }
 
-// 2^-floor(log2 max|dh|) as an exponent, from the finite values' partial maxima (every lane's result is the
-// same): what FP16 gradients of the pre-activations are multiplied by, so that they
-// neither end below fp16's smallest step nor lose bits there whatever the scale of dh.
-__device__ __forceinline__ int most_shift(const uint32_t *most, int lane)
+// FP16 gradients of the pre-activations, in units.  |dg| = |dh u act'(g)| and |du| = |dh act(g)| are
+// at most |dh| B, B = 1.13 max ||x_m|| max ||w_f|| (Cauchy and Schwarz; act' is at most 1.129, and
+// |act(g)| at most |g|).  So an exponent of 13 - floor(log2 max|dh|) - floor(log2 B) keeps them below
+// 2^15 whatever they are, of each row with its own max|dh| for dx and of each column with its
+// own for the weights' gradients, as the sums that they enter are apart in the same way: neither a
+// large sum nor a large row or entry of dh takes bits from the rest.  B is above typical sums of
+// K products by sqrt(K) / 3 or so, 4 of the 29 binades that have all their bits.
+__device__ __forceinline__ int bound_exponent(const float *norms, int lane)
+{
+    float x = 0.0f, w = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kNormParts; j += 256) {
+        const f32x4 px = *reinterpret_cast<const f32x4 *>(norms + j + 4 * lane);
+        const f32x4 pw = *reinterpret_cast<const f32x4 *>(norms + kNormParts + j + 4 * lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x = fmaxf(x, px[i]), w = fmaxf(w, pw[i]);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        x = fmaxf(x, __shfl_xor(x, o));
+        w = fmaxf(w, __shfl_xor(w, o));
+    }
+    // (1.13^2 and 2% for the norms' own roundings; of 2^-96 .. 2^109, or 0)
+    const uint32_t b = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, 1.3f * x * w));
+    return b == 0 ? 0 : ((int)(b >> 23) - 127) >> 1;
+}
+
+// The unit's exponent of what has the largest bits `most` (FP16, finite): -57 .. 86.
+__device__ __forceinline__ int unit_exponent(uint32_t most, int bound)
+{
+    if (most == 0)
+        return 0;
+    const int log2 = most >= 0x400u ? (int)(most >> 10) - 15 : 7 - __builtin_clz(most);
+    return 13 - log2 - bound;
+}
+
+__device__ __forceinline__ uint32_t column_most(const PairedArgs &p, int f)
 {
     uint32_t b = 0;
+    for (int c = 0; c < p.col_chunks; c += 8) {
 #pragma unroll
-    for (int i = 0; i < kMostParts / 64; ++i)
-        b = max(b, most[64 * i + lane]);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        b = max(b, (uint32_t)__shfl_xor((int)b, o));
-    b = __builtin_amdgcn_readfirstlane(b);
-    if (b == 0)
-        return 0;
-    return b >= 0x400u ? 15 - (int)(b >> 10) : 24 - (31 - __builtin_clz(b));
+        for (int i = 0; i < 8; ++i)                  // (all of them at once; past the last, that one again)
+            b = max(b, (uint32_t)p.col_most[(int64_t)min(c + i, p.col_chunks - 1) * p.col_step + f]);
+    }
+    return b;
 }
 
 // The gradients of the pre-activations from their sums, dg = dh u act'(g) and du = dh act(g),
@@ -226,89 +266,147 @@ __device__ __forceinline__ int most_shift(const uint32_t *most, int lane)
 // wave's part of dh, 16 FN columns of 32 rows a pass, comes through its LDS in 16-byte
 // pieces of rows (read in the accumulators' layout a load would touch 32 rows for 8 bytes
 // each), and the results leave the same way.  Columns at or past `cols` (the last group's
-// rest) get zeros.
+// rest) get zeros.  FP16: once in units of the row, once of the column, of at most two fn's columns a
+// pass (as both results of four would not fit the 16 KB that a wave of the ping-pong tile has).
 template <int IN, int FN, int FM>
 __device__ __forceinline__ void store_gate_gradients(const PairedArgs &p, const f32x16 (&acc)[FN][FM], int r0,
                                                      int c0, uint8_t *stage, int lane_id)
 {
-    constexpr int CPR = 2 * FN, ROWB = 16 * CPR, KEYM = CPR - 1, RPS = 64 / CPR;     // dh
-    constexpr int CPO = 4 * FN, ROWO = 16 * CPO, KEYO = CPO - 1, RPO = 64 / CPO;     // results
+    constexpr bool UNITS = IN == IN_FP16;
+    constexpr int PN = UNITS && FN > 2 ? 2 : FN;                                     // fn a pass
+    constexpr int CPR = 2 * PN, ROWB = 16 * CPR, KEYM = CPR - 1, RPS = 64 / CPR;     // dh
+    constexpr int CPO = 4 * PN, ROWO = 16 * CPO, KEYO = CPO - 1, RPO = 64 / CPO;     // results
+    static_assert(32 * (ROWB + (UNITS ? 2 : 1) * ROWO) + (UNITS ? 64 * FN : 0) <= (FN > 1 ? 16384 : 8192),
+                  "the least that a wave has: of the ping-pong tile, and of the two-stage ring");
     const int lane = fresh_lane(lane_id);
-    const int h = lane >> 5, f0 = c0 / 2;
-    uint8_t *out = stage + 32 * ROWB;
+    const int h = lane >> 5;
+    uint8_t *out = stage + 32 * ROWB, *out2 = out + 32 * ROWO;
+    float *columns = reinterpret_cast<float *>(out2 + 32 * ROWO);      // their units
     clear_list(p.clear, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
-    float scale = 1.0f;
-    if constexpr (IN == IN_FP16)
-        scale = __builtin_ldexpf(1.0f, most_shift(p.most, lane));
+    int rows[FM];
+    if constexpr (UNITS) {
+        const int f = c0 / 2 + lane;
+        const uint32_t most = column_most(p, min(f, p.cols - 1));
+        uint32_t mosts[FM];
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+            mosts[fm] = p.row_most[min(r0 + fm * 32 + (lane & 31), p.M - 1)];
+        const int bound = bound_exponent(p.norms, lane), column = unit_exponent(most, bound);
+        if (lane < 16 * FN) {
+            columns[lane] = __builtin_ldexpf(1.0f, column);
+            if (r0 == 0 && f < p.cols)
+                p.col_back[f] = __builtin_ldexpf(1.0f, -column);
+        }
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm) {
+            rows[fm] = unit_exponent(mosts[fm], bound);
+            const int m = r0 + fm * 32 + lane;
+            if (c0 == 0 && lane < 32 && m < p.M)
+                p.row_back[m] = __builtin_ldexpf(1.0f, -rows[fm]);
+        }
+    }
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm) {
-#pragma unroll
-        for (int j = 0; j < 32 / RPS; ++j) {
-            const int r = j * RPS + lane / CPR, c = lane % CPR;
-            const int m = r0 + fm * 32 + r, n = f0 + 8 * c;
-            u32x4 w = {0u, 0u, 0u, 0u};
-            if (m < p.M && n < p.cols) {
-                const uint16_t *src = p.dh + (int64_t)m * p.lddh + n;
-                if (n + 8 <= p.cols) {
-                    w = *reinterpret_cast<const run16_t *>(src);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (n + i < p.cols)
-                            w[i >> 1] |= (uint32_t)src[i] << (16 * (i & 1));
-                }
-            }
-            *reinterpret_cast<u32x4 *>(stage + r * ROWB + ((c ^ (r & KEYM)) * 16)) = w;
-        }
-        wait_lgkmcnt0();
         const int r = lane & 31;
+        float row = 1.0f;
+        if constexpr (UNITS)
+            row = __builtin_ldexpf(1.0f, rows[fm]);
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
+        for (int f1 = 0; f1 < FN; f1 += PN) {
+            const int f0 = c0 / 2 + 16 * f1;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int ch = 2 * fn + u, n = f0 + 8 * ch + 4 * h;
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(stage + r * ROWB + ((ch ^ (r & KEYM)) * 16) + 8 * h);
-                uint32_t dg[4], du[4];
+            for (int j = 0; j < 32 / RPS; ++j) {
+                const int rd = j * RPS + lane / CPR, c = lane % CPR;
+                const int m = r0 + fm * 32 + rd, n = f0 + 8 * c;
+                u32x4 w = {0u, 0u, 0u, 0u};
+                if (m < p.M && n < p.cols) {
+                    const uint16_t *src = p.dh + (int64_t)m * p.lddh + n;
+                    if (n + 8 <= p.cols) {
+                        w = *reinterpret_cast<const run16_t *>(src);
+                    } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = scale * from_bits16(IN, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-                    float slope;
-                    const float a = gate_value<true>(p.act, acc[fn][fm][8 * u + e], slope);
-                    const bool in = n + e < p.cols;
-                    dg[e] = in ? to_bits16<IN>(d * acc[fn][fm][8 * u + 4 + e] * slope) : 0u;
-                    du[e] = in ? to_bits16<IN>(d * a) : 0u;
+                        for (int i = 0; i < 8; ++i)
+                            if (n + i < p.cols)
+                                w[i >> 1] |= (uint32_t)src[i] << (16 * (i & 1));
+                    }
                 }
-                // column 32 fn + 16 u + 4 h of dg and, eight on, of du
-                uint8_t *at = out + r * ROWO + 8 * h;
-                *reinterpret_cast<u32x2 *>(at + (((2 * ch) ^ (r & KEYO)) * 16)) = (u32x2){dg[0] | dg[1] << 16, dg[2] | dg[3] << 16};
-                *reinterpret_cast<u32x2 *>(at + (((2 * ch + 1) ^ (r & KEYO)) * 16)) = (u32x2){du[0] | du[1] << 16, du[2] | du[3] << 16};
+                *reinterpret_cast<u32x4 *>(stage + rd * ROWB + ((c ^ (rd & KEYM)) * 16)) = w;
             }
-        wait_lgkmcnt0();
+            wait_lgkmcnt0();
 #pragma unroll
-        for (int j = 0; j < 32 / RPO; ++j) {
-            const int ro = j * RPO + lane / CPO, c = lane % CPO;
-            const int m = r0 + fm * 32 + ro, n = c0 + 8 * c;
-            const u32x4 v = *reinterpret_cast<const u32x4 *>(out + ro * ROWO + ((c ^ (ro & KEYO)) * 16));
-            if (m < p.M && n < p.N)
-                *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.C) + (int64_t)m * p.ldc + n) = v;
+            for (int fn = 0; fn < PN; ++fn)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int ch = 2 * fn + u, n = f0 + 8 * ch + 4 * h;
+                    const f32x16 &sums = acc[f1 + fn][fm];
+                    const u32x2 w = *reinterpret_cast<const u32x2 *>(stage + r * ROWB + ((ch ^ (r & KEYM)) * 16) + 8 * h);
+                    float dg[4], du[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = from_bits16(IN, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                        float slope;
+                        const float a = gate_value<true>(p.act, sums[8 * u + e], slope);
+                        const bool in = n + e < p.cols;
+                        dg[e] = in ? d * sums[8 * u + 4 + e] * slope : 0.0f;
+                        du[e] = in ? d * a : 0.0f;
+                    }
+                    // column 32 fn + 16 u + 4 h of dg and, eight on, of du
+                    auto put = [&](uint8_t *to, f32x4 unit) {
+                        uint32_t b[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            b[e] = to_bits16<IN>(unit[e] * dg[e]), b[4 + e] = to_bits16<IN>(unit[e] * du[e]);
+                        uint8_t *at = to + r * ROWO + 8 * h;
+                        *reinterpret_cast<u32x2 *>(at + (((2 * ch) ^ (r & KEYO)) * 16)) = (u32x2){b[0] | b[1] << 16, b[2] | b[3] << 16};
+                        *reinterpret_cast<u32x2 *>(at + (((2 * ch + 1) ^ (r & KEYO)) * 16)) = (u32x2){b[4] | b[5] << 16, b[6] | b[7] << 16};
+                    };
+                    put(out, (f32x4){row, row, row, row});
+                    if constexpr (UNITS)
+                        put(out2, *reinterpret_cast<const f32x4 *>(columns + 16 * f1 + 8 * ch + 4 * h));
+                }
+            wait_lgkmcnt0();
+#pragma unroll
+            for (int j = 0; j < 32 / RPO; ++j) {
+                const int ro = j * RPO + lane / CPO, c = lane % CPO;
+                const int m = r0 + fm * 32 + ro, n = c0 + 32 * f1 + 8 * c;
+                const int at = ro * ROWO + ((c ^ (ro & KEYO)) * 16);
+                const bool in = m < p.M && n < p.N;
+                if (in && (!UNITS || p.C))
+                    *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.C) + (int64_t)m * p.ldc + n) =
+                        *reinterpret_cast<const u32x4 *>(out + at);
+                if constexpr (UNITS)
+                    if (in && p.C2)
+                        *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(p.C2) + (int64_t)m * p.ldc + n) =
+                            *reinterpret_cast<const u32x4 *>(out2 + at);
+            }
+            wait_lgkmcnt0();
         }
-        wait_lgkmcnt0();
     }
 }
 
-// Takes FP16 gradients' scale back out of sums over them.
-template <int IN, int FN, int FM>
-__device__ __forceinline__ void unscale(const PairedArgs &p, f32x16 (&acc)[FN][FM], int lane)
+// Takes FP16 gradients' units back out of sums over them: of each of X's rows, or (COLS, weight
+// gradients) of each column of theirs, tile row R the one that store_paired_rows says.
+template <int IN, bool COLS, int FN, int FM>
+__device__ __forceinline__ void unscale(const PairedArgs &p, f32x16 (&acc)[FN][FM], int r0, int lane_id)
 {
     if constexpr (IN == IN_FP16) {
-        const float f = __builtin_ldexpf(1.0f, -most_shift(p.most, lane));
+        const float *back = COLS ? p.col_back : p.row_back;
+        if (!back)                                   // (sums over nothing)
+            return;
+        const int lane = fresh_lane(lane_id);
+        float f[FM];
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
+        for (int fm = 0; fm < FM; ++fm) {
+            const int r = r0 + fm * 32 + (lane & 31);
+            f[fm] = back[COLS ? min((r >> 4) * 8 + (r & 7), p.cols - 1) : min(r, p.M - 1)];
+        }
 #pragma unroll
-            for (int fm = 0; fm < FM; ++fm)
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    acc[fn][fm][e] *= f;
+                    acc[fn][fm][e] *= f[fm];
     }
 }
 

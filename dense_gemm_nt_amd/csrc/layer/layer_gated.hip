@@ -17,43 +17,183 @@
 //
 // dg and du are rounded to the operands' type once, to nearest: the matrix cores take 16 bits,
 // and what the rounding leaves (2^-9 of each BF16 value, 2^-12 FP16, independent) is no more than
-// the rounding of dx and dW themselves.  FP16's would end at 2^-24: dh is multiplied by the
-// power of two that brings its largest magnitude to 1 .. 2, and the sums are divided by it.
+// the rounding of dx and dW themselves.  FP16's would end at 2^-24 and 2^16: they are stored in units
+// of powers of two, once of their row for dx and once of their column for the weights'
+// gradients, and the sums divided by them (bound_exponent).  The units take a launch that reads
+// every operand (gate_units) and a second copy of dg and du; one scale for all of dh, which needs
+// neither, lost the bits of every row beside a large one, and all where a sum was large.
 #include "layer_host.hpp"
 #include "layer_launch.hpp"
 
 namespace gnt {
 
-// The partial maxima of |dh| (16-bit patterns without the sign, which order as the values do), of
-// its finite values: what is not finite has its own row and column only, and no say in the rest's
-// scale.
-__global__ __launch_bounds__(256) void most_of(const uint16_t *x, int64_t M, int F, int ld, uint32_t *most)
+// What the units of FP16 gradients are made of (PairedArgs): the largest finite |dh| of each row,
+// and of the columns of each chunk of rows (16-bit patterns, which order as the values do); and
+// partial maxima of the squared norms of X's rows and of the weights' rows, of those that are
+// finite.  (A value that is not finite makes its own row's and column's gradients what they are,
+// and has no say in the others'.)  The first kNormParts blocks take rows in turn, a wave each or a block
+// those of more than 8192 values; `strips * chunks` after them 64 columns of dh's rows of a
+// chunk each.  Bound by its reads, dh's twice: 470 MB of 8192 x 8192 x 4096 80 us, 5.9 TB/s (with the
+// columns' blocks first and four rows a wave 114); 777 x 1408 x 2048 7.7 us, of which a launch's
+// beginning and end are 4.
+struct UnitArgs {
+    const uint16_t *dh, *x, *wg, *wu;
+    int64_t M, F;
+    int K, lddh, ldx, ldg, ldu;
+    int strips, chunks, chunk_rows;
+    uint16_t *row_most, *col_most;
+    float *norms;
+};
+
+constexpr int kRowsAtOnce = 2;
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float squares8(u32x4 w)
 {
-    __shared__ uint32_t part[4];
-    uint32_t b = 0;
-    auto take1 = [&](uint32_t v) { b = max(b, v < 0x7c00u ? v : 0u); };
-    auto take = [&](uint32_t w) { take1(w & 0x7fffu), take1((w >> 16) & 0x7fffu); };
-    const int64_t step = gridDim.x;
-    for (int64_t m = blockIdx.x; m < M; m += step) {
-        const uint16_t *row = x + m * ld;
-        int n = threadIdx.x * 8;
-        for (; n + 8 <= F; n += 2048) {
-            const u32x4 w = *reinterpret_cast<const run16_t *>(row + n);
-            take(w[0]), take(w[1]), take(w[2]), take(w[3]);
-        }
-        for (; n < F; n += 2048)
-            for (int i = 0; i < 8; ++i)
-                if (n + i < F)
-                    take(row[n + i]);
-    }
+    float s = 0.0f;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        b = max(b, (uint32_t)__shfl_xor((int)b, o));
-    if (threadIdx.x % 64 == 0)
-        part[threadIdx.x / 64] = b;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        most[blockIdx.x] = max(max(part[0], part[1]), max(part[2], part[3]));
+    for (int e = 0; e < 8; ++e) {
+        const float v = from_bits16(IN_FP16, (w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+        s += v * v;
+    }
+    return s;
+}
+
+__global__ __launch_bounds__(256) void gate_units(UnitArgs a)
+{
+    __shared__ uint32_t part[4][32];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // the running maxima of pairs of values: 0x400 is added to a pattern without its sign, so that
+    // what is not finite is negative
+    const s16x2 kZero = {0x400, 0x400};
+    auto take = [&](s16x2 &most, uint32_t w) {
+        most = __builtin_elementwise_max(most, __builtin_bit_cast(s16x2, w & 0x7fff7fffu) + kZero);
+    };
+    auto read = [&](const uint16_t *at, int64_t left) -> u32x4 {      // eight values, or `left` and zeros
+        u32x4 w = {0u, 0u, 0u, 0u};
+        if (left >= 8) {
+            w = *reinterpret_cast<const run16_t *>(at);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    w[i >> 1] |= (uint32_t)at[i] << (16 * (i & 1));
+        }
+        return w;
+    };
+    if (blockIdx.x >= kNormParts) {
+        const int tile = blockIdx.x - kNormParts;
+        const int chunk = tile / a.strips, strip = tile - chunk * a.strips;
+        const int64_t f = (int64_t)strip * 64 + 8 * (lane & 7);
+        const int64_t end = min(a.M, (int64_t)(chunk + 1) * a.chunk_rows);
+        s16x2 most[4] = {kZero, kZero, kZero, kZero};
+        if (f < a.F) {
+#pragma unroll 8
+            for (int64_t m = (int64_t)chunk * a.chunk_rows + (threadIdx.x >> 3); m < end; m += 32) {
+                const u32x4 w = read(a.dh + m * a.lddh + f, a.F - f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    take(most[i], w[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = 8; o < 64; o <<= 1)
+                most[i] = __builtin_elementwise_max(
+                    most[i], __builtin_bit_cast(s16x2, __shfl_xor(__builtin_bit_cast(int, most[i]), o)));
+            if (lane < 8)
+                part[wave][4 * lane + i] = __builtin_bit_cast(uint32_t, most[i] - kZero);
+        }
+        __syncthreads();
+        const int64_t c = (int64_t)strip * 64 + threadIdx.x;
+        if (threadIdx.x < 64 && c < a.F) {
+            uint32_t b = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                b = max(b, (part[w][threadIdx.x >> 1] >> (16 * (threadIdx.x & 1))) & 0xffffu);
+            a.col_most[(int64_t)chunk * a.F + c] = (uint16_t)b;
+        }
+        return;
+    }
+    // (what every wave of the block joins of its waves' values)
+    auto across = [&](uint32_t v, auto join) {
+        __syncthreads();
+        if (lane == 0)
+            part[wave][0] = v;
+        __syncthreads();
+        return join(join(part[0][0], part[1][0]), join(part[2][0], part[3][0]));
+    };
+    // Rows of `len` values from at(r) on, kRowsAtOnce of them read at once: one(i, eight values), then
+    // done(r, i, wide) by every lane.  The `last` first: so that the waves that have the fewest of one
+    // kind of rows begin with the other.
+    auto rows = [&](int64_t count, int64_t len, bool last, auto at, auto one, auto done) {
+        const bool wide = len > 8192;
+        const int threads = wide ? 256 : 64, t = wide ? (int)threadIdx.x : lane;
+        const int64_t units = wide ? kNormParts : 4 * kNormParts;
+        const int64_t id = wide ? blockIdx.x : 4 * blockIdx.x + wave;
+        for (int64_t r = last ? units - 1 - id : id; r < count; r += kRowsAtOnce * units) {
+            const uint16_t *row[kRowsAtOnce];
+#pragma unroll
+            for (int i = 0; i < kRowsAtOnce; ++i)
+                row[i] = at(min(r + i * units, count - 1));      // (past the last, that one again)
+#pragma unroll 4
+            for (int64_t n = 8 * t; n < len; n += 8 * threads)
+#pragma unroll
+                for (int i = 0; i < kRowsAtOnce; ++i)
+                    one(i, read(row[i] + n, len - n));
+#pragma unroll
+            for (int i = 0; i < kRowsAtOnce; ++i)
+                done(min(r + i * units, count - 1), i, wide);
+        }
+    };
+    float sum[kRowsAtOnce] = {}, norm_x = 0.0f, norm_w = 0.0f;
+    rows(2 * a.F + a.M, a.K, false,
+         [&](int64_t r) {
+             return r < a.F ? a.wg + r * a.ldg : r < 2 * a.F ? a.wu + (r - a.F) * a.ldu : a.x + (r - 2 * a.F) * a.ldx;
+         },
+         [&](int i, u32x4 w) { sum[i] += squares8(w); },
+         [&](int64_t r, int i, bool wide) {
+#pragma unroll
+             for (int o = 32; o > 0; o >>= 1)
+                 sum[i] += __shfl_xor(sum[i], o);
+             if (wide)
+                 sum[i] = __builtin_bit_cast(float, across(__builtin_bit_cast(uint32_t, sum[i]), [](uint32_t p, uint32_t q) {
+                     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(float, p) + __builtin_bit_cast(float, q));
+                 }));
+             if (__builtin_isfinite(sum[i])) {
+                 if (r < 2 * a.F)
+                     norm_w = fmaxf(norm_w, sum[i]);
+                 else
+                     norm_x = fmaxf(norm_x, sum[i]);
+             }
+             sum[i] = 0.0f;
+         });
+    s16x2 most[kRowsAtOnce];
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i)
+        most[i] = kZero;
+    rows(a.M, a.F, true, [&](int64_t r) { return a.dh + r * a.lddh; },
+         [&](int i, u32x4 w) { take(most[i], w[0]), take(most[i], w[1]), take(most[i], w[2]), take(most[i], w[3]); },
+         [&](int64_t r, int i, bool wide) {
+#pragma unroll
+             for (int o = 32; o > 0; o >>= 1)
+                 most[i] = __builtin_elementwise_max(most[i], __builtin_bit_cast(s16x2, __shfl_xor(__builtin_bit_cast(int, most[i]), o)));
+             const s16x2 m = most[i] - kZero;
+             uint32_t b = max((uint32_t)(uint16_t)m[0], (uint32_t)(uint16_t)m[1]);
+             if (wide)
+                 b = across(b, [](uint32_t p, uint32_t q) { return max(p, q); });
+             if (wide ? threadIdx.x == 0 : lane == 0)
+                 a.row_most[r] = (uint16_t)b;
+             most[i] = kZero;
+         });
+    auto top = [](uint32_t p, uint32_t q) { return max(p, q); };     // (of values that are not negative)
+    const uint32_t x = across(__builtin_bit_cast(uint32_t, norm_x), top), w = across(__builtin_bit_cast(uint32_t, norm_w), top);
+    if (threadIdx.x == 0) {
+        a.norms[blockIdx.x] = __builtin_bit_cast(float, x);
+        a.norms[kNormParts + blockIdx.x] = __builtin_bit_cast(float, w);
+    }
 }
 
 __global__ __launch_bounds__(256) void clear_words(ClearList l)
@@ -91,9 +231,10 @@ enum : int { SUM_GATED = 0, SUM_GRAD = 1, SUM_ROWS = 2 };
 template <int MODE, int IN, int OUT>
 __global__ __launch_bounds__(256) void paired_sum(PairedArgs p)
 {
-    float scale = 1.0f;                     // (by whole waves, before any lane leaves)
-    if constexpr (MODE == SUM_GRAD && IN == IN_FP16)
-        scale = __builtin_ldexpf(1.0f, most_shift(p.most, threadIdx.x & 63));
+    constexpr bool UNITS = MODE == SUM_GRAD && IN == IN_FP16;
+    int bound = 0;                          // (by whole waves, before any lane leaves)
+    if constexpr (UNITS)
+        bound = bound_exponent(p.norms, threadIdx.x & 63);
     const int per = MODE == SUM_ROWS ? p.N / 4 : p.N / 8;        // threads per row
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (t >= (int64_t)p.M * per)
@@ -126,13 +267,37 @@ __global__ __launch_bounds__(256) void paired_sum(PairedArgs p)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool in = f + e < p.cols;
-                const float d = in ? scale * from_bits16(IN, p.dh[(int64_t)m * p.lddh + f + e]) : 0.0f;
+                const float d = in ? from_bits16(IN, p.dh[(int64_t)m * p.lddh + f + e]) : 0.0f;
                 const float a = gate_value<true>(p.act, g[e], slope);
                 dg[e] = in ? d * u[e] * slope : 0.0f;
                 du[e] = in ? d * a : 0.0f;
             }
-            store4<OUT>(p.C, (int64_t)m * p.ldc + n, dg, true, 4);
-            store4<OUT>(p.C, (int64_t)m * p.ldc + n + 8, du, true, 4);
+            auto put = [&](void *to, f32x4 unit) {
+                store4<OUT>(to, (int64_t)m * p.ldc + n, unit * dg, true, 4);
+                store4<OUT>(to, (int64_t)m * p.ldc + n + 8, unit * du, true, 4);
+            };
+            if constexpr (UNITS) {
+                if (p.C) {
+                    const int row = unit_exponent(p.row_most[m], bound);
+                    const float unit = __builtin_ldexpf(1.0f, row);
+                    put(p.C, (f32x4){unit, unit, unit, unit});
+                    if (i == 0)
+                        p.row_back[m] = __builtin_ldexpf(1.0f, -row);
+                }
+                if (p.C2) {
+                    f32x4 unit;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int column = unit_exponent(column_most(p, min(f + e, p.cols - 1)), bound);
+                        unit[e] = __builtin_ldexpf(1.0f, column);
+                        if (m == 0 && f + e < p.cols)
+                            p.col_back[f + e] = __builtin_ldexpf(1.0f, -column);
+                    }
+                    put(p.C2, unit);
+                }
+            } else {
+                put(p.C, (f32x4){1.0f, 1.0f, 1.0f, 1.0f});
+            }
         }
     }
 }
@@ -215,17 +380,32 @@ struct BackwardWs {
     DxPlan dx;
     Plan plan[2];                       // dx, dW
     SplitWs split[2];
-    uint16_t *d;                        // [M][both(F)]
-    uint32_t *most;
+    uint16_t *d, *dc;                   // dg and du [M][both(F)], FP16's in units of rows and of columns
+    int strips, chunks, chunk_rows;     // gate_units'
+    uint16_t *row_most, *col_most;
+    float *norms, *row_back, *col_back;
     int64_t bytes;
 };
 
-BackwardWs carve_backward(int64_t M, int64_t F, int64_t K, void *base)
+BackwardWs carve_backward(int64_t M, int64_t F, int64_t K, int in_dtype, void *base)
 {
     BackwardWs w{};
     Carver c{static_cast<uint8_t *>(base)};
     w.d = c.take<uint16_t>(M * both(F));
-    w.most = c.take<uint32_t>(kMostParts);
+    w.dc = w.d;
+    if (in_dtype == GEMM_FP16 && M > 0 && F > 0) {
+        w.dc = c.take<uint16_t>(M * both(F));
+        // chunks of 256 rows or more, up to 32 of them, that make about four blocks a compute unit
+        w.strips = (int)cdiv(F, 64);
+        const int64_t most = std::min<int64_t>(32, std::max<int64_t>(1, 4 * kNumCUs / w.strips));
+        w.chunk_rows = (int)std::max<int64_t>(256, cdiv(M, most));
+        w.chunks = (int)cdiv(M, w.chunk_rows);
+        w.row_most = c.take<uint16_t>(M);
+        w.col_most = c.take<uint16_t>(w.chunks * F);
+        w.norms = c.take<float>(2 * kNormParts);
+        w.row_back = c.take<float>(M);
+        w.col_back = c.take<float>(F);
+    }
     // (a product of no rows or columns has no plan)
     if (M > 0 && F > 0)
         w.sums = carve_sums(c, M, F, K);
@@ -252,6 +432,12 @@ PairedArgs piece(PairedArgs a, int64_t row, int64_t col, int64_t cols)
     a.cols = (int)std::min<int64_t>(a.cols - col, cols);
     if (a.dh)
         a.dh += row * a.lddh + col;
+    if (a.norms) {
+        a.row_most += row;
+        a.col_most += col;
+        a.row_back += row;
+        a.col_back += col;
+    }
     return a;
 }
 
@@ -350,10 +536,18 @@ gemm_status_t gemm_gated_backward_workspace(int64_t M, int64_t F, int64_t K, int
 {
     if (!bytes)
         return GEMM_ERR_INVALID_ARG;
-    const gemm_status_t st = check_sizes(M, F, K, GEMM_BF16, GEMM_BF16, GEMM_GATE_SILU);
+    // (FP16's, the larger one)
+    return gemm_gated_backward_workspace_of(M, F, K, GEMM_FP16, bytes);
+}
+
+gemm_status_t gemm_gated_backward_workspace_of(int64_t M, int64_t F, int64_t K, int in_dtype, int64_t *bytes)
+{
+    if (!bytes)
+        return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = check_sizes(M, F, K, in_dtype, GEMM_BF16, GEMM_GATE_SILU);
     if (st != GEMM_OK)
         return st;
-    *bytes = carve_backward(M, F, K, nullptr).bytes;
+    *bytes = carve_backward(M, F, K, in_dtype, nullptr).bytes;
     return GEMM_OK;
 }
 
@@ -390,7 +584,7 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
     if (want_dw && ((st = check_output(dWg, K, K, grad_dtype)) != GEMM_OK ||
                     (st = check_output(dWu, K, K, grad_dtype)) != GEMM_OK))
         return st;
-    const BackwardWs w = carve_backward(M, F, K, workspace);
+    const BackwardWs w = carve_backward(M, F, K, in_dtype, workspace);
     if ((st = check_workspace(workspace, workspace_bytes, w.bytes)) != GEMM_OK)
         return st;
     const bool inner = M > 0 && F > 0;
@@ -411,10 +605,17 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
     a.act = activation;
     a.dh = static_cast<const uint16_t *>(dH);
     a.lddh = (int)lddh;
-    a.most = w.most;
-    if (e == hipSuccess && in_dtype == GEMM_FP16) {
-        hipLaunchKernelGGL(most_of, dim3(kMostParts), dim3(256), 0, stream, a.dh, F > 0 ? M : 0, (int)F, a.lddh,
-                           w.most);
+    a.row_most = w.row_most;
+    a.col_most = w.col_most;
+    a.col_chunks = w.chunks;
+    a.col_step = (int)F;
+    a.norms = w.norms;
+    a.row_back = w.row_back;
+    a.col_back = w.col_back;
+    if (e == hipSuccess && w.norms) {
+        UnitArgs u{a.dh, static_cast<const uint16_t *>(X), a.B, a.B2, M, F, (int)K, a.lddh, (int)ldx, a.ldb, a.ldb2,
+                   w.strips, w.chunks, w.chunk_rows, w.row_most, w.col_most, w.norms};
+        hipLaunchKernelGGL(gate_units, dim3((unsigned)(w.strips * w.chunks + kNormParts)), dim3(256), 0, stream, u);
         e = hipGetLastError();
     }
     for (int i = 0; inner && i < w.sums.pieces.count && e == hipSuccess; ++i) {
@@ -426,7 +627,13 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         b = piece(b, q.row, q.col / 2, q.cols / 2);
         if (clear_first && i == 0)
             b.clear = clear_of(split, splits);
-        fill_args(b, p, w.sums.split[i], w.d + q.row * both_cols + q.col, q.rows, q.cols, K, both_cols, in_dtype);
+        const int64_t at = q.row * both_cols + q.col;
+        fill_args(b, p, w.sums.split[i], w.d + at, q.rows, q.cols, K, both_cols, in_dtype);
+        if (w.norms) {
+            // (a copy that nothing reads is not made)
+            b.C = want_dx ? w.d + at : nullptr;
+            b.C2 = want_dw ? w.dc + at : nullptr;
+        }
         const bool rot = rotate_slabs(1, q.rows);
         paired_fn fn;
         switch (p.cfg) {
@@ -466,7 +673,7 @@ gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void 
         fill_args(b, p, w.split[1], dWg, both_cols, K, M, K, grad_dtype);
         b.vec_store = b.vec_store && (uintptr_t)dWu % (4 * size_of(grad_dtype)) == 0;
         b.C2 = dWu;
-        b.A = w.d;
+        b.A = w.dc;
         b.lda = (int)both_cols;
         b.B = static_cast<const uint16_t *>(X);
         b.ldb = (int)ldx;

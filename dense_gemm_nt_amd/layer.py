@@ -107,8 +107,11 @@ def gemm_gated_backward(dh, x, Wg, Wu, activation="silu", grad_dtype=None, dx_dt
     """(dx, dWg, dWu) of gemm_gated for dh [M, F]: dx [M, K] of dx_dtype and dWg, dWu [F, K]
     of grad_dtype (defaults: x's).  Only the operands are needed: the two sums are
     computed again.  The gradients of the two sums are rounded to x's type once, so
-    FP32 results hold no more than that.  need_dx or need_weights False: that part
-    is not computed, and None."""
+    FP32 results hold no more than that; float16's are held in units of each row of dh for
+    dx and of each column for the weights' gradients, so that neither large or small values of
+    dh nor large sums end its range (include/gemm_layer.h).  An infinity or NaN in dh reaches
+    its row of dx and its column's rows of dWg and dWu.  need_dx or need_weights False: that
+    part is not computed, and None."""
     import torch
     M, F, K, index = _block(x, Wg, Wu)
     if dh.dim() != 2:
@@ -128,7 +131,7 @@ def gemm_gated_backward(dh, x, Wg, Wu, activation="silu", grad_dtype=None, dx_dt
     dx = torch.empty((M, K), dtype=xdt, device=dev) if need_dx else None
     dWg = torch.empty((F, K), dtype=gdt, device=dev) if need_weights else None
     dWu = torch.empty((F, K), dtype=gdt, device=dev) if need_weights else None
-    n = _workspace_bytes("gemm_gated_backward_workspace", M, F, K)
+    n = _workspace_bytes("gemm_gated_backward_workspace_of", M, F, K, _code(dt))
     ws = torch.empty(n, dtype=torch.uint8, device=dev)
     st = _layer.lib().gemm_run_gated_backward(
         dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), _ptr(dx) or None, _ptr(dWg) or None,

@@ -58,14 +58,20 @@ gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void
  *   dg = dH u act'(g), du = dH act(g)
  *   dX = dg Wg + du Wu     [M][K], dx_dtype
  *   dWg = dg^T X, dWu = du^T X     [F][K] contiguous, grad_dtype, written whole
- * Nothing of the forward call is needed: g and u are computed again, in FP32, and
- * so are dg and du, which are then rounded to the operands' type once (relative to the value 2^-9
- * at most for BF16; FP16 2^-12, in units of the power of two that brings dH's largest magnitude to
- * 1 .. 2: dg and du must stay below 2^16 and lose bits below 2^-14 in them).  So an
- * FP32 result is no more exact than that.
+ * Nothing of the forward call is needed: g and u are computed again, in FP32, and so are dg and
+ * du, which are then rounded to the operands' type once, relative to the value 2^-9 at most for
+ * BF16 and 2^-12 for FP16.  So an FP32 result is no more exact than that.  FP16's are held in units
+ * of powers of two, for dX one of each row, for the weights' gradients one of each column of dH:
+ * what is below 2^-28 of the largest finite |dH| of the row (column) times B loses bits, and what
+ * is below 2^-38 all of them, B = 1.13 max ||X[m]|| max(||Wg[f]||, ||Wu[f]||) over the finite rows, which
+ * no factor of dH exceeds.  So no finite gradient ends FP16's range on the way, and an infinity or NaN
+ * in dH is in its own row of dX and its own column's dWg and dWu only.
  * dX may be NULL (not computed), and so may dWg and dWu, both or neither.  act' of ReLU
  * is 0 at 0.  M = 0 writes zeros to dWg and dWu, F = 0 to dX. */
 gemm_status_t gemm_gated_backward_workspace(int64_t M, int64_t F, int64_t K, int64_t *bytes);
+/* (the one above is enough for either type; BF16 operands need about half of it) */
+gemm_status_t gemm_gated_backward_workspace_of(int64_t M, int64_t F, int64_t K, int in_dtype,
+                                               int64_t *bytes);
 gemm_status_t gemm_run_gated_backward(const void *dH, const void *X, const void *Wg,
                                       const void *Wu, void *dX, void *dWg, void *dWu, int64_t M,
                                       int64_t F, int64_t K, int64_t lddh, int64_t ldx,

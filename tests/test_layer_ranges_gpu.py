@@ -5,8 +5,8 @@ import pytest
 import torch
 
 from oracle import layer as o
-from tests.rows_util import randn
-from tests.test_layer_gated_gpu import _operands
+from tests.rows_util import U, check, half_step, randn, rounded
+from tests.test_layer_gated_gpu import SIZES, _operands, _sums, _value_err
 from tests.test_layer_int8_gpu import SIZES as INT8_SIZES
 from tests.test_layer_int8_gpu import _codes, _scales
 
@@ -16,6 +16,79 @@ BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
 
 
 # ------------------------------------------------------------------ FP16 gradients
+
+def _bounds(dh, x, Wg, Wu, act):
+    """Bounds of FP32 (dx, dWg, dWu) of FP16 operands, and the results.  dg and du are rounded to
+    FP16 twice, in units of their row for dx and of their column for the weights' gradients: a unit
+    brings the largest magnitude of the row's (column's) dh times B below 2^15 and above 2^13
+    (both rounded up to powers of two), B = 1.15 max ||x|| max ||W|| at least any |u act'(g)| or
+    |act(g)|; so an absolute 2^-25 of FP16's is at most 2^-38 of that product."""
+    K, F, M = x.shape[1], Wg.shape[0], x.shape[0]
+    d = dh.double()
+    _, g, u = o.gated(x, Wg, Wu, act)
+    eg, eu = _sums(x, Wg, K), _sums(x, Wu, K)
+    a, slope = o.gate(g, act)
+    ea = _value_err(g, a, eg, act)
+    es = 0.8 * eg + 2.0 ** -20 * (1 + g.abs())          # |act''| <= 0.8; the slope's own roundings
+    if act == "relu":                                   # a sum near the corner may fall on its other side
+        es = torch.where(g.abs() <= eg, 1.0, 0.0).double()
+    dg, du = d * u * slope, d * a
+    edg = d.abs() * (u.abs() * es + (slope.abs() + es) * eu) + 2.0 ** -22 * dg.abs()
+    edu = d.abs() * ea + 2.0 ** -22 * du.abs()
+    B = 1.15 * float(x.double().norm(dim=1).max()) * float(torch.cat([Wg, Wu]).double().norm(dim=1).max())
+
+    def held(e, v, most):
+        return e + half_step(FP16) * (v.abs() + e) + 2.0 ** -38 * B * most
+    row, col = d.abs().amax(1, keepdim=True), d.abs().amax(0, keepdim=True)
+    wg, wu, xa = Wg.double().abs(), Wu.double().abs(), x.double().abs()
+    dx_err = held(edg, dg, row) @ wg + held(edu, du, row) @ wu + (2 * F + 64) * U * (dg.abs() @ wg + du.abs() @ wu)
+    wg_err = held(edg, dg, col).t() @ xa + (M + 64) * U * (dg.abs().t() @ xa)
+    wu_err = held(edu, du, col).t() @ xa + (M + 64) * U * (du.abs().t() @ xa)
+    ref = o.gated_backward(dh, x, Wg, Wu, act)[:3]
+    return ref, [rounded(r, e, FP32) for r, e in zip(ref, (dx_err, wg_err, wu_err))]
+
+
+def _check_gradients(dh, x, Wg, Wu, act, what):
+    import dense_gemm_nt_amd as g
+    got = g.gemm_gated_backward(*(t.to(DEV) for t in (dh, x, Wg, Wu)), activation=act, grad_dtype=FP32, dx_dtype=FP32)
+    ref, bounds = _bounds(dh, x, Wg, Wu, act)
+    for name, y, r, b in zip(("dx", "dWg", "dWu"), got, ref, bounds):
+        check(y, r, b, "%s, %s" % (name, what))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("M,F,K", [(20, 77, 136), (130, 264, 136), (300, 520, 2056)])
+def test_fp16_gradients_of_large_sums(M, F, K, act):
+    """Sums past 2^15 beside a dh of 1e-6: no gradient is near FP16's end."""
+    x, Wg, Wu = randn(M, K, seed=1, std=200.0, dtype=FP16), randn(F, K, seed=2, std=K ** -0.5 / 200, dtype=FP16), \
+        randn(F, K, seed=3, std=350 * K ** -0.5, dtype=FP16)
+    dh = randn(M, F, seed=4, std=1e-6, dtype=FP16)
+    assert float(o.gated(x, Wg, Wu, act)[2].abs().max()) > 1e5
+    _check_gradients(dh, x, Wg, Wu, act, "large up values")
+    Wg, Wu = Wu, Wg
+    _check_gradients(dh, x, Wg, Wu, act, "large gates")
+
+
+@pytest.mark.parametrize("M,F,K", SIZES)
+def test_fp16_gradients_beside_a_large_entry(M, F, K):
+    """One entry of dh at 30000 leaves the other rows and columns their own 1e-3."""
+    x, Wg, Wu = _operands(M, F, K, FP16, seed=5)
+    dh = randn(M, F, seed=9, dtype=FP16, std=1e-3)
+    dh[M // 2, F // 3] = 30000.0
+    _check_gradients(dh, x, Wg, Wu, "silu", "one entry")
+
+
+@pytest.mark.parametrize("M,F,K", [(16, 520, 64), (40, 100, 72), (130, 264, 136), (260, 1030, 520)])
+@pytest.mark.parametrize("small", [1e-6, 1e-3])
+def test_fp16_gradients_beside_a_large_row(M, F, K, small):
+    x, Wg, Wu = _operands(M, F, K, FP16, seed=5)
+    dh = randn(M, F, seed=9, std=small)
+    dh[M // 2] = randn(F, seed=10, std=2e4).clamp(-6e4, 6e4)
+    _check_gradients(dh.to(FP16), x, Wg, Wu, "gelu", "one row")
+    dh = randn(M, F, seed=9, std=small)
+    dh[:, F // 2] = randn(M, seed=10, std=2e4).clamp(-6e4, 6e4)
+    _check_gradients(dh.to(FP16), x, Wg, Wu, "gelu", "one column")
+
 
 @pytest.mark.parametrize("std", [1e-6, 1.0, 1e4])
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
@@ -37,6 +110,7 @@ def test_fp16_gradients_beside_a_value_that_is_not_finite(std, value):
     assert torch.equal(bx[rows], dx[rows]) and not bool(torch.isfinite(bx[5]).any())
     assert torch.equal(ba[cols], a[cols]) and torch.equal(bb[cols], b[cols])
     assert not bool(torch.isfinite(ba[20]).any()) and not bool(torch.isfinite(bb[20]).any())
+    _check_gradients(plain, x, Wg, Wu, "silu", "beside it")
 
 
 # ------------------------------------------------------------ the integer product
