@@ -190,3 +190,43 @@ def test_update_of_more_values_than_a_launch():
         U[at] = 0.0
     for i in range(0, m, 512):
         assert not bool(U[i:i + 512].any())
+
+
+# ------------------------------------------------------------- pieces and largest sizes
+
+@pytest.mark.parametrize("M,N,K", [(1868, 9480, 144), (1113, 13080, 144)])
+def test_int8_pieces_have_their_own_bias_and_prior_rows(M, N, K):
+    """The rows, and columns, of a last pass apart: scales, biases and C_old from where they begin."""
+    import dense_gemm_nt_amd as g
+    A, B = _codes(M, K, seed=5, lo=-4, hi=5).to(DEV), _codes(N, K, seed=6, lo=-4, hi=5).to(DEV)
+    sa, sb = 2.0 ** (torch.arange(M, device=DEV) % 5 - 2).float(), 2.0 ** (torch.arange(N, device=DEV) % 7 - 3).float()
+    bn, bm = torch.arange(N, device=DEV) % 64 / 8.0, torch.arange(M, device=DEV) % 128 / 4.0
+    old = (torch.arange(M, device=DEV)[:, None] * 3 + torch.arange(N, device=DEV)) % 256 / 4.0
+    y = (A.float() @ B.float().t()) * sa[:, None] * sb          # (of few bits: exact)
+    for bias, along, add in ((bn, "n", bn), (bm, "m", bm[:, None])):
+        out = old.clone()
+        g.gemm_int8(A, B, sa, sb, out=out, alpha=0.5, beta=2.0, bias=bias, bias_along=along)
+        assert torch.equal(out, 0.5 * y + 2.0 * old + add)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_the_largest_block(dt):
+    """F one below its limit: dg and du in rows of 2^22 values.  Of small integers, so exact."""
+    import dense_gemm_nt_amd as g
+    M, F, K = 300, (1 << 21) - 1, 16
+    gen = torch.Generator(device=DEV).manual_seed(1)
+
+    def ints(*shape):
+        return torch.randint(-1, 2, shape, generator=gen, device=DEV).to(dt)
+    x, Wg, Wu, dh = ints(M, K), ints(F, K), ints(F, K), ints(M, F)
+    h = g.gemm_gated(x, Wg, Wu, activation="relu")
+    dx, a, b = g.gemm_gated_backward(dh, x, Wg, Wu, activation="relu", grad_dtype=FP32, dx_dtype=FP32)
+    want = torch.zeros(M, K, dtype=torch.float64, device=DEV)
+    for f in range(0, F, 1 << 18):
+        c = slice(f, min(F, f + (1 << 18)))
+        gate, up, d = x.float() @ Wg[c].float().t(), x.float() @ Wu[c].float().t(), dh[:, c].float()
+        assert torch.equal(h[:, c].float(), gate.clamp(min=0) * up)
+        dg, du = d * up * (gate > 0), d * gate.clamp(min=0)
+        assert torch.equal(a[c], dg.t().contiguous() @ x.float()) and torch.equal(b[c], du.t().contiguous() @ x.float())
+        want += (dg @ Wg[c].float() + du @ Wu[c].float()).double()
+    assert float(want.abs().max()) < 2 ** 24 and torch.equal(dx.double(), want)
