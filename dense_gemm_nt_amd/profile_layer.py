@@ -18,17 +18,21 @@ from . import profile_rows as p
 
 CASES = "more_operators"
 
-HEAD = p.HEAD.replace("products whose weight is picked per row", "products of a feed-forward layer") \
-    .replace("libgemm_rows.so", "libgemm_layer.so").replace("perf/operators.py", "perf/more_operators.py") \
-    .replace("profile_rows.py", "profile_layer.py")
+
+def product(case, i, n):
+    """The update's two squares share a kernel: in turn X X^T and the polynomial's A^2, once a
+    step each."""
+    if case["op"] == "ortho" and n == 2 * p.cases_module(CASES).STEPS:
+        return "A^2" if i % 2 else "X X^T"
+    return None
 
 
 def main():
     if sys.argv[1:] == ["run"]:
         p.run(CASES)
     elif len(sys.argv) == 3 and sys.argv[1] == "table":
-        lines, scale = p.table(sys.argv[2], CASES)
-        print(HEAD % (p.CALLS, scale["fetch"], scale["write"], p.COPY_MB, p.SIMDS, p.XCDS))
+        lines, scale = p.table(sys.argv[2], CASES, product)
+        print(p.heading("products of a feed-forward layer", "libgemm_layer.so", CASES, "profile_layer", scale))
         print("\n".join(lines))
     else:
         raise SystemExit(__doc__)

@@ -100,8 +100,10 @@ def _blocks(r):
     return "x".join(str(int(r["Grid_Size_" + a]) // int(r["Workgroup_Size_" + a])) for a in "XYZ")
 
 
-def table(folder, cases="operators"):
-    """The lines of the table: per case and kernel its median time and mean counters."""
+def table(folder, cases="operators", product=None):
+    """The lines of the table: per case and kernel its median time and mean counters.  Where one
+    kernel serves several products of a call, product(case, i, n) names the one of the i-th of
+    its n launches in a call (None: they are one)."""
     files = {n: dispatches(os.path.join(folder, "%s_%s.csv" % (n, kind))) for n, kind in (
         ("trace", "kernel_trace"), ("fetch", "counter_collection"), ("write", "counter_collection"),
         ("sq", "counter_collection"))}
@@ -115,9 +117,15 @@ def table(folder, cases="operators"):
     for i, case in enumerate(cases):
         sizes = ", ".join("%s %s" % (k, v) for k, v in case.items() if k != "name")
         out.append("| **%s** (%s) | | | | | | | |" % (case["name"], sizes))
-        groups = OrderedDict()
+        launches = OrderedDict()
         for j, d in enumerate(runs["trace"][i]):
-            groups.setdefault((_short(d["name"]), _blocks(d["row"])), []).append(j)
+            launches.setdefault((_short(d["name"]), _blocks(d["row"])), []).append(j)
+        groups = OrderedDict()
+        for (name, blocks), at in launches.items():
+            n = len(at) // CALLS
+            for k, j in enumerate(at):
+                which = product(case, k % n, n) if product else None
+                groups.setdefault((name + (": " + which if which else ""), blocks), []).append(j)
         for (name, blocks), at in groups.items():
             at = at[len(at) // CALLS * WARM:]
             ns = sorted(int(runs["trace"][i][j]["row"]["End_Timestamp"]) -
@@ -135,14 +143,19 @@ def table(folder, cases="operators"):
     return out, scale
 
 
-HEAD = """# Kernels of the products whose weight is picked per row
+HEAD = """# Kernels of the %(what)s
 
-Traces and counters of `libgemm_rows.so`'s kernels on `perf/operators.py`'s listed cases, made by the commands in `dense_gemm_nt_amd/profile_rows.py` (each case's calls run %d times on three rotating input sets, the first three left out; median of the trace, mean of the counters, one run each).
+Traces and counters of `%(library)s`'s kernels on `perf/%(cases)s.py`'s listed cases, made by the commands in `dense_gemm_nt_amd/%(program)s.py` (each case's calls run %(calls)d times on three rotating input sets, the first three left out; median of the trace, mean of the counters, one run each).
 
-Fabric bytes are the L2's requests to memory (FETCH_SIZE x %.3f, WRITE_SIZE x %.3f, as a device copy of %d MiB calibrates them). MFMA busy = SQ_VALU_MFMA_BUSY_CYCLES / %d SIMDs over GRBM_GUI_ACTIVE / %d XCDs.
+Fabric bytes are the L2's requests to memory (FETCH_SIZE x %(fetch).3f, WRITE_SIZE x %(write).3f, as a device copy of %(copy)d MiB calibrates them). MFMA busy = SQ_VALU_MFMA_BUSY_CYCLES / %(simds)d SIMDs over GRBM_GUI_ACTIVE / %(xcds)d XCDs.
 
 | kernel | blocks | µs | read MB | written MB | TB/s | MFMA busy | LDS bank conflicts (thousands) |
 |---|---|---|---|---|---|---|---|"""
+
+
+def heading(what, library, cases, program, scale):
+    return HEAD % dict(what=what, library=library, cases=cases, program=program, calls=CALLS, fetch=scale["fetch"],
+                       write=scale["write"], copy=COPY_MB, simds=SIMDS, xcds=XCDS)
 
 
 def main():
@@ -150,7 +163,7 @@ def main():
         run()
     elif len(sys.argv) == 3 and sys.argv[1] == "table":
         lines, scale = table(sys.argv[2])
-        print(HEAD % (CALLS, scale["fetch"], scale["write"], COPY_MB, SIMDS, XCDS))
+        print(heading("products whose weight is picked per row", "libgemm_rows.so", "operators", "profile_rows", scale))
         print("\n".join(lines))
     else:
         raise SystemExit(__doc__)
