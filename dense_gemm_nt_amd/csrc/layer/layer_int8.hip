@@ -48,8 +48,9 @@ typedef uint32_t codes8_t __attribute__((ext_vector_type(2), aligned(1)));    //
 // both quotients rounded to FP32 as IEEE division does.  A row of zeros: scale 0, codes 0; a row
 // with an infinity or NaN: scale NaN, codes 0, so that its products are NaN.  TPR threads a
 // row hold its first 32 TPR values in registers between the two passes; what is
-// longer is read again (from L2).  Blocks take 256 / TPR rows each in turn (one launch has
-// fewer than 2^32 threads: kQuantizeBlocks of them at most).
+// longer is read again (from L2).  A launch has fewer than 2^32 threads along an axis of its grid, so
+// the blocks past 2^20 are on its second axis.  (With blocks that take rows in turn instead, 8111 x
+// 8192 FP16 took 45.5 us, and 37.5 so.)
 constexpr int64_t kQuantizeBlocks = (int64_t)1 << 20;
 
 template <int IN, int TPR>
@@ -57,18 +58,19 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
                                                      int64_t ldx, int64_t ldq)
 {
     constexpr int ROWS = 256 / TPR, HELD = 4;
-    __shared__ uint32_t part[2][4];                    // (in turn: one barrier a row)
+    __shared__ uint32_t part[4];
     const int t = threadIdx.x % TPR;
-    int turn = 0;
-    for (int64_t m = (int64_t)blockIdx.x * ROWS + threadIdx.x / TPR; m < M; m += (int64_t)gridDim.x * ROWS) {
-        const int64_t row = m * ldx;
-        float v[HELD][8];
-        uint32_t top = 0;
-        auto most = [&](const float (&y)[8]) {
+    const int64_t m = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / TPR;
+    const bool live = m < M;
+    const int64_t row = (live ? m : 0) * ldx;
+    float v[HELD][8];
+    uint32_t top = 0;
+    auto most = [&](const float (&y)[8]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                top = max(top, __builtin_bit_cast(uint32_t, y[e]) & 0x7fffffffu);
-        };
+        for (int e = 0; e < 8; ++e)
+            top = max(top, __builtin_bit_cast(uint32_t, y[e]) & 0x7fffffffu);
+    };
+    if (live) {
 #pragma unroll
         for (int i = 0; i < HELD; ++i) {
             const int k = (i * TPR + t) * 8;
@@ -82,68 +84,69 @@ __global__ __launch_bounds__(256) void quantize_rows(const void *x, int8_t *code
             read8<IN>(x, row + k, K - k, y);
             most(y);
         }
+    }
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1)
-            top = max(top, (uint32_t)__shfl_xor((int)top, o));
-        if constexpr (TPR > 64) {                      // (the whole block has this row)
-            if (threadIdx.x % 64 == 0)
-                part[turn][threadIdx.x / 64] = top;
-            __syncthreads();
-            top = max(max(part[turn][0], part[turn][1]), max(part[turn][2], part[turn][3]));
-            turn ^= 1;
+    for (int o = 32; o > 0; o >>= 1)
+        top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    if constexpr (TPR > 64) {
+        if (threadIdx.x % 64 == 0)
+            part[threadIdx.x / 64] = top;
+        __syncthreads();
+        top = max(max(part[0], part[1]), max(part[2], part[3]));
+    }
+    if (!live)
+        return;
+    const bool finite = top < 0x7f800000u;
+    const float s = finite ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
+    if (t == 0)
+        scale[m] = s;
+    const bool some = finite && s > 0.0f;
+    // x times the reciprocal is within 127 * 2^-22 = 3.1e-5 of the quotient (s and its reciprocal
+    // normal numbers, two roundings and the quotient's own), so further than that from a half it
+    // rounds to the same integer; the eight values that hold a nearer one are divided.  Adding
+    // 1.5 * 2^23 rounds to the integer, even at a tie, which is then in the low byte.
+    // 8111 x 8192 FP16 40 us (4.9 TB/s), with eight divisions 53.
+    constexpr float kRound = 12582912.0f;
+    const bool quick = some && s > 1e-35f && s < 1e35f;
+    const float inv = quick ? 1.0f / s : 0.0f;
+    auto put = [&](int k, const float (&y)[8]) {
+        uint32_t q[8];
+        float far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float t = y[e] * inv, r = t + kRound;
+            far = fmaxf(far, fabsf(t - (r - kRound)));
+            q[e] = __builtin_bit_cast(uint32_t, r);
         }
-        const bool finite = top < 0x7f800000u;
-        const float s = finite ? __builtin_bit_cast(float, top) / 127.0f : __builtin_nanf("");
-        if (t == 0)
-            scale[m] = s;
-        const bool some = finite && s > 0.0f;
-        // x times the reciprocal is within 127 * 2^-22 = 3.1e-5 of the quotient (s and its reciprocal
-        // normal numbers, two roundings and the quotient's own), so further than that from a half it
-        // rounds to the same integer; the eight values that hold a nearer one are divided.  Adding
-        // 1.5 * 2^23 rounds to the integer, even at a tie, which is then in the low byte.
-        // 8111 x 8192 FP16 40 us (4.9 TB/s), with eight divisions 53.
-        constexpr float kRound = 12582912.0f;
-        const bool quick = some && s > 1e-35f && s < 1e35f;
-        const float inv = quick ? 1.0f / s : 0.0f;
-        auto put = [&](int k, const float (&y)[8]) {
-            uint32_t q[8];
-            float far = 0.0f;
+        if (!quick || far > 0.4999f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float t = y[e] * inv, r = t + kRound;
-                far = fmaxf(far, fabsf(t - (r - kRound)));
-                q[e] = __builtin_bit_cast(uint32_t, r);
-            }
-            if (!quick || far > 0.4999f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    q[e] = some ? (uint32_t)(int)fminf(fmaxf(__builtin_rintf(y[e] / s), -127.0f), 127.0f) : 0u;
-            }
-            int8_t *dst = codes + m * ldq + k;
-            if (k + 8 <= K) {
-                codes8_t w;
-#pragma unroll
-                for (int d = 0; d < 2; ++d)
-                    w[d] = (q[4 * d] & 0xffu) | (q[4 * d + 1] & 0xffu) << 8 | (q[4 * d + 2] & 0xffu) << 16 | q[4 * d + 3] << 24;
-                *reinterpret_cast<codes8_t *>(dst) = w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (k + e < K)
-                        dst[e] = (int8_t)q[e];
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < HELD; ++i) {
-            const int k = (i * TPR + t) * 8;
-            if (k < K)
-                put(k, v[i]);
+            for (int e = 0; e < 8; ++e)
+                q[e] = some ? (uint32_t)(int)fminf(fmaxf(__builtin_rintf(y[e] / s), -127.0f), 127.0f) : 0u;
         }
-        for (int k = (HELD * TPR + t) * 8; k < K; k += TPR * 8) {
-            float y[8];
-            read8<IN>(x, row + k, K - k, y);
-            put(k, y);
+        int8_t *dst = codes + m * ldq + k;
+        if (k + 8 <= K) {
+            codes8_t w;
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+                w[d] = (q[4 * d] & 0xffu) | (q[4 * d + 1] & 0xffu) << 8 | (q[4 * d + 2] & 0xffu) << 16 | q[4 * d + 3] << 24;
+            *reinterpret_cast<codes8_t *>(dst) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (k + e < K)
+                    dst[e] = (int8_t)q[e];
         }
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int k = (i * TPR + t) * 8;
+        if (k < K)
+            put(k, v[i]);
+    }
+    for (int k = (HELD * TPR + t) * 8; k < K; k += TPR * 8) {
+        float y[8];
+        read8<IN>(x, row + k, K - k, y);
+        put(k, y);
     }
 }
 
@@ -324,13 +327,14 @@ gemm_status_t gemm_run_quantize_int8(const void *X, void *codes, float *scale, i
     if ((uintptr_t)scale % 4 || (uintptr_t)X % size)
         return GEMM_ERR_MISALIGNED;
     const bool wave = K <= 2048;
-    const unsigned grid = (unsigned)std::min(cdiv(M, wave ? 4 : 1), kQuantizeBlocks);
+    const int64_t blocks = cdiv(M, wave ? 4 : 1);
+    const dim3 grid((unsigned)std::min(blocks, kQuantizeBlocks), (unsigned)cdiv(blocks, kQuantizeBlocks));
     auto launch = [&](auto in) {
         if (wave)
-            hipLaunchKernelGGL((quantize_rows<in.value, 64>), dim3(grid), dim3(256), 0, stream, X,
+            hipLaunchKernelGGL((quantize_rows<in.value, 64>), grid, dim3(256), 0, stream, X,
                                static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq);
         else
-            hipLaunchKernelGGL((quantize_rows<in.value, 256>), dim3(grid), dim3(256), 0, stream, X,
+            hipLaunchKernelGGL((quantize_rows<in.value, 256>), grid, dim3(256), 0, stream, X,
                                static_cast<int8_t *>(codes), scale, M, (int)K, ldx, ldq);
     };
     if (in_dtype == GEMM_BF16)
