@@ -8,7 +8,8 @@
 // The two weights are one B whose rows alternate in groups of eight between them
 // (GNT_EXT_PAIRED), so one product of 2 F columns makes both sums, and a gate and its up value
 // are in one lane's registers: the activation and the product need nothing from another
-// lane, and neither sum goes through memory.  The backward call makes the sums again rather
+// lane, and neither sum goes through memory but for K splits' partials (few rows or columns, which
+// the last of a tile's splits or a second pass adds up).  The backward call makes the sums again rather
 // than read them (its caller keeps x alone; 12 M F K operations against 8, and 4 M F
 // values less to keep and read), turns them into dg and du where they are, and stores those
 // once, in the sums' column order: the contraction of dx then runs over both weights'

@@ -51,10 +51,14 @@ inline void fill_args(KernelArgs &a, const Plan &p, const SplitWs &w, void *C, i
 
 // What a plan's launches are expected to take, in us, M x N: the passes over the machine of a
 // beginning and its slabs each, and the partials of K splits at 4 TB/s (less where the kernel sums
-// them: they meet in an L2).  From sweeps of tiles and splits (us, predicted / measured):
-// 200 x 10240 x 4096 four-wave tile 3 splits 43 / 43, 128 x 128 1 split 36 / 43, ping-pong 6 splits
-// 50 / 46; 512 x 8192 x 4096 128 x 128 36 / 45, ping-pong 4 splits 69 / 56; 400 x 16384 x 4096 four-wave
-// 61 / 65, ping-pong 2 splits 80 / 78; 1500 x 10928 x 4096 ping-pong 204 / 187, 128 x 128 179 / 186.
+// them: they meet in an L2).  From sweeps of tiles and splits during development (K in elements of
+// 16 bits; us, predicted / measured): 200 x 10240 x 4096 four-wave tile 3 splits 43 / 43, 128 x 128 1
+// split 36 / 43, ping-pong 6 splits 54 / 46; 512 x 8192 x 4096 128 x 128 36 / 45, ping-pong 4 splits
+// 70 / 56; 400 x 16384 x 4096 four-wave 62 / 65, ping-pong 2 splits 78 / 78; 1500 x 10928 x 4096
+// ping-pong 204 / 187, 128 x 128 179 / 186.  So the 128 x 128 tile is taken to be up to a fifth faster
+// than it is, and ping-pong plans with splits up to a quarter slower: the order of the plans of
+// 129 to 2000 rows is only as good as that (the 8-bit product's slabs were measured at 0.57 us on
+// the 128 x 128 tile, and have the 16-bit ones' 0.45 here).
 inline double plan_us(const Plan &p, int64_t M, int64_t N)
 {
     const double per = p.kt_per_split;

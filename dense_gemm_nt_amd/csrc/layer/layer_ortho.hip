@@ -200,8 +200,8 @@ struct OrthoPlan {
 // the kernels' times: steps of 12 matrices of 768 x 2048 and of one of 4096 x 8192 (12 and 64 slabs)
 // on 256_MN 32 and 117 a pass, 128_MN 19 and 83, 128_S2 21 and 86, 128 16 and 45; squares of 4096 on
 // 256 88 (64 slabs) and 155 (128), of 12 x 768 on 128 16 (12) and 26 (32), of 1000 on 64 9 (16), 11 (32) and
-// 28 (125); steps of 1000 on 64_MN 8.  Over twenty-two shapes the choices were within 4% of the best
-// tile and split of each product.
+// 28 (125); steps of 1000 on 64_MN 8.  Over twenty-two shapes swept during development the choices
+// were within 4% of the best tile and split of each product.
 struct OrthoKind {
     OrthoTile tile;
     int size, at_once, splits;

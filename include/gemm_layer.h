@@ -45,7 +45,10 @@ typedef enum { GEMM_GATE_RELU = 1, GEMM_GATE_GELU = 2, GEMM_GATE_SILU = 3 } gemm
 
 /* The gated block: H = act(X Wg^T) * (X Wu^T), X [M][K], Wg and Wu [F][K], H [M][F] of
  * out_dtype (GEMM_BF16, GEMM_FP16, GEMM_FP32).  Both sums, the activation and the product
- * are FP32, in one kernel; H is rounded once.
+ * are FP32; H is rounded once.  One kernel makes both sums and H of them, in one launch or, where
+ * the tiles' last pass over the machine would be mostly empty, two.  K splits (few tiles) put FP32
+ * partials of the sums into the workspace, which the kernel adds up (a launch that clears counters
+ * is before it) or a second pass.
  *   K % 8 == 0; F below 2^21.  K = 0: act(0) * 0. */
 gemm_status_t gemm_gated_workspace(int64_t M, int64_t F, int64_t K, int64_t *bytes);
 gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void *H, int64_t M,
@@ -62,7 +65,7 @@ gemm_status_t gemm_run_gated(const void *X, const void *Wg, const void *Wu, void
  * du, which are then rounded to the operands' type once, relative to the value 2^-9 at most for
  * BF16 and 2^-12 for FP16.  So an FP32 result is no more exact than that.  FP16's are held in units
  * of powers of two, for dX one of each row, for the weights' gradients one of each column of dH:
- * what is below 2^-28 of the largest finite |dH| of the row (column) times B loses bits, and what
+ * what is below 2^-27 of the largest finite |dH| of the row (column) times B loses bits, and what
  * is below 2^-38 all of them, B = 1.13 max ||X[m]|| max(||Wg[f]||, ||Wu[f]||) over the finite rows, which
  * no factor of dH exceeds.  So no finite gradient ends FP16's range on the way, and an infinity or NaN
  * in dH is in its own row of dX and its own column's dWg and dWu only.
